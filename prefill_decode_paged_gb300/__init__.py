@@ -15,9 +15,13 @@ Public API (see ``include/kv_relayout.h`` for the C ABI it binds):
   the relayout beside other kernels.
 * :func:`relayout_all_prealloc` -- ``run_all`` without any device allocation, for
   callers that cannot allocate (work lists up to 1 MiB).
+* :class:`KVCache` -- a decode pool after the hand-off: ``append()`` new tokens with the position
+  rotation applied on the way, ``attend()`` to the paged keys and values or latents
+  (``include/kv_cache.h``); :func:`rotary_table` fills the table of rotations.
 * ``kv_relayout.checked_library()`` / ``build.build_checked()`` -- the same C ABI
   built with device-side address checks (tests).
 """
 from .kv_relayout import (KVRelayoutError, RelayoutPlan, desc_bytes, library,  # noqa: F401
                           LIB_PATH, STATUS, EXPORTS, relayout_all_prealloc, layout_of_views,
-                          pack_plan, unpack_plan, SmStream)
+                          pack_plan, unpack_plan, SmStream, DTYPE_BF16, DTYPE_FP8_E4M3)
+from .kv_cache import KVCache, rotary_table, DTYPE_F16  # noqa: F401

@@ -13,7 +13,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libkv_relayout.so")
 # the same library with device-side address checks (KVR_DEVICE_CHECKS; tests only)
 LIB_CHECKED = os.path.join(BUILD, "libkv_relayout_checked.so")
-SOURCES = ["plan.cpp", "relayout.cu", "sm_stream.cpp"]
+SOURCES = ["plan.cpp", "relayout.cu", "sm_stream.cpp", "cache.cpp", "cache_append.cu",
+           "cache_attend.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -38,7 +39,7 @@ def _cuda_libdir(nvcc: str) -> str:
 def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".h", ".cuh"))]
-    files.append(os.path.join(INCLUDE, "kv_relayout.h"))
+    files += [os.path.join(INCLUDE, h) for h in os.listdir(INCLUDE) if h.endswith(".h")]
     return files
 
 

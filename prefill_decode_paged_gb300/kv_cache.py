@@ -1,0 +1,336 @@
+"""ctypes binding of the C ABI in ``include/kv_cache.h`` (argument marshalling only).
+
+What a decode instance does with the KV it was handed: :class:`KVCache` appends new tokens to
+one shard pool and attends to it, :func:`rotary_table` fills the table of rotations. Every step
+runs in the CUDA library; there is no fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import numpy as np
+
+from .kv_relayout import (KVRelayoutError, KvrLayout, _contiguous, _Layout, _nbytes, _ptr,
+                          library)
+
+DTYPE_F16 = 3
+INTERLEAVED = 1
+ROTATE_LAST = 2
+FLAGS = {1: "request index", 2: "position", 4: "length", 8: "block id"}
+SCALINGS = {"linear": 1, "base": 2, "ramp": 3, "bands": 4}
+CACHE_EXPORTS = ("kv_cache_create", "kv_cache_destroy", "kv_cache_workspace_bytes",
+                 "kv_cache_append", "kv_cache_attend", "kv_cache_status",
+                 "kv_cache_rotary_table")
+
+# kvc_append and kvc_attend as the C header lays them out (no padding between their fields)
+_APPEND = struct.Struct("=iiQQQqiiQQqqqqQiiIiiiQQqqqq")
+_ATTEND = struct.Struct("=iiiifiQQqiiQQQqqqqqq")
+
+
+class KvcDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("num_layers", "num_components", "kv_heads", "head_dim", "value_dim", "dtype",
+                 "block_size", "per_head")] + \
+               [("num_blocks", ctypes.c_int64), ("pool", ctypes.c_void_p),
+                ("layout", ctypes.POINTER(KvrLayout)), ("scales", ctypes.c_void_p),
+                ("query_heads", ctypes.c_int32), ("max_requests", ctypes.c_int32),
+                ("max_new", ctypes.c_int32)]
+
+
+class KvcScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("original", ctypes.c_int32),
+                ("factor", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("magnitude", ctypes.c_double)]
+
+
+_bound = None
+
+
+def _library() -> ctypes.CDLL:
+    global _bound
+    if _bound is None:
+        lib = library()
+        i32, p = ctypes.c_int32, ctypes.c_void_p
+        for name, args in (("kv_cache_create", [p, p]),
+                           ("kv_cache_workspace_bytes", [p, i32, p]),
+                           ("kv_cache_append", [p, i32, p, p]),
+                           ("kv_cache_attend", [p, i32, p, p]), ("kv_cache_status", [p, p]),
+                           ("kv_cache_rotary_table", [p, i32, i32, ctypes.c_double, p])):
+            fn = getattr(lib, name)
+            fn.restype, fn.argtypes = i32, args
+        lib.kv_cache_destroy.restype, lib.kv_cache_destroy.argtypes = None, [p]
+        _bound = lib
+    return _bound
+
+
+def rotary_table(rows, rotary_dim, base=10000.0, scaling=None):
+    """Cosines and sines of positions [0, rows): a float32 numpy array [rows][rotary_dim] to
+    copy to the device (``kv_cache_rotary_table``). ``scaling``: None or dict(kind="linear" |
+    "base" | "ramp" | "bands", factor=..., original=..., beta_fast=32.0, beta_slow=1.0,
+    magnitude=0.0)."""
+    out = np.empty((rows, rotary_dim), dtype=np.float32)
+    sc = None
+    if scaling is not None:
+        s = dict(scaling)
+        kind = s.pop("kind")
+        if kind not in SCALINGS:
+            raise ValueError(f"scaling kind {kind!r} is none of {sorted(SCALINGS)}")
+        sc = KvcScaling(SCALINGS[kind], int(s.pop("original", 0)), float(s.pop("factor")),
+                        float(s.pop("beta_fast", 32.0)), float(s.pop("beta_slow", 1.0)),
+                        float(s.pop("magnitude", 0.0)))
+        if s:
+            raise ValueError(f"unknown scaling entries {sorted(s)}")
+    st = _library().kv_cache_rotary_table(out.ctypes.data, int(rows), int(rotary_dim),
+                                          float(base), ctypes.byref(sc) if sc else None)
+    if st != 0:
+        raise KVRelayoutError(st, "kv_cache_rotary_table")
+    return out
+
+
+def _desc(pool, layout, scales, per_head, geometry):
+    """The C descriptor and the host objects that it points to."""
+    d = KvcDesc()
+    lay = None if layout is None else _Layout(**layout)
+    sc = None if scales is None else np.ascontiguousarray(scales, dtype=np.float32)
+    for name in ("num_layers", "num_components", "kv_heads", "head_dim", "dtype", "num_blocks",
+                 "query_heads", "max_requests", "max_new", "value_dim"):
+        setattr(d, name, int(geometry[name]))
+    d.block_size, d.per_head = int(geometry["block"]), int(bool(per_head)) if sc is not None else 0
+    d.pool = None if pool is None else _ptr(pool)
+    d.layout = ctypes.pointer(lay.layout) if lay is not None else None
+    d.scales = sc.ctypes.data if sc is not None else None
+    return d, (lay, sc)
+
+
+def workspace_bytes(sm_count, pool=1 << 40, layout=None, scales=None, per_head=False, **geometry):
+    """Validate a cache's geometry on the host; the device bytes of its workspace."""
+    d, keep = _desc(pool, layout, scales, per_head, _defaults(geometry))
+    out = ctypes.c_int64()
+    st = _library().kv_cache_workspace_bytes(ctypes.byref(d), int(sm_count), ctypes.byref(out))
+    if st != 0:
+        raise KVRelayoutError(st, "kv_cache_workspace_bytes")
+    return out.value
+
+
+def _defaults(g):
+    return dict(dict(query_heads=0, max_requests=1, max_new=1, value_dim=0), **g)
+
+
+def _strides(t, n):
+    """Byte strides of the first ``n`` dimensions (0 where the extent is 1)."""
+    es = t.element_size()
+    return [s * es if e > 1 else 0 for s, e in zip(t.stride()[:n], t.shape[:n])]
+
+
+class KVCache:
+    """One shard pool of a decode side: append tokens to it, attend to it.
+
+    ``pool``: a contiguous tensor (or address) [num_layers][num_components][num_blocks][block]
+    [kv_heads][head_dim] -- the decode pool that a :class:`RelayoutPlan` wrote -- with ``kv_heads``
+    the shard's heads; or ``layout=layout_of_views([views])`` for any strided one. ``dtype``:
+    DTYPE_BF16, DTYPE_F16 or DTYPE_FP8_E4M3, the last with ``scales`` [L][C] (``per_head``:
+    [L][C][H]) as the relayout's conversion takes them. Two components hold keys and values
+    (head_dim a multiple of 16, at most 256), one a latent (head_dim 576, of which the first
+    512 are the values). ``query_heads`` (0: append only), ``max_requests`` and ``max_new`` size
+    the workspace of the attention calls; calls on different streams that share a cache must
+    be ordered. Tensors that the calls do not hold for are ValueErrors, what the C library
+    refuses is a KVRelayoutError.
+    """
+
+    def __init__(self, pool, *, num_layers, num_components, kv_heads, head_dim, block,
+                 num_blocks, dtype, scales=None, per_head=False, layout=None, query_heads=0,
+                 max_requests=1, max_new=1, value_dim=0):
+        self._h = None
+        g = dict(num_layers=num_layers, num_components=num_components, kv_heads=kv_heads,
+                 head_dim=head_dim, block=block, num_blocks=num_blocks, dtype=dtype,
+                 query_heads=query_heads, max_requests=max_requests, max_new=max_new,
+                 value_dim=value_dim)
+        es = 1 if dtype == 2 else 2
+        if layout is not None:
+            shape, elem = layout.get("shape"), layout.get("elem_bytes")
+            need = (num_blocks, block, kv_heads, head_dim)
+            if elem is not None and elem != es:
+                raise ValueError(f"views hold {elem}-byte elements; the cache holds {es}-byte ones")
+            if shape is not None and any(h < n for h, n in zip(shape, need)):
+                raise ValueError(f"views are {list(shape)} ([block][token][head][dim]); "
+                                 f"the geometry addresses {list(need)}")
+            if len(layout["bases"]) != num_layers * num_components:
+                raise ValueError(f"{len(layout['bases'])} views; the geometry has "
+                                 f"{num_layers} layers of {num_components} components")
+        elif pool is not None:
+            if not _contiguous(pool):
+                raise ValueError("pool is not contiguous: describe it with a layout")
+            need = num_layers * num_components * num_blocks * block * kv_heads * head_dim * es
+            have = _nbytes(pool)
+            if have is not None and have < need:
+                raise ValueError(f"pool holds {have} bytes; the geometry addresses {need}")
+        if scales is not None:
+            n = num_layers * num_components * (kv_heads if per_head else 1)
+            if np.size(scales) != n:
+                raise ValueError(f"{np.size(scales)} scales; {n} expected")
+        d, _ = _desc(pool, layout, scales, per_head, g)
+        h = ctypes.c_void_p()
+        st = _library().kv_cache_create(ctypes.byref(d), ctypes.byref(h))
+        if st != 0:
+            raise KVRelayoutError(st, "kv_cache_create")
+        import torch
+        self._h, self._pool, self._torch = h.value, (pool, layout), torch
+        self._device = torch.device("cuda", torch.cuda.current_device())
+        self._i32, self._f32 = torch.int32, torch.float32
+        self._types = {torch.bfloat16: 1, torch.float16: DTYPE_F16}
+        self.kv_heads, self.head_dim, self.query_heads = kv_heads, head_dim, query_heads
+        self.value_dim = value_dim or (512 if num_components == 1 else head_dim)
+        self.latent = num_components == 1
+
+    # -- arguments ---------------------------------------------------------------
+
+    def _handle(self):
+        if self._h is None:
+            raise RuntimeError("cache already closed")
+        return self._h
+
+    def _stream(self, stream):
+        if stream is None:
+            return self._torch.cuda.current_stream(self._device).cuda_stream
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def _rows(self, t, name, shape, dtype=None):
+        """Check a tensor of head rows; its byte strides but the last."""
+        if t.device != self._device or tuple(t.shape) != shape or t.stride(-1) != 1 or \
+                (t.dtype is not dtype if dtype is not None else t.dtype not in self._types):
+            raise ValueError(f"{name} is {t.dtype} {list(t.shape)} on {t.device} with strides "
+                             f"{list(t.stride())}; expected {dtype or 'bfloat16 or float16'} "
+                             f"{list(shape)} on {self._device}, rows contiguous")
+        return _strides(t, t.dim() - 1)
+
+    def _list(self, t, name, n):
+        if t.dtype is not self._i32 or t.dim() != 1 or t.shape[0] != n or \
+                t.device != self._device or (n > 1 and t.stride(0) != 1):
+            raise ValueError(f"{name} is {t.dtype} {list(t.shape)} on {t.device}; expected "
+                             f"contiguous int32 [{n}] on {self._device}")
+        return t.data_ptr()
+
+    def _table(self, t):
+        if t.dtype is not self._i32 or t.dim() != 2 or t.device != self._device or \
+                (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"block table is {t.dtype} {list(t.shape)} on {t.device}; expected "
+                             f"int32 [rows][width] on {self._device}, rows contiguous")
+        rows, width = t.shape
+        return t.data_ptr(), max(t.stride(0), width) if rows > 1 else width, rows, width
+
+    # -- calls -------------------------------------------------------------------
+
+    def append(self, layer, k, v, requests, positions, block_table, *, rotary=None,
+               interleaved=False, rotate_last=False, q=None, q_out=None, stream=None):
+        """Append tokens to ``layer``: ``k`` and ``v`` [T][H][D] (``v`` None for latents), token t
+        of request ``requests[t]`` (a row of ``block_table``) at ``positions[t]``, negative for
+        padding. ``rotary``: the table of :func:`rotary_table` on the device, by which the first
+        (``rotate_last``: the last) of each row's elements are rotated; ``q`` [T][heads][dim], where
+        given, is rotated into ``q_out`` (a new tensor by default). Returns ``q_out``."""
+        if not self.latent and v is None:
+            raise ValueError("values are missing")
+        T = k.shape[0]
+        shape = (T, self.kv_heads, self.head_dim)
+        ks = self._rows(k, "k", shape)
+        vs = [0, 0] if v is None else self._rows(v, "v", shape, k.dtype)
+        ids, stride, rows, width = self._table(block_table)
+        rot = rot_rows = rot_dim = q_heads = q_dim = qp = qo = 0
+        qs = os = (0, 0)
+        if rotary is not None:
+            if rotary.dtype is not self._f32 or rotary.dim() != 2 or \
+                    not rotary.is_contiguous() or rotary.device != self._device:
+                raise ValueError("the rotation table is contiguous float32 [positions][rotated] "
+                                 f"on {self._device}")
+            rot, (rot_rows, rot_dim) = rotary.data_ptr(), rotary.shape
+        if q is not None:
+            if q.dim() != 3:
+                raise ValueError(f"q is {list(q.shape)}; expected [T][heads][dim]")
+            _, q_heads, q_dim = q.shape
+            qs = self._rows(q, "q", (T, q_heads, q_dim), k.dtype)
+            if q_out is None:
+                q_out = self._torch.empty((T, q_heads, q_dim), dtype=q.dtype, device=q.device)
+            os = self._rows(q_out, "q_out", (T, q_heads, q_dim), k.dtype)
+            qp, qo = q.data_ptr(), q_out.data_ptr()
+        st = _library().kv_cache_append(
+            self._handle(), layer,
+            _APPEND.pack(T, self._types[k.dtype], self._list(requests, "requests", T),
+                         self._list(positions, "positions", T), ids, stride, rows, width,
+                         k.data_ptr(), 0 if v is None else v.data_ptr(), ks[0], ks[1], vs[0],
+                         vs[1], rot, rot_rows, rot_dim,
+                         (INTERLEAVED if interleaved else 0) | (ROTATE_LAST if rotate_last else 0),
+                         q_heads, q_dim, 0, qp, qo, qs[0], qs[1], os[0], os[1]),
+            self._stream(stream))
+        if st != 0:
+            raise KVRelayoutError(st, "kv_cache_append")
+        return q_out
+
+    def attend(self, layer, q, lengths, block_table, *, out=None, lse=None, scale=None, window=0,
+               stream=None):
+        """Attention of each request's newest tokens over ``layer``: ``q`` [R][new][Hq][D], or
+        [R][Hq][D] for one; ``lengths`` int32 [R] counts the cached tokens, the newest included.
+        ``scale``: D ** -0.5 by default; ``window`` > 0: only that many keys, the token's own
+        included. Returns (out, lse): ``out`` like q with ``value_dim`` elements, ``lse`` float32
+        [R][new][Hq], new tensors by default (``lse=False``: none)."""
+        one = q.dim() == 3
+        if q.dim() not in (3, 4):
+            raise ValueError(f"q is {list(q.shape)}; expected [R][new][heads][dim]")
+        lead = tuple(q.shape[:-2])
+        R, m = lead[0], 1 if one else lead[1]
+        lead += (self.query_heads,)
+        qs = self._rows(q, "q", lead + (self.head_dim,))
+        if out is None:
+            out = self._torch.empty(lead + (self.value_dim,), dtype=q.dtype, device=q.device)
+        os = self._rows(out, "out", lead + (self.value_dim,), q.dtype)
+        if lse is None:
+            lse = self._torch.empty(lead, dtype=self._f32, device=q.device)
+        if lse is False:
+            lse, lp = None, 0
+        else:
+            if lse.dtype is not self._f32 or tuple(lse.shape) != lead or \
+                    not lse.is_contiguous() or lse.device != self._device:
+                raise ValueError(f"lse is {lse.dtype} {list(lse.shape)}; expected contiguous "
+                                 f"float32 {list(lead)} on {self._device}")
+            lp = lse.data_ptr()
+        if one:
+            qs, os = (qs[0], 0, qs[1]), (os[0], 0, os[1])
+        ids, stride, rows, width = self._table(block_table)
+        st = _library().kv_cache_attend(
+            self._handle(), layer,
+            _ATTEND.pack(R, m, self._types[q.dtype], window,
+                         self.head_dim ** -0.5 if scale is None else scale, 0,
+                         self._list(lengths, "lengths", R), ids, stride, rows, width,
+                         q.data_ptr(), out.data_ptr(), lp, qs[0], qs[1], qs[2], os[0], os[1],
+                         os[2]),
+            self._stream(stream))
+        if st != 0:
+            raise KVRelayoutError(st, "kv_cache_attend")
+        return out, lse
+
+    def check(self):
+        """Wait for the device; raise KVRelayoutError (KVR_ERR_DEVICE_BOUNDS) if a call since
+        the last check met a request index, position, length or block id out of range (what
+        was out of range was neither read nor written)."""
+        flags = ctypes.c_uint32()
+        st = _library().kv_cache_status(self._handle(), ctypes.byref(flags))
+        if st != 0:
+            what = ", ".join(n for b, n in FLAGS.items() if flags.value & b)
+            raise KVRelayoutError(st, f"kv_cache_status: {what} out of range" if what
+                                  else "kv_cache_status")
+
+    def close(self):
+        if getattr(self, "_h", None) is not None:
+            _library().kv_cache_destroy(self._h)
+            self._h = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
