@@ -1,0 +1,670 @@
+// cache_attend.cuh -- attention of a request's newest tokens over its paged keys and values.
+//
+// For each key head h of each request, the M = m G rows (m newest tokens, G query heads of h)
+// meet the same keys, so one pass over the cache serves them all. It is bound by HBM: at G = 8
+// and 16-bit elements there are 8 flops a byte of cache, 1/30 of what the card can do.
+//
+// Split. The keys of all (request, head) JOBS, in UNITS of 4 KT keys, form one line that is cut
+// into equal parts, one a resident block, whatever the lengths are; each block works the prefix
+// sums of the lengths out by itself, so that the lengths can stay on the device. A part of a
+// job that is not the whole of it leaves (max, sum, accumulator) in the workspace, and the last
+// of the job's blocks to arrive joins them, in the order of the keys: results do not depend on
+// who is last.
+//
+// Inside a block each of 4 warps takes every fourth tile of KT keys and keeps its own ring of
+// STAGES tiles filled by 16-byte cp.async: nothing in the loop waits for another warp. Rows of
+// padding (beyond the length, or beyond D) are written as zeros, so that what the pool holds
+// there never meets the arithmetic.
+//
+// Products. S^T = K Q^T and O^T += V^T P^T by mma.sync m16n8k16 with keys (then head elements)
+// as the 16 rows and the queries as the 8 columns: with M = 8 nothing is padded, where 128-row
+// tcgen05 tiles would be 15/16 empty; the tensor work is far below the loads at any M here. K
+// and V^T fragments come by ldmatrix (.trans for V), P^T is P's accumulator fragment transposed
+// in registers by movmatrix.
+//
+// Numbers. S, the running maximum and sum, and O are fp32. P enters its product as two 16-bit
+// numbers (rounded, and the rest), so 16 bits of it count: one rounding of P alone would be as
+// large as that of the output. With an E4M3 cache the codes become f16 (exact), Q is scaled per
+// row by a power of two to f16 (exact but for elements 2^-14 of the row's largest), P is f16
+// alone: 11 bits against the output's rounding and the codes' 4 bits. P is scaled by 2^10 in f16
+// so that weights down to 2^-24 of the largest are normal numbers.
+#pragma once
+
+#include <math.h>
+
+#include "cache.h"
+
+namespace kvc {
+
+struct AttendArgs {
+    KvcPlane k_plane, v_plane;
+    KvcSlots slots;
+    const int32_t *lengths;
+    const unsigned char *q;
+    unsigned char *out;
+    float *lse;
+    int64_t q_request, q_token, q_head, out_request, out_token, out_head;
+    const float *k_scale, *v_scale;
+    float *partial;
+    uint32_t *arrived, *flags;
+    int32_t requests, m, H, G, D, window, f16;
+    int32_t chunks;           // passes over a job's keys, RP rows each
+    KvrDiv group;             // by G
+    float scale;
+};
+
+constexpr int ATTEND_WARPS = 4;
+constexpr int ATTEND_THREADS = 32 * ATTEND_WARPS;
+constexpr float P_SHIFT = 10.0f;      // log2 of P's scale in f16
+
+template <int DP, int POOL, int NT>
+struct Attend {
+    static constexpr int ES = POOL == KVR_DTYPE_FP8_E4M3 ? 1 : 2;
+    static constexpr bool F16 = POOL != KVR_DTYPE_BF16;          // type of the products
+    static constexpr bool SPLIT = POOL != KVR_DTYPE_FP8_E4M3;    // P as two numbers
+    static constexpr int ROW = DP * ES;                          // bytes of a row in the ring
+    static constexpr int KT = 2 * 16 * ROW >= 8192 ? 16 : 32;    // keys of a tile
+    static constexpr int KS = KT / 16;
+    static constexpr int STAGE = 2 * KT * ROW;
+    static constexpr int STAGES = STAGE >= 8192 ? 3 : 6;
+    static constexpr int RING = ATTEND_WARPS * STAGES * STAGE;
+    static constexpr int UNIT = ATTEND_WARPS * KT;               // keys of a unit
+    static constexpr int RP = 8 * NT;
+    static constexpr int MT = DP / 16;
+    static constexpr int PITCH = DP + 4;                         // floats of a row to be joined
+    static constexpr int BLOCKS = STAGE > 8192 ? 1 : 2;          // resident on an SM
+    static constexpr int Q_BYTES = RP * DP * 2;
+    static_assert(ATTEND_WARPS * RP * PITCH * 4 <= RING, "the join reuses the ring");
+    // ring, queries, then floats: row scales [RP], per-warp statistics [4][RP][2]; then prefix
+    static constexpr int FIXED = RING + Q_BYTES + 4 * RP + 4 * ATTEND_WARPS * RP * 2 + 16;
+    static constexpr size_t smem(int32_t requests) { return FIXED + 4 * (size_t)(requests + 1); }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t r[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4t(uint32_t r[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+template <bool F16>
+__device__ __forceinline__ void mma(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+    if (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+                     "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+                     "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte chunk `c` of row `r` in an array of rows of ROW bytes, spread so that 8
+// consecutive rows' same chunk lies in 8 different 16-byte columns of shared memory.
+template <int ROW>
+__device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) {
+    if (ROW >= 128) return r * ROW + ((c ^ (r & 7)) << 4);
+    return r * ROW + ((c ^ ((r >> 1) & 3)) << 4);       // 64-byte rows: two share 128 bytes
+}
+
+// A request's visible keys: [lo, n), lo at a multiple of the tile.
+struct Span {
+    int32_t n, lo;
+};
+template <int KT>
+__device__ __forceinline__ Span span_of(const AttendArgs &a, int32_t r, uint32_t *bad) {
+    Span s;
+    s.n = a.lengths[r];
+    const int32_t most = a.slots.width * (int32_t)a.slots.block.d;
+    if (s.n < 0 || s.n > most) {
+        *bad = KVC_FLAG_LENGTH;
+        s.n = s.n < 0 ? 0 : most;
+    }
+    s.lo = a.window > 0 ? max(0, s.n - a.m + 1 - a.window) / KT * KT : 0;
+    return s;
+}
+
+// out (16-bit), four elements of one row, from floats
+template <bool F16>
+__device__ __forceinline__ uint2 narrow4(float4 v) {
+    return make_uint2(narrow2<F16>(v.x, v.y), narrow2<F16>(v.z, v.w));
+}
+
+template <int DP, int POOL, int NT>
+__global__ void __launch_bounds__(ATTEND_THREADS, (Attend<DP, POOL, NT>::BLOCKS))
+attend_kernel(AttendArgs a) {
+    using C = Attend<DP, POOL, NT>;
+    constexpr int KT = C::KT, KS = C::KS, RP = C::RP, MT = C::MT, ROW = C::ROW;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t smem0 = (uint32_t)__cvta_generic_to_shared(smem);
+    unsigned char *q_smem = smem + C::RING;
+    float *row_scale = (float *)(q_smem + C::Q_BYTES);
+    float *stat = row_scale + RP;                       // [warp][RP][max, sum]
+    int32_t *shared_int = (int32_t *)(stat + ATTEND_WARPS * RP * 2);   // [4]
+    int32_t *prefix = shared_int + 4;                   // [requests + 1], in units of one job
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
+
+    wait_for_previous();
+    let_next_start();
+
+    // prefix sums of the requests' units
+    {
+        uint32_t bad = 0;
+        const int32_t per = (a.requests + ATTEND_THREADS - 1) / ATTEND_THREADS;
+        const int32_t r0 = min(a.requests, tid * per), r1 = min(a.requests, r0 + per);
+        int32_t sum = 0;
+        for (int32_t r = r0; r < r1; ++r) {
+            const Span s = span_of<KT>(a, r, &bad);
+            sum += max(1, (s.n - s.lo + C::UNIT - 1) / C::UNIT);
+            prefix[r + 1] = sum;
+        }
+        if (bad != 0 && blockIdx.x == 0) atomicOr(a.flags, bad);
+        int32_t incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int32_t y = __shfl_up_sync(~0u, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) shared_int[warp] = incl;
+        __syncthreads();
+        int32_t before = incl - sum;
+        for (int w = 0; w < warp; ++w) before += shared_int[w];
+        for (int32_t r = r0; r < r1; ++r) prefix[r + 1] += before;
+        if (tid == 0) prefix[0] = 0;
+        __syncthreads();
+    }
+    const int32_t HJ = a.H * a.chunks;
+    const int64_t total = (int64_t)prefix[a.requests] * HJ;
+    const int64_t parts = gridDim.x < total ? (int64_t)gridDim.x : total;
+    if (blockIdx.x >= parts) return;
+    int64_t x = blockIdx.x * total / parts;
+    const int64_t x_end = (blockIdx.x + 1) * total / parts;
+
+    const int32_t M = a.m * a.G;
+    const size_t slot_floats = (size_t)RP * (a.D + 2);
+    const uint32_t ring = smem0 + (uint32_t)(warp * C::STAGES * C::STAGE);
+    const float log2e = 1.4426950408889634f;
+
+    while (x < x_end) {
+        // request (the last r with HJ prefix[r] <= x), job and units of this segment
+        int32_t lo = 0, hi = a.requests - 1;
+        const int32_t xj = (int32_t)(x / HJ);
+        while (lo < hi) {
+            const int32_t mid = (lo + hi + 1) / 2;
+            if (prefix[mid] <= xj) lo = mid; else hi = mid - 1;
+        }
+        const int32_t r = lo;
+        const int32_t units = prefix[r + 1] - prefix[r];
+        const int64_t start = (int64_t)prefix[r] * HJ;
+        const int32_t job = (int32_t)((x - start) / units);
+        const int32_t u0 = (int32_t)((x - start) - (int64_t)job * units);
+        const int32_t u1 = (int32_t)min((int64_t)units, u0 + (x_end - x));
+        const int64_t job_first = start + (int64_t)job * units;
+        x += u1 - u0;
+        const int32_t h = job / a.chunks, row0 = (job - h * a.chunks) * RP;
+        const int32_t rows = min(RP, M - row0);
+        uint32_t bad = 0;
+        const Span sp = span_of<KT>(a, r, &bad);
+        const float ks = POOL == KVR_DTYPE_FP8_E4M3 ? a.k_scale[h] : 1.0f;
+
+        // this warp's tiles; the lane's key of a tile (lane < KT) and its slot
+        const int32_t tiles = (sp.n - sp.lo + KT - 1) / KT;
+        const int32_t t_begin = u0 * ATTEND_WARPS + warp, t_end = min(u1 * ATTEND_WARPS, tiles);
+        const int32_t *table = a.slots.ids + (int64_t)r * a.slots.stride;
+        const int64_t head_off = (int64_t)h * a.k_plane.head_stride;
+        auto slot_of = [&](int32_t t) -> int64_t {      // byte offset in a plane, -1: no key
+            const int32_t j = sp.lo + t * KT + (lane & (KT - 1));
+            if (t >= t_end || j >= sp.n) return -1;
+            const uint32_t entry = a.slots.block.div((uint32_t)j);
+            const int32_t id = __ldg(table + entry);
+            if (id < 0 || id >= a.slots.num_blocks) {
+                bad = KVC_FLAG_BLOCK;
+                return -1;
+            }
+            return id * a.k_plane.block_stride +
+                   (int64_t)(j - (int32_t)(entry * a.slots.block.d)) * a.k_plane.token_stride +
+                   head_off;
+        };
+        auto issue = [&](int32_t stage, int64_t slot) {
+            constexpr int CPR = ROW / 16, RPI = 32 / CPR;   // chunks of a row, rows at a time
+            const uint32_t base = ring + (uint32_t)(stage * C::STAGE);
+            const int c = lane % CPR;
+            const bool in_row = c * 16 < a.D * C::ES;
+#pragma unroll
+            for (int i = 0; i < KT / RPI; ++i) {
+                const int row = i * RPI + lane / CPR;
+                const int64_t off = __shfl_sync(~0u, slot, row);
+                const bool there = off >= 0 && in_row;
+                const int64_t at = there ? off + c * 16 : 0;
+                const uint32_t dst = base + swizzled<ROW>(row, c), n = there ? 16 : 0;
+                cp_async16(dst, a.k_plane.base + at, n);
+                cp_async16(dst + KT * ROW, a.v_plane.base + at, n);
+            }
+        };
+        int64_t next_slot;
+        {
+            int64_t s[C::STAGES];
+#pragma unroll
+            for (int k = 0; k < C::STAGES; ++k) s[k] = slot_of(t_begin + k * ATTEND_WARPS);
+#pragma unroll
+            for (int k = 0; k < C::STAGES - 1; ++k) {
+                if (t_begin + k * ATTEND_WARPS < t_end) issue(k, s[k]);
+                cp_async_commit();
+            }
+            next_slot = s[C::STAGES - 1];
+        }
+
+        // the queries: one warp a row, in the type of the products; rows beyond M are zero
+        for (int row = warp; row < RP; row += ATTEND_WARPS) {
+            const int32_t rho = row0 + row;
+            const int32_t i = (int32_t)a.group.div((uint32_t)rho), gq = rho - i * a.G;
+            const unsigned char *q = a.q + r * a.q_request + i * a.q_token +
+                                     ((int64_t)h * a.G + gq) * a.q_head;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (row < rows && lane * 8 < a.D) w = *(const uint4 *)(q + lane * 16);
+            float factor = a.scale * log2e * ks;
+            if (POOL != KVR_DTYPE_FP8_E4M3) {
+                if (lane * 8 < DP)
+                    *(uint4 *)(q_smem + swizzled<DP * 2>(row, lane)) = w;
+            } else {
+                float f[8], top = 0.0f;
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 p = a.f16 ? widen2<true>(ws[k]) : widen2<false>(ws[k]);
+                    f[2 * k] = p.x, f[2 * k + 1] = p.y;
+                    top = fmaxf(top, fmaxf(fabsf(p.x), fabsf(p.y)));
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+                // down = 2^-e with 2^e <= top < 2^(e+1): exponents kept where both are normal
+                uint32_t e = __float_as_uint(top) >> 23;
+                e = e < 2 || e > 252 ? 127 : e;
+                const float down = __uint_as_float((254 - e) << 23);
+                factor *= __uint_as_float(e << 23);
+                // element d = 4 t + x of 16 is at 2 t + x (x < 2) or 8 + 2 t + x - 2: where the
+                // codes of four neighbours land when two 8-bit elements load as one 16-bit one
+                if (lane * 8 < DP) {
+                    const int grp = lane / 2, half = lane % 2;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int pos = (k & 1 ? 8 : 0) + 4 * half + (k & 2);
+                        *(uint32_t *)(q_smem + swizzled<DP * 2>(row, grp * 2 + pos / 8) +
+                                      (pos % 8) * 2) = narrow2<true>(f[2 * k] * down, f[2 * k + 1] * down);
+                    }
+                }
+            }
+            if (lane == 0) row_scale[row] = factor;
+        }
+        __syncthreads();
+
+        float sc[NT][2], top[NT][2], sum[NT][2];
+        int32_t end[NT][2];                             // first key that the row does not see
+        int32_t seen_all = sp.n;                        // keys below it are seen by every row
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = n * 8 + 2 * t4 + e;
+                sc[n][e] = row_scale[row];
+                top[n][e] = -INFINITY;
+                sum[n][e] = 0.0f;
+                const int32_t i = (int32_t)a.group.div((uint32_t)(row0 + min(row, rows - 1)));
+                end[n][e] = sp.n - a.m + i + 1;
+            }
+        seen_all = sp.n - a.m + 1;
+        const int32_t seen_from = a.window > 0 ? sp.n - a.window : 0;   // keys from it on, by all
+
+        float o[MT][NT][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][n][e] = 0.0f;
+
+        int stage = 0;
+        for (int32_t t = t_begin; t < t_end; t += ATTEND_WARPS) {
+            cp_async_wait<C::STAGES - 2>();
+            __syncwarp();
+            {
+                const int32_t tn = t + (C::STAGES - 1) * ATTEND_WARPS;
+                const int into = stage == 0 ? C::STAGES - 1 : stage - 1;
+                if (tn < t_end) issue(into, next_slot);
+                cp_async_commit();
+                next_slot = slot_of(tn + ATTEND_WARPS);
+            }
+            const uint32_t kbase = ring + (uint32_t)(stage * C::STAGE), vbase = kbase + KT * ROW;
+            stage = stage == C::STAGES - 1 ? 0 : stage + 1;
+
+            // S^T: keys by rows
+            float s[KS][NT][4];
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[k][n][e] = 0.0f;
+            const uint32_t q_base = smem0 + C::RING;
+#pragma unroll
+            for (int d2 = 0; d2 < DP / 32; ++d2) {      // two steps of 16 elements
+                uint32_t b[NT][4];                      // [row tile][step][half]
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    ldmatrix4(b[n], q_base + swizzled<DP * 2>(n * 8 + lane % 8, d2 * 4 + lane / 8));
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    if (C::ES == 2) {
+#pragma unroll
+                        for (int st = 0; st < 2; ++st) {
+                            uint32_t f[4];
+                            ldmatrix4(f, kbase + swizzled<ROW>(k * 16 + lane % 16,
+                                                               (d2 * 2 + st) * 2 + lane / 16));
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma<C::F16>(s[k][n], f, b[n][2 * st], b[n][2 * st + 1]);
+                        }
+                    } else {
+                        uint32_t w[4];                  // keys 0-7, 8-15 of the 1st, 2nd 16 elements
+                        ldmatrix4(w, kbase + swizzled<ROW>(k * 16 + lane % 16, d2 * 2 + lane / 16));
+#pragma unroll
+                        for (int st = 0; st < 2; ++st) {
+                            uint32_t f[4];
+                            f[0] = e4m3_to_f16x2(w[2 * st]);
+                            f[1] = e4m3_to_f16x2(w[2 * st + 1]);
+                            f[2] = e4m3_to_f16x2(w[2 * st] >> 16);
+                            f[3] = e4m3_to_f16x2(w[2 * st + 1] >> 16);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma<C::F16>(s[k][n], f, b[n][2 * st], b[n][2 * st + 1]);
+                        }
+                    }
+                }
+            }
+
+            // softmax over the tile's keys, one pass with the running maximum
+            const int32_t j0 = sp.lo + t * KT;
+            const bool mixed = j0 + KT > seen_all || j0 < seen_from;
+            float shrink[NT][2];
+            bool changed = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float best = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            float &v = s[k][n][2 * u + e];
+                            v *= sc[n][e];
+                            if (mixed) {
+                                const int32_t j = j0 + k * 16 + u * 8 + g;
+                                if (j >= end[n][e] ||
+                                    (a.window > 0 && j < end[n][e] - a.window))
+                                    v = -INFINITY;
+                            }
+                            best = fmaxf(best, v);
+                        }
+#pragma unroll
+                    for (int w = 4; w < 32; w *= 2)
+                        best = fmaxf(best, __shfl_xor_sync(~0u, best, w));
+                    const float next = fmaxf(top[n][e], best);
+                    const float at = (next == -INFINITY ? 0.0f : next) - (C::F16 ? P_SHIFT : 0.0f);
+                    shrink[n][e] = next == top[n][e] ? 1.0f : ex2(top[n][e] - next);
+                    changed |= next != top[n][e];
+                    top[n][e] = next;
+                    float add = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            float &v = s[k][n][2 * u + e];
+                            v = ex2(v - at);
+                            add += v;
+                        }
+                    sum[n][e] = sum[n][e] * shrink[n][e] + add;
+                }
+            if (__any_sync(~0u, changed)) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[i][n][e] *= shrink[n][e & 1];
+            }
+
+            // O^T += V^T P^T
+            uint32_t ph[KS][NT][2], pl[KS][NT][2];
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float p0 = s[k][n][2 * u], p1 = s[k][n][2 * u + 1];
+                        const uint32_t w = narrow2<C::F16>(p0, p1);
+                        ph[k][n][u] = movmatrix(w);
+                        if (C::SPLIT) {
+                            const float2 f = widen2<C::F16>(w);
+                            pl[k][n][u] = movmatrix(narrow2<C::F16>(p0 - f.x, p1 - f.y));
+                        }
+                    }
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                if (C::ES == 2) {
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        uint32_t f[4];
+                        ldmatrix4t(f, vbase + swizzled<ROW>(k * 16 + lane % 8 + (lane / 16) * 8,
+                                                            i * 2 + (lane / 8) % 2));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma<C::F16>(o[i][n], f, ph[k][n][0], ph[k][n][1]);
+                            if (C::SPLIT) mma<C::F16>(o[i][n], f, pl[k][n][0], pl[k][n][1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i2 = 0; i2 < MT / 2; ++i2) {
+                        uint32_t w[4];      // keys 0-7, 8-15 of the 1st, 2nd 16 elements, by pairs
+                        ldmatrix4t(w, vbase + swizzled<ROW>(k * 16 + lane % 16, i2 * 2 + lane / 16));
+#pragma unroll
+                        for (int st = 0; st < 2; ++st) {
+                            uint32_t f[4];  // even elements, odd elements; keys 0-7, then 8-15
+                            f[0] = e4m3_to_f16x2(__byte_perm(w[2 * st], 0, 0x4420));
+                            f[1] = e4m3_to_f16x2(__byte_perm(w[2 * st], 0, 0x4431));
+                            f[2] = e4m3_to_f16x2(__byte_perm(w[2 * st + 1], 0, 0x4420));
+                            f[3] = e4m3_to_f16x2(__byte_perm(w[2 * st + 1], 0, 0x4431));
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma<C::F16>(o[2 * i2 + st][n], f, ph[k][n][0], ph[k][n][1]);
+                        }
+                    }
+                }
+            }
+        }
+        if (bad != 0) atomicOr(a.flags, bad);
+
+        // join the four warps: statistics and accumulators through the ring's memory
+        cp_async_wait<0>();
+        __syncthreads();
+        float *acc = (float *)smem;                     // [warp][RP][PITCH]
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l = sum[n][e];
+#pragma unroll
+                for (int w = 4; w < 32; w *= 2) l += __shfl_xor_sync(~0u, l, w);
+                const int row = n * 8 + 2 * t4 + e;
+                if (g == 0) {
+                    stat[(warp * RP + row) * 2] = top[n][e];
+                    stat[(warp * RP + row) * 2 + 1] = l;
+                }
+                float *to = acc + (warp * RP + row) * C::PITCH;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    to[i * 16 + (C::ES == 2 ? g : 2 * g)] = o[i][n][e];
+                    to[i * 16 + (C::ES == 2 ? g + 8 : 2 * g + 1)] = o[i][n][2 + e];
+                }
+            }
+        __syncthreads();
+        const int64_t job_index = (int64_t)r * HJ + job;
+        const bool whole = u0 == 0 && u1 == units;
+        const int32_t D4 = a.D / 4;
+        float *slot = a.partial + (size_t)(2 * blockIdx.x + (u0 == 0 ? 1 : 0)) * slot_floats;
+        const float vs = POOL == KVR_DTYPE_FP8_E4M3 ? a.v_scale[h] : 1.0f;
+        auto finish = [&](int row, int d4, float4 v, float m, float l) {
+            const int32_t rho = row0 + row;
+            const int32_t i = (int32_t)a.group.div((uint32_t)rho), gq = rho - i * a.G;
+            const int64_t hq = (int64_t)h * a.G + gq;
+            const float inv = l > 0.0f || l != l ? vs / l : 0.0f;
+            v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+            unsigned char *to = a.out + r * a.out_request + i * a.out_token + hq * a.out_head;
+            *(uint2 *)(to + d4 * 8) = a.f16 ? narrow4<true>(v) : narrow4<false>(v);
+            if (d4 == 0 && a.lse != nullptr)
+                a.lse[((int64_t)r * a.m + i) * ((int64_t)a.H * a.G) + hq] =
+                    l > 0.0f || l != l ? (m - (C::F16 ? P_SHIFT : 0.0f) + log2f(l)) * 0.6931471805599453f
+                                       : -INFINITY;
+        };
+        for (int k = tid; k < rows * D4; k += ATTEND_THREADS) {
+            const int row = k / D4, d4 = k - row * D4;
+            float m = -INFINITY, l = 0.0f;
+#pragma unroll
+            for (int w = 0; w < ATTEND_WARPS; ++w) m = fmaxf(m, stat[(w * RP + row) * 2]);
+            float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int w = 0; w < ATTEND_WARPS; ++w) {
+                const float mw = stat[(w * RP + row) * 2];
+                const float f = mw == -INFINITY ? 0.0f : ex2(mw - m);
+                const float4 p = *(const float4 *)(acc + (w * RP + row) * C::PITCH + d4 * 4);
+                if (mw == -INFINITY && stat[(w * RP + row) * 2 + 1] == 0.0f) continue;
+                l += f * stat[(w * RP + row) * 2 + 1];
+                v.x += f * p.x, v.y += f * p.y, v.z += f * p.z, v.w += f * p.w;
+            }
+            if (whole) {
+                finish(row, d4, v, m, l);
+            } else {
+                __stcg((float4 *)(slot + (size_t)row * a.D) + d4, v);
+                if (d4 == 0)
+                    __stcg((float2 *)(slot + (size_t)RP * a.D) + row, make_float2(m, l));
+            }
+        }
+        if (!whole) {
+            // the job's parts: the blocks that hold its first and its last unit, and all between
+            const int64_t c0 = ((job_first + 1) * parts - 1) / total;
+            const int64_t c1 = ((job_first + units) * parts - 1) / total;
+            const int32_t n = (int32_t)(c1 - c0 + 1);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const uint32_t before = atomicAdd(a.arrived + job_index, 1u);
+                shared_int[0] = before == (uint32_t)(n - 1);
+                if (before == (uint32_t)(n - 1)) a.arrived[job_index] = 0;
+            }
+            __syncthreads();
+            if (shared_int[0]) {
+                __threadfence();
+                auto part = [&](int32_t k) {
+                    return a.partial + (size_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * slot_floats;
+                };
+                // weights of the parts, row by row: [n][RP], in the ring's memory
+                float *weight = (float *)smem;
+                for (int row = warp; row < rows; row += ATTEND_WARPS) {
+                    float m = -INFINITY;
+                    for (int k = lane; k < n; k += 32)
+                        m = fmaxf(m, __ldcg((const float2 *)(part(k) + (size_t)RP * a.D) + row).x);
+#pragma unroll
+                    for (int w = 16; w > 0; w /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, w));
+                    float l = 0.0f;
+                    for (int k = lane; k < n; k += 32) {
+                        const float2 p = __ldcg((const float2 *)(part(k) + (size_t)RP * a.D) + row);
+                        const float f = p.x == -INFINITY ? 0.0f : ex2(p.x - m);
+                        weight[k * RP + row] = f;
+                        if (p.x != -INFINITY || p.y != 0.0f) l += f * p.y;
+                    }
+#pragma unroll
+                    for (int w = 16; w > 0; w /= 2) l += __shfl_xor_sync(~0u, l, w);
+                    if (lane == 0) {
+                        stat[row * 2] = m;
+                        stat[row * 2 + 1] = l;
+                    }
+                }
+                __syncthreads();
+                for (int k = tid; k < rows * D4; k += ATTEND_THREADS) {
+                    const int row = k / D4, d4 = k - row * D4;
+                    float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+                    for (int32_t c = 0; c < n; ++c) {
+                        const float f = weight[c * RP + row];
+                        const float4 p = __ldcg((const float4 *)(part(c) + (size_t)row * a.D) + d4);
+                        v.x += f * p.x, v.y += f * p.y, v.z += f * p.z, v.w += f * p.w;
+                    }
+                    finish(row, d4, v, stat[row * 2], stat[row * 2 + 1]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// What the host needs of an instance.
+struct AttendPick {
+    void (*kernel)(AttendArgs);
+    size_t (*smem)(int32_t requests);
+    int32_t unit, rp, blocks;
+};
+
+template <int DP, int POOL, int NT>
+inline AttendPick attend_instance() {
+    using C = Attend<DP, POOL, NT>;
+    return {attend_kernel<DP, POOL, NT>, &C::smem, C::UNIT, C::RP, C::BLOCKS};
+}
+
+// The instance for head dimension D and M rows a job: rows in passes of 8, 16 or 32 (at most 16
+// for D > 128, where 32 rows' accumulators would not fit the registers).
+template <int POOL>
+inline AttendPick attend_pick(int32_t D, int32_t M) {
+    const int nt = M <= 8 ? 1 : M <= 16 || D > 128 ? 2 : 4;
+    if (D <= 64)
+        return nt == 1 ? attend_instance<64, POOL, 1>()
+               : nt == 2 ? attend_instance<64, POOL, 2>() : attend_instance<64, POOL, 4>();
+    if (D <= 128)
+        return nt == 1 ? attend_instance<128, POOL, 1>()
+               : nt == 2 ? attend_instance<128, POOL, 2>() : attend_instance<128, POOL, 4>();
+    return nt == 1 ? attend_instance<256, POOL, 1>() : attend_instance<256, POOL, 2>();
+}
+
+AttendPick attend_pick_bf16(int32_t D, int32_t M);   // one translation unit each
+AttendPick attend_pick_f16(int32_t D, int32_t M);
+AttendPick attend_pick_e4m3(int32_t D, int32_t M);
+
+}  // namespace kvc
