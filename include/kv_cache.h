@@ -11,7 +11,8 @@
  * Step inputs (lengths, positions, block tables) are DEVICE arrays, so that a step can be
  * enqueued, or captured in a CUDA graph, without the host knowing them. They cannot be checked
  * on the host; the kernels check every request index, position, length and block id that they
- * use. What is out of range is neither read nor written, it sets a flag, and
+ * use. What is out of range is neither read nor written (keys and values of a block id out of
+ * range count as zeros, a length out of range as the nearest that is in range), it sets a flag, and
  * kv_cache_status() returns KVR_ERR_DEVICE_BOUNDS with the flags.
  *
  * Launch calls are asynchronous on `stream` (a cudaStream_t; NULL = the legacy default stream),
@@ -43,6 +44,7 @@ extern "C" {
 #define KVC_FLAG_POSITION 2u   /* append: a position beyond the block table or the rotation table */
 #define KVC_FLAG_LENGTH 4u     /* attend: a negative length, or one beyond the block table */
 #define KVC_FLAG_BLOCK 8u      /* a block id outside [0, num_blocks) */
+#define KVC_FLAG_TIMEOUT 16u   /* a wait inside a kernel gave up (a defect of the library) */
 
 typedef struct kvc_desc {
     int32_t num_layers;        /* L >= 1 */

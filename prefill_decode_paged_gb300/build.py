@@ -14,7 +14,8 @@ LIB = os.path.join(BUILD, "libkv_relayout.so")
 # the same library with device-side address checks (KVR_DEVICE_CHECKS; tests only)
 LIB_CHECKED = os.path.join(BUILD, "libkv_relayout_checked.so")
 SOURCES = ["plan.cpp", "relayout.cu", "sm_stream.cpp", "cache.cpp", "cache_append.cu",
-           "cache_attend.cu", "cache_attend_bf16.cu", "cache_attend_f16.cu", "cache_attend_e4m3.cu"]
+           "cache_attend.cu", "cache_latent.cu", "cache_attend_bf16.cu", "cache_attend_f16.cu",
+           "cache_attend_e4m3.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

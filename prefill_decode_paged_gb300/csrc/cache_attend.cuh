@@ -33,21 +33,21 @@
 #include <math.h>
 
 #include "cache.h"
+#include "cache_split.cuh"
 
 namespace kvc {
 
 struct AttendArgs {
     KvcPlane k_plane, v_plane;
-    KvcSlots slots;
-    const int32_t *lengths;
+    SplitArgs split;
     const unsigned char *q;
     unsigned char *out;
     float *lse;
     int64_t q_request, q_token, q_head, out_request, out_token, out_head;
     const float *k_scale, *v_scale;
     float *partial;
-    uint32_t *arrived, *flags;
-    int32_t requests, m, H, G, D, window, f16;
+    uint32_t *arrived;
+    int32_t m, H, G, D, f16;
     int32_t chunks;           // passes over a job's keys, RP rows each
     KvrDiv group;             // by G
     float scale;
@@ -134,23 +134,6 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) {
     return r * ROW + ((c ^ ((r >> 1) & 3)) << 4);       // 64-byte rows: two share 128 bytes
 }
 
-// A request's visible keys: [lo, n), lo at a multiple of the tile.
-struct Span {
-    int32_t n, lo;
-};
-template <int KT>
-__device__ __forceinline__ Span span_of(const AttendArgs &a, int32_t r, uint32_t *bad) {
-    Span s;
-    s.n = a.lengths[r];
-    const int32_t most = a.slots.width * (int32_t)a.slots.block.d;
-    if (s.n < 0 || s.n > most) {
-        *bad = KVC_FLAG_LENGTH;
-        s.n = s.n < 0 ? 0 : most;
-    }
-    s.lo = a.window > 0 ? max(0, s.n - a.m + 1 - a.window) / KT * KT : 0;
-    return s;
-}
-
 // out (16-bit), four elements of one row, from floats
 template <bool F16>
 __device__ __forceinline__ uint2 narrow4(float4 v) {
@@ -174,34 +157,9 @@ attend_kernel(AttendArgs a) {
     wait_for_previous();
     let_next_start();
 
-    // prefix sums of the requests' units
-    {
-        uint32_t bad = 0;
-        const int32_t per = (a.requests + ATTEND_THREADS - 1) / ATTEND_THREADS;
-        const int32_t r0 = min(a.requests, tid * per), r1 = min(a.requests, r0 + per);
-        int32_t sum = 0;
-        for (int32_t r = r0; r < r1; ++r) {
-            const Span s = span_of<KT>(a, r, &bad);
-            sum += max(1, (s.n - s.lo + C::UNIT - 1) / C::UNIT);
-            prefix[r + 1] = sum;
-        }
-        if (bad != 0 && blockIdx.x == 0) atomicOr(a.flags, bad);
-        int32_t incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const int32_t y = __shfl_up_sync(~0u, incl, o);
-            if (lane >= o) incl += y;
-        }
-        if (lane == 31) shared_int[warp] = incl;
-        __syncthreads();
-        int32_t before = incl - sum;
-        for (int w = 0; w < warp; ++w) before += shared_int[w];
-        for (int32_t r = r0; r < r1; ++r) prefix[r + 1] += before;
-        if (tid == 0) prefix[0] = 0;
-        __syncthreads();
-    }
+    unit_prefix<C::UNIT>(a.split, KT, prefix, shared_int);
     const int32_t HJ = a.H * a.chunks;
-    const int64_t total = (int64_t)prefix[a.requests] * HJ;
+    const int64_t total = (int64_t)prefix[a.split.requests] * HJ;
     const int64_t parts = gridDim.x < total ? (int64_t)gridDim.x : total;
     if (blockIdx.x >= parts) return;
     int64_t x = blockIdx.x * total / parts;
@@ -213,43 +171,31 @@ attend_kernel(AttendArgs a) {
     const float log2e = 1.4426950408889634f;
 
     while (x < x_end) {
-        // request (the last r with HJ prefix[r] <= x), job and units of this segment
-        int32_t lo = 0, hi = a.requests - 1;
-        const int32_t xj = (int32_t)(x / HJ);
-        while (lo < hi) {
-            const int32_t mid = (lo + hi + 1) / 2;
-            if (prefix[mid] <= xj) lo = mid; else hi = mid - 1;
-        }
-        const int32_t r = lo;
-        const int32_t units = prefix[r + 1] - prefix[r];
-        const int64_t start = (int64_t)prefix[r] * HJ;
-        const int32_t job = (int32_t)((x - start) / units);
-        const int32_t u0 = (int32_t)((x - start) - (int64_t)job * units);
-        const int32_t u1 = (int32_t)min((int64_t)units, u0 + (x_end - x));
-        const int64_t job_first = start + (int64_t)job * units;
+        const Segment seg = segment_at(x, x_end, prefix, a.split.requests, HJ);
+        const int32_t r = seg.r, job = seg.job, u0 = seg.u0, u1 = seg.u1, units = seg.units;
         x += u1 - u0;
         const int32_t h = job / a.chunks, row0 = (job - h * a.chunks) * RP;
         const int32_t rows = min(RP, M - row0);
         uint32_t bad = 0;
-        const Span sp = span_of<KT>(a, r, &bad);
+        const Span sp = span_of(a.split, r, KT, &bad);
         const float ks = POOL == KVR_DTYPE_FP8_E4M3 ? a.k_scale[h] : 1.0f;
 
         // this warp's tiles; the lane's key of a tile (lane < KT) and its slot
         const int32_t tiles = (sp.n - sp.lo + KT - 1) / KT;
         const int32_t t_begin = u0 * ATTEND_WARPS + warp, t_end = min(u1 * ATTEND_WARPS, tiles);
-        const int32_t *table = a.slots.ids + (int64_t)r * a.slots.stride;
+        const int32_t *table = a.split.slots.ids + (int64_t)r * a.split.slots.stride;
         const int64_t head_off = (int64_t)h * a.k_plane.head_stride;
         auto slot_of = [&](int32_t t) -> int64_t {      // byte offset in a plane, -1: no key
             const int32_t j = sp.lo + t * KT + (lane & (KT - 1));
             if (t >= t_end || j >= sp.n) return -1;
-            const uint32_t entry = a.slots.block.div((uint32_t)j);
+            const uint32_t entry = a.split.slots.block.div((uint32_t)j);
             const int32_t id = __ldg(table + entry);
-            if (id < 0 || id >= a.slots.num_blocks) {
+            if (id < 0 || id >= a.split.slots.num_blocks) {
                 bad = KVC_FLAG_BLOCK;
                 return -1;
             }
             return id * a.k_plane.block_stride +
-                   (int64_t)(j - (int32_t)(entry * a.slots.block.d)) * a.k_plane.token_stride +
+                   (int64_t)(j - (int32_t)(entry * a.split.slots.block.d)) * a.k_plane.token_stride +
                    head_off;
         };
         auto issue = [&](int32_t stage, int64_t slot) {
@@ -340,7 +286,7 @@ attend_kernel(AttendArgs a) {
                 end[n][e] = sp.n - a.m + i + 1;
             }
         seen_all = sp.n - a.m + 1;
-        const int32_t seen_from = a.window > 0 ? sp.n - a.window : 0;   // keys from it on, by all
+        const int32_t seen_from = a.split.window > 0 ? sp.n - a.split.window : 0;   // keys from it on, by all
 
         float o[MT][NT][4];
 #pragma unroll
@@ -428,7 +374,7 @@ attend_kernel(AttendArgs a) {
                             if (mixed) {
                                 const int32_t j = j0 + k * 16 + u * 8 + g;
                                 if (j >= end[n][e] ||
-                                    (a.window > 0 && j < end[n][e] - a.window))
+                                    (a.split.window > 0 && j < end[n][e] - a.split.window))
                                     v = -INFINITY;
                             }
                             best = fmaxf(best, v);
@@ -511,7 +457,7 @@ attend_kernel(AttendArgs a) {
                 }
             }
         }
-        if (bad != 0) atomicOr(a.flags, bad);
+        if (bad != 0) atomicOr(a.split.flags, bad);
 
         // join the four warps: statistics and accumulators through the ring's memory
         cp_async_wait<0>();
@@ -580,8 +526,8 @@ attend_kernel(AttendArgs a) {
         }
         if (!whole) {
             // the job's parts: the blocks that hold its first and its last unit, and all between
-            const int64_t c0 = ((job_first + 1) * parts - 1) / total;
-            const int64_t c1 = ((job_first + units) * parts - 1) / total;
+            const int64_t c0 = part_of(seg.job_first, parts, total);
+            const int64_t c1 = part_of(seg.job_first + units - 1, parts, total);
             const int32_t n = (int32_t)(c1 - c0 + 1);
             __threadfence();
             __syncthreads();

@@ -1,0 +1,701 @@
+// cache_latent.cu -- attention of a request's newest tokens over its paged latents (tcgen05).
+//
+// A latent row is 576 elements: it is the key of all query heads, and its first 512 elements are
+// the value. The R = m Hq rows of a request (in passes of 128) meet each latent once: 2 x 1088
+// flops a row and latent against its 1152 bytes. With 128 rows that is 242 flops a byte, close
+// to what the card has (278), so both HBM and the tensor cores have to be kept busy; with 16 rows
+// it is HBM alone, and the 128-row products cost nothing that is missed.
+//
+// Why a cluster of two. O is 128 x 512 in fp32, all of an SM's 512 columns of tensor memory, and
+// leaves no room for S. So two SMs share a tile of KT keys, each with HALF OF THE ELEMENTS (256
+// of the value and 32 of the rest): each loads its half of every latent, and nothing twice; each
+// computes the partial S = Q K^T of its half and sends it to the other through distributed
+// shared memory (24 KB a tile); each adds the two halves in the same way, so both hold the same
+// softmax, and multiplies P with its 256 value elements. No product and no load is done twice;
+// the exponentials are.
+//
+// Tensor memory: O [128 x 256] fp32 in columns 0-255; Q, 288 16-bit elements a row, in 144
+// columns, where the products read it as operand A (from shared memory it would take 72 KB of it
+// and cost more of its bandwidth than all of K); two S of KT = 48 columns each, which P (24
+// columns of 16-bit pairs) overwrites. 496 of 512. KT = 48 is what that leaves.
+//
+// Shared memory: a ring of 6 tiles' halves (27 KB each) that 4 warps fill by 16-byte cp.async,
+// one row after another, so that any block size and stride will do and rows of padding are
+// zeros; and the two halves of S that the other SM sends. A tile is laid out in 128-byte rows of
+// 64 elements (swizzled), which serve as the K-major operand of S and as the MN-major operand
+// of O.
+//
+// Warps: 4 of softmax (one thread a row), 4 of loads, 1 that issues the products. S of tile i + 1
+// is computed, read and sent before the softmax of tile i waits for the other half, so the
+// exchange is off the path. O is rescaled only when a row's maximum grows by more than 2^8 over
+// the one that its P is relative to (P is then at most 2^8, fine in either 16-bit type); that
+// happens in the first tiles of a job and hardly again.
+//
+// Numbers: S, maxima, sums, O and all joins are fp32. P is rounded once to the pool's 16-bit type
+// for its product: rounding it twice as fine would cost half of the products again.
+//
+// Every wait ends: after two seconds it gives up, flags KVC_FLAG_TIMEOUT, and all warps run out
+// of their loops to the end of the kernel.
+#include <math.h>
+
+#include <algorithm>
+
+#include "cache_latent.h"
+#include "cache_split.cuh"
+
+namespace {
+
+using namespace kvc;
+
+constexpr int KT = 48;                    // keys of a tile
+constexpr int ROWS = 128;                 // query rows of a pass
+constexpr int HALF = 256, REST = 32;      // value elements and others of an SM
+constexpr int STAGES = 6, LAG = 3;        // tiles in the ring; loads in flight before a wait
+constexpr int CHUNK = KT * 128;           // 64 elements of each key
+constexpr int STAGE = 4 * CHUNK + KT * 64;
+constexpr int XBUF = ROWS * KT * 4;
+constexpr int WARPS = 9, THREADS = 32 * WARPS;
+constexpr int OFF_XBUF = STAGES * STAGE, OFF_BARS = OFF_XBUF + 2 * XBUF, OFF_PREFIX = OFF_BARS + 256;
+constexpr uint32_t COL_O = 0, COL_Q = 256, COL_S = 400;
+constexpr int VALUES = KVC_LATENT_VALUES;
+// floats of one part's results: [element / 4][row][4], then (max, sum) a row
+constexpr size_t SLOT = (size_t)ROWS * VALUES + 2 * ROWS;
+
+// barriers, in 8-byte words after OFF_BARS
+enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, S_FULL = K_EMPTY + STAGES, P_FULL = S_FULL + 2,
+       X_FULL = P_FULL + 2, X_EMPTY = X_FULL + 2, O_DONE = X_EMPTY + 2, Q_FULL = O_DONE + 2, DRAIN,
+       BARS };
+constexpr int OFF_TMEM = BARS * 8, OFF_ABORT = OFF_TMEM + 4, OFF_SCRATCH = OFF_TMEM + 16;
+static_assert(OFF_SCRATCH + 4 * WARPS <= 256, "the words after the barriers");
+
+struct LatentArgs {
+    KvcPlane plane;
+    SplitArgs split;
+    const unsigned char *q;
+    unsigned char *out;
+    float *lse;
+    int64_t q_request, q_token, q_head, out_request, out_token, out_head;
+    float *partial;
+    int32_t m, Hq, chunks, parts, least;
+    KvrDiv heads;             // by Hq
+    float scale;
+};
+
+// -- barriers -------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// the same barrier of the other SM of the cluster
+__device__ __forceinline__ void bar_arrive_remote(uint32_t remote) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t remote_addr(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint64_t now_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+
+struct Waits {
+    volatile int32_t *abort;
+    uint32_t *flags;
+    // waits for the phase of `parity`; false after two seconds, or once another wait gave up
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+        uint64_t began = 0;
+        for (uint32_t n = 0;; ++n) {
+            uint32_t done;
+            asm volatile("{\n\t.reg .pred p;\n\t"
+                         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                         "selp.u32 %0, 1, 0, p;\n\t}"
+                         : "=r"(done)
+                         : "r"(bar), "r"(parity)
+                         : "memory");
+            if (done) return true;
+            if ((n & 63) == 63) {
+                if (*abort) return false;
+                const uint64_t t = now_ns();
+                if (began == 0) began = t;
+                if (t - began > 2000000000ull) {
+                    *abort = 1;
+                    atomicOr(flags, KVC_FLAG_TIMEOUT);
+                    return false;
+                }
+            }
+        }
+    }
+    // the same answer for all lanes of a warp, which go on together
+    __device__ __forceinline__ bool all(uint32_t bar, uint32_t parity) const {
+        return __all_sync(~0u, (*this)(bar, parity));
+    }
+};
+
+// -- tensor memory and products ---------------------------------------------------
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tm_load16(uint32_t v[16], uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+                 "%10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                   "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]),
+                   "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t v[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, "
+                 "%10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+                 "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
+                 "r"(v[14]), "r"(v[15])
+                 : "memory");
+}
+__device__ __forceinline__ void tm_store8(uint32_t addr, const uint32_t v[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+// D (+)= A B with A in tensor memory, B in shared memory
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(add)
+                 : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+// Shared-memory operand: start, leading and stride offsets in bytes; layout 2 = 128-byte
+// swizzle, 4 = 64-byte swizzle. (A shared address of a cluster holds the rank above its 18 bits.)
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride,
+                                            uint32_t layout) {
+    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
+           (1ull << 46) | ((uint64_t)layout << 61);
+}
+
+// fp32 accumulation of 16-bit operands: type (0 f16, 1 bf16) of both, B transposed (MN-major), N
+__host__ __device__ constexpr uint32_t idesc(bool bf16, bool mn_major, uint32_t n) {
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
+           ((mn_major ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((ROWS >> 4) << 24);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// -- the kernel -------------------------------------------------------------------
+
+template <bool F16>
+__global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t smem0 = smem_addr(smem), bars = smem0 + OFF_BARS;
+    int32_t *prefix = (int32_t *)(smem + OFF_PREFIX);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    uint32_t rank;
+    asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
+    const Waits wait = {(volatile int32_t *)(smem + OFF_BARS + OFF_ABORT), a.split.flags};
+    auto bar = [&](int which) { return bars + 8 * which; };
+
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         bars + OFF_TMEM)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            bar_init(bar(K_FULL + i), 4);         // the loading warps
+            bar_init(bar(K_EMPTY + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(bar(S_FULL + i), 1);
+            bar_init(bar(P_FULL + i), 4);         // the softmax warps
+            bar_init(bar(X_FULL + i), 4);         // those of the other SM
+            bar_init(bar(X_EMPTY + i), 4);
+            bar_init(bar(O_DONE + i), 1);
+        }
+        bar_init(bar(Q_FULL), 4);
+        bar_init(bar(DRAIN), 1);
+        *wait.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    wait_for_previous();
+    let_next_start();
+    unit_prefix<KT>(a.split, 1, prefix, (int32_t *)(smem + OFF_BARS + OFF_SCRATCH));
+    fence_before();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    fence_after();
+    const uint32_t tmem = *(volatile uint32_t *)(smem + OFF_BARS + OFF_TMEM);
+
+    const int64_t total = (int64_t)prefix[a.split.requests] * a.chunks;
+    const int64_t parts = max((int64_t)1, min((int64_t)a.parts, total / a.least));
+    const int64_t part = blockIdx.x / 2;
+    int64_t x = part < parts ? part * total / parts : 0;
+    const int64_t x_end = part < parts ? (part + 1) * total / parts : 0;
+    const int32_t M = a.m * a.Hq;
+
+    if (warp < 4) {
+        // ---- softmax: thread `tid` has query row `tid` of the pass (lane of tensor memory) ----
+        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        const uint32_t x_remote = remote_addr(smem0 + OFF_XBUF, rank ^ 1u);
+        const uint32_t bars_remote = remote_addr(bars, rank ^ 1u);
+        const float sc = a.scale * 1.4426950408889634f;
+        uint32_t it = 0;                          // tiles so far
+        uint32_t ok = 1;
+
+        // this SM's half of S of tile `i`, in registers and on its way to the other SM
+        auto fetch = [&](uint32_t i, uint32_t s[KT]) -> bool {
+            const uint32_t b = i & 1, ph = (i >> 1) & 1;
+            if (!wait.all(bar(S_FULL + b), ph)) return false;
+            fence_after();
+#pragma unroll
+            for (int k = 0; k < KT / 16; ++k) tm_load16(s + 16 * k, lanes + COL_S + b * KT + 16 * k);
+            wait_ld();
+            if (!wait.all(bar(X_EMPTY + b), ph ^ 1)) return false;
+            const uint32_t to = x_remote + b * XBUF + tid * 16;
+#pragma unroll
+            for (int k = 0; k < KT / 4; ++k)
+                asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + k * ROWS * 16),
+                             "r"(s[4 * k]), "r"(s[4 * k + 1]), "r"(s[4 * k + 2]), "r"(s[4 * k + 3])
+                             : "memory");
+            __syncwarp();
+            if (lane == 0) bar_arrive_remote(bars_remote + 8 * (X_FULL + b));
+            return true;
+        };
+
+        // the thread's row of q in a segment, and this SM's half of it into tensor memory
+        struct Row {
+            int32_t token, hq;
+            bool mine;
+        };
+        auto row_of = [&](const Segment &seg) -> Row {
+            const int32_t rho = seg.job * ROWS + tid;
+            const int32_t token = (int32_t)a.heads.div((uint32_t)rho);
+            return {token, rho - token * a.Hq, rho < M};
+        };
+        auto load_q = [&](const Segment &seg) {
+            const Row row = row_of(seg);
+            const unsigned char *q = a.q + seg.r * a.q_request + row.token * a.q_token + row.hq * a.q_head;
+            const unsigned char *first = q + rank * (HALF * 2), *rest = q + (VALUES + rank * REST) * 2;
+#pragma unroll
+            for (int k = 0; k < 9; ++k) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (row.mine) v = __ldg((const uint4 *)(k < 8 ? first + k * 64 : rest) + e);
+                    w[4 * e] = v.x, w[4 * e + 1] = v.y, w[4 * e + 2] = v.z, w[4 * e + 3] = v.w;
+                }
+                tm_store16(lanes + COL_Q + 16 * k, w);
+            }
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(Q_FULL));
+        };
+
+        Segment seg = {};
+        if (x < x_end) {
+            seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
+            load_q(seg);
+        }
+        while (ok && x < x_end) {
+            x += seg.u1 - seg.u0;
+            uint32_t bad = 0;
+            const Span sp = span_of(a.split, seg.r, 1, &bad);
+            const Row row = row_of(seg);
+            const int32_t token = row.token, hq = row.hq;
+            const bool mine = row.mine;
+
+            const int32_t end = sp.n - a.m + token + 1;
+            const int32_t seen_all = sp.n - a.m + 1;
+            const int32_t seen_from = a.split.window > 0 ? sp.n - a.split.window : 0;
+            float top = -INFINITY, sum = 0.0f;    // what P and O are relative to; sum of P
+
+            // softmax of tile `i` (unit u of the job) whose own half is in s
+            auto finish = [&](uint32_t i, int32_t u, uint32_t s[KT]) -> bool {
+                const uint32_t b = i & 1, ph = (i >> 1) & 1;
+                if (!wait.all(bar(X_FULL + b), ph)) return false;
+                float best = -INFINITY;
+                const int32_t j0 = sp.lo + u * KT;
+                const bool mixed = j0 + KT > seen_all || j0 < seen_from;
+                const float4 *from = (const float4 *)(smem + OFF_XBUF + b * XBUF) + tid;
+#pragma unroll
+                for (int k = 0; k < KT / 4; ++k) {
+                    const float4 o = from[k * ROWS];
+                    const float add[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v = (__uint_as_float(s[4 * k + e]) + add[e]) * sc;
+                        if (mixed) {
+                            const int32_t j = j0 + 4 * k + e;
+                            if (j >= end || (a.split.window > 0 && j < end - a.split.window))
+                                v = -INFINITY;
+                        }
+                        s[4 * k + e] = __float_as_uint(v);
+                        best = fmaxf(best, v);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) bar_arrive_remote(bars_remote + 8 * (X_EMPTY + b));
+                if (u == seg.u0) {
+                    top = best;                   // O starts from this tile's product
+                } else if (__any_sync(~0u, best > top + 8.0f)) {
+                    const float next = fmaxf(top, best);
+                    const float shrink = next == top ? 1.0f : ex2(top - next);
+                    top = next;
+                    sum *= shrink;
+                    if (!wait.all(bar(O_DONE + (b ^ 1)), ((i - 1) >> 1) & 1)) return false;
+                    fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < HALF; c += 16) {
+                        uint32_t w[16];
+                        tm_load16(w, lanes + COL_O + c);
+                        wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            w[e] = __float_as_uint(__uint_as_float(w[e]) * shrink);
+                        tm_store16(lanes + COL_O + c, w);
+                    }
+                    wait_st();
+                }
+                const float at = top == -INFINITY ? 0.0f : top;
+                uint32_t p[KT / 2];
+#pragma unroll
+                for (int k = 0; k < KT / 2; ++k) {
+                    const float p0 = ex2(__uint_as_float(s[2 * k]) - at);
+                    const float p1 = ex2(__uint_as_float(s[2 * k + 1]) - at);
+                    sum += p0 + p1;
+                    p[k] = narrow2<F16>(p0, p1);
+                }
+                tm_store16(lanes + COL_S + b * KT, p);
+                tm_store8(lanes + COL_S + b * KT + 16, p + 16);
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(P_FULL + b));
+                return true;
+            };
+
+            // two tiles a turn, S of the next always fetched ahead of this one's softmax
+            uint32_t s0[KT], s1[KT];
+            int32_t u = seg.u0;
+            ok = fetch(it, s0);
+            while (ok) {
+                if (u + 1 < seg.u1) ok = fetch(it + 1, s1);
+                if (!ok || !(ok = finish(it, u, s0))) break;
+                ++it, ++u;
+                if (u >= seg.u1) break;
+                if (u + 1 < seg.u1) ok = fetch(it + 1, s0);
+                if (!ok || !(ok = finish(it, u, s1))) break;
+                ++it, ++u;
+                if (u >= seg.u1) break;
+            }
+            if (!ok) break;
+            // all products with this q are done: the next segment's may start
+            const Segment done = seg;
+            if (x < x_end) {
+                seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
+                load_q(seg);
+            }
+            if (!(ok = wait.all(bar(O_DONE + ((it - 1) & 1)), ((it - 1) >> 1) & 1))) break;
+            fence_after();
+
+            const bool whole = done.u0 == 0 && done.u1 == done.units;
+            const bool some = sum > 0.0f || sum != sum;
+            const float inv = some ? 1.0f / sum : 0.0f;
+            float *slot = a.partial + (size_t)(2 * part + (done.u0 == 0 ? 1 : 0)) * SLOT;
+            unsigned char *out = a.out + done.r * a.out_request + token * a.out_token +
+                                 hq * a.out_head + rank * (HALF * 2);
+#pragma unroll 1
+            for (int c = 0; c < HALF; c += 16) {
+                uint32_t w[16];
+                tm_load16(w, lanes + COL_O + c);
+                wait_ld();
+                if (mine && whole) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float v = __uint_as_float(w[e]);
+                        w[e] = some ? __float_as_uint(v * inv) : 0u;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint4 v;
+                        const float *f = (const float *)w + 8 * e;
+                        v.x = narrow2<F16>(f[0], f[1]), v.y = narrow2<F16>(f[2], f[3]);
+                        v.z = narrow2<F16>(f[4], f[5]), v.w = narrow2<F16>(f[6], f[7]);
+                        *(uint4 *)(out + c * 2 + e * 16) = v;
+                    }
+                } else if (mine) {
+                    float4 *to = (float4 *)slot + (size_t)((rank * HALF + c) / 4) * ROWS + tid;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        __stcg(to + e * ROWS, *(const float4 *)((const float *)w + 4 * e));
+                }
+                __syncwarp();
+            }
+            fence_before();
+            if (mine && rank == 0) {
+                if (whole) {
+                    if (a.lse != nullptr)
+                        a.lse[((int64_t)done.r * a.m + token) * a.Hq + hq] =
+                            some ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+                } else {
+                    __stcg((float2 *)(slot + (size_t)ROWS * VALUES) + tid, make_float2(top, sum));
+                }
+            }
+        }
+    } else if (warp < 8) {
+        // ---- loads: warp w of 4 has 12 keys of a tile ----
+        const int w = warp - 4;
+        constexpr int MINE = KT / 4;
+        uint32_t it = 0, bad = 0, ok = 1;
+        while (ok && x < x_end) {
+            const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
+            x += seg.u1 - seg.u0;
+            const Span sp = span_of(a.split, seg.r, 1, &bad);
+            const int32_t *table = a.split.slots.ids + (int64_t)seg.r * a.split.slots.stride;
+            auto slot_of = [&](int32_t u) -> int64_t {      // of the lane's key, -1: none
+                const int32_t j = sp.lo + u * KT + w * MINE + lane;
+                if (lane >= MINE || u >= seg.u1 || j >= sp.n) return -1;
+                const uint32_t entry = a.split.slots.block.div((uint32_t)j);
+                const int32_t id = __ldg(table + entry);
+                if (id < 0 || id >= a.split.slots.num_blocks) {
+                    bad |= KVC_FLAG_BLOCK;
+                    return -1;
+                }
+                return id * a.plane.block_stride +
+                       (int64_t)(j - (int32_t)(entry * a.split.slots.block.d)) * a.plane.token_stride;
+            };
+            int64_t next = slot_of(seg.u0);
+            for (int32_t u = seg.u0; u < seg.u1; ++u, ++it) {
+                const int64_t slot = next;
+                next = slot_of(u + 1);
+                const uint32_t stage = it % STAGES;
+                if (!(ok = wait.all(bar(K_EMPTY + stage), (it / STAGES + 1) & 1))) break;
+                const uint32_t base = smem0 + stage * STAGE;
+                const unsigned char *src = a.plane.base;
+                // values: 32 pieces of 16 bytes a key, one key at a time
+#pragma unroll
+                for (int k = 0; k < MINE; ++k) {
+                    const int64_t off = __shfl_sync(~0u, slot, k);
+                    const uint32_t row = w * MINE + k;
+                    const int64_t at = off >= 0 ? off + rank * (HALF * 2) + lane * 16 : 0;
+                    const uint32_t dst = base + (lane / 8) * CHUNK + row * 128 + (((lane % 8) ^ (row & 7)) << 4);
+                    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst),
+                                 "l"(src + at), "r"(off >= 0 ? 16 : 0)
+                                 : "memory");
+                }
+                // the rest: 4 pieces a key, 8 keys at a time
+#pragma unroll
+                for (int k = 0; k < MINE; k += 8) {
+                    const int mine = k + lane / 4;
+                    const int64_t off = __shfl_sync(~0u, slot, mine < MINE ? mine : 0);
+                    const uint32_t row = w * MINE + mine, c = lane % 4;
+                    const int64_t at = off >= 0 ? off + (VALUES + rank * REST) * 2 + c * 16 : 0;
+                    const uint32_t dst = base + 4 * CHUNK + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+                    if (mine < MINE)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                                     "l"(src + at), "r"(off >= 0 ? 16 : 0)
+                                     : "memory");
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (it >= LAG) {                  // the tile LAG before this one has come
+                    asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(bar(K_FULL + (it - LAG) % STAGES));
+                }
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0)
+            for (uint32_t i = it > LAG ? it - LAG : 0; i < it; ++i) bar_arrive(bar(K_FULL + i % STAGES));
+        if (bad != 0) atomicOr(a.split.flags, bad);
+    } else if (lane == 0) {
+        // ---- products: S of a tile, then O of the tile before ----
+        constexpr uint32_t ID_S = idesc(!F16, false, KT), ID_O = idesc(!F16, true, HALF);
+        uint32_t it = 0, segments = 0;
+        uint32_t ok = 1, begun = 0;               // the tile before: is it a segment's first?
+        auto multiply_v = [&](uint32_t i, uint32_t first) -> bool {
+            const uint32_t b = i & 1, stage = i % STAGES;
+            if (!wait(bar(P_FULL + b), (i >> 1) & 1)) return false;
+            fence_after();
+            const uint32_t base = smem0 + stage * STAGE;
+#pragma unroll
+            for (int k = 0; k < KT / 16; ++k)
+                product(tmem + COL_O, tmem + COL_S + b * KT + 8 * k,
+                        operand(base + k * 2048, CHUNK, 1024, 2), ID_O, !(first && k == 0));
+            commit(bar(K_EMPTY + stage));
+            commit(bar(O_DONE + b));
+            return true;
+        };
+        while (ok && x < x_end) {
+            const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
+            x += seg.u1 - seg.u0;
+            for (int32_t u = seg.u0; u < seg.u1; ++u, ++it) {
+                const uint32_t b = it & 1, stage = it % STAGES;
+                if (u == seg.u0) {
+                    // the segment before ends first: its results are waited for
+                    if (it > 0 && !(ok = multiply_v(it - 1, begun))) break;
+                    if (!(ok = wait(bar(Q_FULL), segments++ & 1))) break;
+                }
+                if (!(ok = wait(bar(K_FULL + stage), (it / STAGES) & 1))) break;
+                fence_after();
+                const uint32_t base = smem0 + stage * STAGE;
+#pragma unroll
+                for (int k = 0; k < HALF / 16; ++k)
+                    product(tmem + COL_S + b * KT, tmem + COL_Q + 8 * k,
+                            operand(base + (k / 4) * CHUNK + (k % 4) * 32, 16, 1024, 2), ID_S, k > 0);
+#pragma unroll
+                for (int k = 0; k < REST / 16; ++k)
+                    product(tmem + COL_S + b * KT, tmem + COL_Q + HALF / 2 + 8 * k,
+                            operand(base + 4 * CHUNK + k * 32, 16, 512, 4), ID_S, 1);
+                commit(bar(S_FULL + b));
+                if (u > seg.u0 && !(ok = multiply_v(it - 1, begun))) break;
+                begun = u == seg.u0;
+            }
+        }
+        if (ok && it > 0) multiply_v(it - 1, begun);
+        // nothing that was issued outlives the block's memory, whatever gave up above
+        commit(bar(DRAIN));
+        for (uint32_t n = 0, done = 0; !done && n < (1u << 20); ++n)
+            asm volatile("{\n\t.reg .pred p;\n\t"
+                         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0;\n\t"
+                         "selp.u32 %0, 1, 0, p;\n\t}"
+                         : "=r"(done)
+                         : "r"(bar(DRAIN))
+                         : "memory");
+    }
+
+    // both SMs stay until neither has anything under way to the other
+    __syncwarp();
+    fence_before();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    fence_after();
+    if (warp == 8)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// -- joining the parts ------------------------------------------------------------
+
+constexpr int JOIN_ROWS = 8, JOIN_THREADS = JOIN_ROWS * (VALUES / 8);
+
+// One block a job and 8 of its rows: the parts' accumulators weighted by their maxima, in the
+// order of the keys. Jobs that one part did whole are not touched.
+template <bool F16>
+__global__ void __launch_bounds__(JOIN_THREADS) latent_join(LatentArgs a) {
+    extern __shared__ int32_t join_smem[];
+    int32_t *scratch = join_smem, *prefix = join_smem + 32;
+    wait_for_previous();
+    let_next_start();
+    unit_prefix<KT>(a.split, 1, prefix, scratch);
+    const int64_t total = (int64_t)prefix[a.split.requests] * a.chunks;
+    const int64_t parts = max((int64_t)1, min((int64_t)a.parts, total / a.least));
+    const int32_t groups = ROWS / JOIN_ROWS;
+    const int32_t jg = blockIdx.x / groups, r = jg / a.chunks, job = jg - r * a.chunks;
+    const int32_t M = a.m * a.Hq, row0 = job * ROWS;
+    const int32_t row = (blockIdx.x % groups) * JOIN_ROWS + threadIdx.x % JOIN_ROWS;
+    const int32_t rho = row0 + row, e8 = threadIdx.x / JOIN_ROWS;    // 8 elements
+    if (rho >= M || row >= ROWS) return;
+    const int32_t units = prefix[r + 1] - prefix[r];
+    const int64_t first = (int64_t)prefix[r] * a.chunks + (int64_t)job * units;
+    const int64_t c0 = part_of(first, parts, total), c1 = part_of(first + units - 1, parts, total);
+    if (c0 == c1) return;
+    auto slot = [&](int64_t c) { return a.partial + (size_t)(2 * c + (c == c0 ? 1 : 0)) * SLOT; };
+    float m = -INFINITY, l = 0.0f, v[8] = {};
+    for (int64_t c = c0; c <= c1; ++c)
+        m = fmaxf(m, __ldcg((const float2 *)(slot(c) + (size_t)ROWS * VALUES) + row).x);
+#pragma unroll 4
+    for (int64_t c = c0; c <= c1; ++c) {
+        const float *s = slot(c);
+        const float2 ml = __ldcg((const float2 *)(s + (size_t)ROWS * VALUES) + row);
+        const float4 p0 = __ldcg((const float4 *)s + (size_t)(2 * e8) * ROWS + row);
+        const float4 p1 = __ldcg((const float4 *)s + (size_t)(2 * e8 + 1) * ROWS + row);
+        if (ml.x == -INFINITY && ml.y == 0.0f) continue;
+        const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
+        l += f * ml.y;
+        v[0] += f * p0.x, v[1] += f * p0.y, v[2] += f * p0.z, v[3] += f * p0.w;
+        v[4] += f * p1.x, v[5] += f * p1.y, v[6] += f * p1.z, v[7] += f * p1.w;
+    }
+    const bool some = l > 0.0f || l != l;
+    const float inv = some ? 1.0f / l : 0.0f;
+    const int32_t token = (int32_t)a.heads.div((uint32_t)rho), hq = rho - token * a.Hq;
+    uint4 w;
+    w.x = narrow2<F16>(v[0] * inv, v[1] * inv), w.y = narrow2<F16>(v[2] * inv, v[3] * inv);
+    w.z = narrow2<F16>(v[4] * inv, v[5] * inv), w.w = narrow2<F16>(v[6] * inv, v[7] * inv);
+    *(uint4 *)(a.out + r * a.out_request + token * a.out_token + hq * a.out_head + e8 * 16) = w;
+    if (e8 == 0 && a.lse != nullptr)
+        a.lse[((int64_t)r * a.m + token) * a.Hq + hq] =
+            some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+}  // namespace
+
+size_t kvc_latent_partial_bytes(int32_t sm_count) {
+    return (size_t)(sm_count / 2) * 2 * SLOT * sizeof(float);
+}
+
+kvr_status kvc_latent_setup() {
+    const int smem = OFF_PREFIX + 4 * (KVC_MAX_REQUESTS + 1);
+    static_assert(OFF_PREFIX + 4 * (KVC_MAX_REQUESTS + 1) <= 227 * 1024, "");
+    for (auto k : {latent_kernel<false>, latent_kernel<true>})
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+            cudaGetLastError();
+            return KVR_ERR_CUDA;
+        }
+    return KVR_OK;
+}
+
+kvr_status kvc_latent_launch(const kvc_cache *c, int32_t layer, const kvc_attend *p, void *stream) {
+    LatentArgs a = {};
+    a.plane = c->plane(layer, 0);
+    a.split = {c->slots(p->table), p->lengths, c->ws.flags, p->num_requests, p->num_new, p->window};
+    a.q = (const unsigned char *)p->q;
+    a.out = (unsigned char *)p->out;
+    a.lse = p->lse;
+    a.q_request = p->q_request_stride, a.q_token = p->q_token_stride, a.q_head = p->q_head_stride;
+    a.out_request = p->out_request_stride, a.out_token = p->out_token_stride;
+    a.out_head = p->out_head_stride;
+    a.partial = c->ws.partial;
+    a.m = p->num_new, a.Hq = c->d.query_heads;
+    a.heads = kvr_make_div((uint32_t)a.Hq);
+    a.scale = p->scale;
+    const int64_t M = (int64_t)a.m * a.Hq;
+    a.chunks = (int32_t)((M + ROWS - 1) / ROWS);
+    const int64_t most = ((int64_t)p->table.width * c->d.block_size + KT - 1) / KT + 1;
+    if (most * p->num_requests > INT32_MAX) return KVR_ERR_UNSUPPORTED;
+    a.least = 2;
+    a.parts = (int32_t)std::min<int64_t>(std::max(kvc_stream_sms(c, stream) / 2, 1),
+                                         most * p->num_requests * a.chunks);
+    const bool f16 = c->d.dtype == KVC_DTYPE_F16;
+    const size_t smem = OFF_PREFIX + 4 * (size_t)(p->num_requests + 1);
+    const kvr_status st = kvc_launch(f16 ? latent_kernel<true> : latent_kernel<false>, a,
+                                     dim3((unsigned)(2 * a.parts)), THREADS, smem, stream, 2);
+    if (st != KVR_OK) return st;
+    const int64_t blocks = (int64_t)p->num_requests * a.chunks * (ROWS / JOIN_ROWS);
+    return kvc_launch(f16 ? latent_join<true> : latent_join<false>, a, dim3((unsigned)blocks),
+                      JOIN_THREADS, 4 * (32 + (size_t)p->num_requests + 1), stream);
+}

@@ -1,0 +1,99 @@
+// cache_split.cuh -- how the attention kernels divide the keys of all requests among their parts.
+//
+// The units (a fixed number of keys) of all jobs form one line: request by request, job by job of
+// a request (key heads, or passes of query rows), units of a job in the order of its keys. It is
+// cut into equal parts, one a block or cluster.
+#pragma once
+
+#include "cache.h"
+
+namespace kvc {
+
+// A request's keys that some of its newest tokens see: [lo, n).
+struct Span {
+    int32_t n, lo;
+};
+
+struct SplitArgs {
+    KvcSlots slots;
+    const int32_t *lengths;
+    uint32_t *flags;
+    int32_t requests, m, window;
+};
+
+// `align`: lo is a multiple of it. A length out of range counts as the nearest in range.
+__device__ __forceinline__ Span span_of(const SplitArgs &a, int32_t r, int32_t align,
+                                        uint32_t *bad) {
+    Span s;
+    s.n = __ldg(a.lengths + r);
+    const int32_t most = a.slots.width * (int32_t)a.slots.block.d;
+    if (s.n < 0 || s.n > most) {
+        *bad = KVC_FLAG_LENGTH;
+        s.n = s.n < 0 ? 0 : most;
+    }
+    s.lo = a.window > 0 ? max(0, s.n - a.m + 1 - a.window) / align * align : 0;
+    return s;
+}
+
+// prefix[r] = units of one job of each of the requests before r (at least one a request, so that
+// a request without keys still has its outputs written). All threads of the block, a multiple of
+// 32 of them; `scratch` holds one int a warp; ends with a barrier.
+template <int UNIT>
+__device__ __forceinline__ void unit_prefix(const SplitArgs &a, int32_t align, int32_t *prefix,
+                                            int32_t *scratch) {
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    uint32_t bad = 0;
+    const int32_t per = (a.requests + (int)blockDim.x - 1) / (int)blockDim.x;
+    const int32_t r0 = min(a.requests, tid * per), r1 = min(a.requests, r0 + per);
+    int32_t sum = 0;
+    for (int32_t r = r0; r < r1; ++r) {
+        const Span s = span_of(a, r, align, &bad);
+        sum += max(1, (s.n - s.lo + UNIT - 1) / UNIT);
+        prefix[r + 1] = sum;
+    }
+    if (bad != 0 && blockIdx.x == 0) atomicOr(a.flags, bad);
+    int32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int32_t y = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    int32_t before = incl - sum;
+    for (int w = 0; w < warp; ++w) before += scratch[w];
+    for (int32_t r = r0; r < r1; ++r) prefix[r + 1] += before;
+    if (tid == 0) prefix[0] = 0;
+    __syncthreads();
+}
+
+// The part that holds unit x of `total`, when part c holds [c total / parts, (c + 1) total / parts).
+__device__ __forceinline__ int64_t part_of(int64_t x, int64_t parts, int64_t total) {
+    return ((x + 1) * parts - 1) / total;
+}
+
+// What of the line a part does next: units [u0, u1) of job `job` (of `units`) of request r.
+struct Segment {
+    int32_t r, job, u0, u1, units;
+    int64_t job_first;        // the job's first unit in the line
+};
+__device__ __forceinline__ Segment segment_at(int64_t x, int64_t x_end, const int32_t *prefix,
+                                              int32_t requests, int32_t jobs) {
+    Segment s;
+    int32_t lo = 0, hi = requests - 1;
+    const int32_t xj = (int32_t)(x / jobs);
+    while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) / 2;
+        if (prefix[mid] <= xj) lo = mid; else hi = mid - 1;
+    }
+    s.r = lo;
+    s.units = prefix[lo + 1] - prefix[lo];
+    const int64_t start = (int64_t)prefix[lo] * jobs;
+    s.job = (int32_t)((x - start) / s.units);
+    s.job_first = start + (int64_t)s.job * s.units;
+    s.u0 = (int32_t)(x - s.job_first);
+    s.u1 = (int32_t)min((int64_t)s.units, s.u0 + (x_end - x));
+    return s;
+}
+
+}  // namespace kvc

@@ -17,7 +17,7 @@ from .kv_relayout import (KVRelayoutError, KvrLayout, _contiguous, _Layout, _nby
 DTYPE_F16 = 3
 INTERLEAVED = 1
 ROTATE_LAST = 2
-FLAGS = {1: "request index", 2: "position", 4: "length", 8: "block id"}
+FLAGS = {1: "request index", 2: "position", 4: "length", 8: "block id", 16: "wait"}
 SCALINGS = {"linear": 1, "base": 2, "ramp": 3, "bands": 4}
 CACHE_EXPORTS = ("kv_cache_create", "kv_cache_destroy", "kv_cache_workspace_bytes",
                  "kv_cache_append", "kv_cache_attend", "kv_cache_status",
