@@ -10,26 +10,27 @@
 // leaves no room for S. So two SMs share a tile of KT keys, each with HALF OF THE ELEMENTS (256
 // of the value and 32 of the rest): each loads its half of every latent, and nothing twice; each
 // computes the partial S = Q K^T of its half and sends it to the other through distributed
-// shared memory (24 KB a tile); each adds the two halves in the same way, so both hold the same
+// shared memory (16 KB a tile); each adds the two halves in the same way, so both hold the same
 // softmax, and multiplies P with its 256 value elements. No product and no load is done twice;
 // the exponentials are.
 //
 // Tensor memory: O [128 x 256] fp32 in columns 0-255; Q, 288 16-bit elements a row, in 144
 // columns, where the products read it as operand A (from shared memory it would take 72 KB of it
-// and cost more of its bandwidth than all of K); two S of KT = 48 columns each, which P (24
-// columns of 16-bit pairs) overwrites. 496 of 512. KT = 48 is what that leaves.
+// and cost more of its bandwidth than all of K); two S of KT = 32 columns and two P of 16. That
+// is 496 of 512. P apart from S lets S run two tiles ahead of O: with KT = 48 and P over S, S of
+// the tile after next waited for this tile's softmax, and a tile took 3.7 us.
 //
-// Shared memory: a ring of 6 tiles' halves (27 KB each) that 4 warps fill by 16-byte cp.async,
+// Shared memory: a ring of 9 tiles' halves (18 KB each) that 4 warps fill by 16-byte cp.async,
 // one row after another, so that any block size and stride will do and rows of padding are
 // zeros; and the two halves of S that the other SM sends. A tile is laid out in 128-byte rows of
 // 64 elements (swizzled), which serve as the K-major operand of S and as the MN-major operand
 // of O.
 //
 // Warps: 4 of softmax (one thread a row), 4 of loads, 1 that issues the products. S of tile i + 1
-// is computed, read and sent before the softmax of tile i waits for the other half, so the
-// exchange is off the path. O is rescaled only when a row's maximum grows by more than 2^8 over
-// the one that its P is relative to (P is then at most 2^8, fine in either 16-bit type); that
-// happens in the first tiles of a job and hardly again.
+// is read and sent before the softmax of tile i waits for the other half, so the exchange is off
+// the path. O is rescaled only when a row's maximum grows by more than 2^8 over the one that its
+// P is relative to (P is then at most 2^8, fine in either 16-bit type); that happens in the first
+// tiles of a job and hardly again.
 //
 // Numbers: S, maxima, sums, O and all joins are fp32. P is rounded once to the pool's 16-bit type
 // for its product: rounding it twice as fine would cost half of the products again.
@@ -47,26 +48,27 @@ namespace {
 
 using namespace kvc;
 
-constexpr int KT = 48;                    // keys of a tile
+constexpr int KT = 32;                    // keys of a tile
 constexpr int ROWS = 128;                 // query rows of a pass
 constexpr int HALF = 256, REST = 32;      // value elements and others of an SM
-constexpr int STAGES = 6, LAG = 3;        // tiles in the ring; loads in flight before a wait
+constexpr int STAGES = 9, LAG = 5;        // tiles in the ring; loads in flight before a wait
 constexpr int CHUNK = KT * 128;           // 64 elements of each key
 constexpr int STAGE = 4 * CHUNK + KT * 64;
 constexpr int XBUF = ROWS * KT * 4;
 constexpr int WARPS = 9, THREADS = 32 * WARPS;
-constexpr int OFF_XBUF = STAGES * STAGE, OFF_BARS = OFF_XBUF + 2 * XBUF, OFF_PREFIX = OFF_BARS + 256;
-constexpr uint32_t COL_O = 0, COL_Q = 256, COL_S = 400;
+constexpr int OFF_XBUF = STAGES * STAGE, OFF_BARS = OFF_XBUF + 2 * XBUF, OFF_PREFIX = OFF_BARS + 512;
+constexpr uint32_t COL_O = 0, COL_Q = 256, COL_S = 400, COL_P = COL_S + 2 * KT;
+static_assert(COL_P + KT <= 512, "tensor memory");
 constexpr int VALUES = KVC_LATENT_VALUES;
 // floats of one part's results: [element / 4][row][4], then (max, sum) a row
 constexpr size_t SLOT = (size_t)ROWS * VALUES + 2 * ROWS;
 
 // barriers, in 8-byte words after OFF_BARS
-enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, S_FULL = K_EMPTY + STAGES, P_FULL = S_FULL + 2,
+enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, S_FULL = K_EMPTY + STAGES, S_FREE = S_FULL + 2, P_FULL = S_FREE + 2,
        X_FULL = P_FULL + 2, X_EMPTY = X_FULL + 2, O_DONE = X_EMPTY + 2, Q_FULL = O_DONE + 2, DRAIN,
        BARS };
 constexpr int OFF_TMEM = BARS * 8, OFF_ABORT = OFF_TMEM + 4, OFF_SCRATCH = OFF_TMEM + 16;
-static_assert(OFF_SCRATCH + 4 * WARPS <= 256, "the words after the barriers");
+static_assert(OFF_SCRATCH + 4 * WARPS <= 512, "the words after the barriers");
 
 struct LatentArgs {
     KvcPlane plane;
@@ -94,8 +96,7 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 }
 // the same barrier of the other SM of the cluster
 __device__ __forceinline__ void bar_arrive_remote(uint32_t remote) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote)
-                 : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 __device__ __forceinline__ uint32_t remote_addr(uint32_t addr, uint32_t rank) {
     uint32_t r;
@@ -117,7 +118,7 @@ struct Waits {
         for (uint32_t n = 0;; ++n) {
             uint32_t done;
             asm volatile("{\n\t.reg .pred p;\n\t"
-                         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                          "selp.u32 %0, 1, 0, p;\n\t}"
                          : "=r"(done)
                          : "r"(bar), "r"(parity)
@@ -165,11 +166,6 @@ __device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t v[16]) 
                  "r"(v[14]), "r"(v[15])
                  : "memory");
 }
-__device__ __forceinline__ void tm_store8(uint32_t addr, const uint32_t v[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
-                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
 // D (+)= A B with A in tensor memory, B in shared memory
 __device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                         uint32_t add) {
@@ -203,6 +199,37 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// two fp32 numbers in one register pair, and what is done to both at once
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t d) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(d));
+    return f;
+}
+__device__ __forceinline__ uint64_t splat2(float f) {
+    return pack2(__float_as_uint(f), __float_as_uint(f));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    return d;
+}
+// s[0..1] = (s[0..1] + (x, y)) * sc: the same on both SMs, whose halves change places
+__device__ __forceinline__ void scaled_sum(uint32_t *s, float x, float y, uint64_t sc2) {
+    uint64_t d = add2(pack2(s[0], s[1]), pack2(__float_as_uint(x), __float_as_uint(y)));
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(sc2));
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(s[0]), "=r"(s[1]) : "l"(d));
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
+    return d;
+}
+
 // -- the kernel -------------------------------------------------------------------
 
 template <bool F16>
@@ -229,9 +256,10 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(bar(S_FULL + i), 1);
-            bar_init(bar(P_FULL + i), 4);         // the softmax warps
-            bar_init(bar(X_FULL + i), 4);         // those of the other SM
-            bar_init(bar(X_EMPTY + i), 4);
+            bar_init(bar(S_FREE + i), 4);         // the softmax warps
+            bar_init(bar(P_FULL + i), 4);
+            bar_init(bar(X_FULL + i), 1);         // and the bytes that the other SM stores
+            bar_init(bar(X_EMPTY + i), 4);        // its softmax warps
             bar_init(bar(O_DONE + i), 1);
         }
         bar_init(bar(Q_FULL), 4);
@@ -259,27 +287,30 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         const uint32_t x_remote = remote_addr(smem0 + OFF_XBUF, rank ^ 1u);
         const uint32_t bars_remote = remote_addr(bars, rank ^ 1u);
-        const float sc = a.scale * 1.4426950408889634f;
+        const uint64_t sc2 = splat2(a.scale * 1.4426950408889634f);
         uint32_t it = 0;                          // tiles so far
         uint32_t ok = 1;
 
         // this SM's half of S of tile `i`, in registers and on its way to the other SM
-        auto fetch = [&](uint32_t i, uint32_t s[KT]) -> bool {
+        auto fetch = [&](uint32_t i, uint32_t *s) -> bool {
             const uint32_t b = i & 1, ph = (i >> 1) & 1;
             if (!wait.all(bar(S_FULL + b), ph)) return false;
             fence_after();
 #pragma unroll
             for (int k = 0; k < KT / 16; ++k) tm_load16(s + 16 * k, lanes + COL_S + b * KT + 16 * k);
             wait_ld();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(S_FREE + b));
             if (!wait.all(bar(X_EMPTY + b), ph ^ 1)) return false;
             const uint32_t to = x_remote + b * XBUF + tid * 16;
 #pragma unroll
             for (int k = 0; k < KT / 4; ++k)
-                asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + k * ROWS * 16),
-                             "r"(s[4 * k]), "r"(s[4 * k + 1]), "r"(s[4 * k + 2]), "r"(s[4 * k + 3])
+                asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], "
+                             "{%1, %2, %3, %4}, [%5];" ::"r"(to + k * ROWS * 16),
+                             "r"(s[4 * k]), "r"(s[4 * k + 1]), "r"(s[4 * k + 2]), "r"(s[4 * k + 3]),
+                             "r"(bars_remote + 8 * (X_FULL + b))
                              : "memory");
-            __syncwarp();
-            if (lane == 0) bar_arrive_remote(bars_remote + 8 * (X_FULL + b));
             return true;
         };
 
@@ -333,31 +364,34 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
             float top = -INFINITY, sum = 0.0f;    // what P and O are relative to; sum of P
 
             // softmax of tile `i` (unit u of the job) whose own half is in s
-            auto finish = [&](uint32_t i, int32_t u, uint32_t s[KT]) -> bool {
+            auto finish = [&](uint32_t i, int32_t u, uint32_t *s) -> bool {
                 const uint32_t b = i & 1, ph = (i >> 1) & 1;
+                if (tid == 0)
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
+                                     bar(X_FULL + b)),
+                                 "r"(XBUF)
+                                 : "memory");
                 if (!wait.all(bar(X_FULL + b), ph)) return false;
-                float best = -INFINITY;
-                const int32_t j0 = sp.lo + u * KT;
-                const bool mixed = j0 + KT > seen_all || j0 < seen_from;
                 const float4 *from = (const float4 *)(smem + OFF_XBUF + b * XBUF) + tid;
 #pragma unroll
                 for (int k = 0; k < KT / 4; ++k) {
                     const float4 o = from[k * ROWS];
-                    const float add[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v = (__uint_as_float(s[4 * k + e]) + add[e]) * sc;
-                        if (mixed) {
-                            const int32_t j = j0 + 4 * k + e;
-                            if (j >= end || (a.split.window > 0 && j < end - a.split.window))
-                                v = -INFINITY;
-                        }
-                        s[4 * k + e] = __float_as_uint(v);
-                        best = fmaxf(best, v);
-                    }
+                    scaled_sum(s + 4 * k, o.x, o.y, sc2);
+                    scaled_sum(s + 4 * k + 2, o.z, o.w, sc2);
                 }
                 __syncwarp();
                 if (lane == 0) bar_arrive_remote(bars_remote + 8 * (X_EMPTY + b));
+                const int32_t j0 = sp.lo + u * KT;
+                if (j0 + KT > seen_all || j0 < seen_from) {
+#pragma unroll
+                    for (int k = 0; k < KT; ++k)
+                        if (j0 + k >= end || (a.split.window > 0 && j0 + k < end - a.split.window))
+                            s[k] = 0xFF800000u;   // -infinity
+                }
+                float best = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < KT; k += 2)
+                    best = max3(best, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
                 if (u == seg.u0) {
                     top = best;                   // O starts from this tile's product
                 } else if (__any_sync(~0u, best > top + 8.0f)) {
@@ -380,16 +414,21 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
                     wait_st();
                 }
                 const float at = top == -INFINITY ? 0.0f : top;
+                const uint64_t minus = splat2(-at);
                 uint32_t p[KT / 2];
+                uint64_t add = 0;                 // two sums
 #pragma unroll
                 for (int k = 0; k < KT / 2; ++k) {
-                    const float p0 = ex2(__uint_as_float(s[2 * k]) - at);
-                    const float p1 = ex2(__uint_as_float(s[2 * k + 1]) - at);
-                    sum += p0 + p1;
+                    const float2 d = unpack2(add2(pack2(s[2 * k], s[2 * k + 1]), minus));
+                    const float p0 = ex2(d.x), p1 = ex2(d.y);
+                    add = add2(add, pack2(__float_as_uint(p0), __float_as_uint(p1)));
                     p[k] = narrow2<F16>(p0, p1);
                 }
-                tm_store16(lanes + COL_S + b * KT, p);
-                tm_store8(lanes + COL_S + b * KT + 16, p + 16);
+                const float2 both = unpack2(add);
+                sum += both.x + both.y;
+                // the product two tiles ago has read what P goes over
+                if (i >= 2 && !wait.all(bar(O_DONE + b), ph ^ 1)) return false;
+                tm_store16(lanes + COL_P + b * (KT / 2), p);
                 wait_st();
                 fence_before();
                 __syncwarp();
@@ -466,9 +505,10 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
             }
         }
     } else if (warp < 8) {
-        // ---- loads: warp w of 4 has 12 keys of a tile ----
+        // ---- loads: warp w of 4 has 8 keys of a tile ----
         const int w = warp - 4;
         constexpr int MINE = KT / 4;
+        static_assert(MINE == 8, "the rest of its keys is one load a warp");
         uint32_t it = 0, bad = 0, ok = 1;
         while (ok && x < x_end) {
             const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
@@ -506,18 +546,15 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
                                  "l"(src + at), "r"(off >= 0 ? 16 : 0)
                                  : "memory");
                 }
-                // the rest: 4 pieces a key, 8 keys at a time
-#pragma unroll
-                for (int k = 0; k < MINE; k += 8) {
-                    const int mine = k + lane / 4;
-                    const int64_t off = __shfl_sync(~0u, slot, mine < MINE ? mine : 0);
-                    const uint32_t row = w * MINE + mine, c = lane % 4;
+                // the rest: 4 pieces a key, all 8 keys at once
+                {
+                    const int64_t off = __shfl_sync(~0u, slot, lane / 4);
+                    const uint32_t row = w * MINE + lane / 4, c = lane % 4;
                     const int64_t at = off >= 0 ? off + (VALUES + rank * REST) * 2 + c * 16 : 0;
                     const uint32_t dst = base + 4 * CHUNK + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-                    if (mine < MINE)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                                     "l"(src + at), "r"(off >= 0 ? 16 : 0)
-                                     : "memory");
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                                 "l"(src + at), "r"(off >= 0 ? 16 : 0)
+                                 : "memory");
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
                 if (it >= LAG) {                  // the tile LAG before this one has come
@@ -534,53 +571,66 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
         if (lane == 0)
             for (uint32_t i = it > LAG ? it - LAG : 0; i < it; ++i) bar_arrive(bar(K_FULL + i % STAGES));
         if (bad != 0) atomicOr(a.split.flags, bad);
-    } else if (lane == 0) {
-        // ---- products: S of a tile, then O of the tile before ----
+    } else {
+        // ---- products: S two tiles ahead of O; the warp runs as one, so that operand
+        // descriptors stay in uniform registers, and one elected lane issues ----
+        uint32_t leader;
+        asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(leader));
+        const uint32_t tm = __shfl_sync(~0u, tmem, 0), ring = __shfl_sync(~0u, smem0, 0);
         constexpr uint32_t ID_S = idesc(!F16, false, KT), ID_O = idesc(!F16, true, HALF);
-        uint32_t it = 0, segments = 0;
-        uint32_t ok = 1, begun = 0;               // the tile before: is it a segment's first?
-        auto multiply_v = [&](uint32_t i, uint32_t first) -> bool {
+        auto multiply_k = [&](uint32_t i) -> bool {
             const uint32_t b = i & 1, stage = i % STAGES;
-            if (!wait(bar(P_FULL + b), (i >> 1) & 1)) return false;
+            if (!wait.all(bar(K_FULL + stage), (i / STAGES) & 1)) return false;
+            if (!wait.all(bar(S_FREE + b), ((i >> 1) & 1) ^ 1)) return false;
             fence_after();
-            const uint32_t base = smem0 + stage * STAGE;
+            const uint32_t base = __shfl_sync(~0u, ring + stage * STAGE, 0);
+            const uint32_t s_col = __shfl_sync(~0u, tm + COL_S + b * KT, 0);
+            if (leader) {
+#pragma unroll
+            for (int k = 0; k < HALF / 16; ++k)
+                product(s_col, tm + COL_Q + 8 * k,
+                        operand(base + (k / 4) * CHUNK + (k % 4) * 32, 16, 1024, 2), ID_S, k > 0);
+#pragma unroll
+            for (int k = 0; k < REST / 16; ++k)
+                product(s_col, tm + COL_Q + HALF / 2 + 8 * k,
+                        operand(base + 4 * CHUNK + k * 32, 16, 512, 4), ID_S, 1);
+            commit(bar(S_FULL + b));
+            }
+            __syncwarp();
+            return true;
+        };
+        auto multiply_v = [&](uint32_t i, bool first) -> bool {
+            const uint32_t b = i & 1, stage = i % STAGES;
+            if (!wait.all(bar(P_FULL + b), (i >> 1) & 1)) return false;
+            fence_after();
+            const uint32_t base = __shfl_sync(~0u, ring + stage * STAGE, 0);
+            const uint32_t p_col = __shfl_sync(~0u, tm + COL_P + b * (KT / 2), 0);
+            if (leader) {
 #pragma unroll
             for (int k = 0; k < KT / 16; ++k)
-                product(tmem + COL_O, tmem + COL_S + b * KT + 8 * k,
+                product(tm + COL_O, p_col + 8 * k,
                         operand(base + k * 2048, CHUNK, 1024, 2), ID_O, !(first && k == 0));
             commit(bar(K_EMPTY + stage));
             commit(bar(O_DONE + b));
+            }
+            __syncwarp();
             return true;
         };
+        uint32_t it = 0, segments = 0;
+        bool ok = true;
         while (ok && x < x_end) {
             const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
-            x += seg.u1 - seg.u0;
-            for (int32_t u = seg.u0; u < seg.u1; ++u, ++it) {
-                const uint32_t b = it & 1, stage = it % STAGES;
-                if (u == seg.u0) {
-                    // the segment before ends first: its results are waited for
-                    if (it > 0 && !(ok = multiply_v(it - 1, begun))) break;
-                    if (!(ok = wait(bar(Q_FULL), segments++ & 1))) break;
-                }
-                if (!(ok = wait(bar(K_FULL + stage), (it / STAGES) & 1))) break;
-                fence_after();
-                const uint32_t base = smem0 + stage * STAGE;
-#pragma unroll
-                for (int k = 0; k < HALF / 16; ++k)
-                    product(tmem + COL_S + b * KT, tmem + COL_Q + 8 * k,
-                            operand(base + (k / 4) * CHUNK + (k % 4) * 32, 16, 1024, 2), ID_S, k > 0);
-#pragma unroll
-                for (int k = 0; k < REST / 16; ++k)
-                    product(tmem + COL_S + b * KT, tmem + COL_Q + HALF / 2 + 8 * k,
-                            operand(base + 4 * CHUNK + k * 32, 16, 512, 4), ID_S, 1);
-                commit(bar(S_FULL + b));
-                if (u > seg.u0 && !(ok = multiply_v(it - 1, begun))) break;
-                begun = u == seg.u0;
-            }
+            const uint32_t n = (uint32_t)(seg.u1 - seg.u0);
+            x += n;
+            ok = wait.all(bar(Q_FULL), segments++ & 1) && multiply_k(it) && (n < 2 || multiply_k(it + 1));
+            for (uint32_t k = 0; ok && k < n; ++k)
+                ok = (k + 2 >= n || multiply_k(it + k + 2)) && multiply_v(it + k, k == 0);
+            it += n;
         }
-        if (ok && it > 0) multiply_v(it - 1, begun);
         // nothing that was issued outlives the block's memory, whatever gave up above
-        commit(bar(DRAIN));
+        if (leader) commit(bar(DRAIN));
+        __syncwarp();
         for (uint32_t n = 0, done = 0; !done && n < (1u << 20); ++n)
             asm volatile("{\n\t.reg .pred p;\n\t"
                          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0;\n\t"
