@@ -37,7 +37,7 @@ extern "C" {
 #define KVC_DTYPE_F16 3
 
 /* Most requests of one attention call. */
-#define KVC_MAX_REQUESTS 4096
+#define KVC_MAX_REQUESTS 2048
 
 /* Flags of kv_cache_status(). */
 #define KVC_FLAG_REQUEST 1u    /* append: a request index outside the block table's rows */

@@ -10,27 +10,30 @@
 // leaves no room for S. So two SMs share a tile of KT keys, each with HALF OF THE ELEMENTS (256
 // of the value and 32 of the rest): each loads its half of every latent, and nothing twice; each
 // computes the partial S = Q K^T of its half and sends it to the other through distributed
-// shared memory (16 KB a tile); each adds the two halves in the same way, so both hold the same
+// shared memory (32 KB a tile); each adds the two halves in the same way, so both hold the same
 // softmax, and multiplies P with its 256 value elements. No product and no load is done twice;
 // the exponentials are.
 //
 // Tensor memory: O [128 x 256] fp32 in columns 0-255; Q, 288 16-bit elements a row, in 144
 // columns, where the products read it as operand A (from shared memory it would take 72 KB of it
-// and cost more of its bandwidth than all of K); two S of KT = 32 columns and two P of 16. That
-// is 496 of 512. P apart from S lets S run two tiles ahead of O: with KT = 48 and P over S, S of
-// the tile after next waited for this tile's softmax, and a tile took 3.7 us.
+// and cost more of its bandwidth than all of K); S of KT = 64 columns, and P of 32. That is 496
+// of 512. One S is enough, as S of the next tile is computed once this tile's is in registers;
+// tiles of 32 keys with two S and two P took 1.8 times as long, for the time from a tile's S to
+// its P, through the other SM and back, is nearly the same for 32 keys.
 //
-// Shared memory: a ring of 9 tiles' halves (18 KB each) that 4 warps fill by 16-byte cp.async,
+// Shared memory: a ring of 4 tiles' halves (36 KB each) that 4 warps fill by 16-byte cp.async,
 // one row after another, so that any block size and stride will do and rows of padding are
-// zeros; and the two halves of S that the other SM sends. A tile is laid out in 128-byte rows of
-// 64 elements (swizzled), which serve as the K-major operand of S and as the MN-major operand
+// zeros; and two times the half of S that the other SM sends. A tile is laid out in 128-byte rows
+// of 64 elements (swizzled), which serve as the K-major operand of S and as the MN-major operand
 // of O.
 //
-// Warps: 4 of softmax (one thread a row), 4 of loads, 1 that issues the products. S of tile i + 1
-// is read and sent before the softmax of tile i waits for the other half, so the exchange is off
-// the path. O is rescaled only when a row's maximum grows by more than 2^8 over the one that its
-// P is relative to (P is then at most 2^8, fine in either 16-bit type); that happens in the first
-// tiles of a job and hardly again.
+// Warps: twice 4 of softmax (one thread a row; even and odd tiles), 4 that send S to the other
+// SM, 4 of loads, 1 that issues the products. With one set of softmax warps that also sent, they
+// were busy for 2100 cycles a tile, of which HBM wants 780. A tile's softmax needs of the one
+// before only what P is relative to, which goes through shared memory as soon as it is known.
+// O is rescaled only when a row's maximum grows by more than 2^8 over the one that its P is
+// relative to (P is then at most 2^8, fine in either 16-bit type); that happens in the first tiles
+// of a job and hardly again.
 //
 // Numbers: S, maxima, sums, O and all joins are fp32. P is rounded once to the pool's 16-bit type
 // for its product: rounding it twice as fine would cost half of the products again.
@@ -48,25 +51,27 @@ namespace {
 
 using namespace kvc;
 
-constexpr int KT = 32;                    // keys of a tile
+constexpr int KT = 64;                    // keys of a tile
 constexpr int ROWS = 128;                 // query rows of a pass
 constexpr int HALF = 256, REST = 32;      // value elements and others of an SM
-constexpr int STAGES = 9, LAG = 5;        // tiles in the ring; loads in flight before a wait
+constexpr int STAGES = 4;                 // tiles in the ring
 constexpr int CHUNK = KT * 128;           // 64 elements of each key
 constexpr int STAGE = 4 * CHUNK + KT * 64;
 constexpr int XBUF = ROWS * KT * 4;
-constexpr int WARPS = 9, THREADS = 32 * WARPS;
-constexpr int OFF_XBUF = STAGES * STAGE, OFF_BARS = OFF_XBUF + 2 * XBUF, OFF_PREFIX = OFF_BARS + 512;
-constexpr uint32_t COL_O = 0, COL_Q = 256, COL_S = 400, COL_P = COL_S + 2 * KT;
-static_assert(COL_P + KT <= 512, "tensor memory");
+// warps: softmax of even tiles, of odd tiles, sending, loading (4 each), products
+constexpr int SEND = 8, LOAD = 12, ISSUE = 16, WARPS = 17, THREADS = 32 * WARPS;
+constexpr int OFF_XBUF = STAGES * STAGE, OFF_BARS = OFF_XBUF + 2 * XBUF, OFF_TOPS = OFF_BARS + 512,
+              OFF_PREFIX = OFF_TOPS + 6 * ROWS * 4;
+constexpr uint32_t COL_O = 0, COL_Q = 256, COL_S = 400, COL_P = COL_S + KT;
+static_assert(COL_P + KT / 2 <= 512, "tensor memory");
 constexpr int VALUES = KVC_LATENT_VALUES;
 // floats of one part's results: [element / 4][row][4], then (max, sum) a row
 constexpr size_t SLOT = (size_t)ROWS * VALUES + 2 * ROWS;
 
 // barriers, in 8-byte words after OFF_BARS
-enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, S_FULL = K_EMPTY + STAGES, S_FREE = S_FULL + 2, P_FULL = S_FREE + 2,
-       X_FULL = P_FULL + 2, X_EMPTY = X_FULL + 2, O_DONE = X_EMPTY + 2, Q_FULL = O_DONE + 2, DRAIN,
-       BARS };
+enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, S_FULL = K_EMPTY + STAGES, S_FREE = S_FULL + 2,
+       P_FULL = S_FREE + 2, X_FULL = P_FULL + 2, X_EMPTY = X_FULL + 2, O_DONE = X_EMPTY + 2,
+       TOP = O_DONE + 2, Q_FULL = TOP + 8, O_FREE, SUMS, DRAIN, BARS };
 constexpr int OFF_TMEM = BARS * 8, OFF_ABORT = OFF_TMEM + 4, OFF_SCRATCH = OFF_TMEM + 16;
 static_assert(OFF_SCRATCH + 4 * WARPS <= 512, "the words after the barriers");
 
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
     const Waits wait = {(volatile int32_t *)(smem + OFF_BARS + OFF_ABORT), a.split.flags};
     auto bar = [&](int which) { return bars + 8 * which; };
 
-    if (warp == 8) {
+    if (warp == ISSUE) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          bars + OFF_TMEM)
                      : "memory");
@@ -251,18 +256,21 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
     }
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            bar_init(bar(K_FULL + i), 4);         // the loading warps
+            bar_init(bar(K_FULL + i), 128);       // the loading threads
             bar_init(bar(K_EMPTY + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(bar(S_FULL + i), 1);
-            bar_init(bar(S_FREE + i), 4);         // the softmax warps
+            bar_init(bar(S_FREE + i), 8);         // softmax and sending warps
             bar_init(bar(P_FULL + i), 4);
             bar_init(bar(X_FULL + i), 1);         // and the bytes that the other SM stores
             bar_init(bar(X_EMPTY + i), 4);        // its softmax warps
             bar_init(bar(O_DONE + i), 1);
         }
+        for (int i = 0; i < 8; ++i) bar_init(bar(TOP + i), 1);
         bar_init(bar(Q_FULL), 4);
+        bar_init(bar(O_FREE), 8);
+        bar_init(bar(SUMS), 8);
         bar_init(bar(DRAIN), 1);
         *wait.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -282,192 +290,160 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
     const int64_t x_end = part < parts ? (part + 1) * total / parts : 0;
     const int32_t M = a.m * a.Hq;
 
-    if (warp < 4) {
-        // ---- softmax: thread `tid` has query row `tid` of the pass (lane of tensor memory) ----
-        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-        const uint32_t x_remote = remote_addr(smem0 + OFF_XBUF, rank ^ 1u);
+    // a thread's query row in a segment: lane of tensor memory, row of the pass
+    const int row = tid % ROWS;
+    const uint32_t lanes = tmem + ((uint32_t)(row & ~31) << 16);
+    struct Query {
+        int32_t token, hq;
+        bool mine;
+    };
+    auto query_of = [&](const Segment &seg) -> Query {
+        const int32_t rho = seg.job * ROWS + row;
+        const int32_t token = (int32_t)a.heads.div((uint32_t)rho);
+        return {token, rho - token * a.Hq, rho < M};
+    };
+
+    if (warp < SEND) {
+        // ---- softmax of every other tile ----
+        // (registers: 2 x 128 x 128 here, 128 x 72 and 128 x 56 below, 32 x 96: the 544 x 96 of the launch)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+        const uint32_t b = warp / 4;              // of even or odd tiles, and their buffers
         const uint32_t bars_remote = remote_addr(bars, rank ^ 1u);
         const uint64_t sc2 = splat2(a.scale * 1.4426950408889634f);
-        uint32_t it = 0;                          // tiles so far
-        uint32_t ok = 1;
-
-        // this SM's half of S of tile `i`, in registers and on its way to the other SM
-        auto fetch = [&](uint32_t i, uint32_t *s) -> bool {
-            const uint32_t b = i & 1, ph = (i >> 1) & 1;
-            if (!wait.all(bar(S_FULL + b), ph)) return false;
-            fence_after();
-#pragma unroll
-            for (int k = 0; k < KT / 16; ++k) tm_load16(s + 16 * k, lanes + COL_S + b * KT + 16 * k);
-            wait_ld();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(S_FREE + b));
-            if (!wait.all(bar(X_EMPTY + b), ph ^ 1)) return false;
-            const uint32_t to = x_remote + b * XBUF + tid * 16;
-#pragma unroll
-            for (int k = 0; k < KT / 4; ++k)
-                asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], "
-                             "{%1, %2, %3, %4}, [%5];" ::"r"(to + k * ROWS * 16),
-                             "r"(s[4 * k]), "r"(s[4 * k + 1]), "r"(s[4 * k + 2]), "r"(s[4 * k + 3]),
-                             "r"(bars_remote + 8 * (X_FULL + b))
-                             : "memory");
-            return true;
-        };
-
-        // the thread's row of q in a segment, and this SM's half of it into tensor memory
-        struct Row {
-            int32_t token, hq;
-            bool mine;
-        };
-        auto row_of = [&](const Segment &seg) -> Row {
-            const int32_t rho = seg.job * ROWS + tid;
-            const int32_t token = (int32_t)a.heads.div((uint32_t)rho);
-            return {token, rho - token * a.Hq, rho < M};
-        };
-        auto load_q = [&](const Segment &seg) {
-            const Row row = row_of(seg);
-            const unsigned char *q = a.q + seg.r * a.q_request + row.token * a.q_token + row.hq * a.q_head;
-            const unsigned char *first = q + rank * (HALF * 2), *rest = q + (VALUES + rank * REST) * 2;
-#pragma unroll
-            for (int k = 0; k < 9; ++k) {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (row.mine) v = __ldg((const uint4 *)(k < 8 ? first + k * 64 : rest) + e);
-                    w[4 * e] = v.x, w[4 * e + 1] = v.y, w[4 * e + 2] = v.z, w[4 * e + 3] = v.w;
-                }
-                tm_store16(lanes + COL_Q + 16 * k, w);
-            }
-            wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(Q_FULL));
-        };
-
-        Segment seg = {};
-        if (x < x_end) {
-            seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
-            load_q(seg);
-        }
+        float *tops = (float *)(smem + OFF_TOPS), *sums = tops + 2 * ROWS;   // [2][ROWS], [2][2][ROWS]
+        const float4 *from = (const float4 *)(smem + OFF_XBUF + b * XBUF) + row;
+        uint32_t it = 0, segments = 0;            // tiles and segments so far
+        bool ok = true;
         while (ok && x < x_end) {
-            x += seg.u1 - seg.u0;
+            const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
+            const uint32_t n = (uint32_t)(seg.u1 - seg.u0);
+            x += n;
             uint32_t bad = 0;
             const Span sp = span_of(a.split, seg.r, 1, &bad);
-            const Row row = row_of(seg);
-            const int32_t token = row.token, hq = row.hq;
-            const bool mine = row.mine;
-
-            const int32_t end = sp.n - a.m + token + 1;
+            const Query query = query_of(seg);
+            const int32_t end = sp.n - a.m + query.token + 1;
             const int32_t seen_all = sp.n - a.m + 1;
             const int32_t seen_from = a.split.window > 0 ? sp.n - a.split.window : 0;
-            float top = -INFINITY, sum = 0.0f;    // what P and O are relative to; sum of P
+            // the row's sum of P over these warps' tiles, relative to 2^ref
+            float ref = -INFINITY, sum = 0.0f;
 
-            // softmax of tile `i` (unit u of the job) whose own half is in s
-            auto finish = [&](uint32_t i, int32_t u, uint32_t *s) -> bool {
-                const uint32_t b = i & 1, ph = (i >> 1) & 1;
-                if (tid == 0)
+            for (uint32_t k = (it & 1) == b ? 0 : 1; k < n; k += 2) {
+                const uint32_t i = it + k, ph = (i >> 1) & 1;
+                uint32_t s[KT];
+                if (!(ok = wait.all(bar(S_FULL + b), ph))) break;
+                fence_after();
+#pragma unroll
+                for (int e = 0; e < KT / 16; ++e) tm_load16(s + 16 * e, lanes + COL_S + 16 * e);
+                wait_ld();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(S_FREE + b));
+                if (row == 0)
                     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
                                      bar(X_FULL + b)),
                                  "r"(XBUF)
                                  : "memory");
-                if (!wait.all(bar(X_FULL + b), ph)) return false;
-                const float4 *from = (const float4 *)(smem + OFF_XBUF + b * XBUF) + tid;
+                if (!(ok = wait.all(bar(X_FULL + b), ph))) break;
 #pragma unroll
-                for (int k = 0; k < KT / 4; ++k) {
-                    const float4 o = from[k * ROWS];
-                    scaled_sum(s + 4 * k, o.x, o.y, sc2);
-                    scaled_sum(s + 4 * k + 2, o.z, o.w, sc2);
+                for (int e = 0; e < KT / 4; ++e) {
+                    const float4 o = from[e * ROWS];
+                    scaled_sum(s + 4 * e, o.x, o.y, sc2);
+                    scaled_sum(s + 4 * e + 2, o.z, o.w, sc2);
                 }
                 __syncwarp();
                 if (lane == 0) bar_arrive_remote(bars_remote + 8 * (X_EMPTY + b));
-                const int32_t j0 = sp.lo + u * KT;
+                const int32_t j0 = sp.lo + (seg.u0 + (int32_t)k) * KT;
                 if (j0 + KT > seen_all || j0 < seen_from) {
 #pragma unroll
-                    for (int k = 0; k < KT; ++k)
-                        if (j0 + k >= end || (a.split.window > 0 && j0 + k < end - a.split.window))
-                            s[k] = 0xFF800000u;   // -infinity
+                    for (int e = 0; e < KT; ++e)
+                        if (j0 + e >= end || (a.split.window > 0 && j0 + e < end - a.split.window))
+                            s[e] = 0xFF800000u;   // -infinity
                 }
-                float best = -INFINITY;
+                float best = -INFINITY, more = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < KT; k += 2)
-                    best = max3(best, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-                if (u == seg.u0) {
-                    top = best;                   // O starts from this tile's product
-                } else if (__any_sync(~0u, best > top + 8.0f)) {
-                    const float next = fmaxf(top, best);
-                    const float shrink = next == top ? 1.0f : ex2(top - next);
-                    top = next;
-                    sum *= shrink;
-                    if (!wait.all(bar(O_DONE + (b ^ 1)), ((i - 1) >> 1) & 1)) return false;
-                    fence_after();
+                for (int e = 0; e < KT; e += 4) {
+                    best = max3(best, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                    more = max3(more, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+                }
+                best = fmaxf(best, more);
+                // what P and O are relative to: as the tile before left it, or more
+                float top = best;                 // O starts from a segment's first tile
+                if (k > 0) {
+                    if (!(ok = wait.all(bar(TOP + (b ^ 1) * 4 + warp % 4), ((i - 1) >> 1) & 1))) break;
+                    top = tops[(b ^ 1) * ROWS + row];
+                    if (__any_sync(~0u, best > top + 8.0f)) {
+                        const float next = fmaxf(top, best);
+                        const float shrink = next == top ? 1.0f : ex2(top - next);
+                        top = next;
+                        if (!(ok = wait.all(bar(O_DONE + (b ^ 1)), ((i - 1) >> 1) & 1))) break;
+                        fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < HALF; c += 16) {
-                        uint32_t w[16];
-                        tm_load16(w, lanes + COL_O + c);
-                        wait_ld();
+                        for (int c = 0; c < HALF; c += 16) {
+                            uint32_t w[16];
+                            tm_load16(w, lanes + COL_O + c);
+                            wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            w[e] = __float_as_uint(__uint_as_float(w[e]) * shrink);
-                        tm_store16(lanes + COL_O + c, w);
+                            for (int e = 0; e < 16; ++e)
+                                w[e] = __float_as_uint(__uint_as_float(w[e]) * shrink);
+                            tm_store16(lanes + COL_O + c, w);
+                        }
+                        wait_st();
                     }
-                    wait_st();
                 }
-                const float at = top == -INFINITY ? 0.0f : top;
-                const uint64_t minus = splat2(-at);
+                tops[b * ROWS + row] = top;
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(TOP + b * 4 + warp % 4));
+                if (top != ref) sum *= ref == -INFINITY ? 0.0f : ex2(ref - top);
+                ref = top;
+                const uint64_t minus = splat2(top == -INFINITY ? 0.0f : -top);
                 uint32_t p[KT / 2];
                 uint64_t add = 0;                 // two sums
 #pragma unroll
-                for (int k = 0; k < KT / 2; ++k) {
-                    const float2 d = unpack2(add2(pack2(s[2 * k], s[2 * k + 1]), minus));
+                for (int e = 0; e < KT / 2; ++e) {
+                    const float2 d = unpack2(add2(pack2(s[2 * e], s[2 * e + 1]), minus));
                     const float p0 = ex2(d.x), p1 = ex2(d.y);
                     add = add2(add, pack2(__float_as_uint(p0), __float_as_uint(p1)));
-                    p[k] = narrow2<F16>(p0, p1);
+                    p[e] = narrow2<F16>(p0, p1);
                 }
                 const float2 both = unpack2(add);
                 sum += both.x + both.y;
-                // the product two tiles ago has read what P goes over
-                if (i >= 2 && !wait.all(bar(O_DONE + b), ph ^ 1)) return false;
-                tm_store16(lanes + COL_P + b * (KT / 2), p);
+                // the product before has read the P that this one's goes over
+                if (i > 0 && !(ok = wait.all(bar(O_DONE + (b ^ 1)), ((i - 1) >> 1) & 1))) break;
+                tm_store16(lanes + COL_P, p);
+                tm_store16(lanes + COL_P + 16, p + 16);
                 wait_st();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(bar(P_FULL + b));
-                return true;
-            };
-
-            // two tiles a turn, S of the next always fetched ahead of this one's softmax
-            uint32_t s0[KT], s1[KT];
-            int32_t u = seg.u0;
-            ok = fetch(it, s0);
-            while (ok) {
-                if (u + 1 < seg.u1) ok = fetch(it + 1, s1);
-                if (!ok || !(ok = finish(it, u, s0))) break;
-                ++it, ++u;
-                if (u >= seg.u1) break;
-                if (u + 1 < seg.u1) ok = fetch(it + 1, s0);
-                if (!ok || !(ok = finish(it, u, s1))) break;
-                ++it, ++u;
-                if (u >= seg.u1) break;
             }
             if (!ok) break;
-            // all products with this q are done: the next segment's may start
-            const Segment done = seg;
-            if (x < x_end) {
-                seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
-                load_q(seg);
-            }
-            if (!(ok = wait.all(bar(O_DONE + ((it - 1) & 1)), ((it - 1) >> 1) & 1))) break;
+            it += n;
+
+            // the segment's maximum and sum, then its O: each of the two halves of the warps has
+            // half of the columns
+            const uint32_t last = it - 1, lb = last & 1;
+            if (lb != b && !(ok = wait.all(bar(TOP + lb * 4 + warp % 4), (last >> 1) & 1))) break;
+            const float top = tops[lb * ROWS + row];
+            if (top != ref) sum *= ref == -INFINITY ? 0.0f : ex2(ref - top);
+            float *mine_sum = sums + (segments & 1) * 2 * ROWS;
+            mine_sum[b * ROWS + row] = sum;
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(SUMS));
+            if (!(ok = wait.all(bar(SUMS), segments & 1))) break;
+            sum = mine_sum[row] + mine_sum[ROWS + row];
+            ++segments;
+            if (last > 0 && !(ok = wait.all(bar(O_DONE + (lb ^ 1)), ((last - 1) >> 1) & 1))) break;
+            if (!(ok = wait.all(bar(O_DONE + lb), (last >> 1) & 1))) break;
             fence_after();
 
-            const bool whole = done.u0 == 0 && done.u1 == done.units;
+            const bool whole = seg.u0 == 0 && seg.u1 == seg.units, mine = query.mine;
             const bool some = sum > 0.0f || sum != sum;
             const float inv = some ? 1.0f / sum : 0.0f;
-            float *slot = a.partial + (size_t)(2 * part + (done.u0 == 0 ? 1 : 0)) * SLOT;
-            unsigned char *out = a.out + done.r * a.out_request + token * a.out_token +
-                                 hq * a.out_head + rank * (HALF * 2);
+            float *slot = a.partial + (size_t)(2 * part + (seg.u0 == 0 ? 1 : 0)) * SLOT;
+            unsigned char *out = a.out + seg.r * a.out_request + query.token * a.out_token +
+                                 query.hq * a.out_head + rank * (HALF * 2);
 #pragma unroll 1
-            for (int c = 0; c < HALF; c += 16) {
+            for (int c = b * (HALF / 2); c < (int)(b + 1) * (HALF / 2); c += 16) {
                 uint32_t w[16];
                 tm_load16(w, lanes + COL_O + c);
                 wait_ld();
@@ -486,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
                         *(uint4 *)(out + c * 2 + e * 16) = v;
                     }
                 } else if (mine) {
-                    float4 *to = (float4 *)slot + (size_t)((rank * HALF + c) / 4) * ROWS + tid;
+                    float4 *to = (float4 *)slot + (size_t)((rank * HALF + c) / 4) * ROWS + row;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         __stcg(to + e * ROWS, *(const float4 *)((const float *)w + 4 * e));
@@ -494,22 +470,87 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
                 __syncwarp();
             }
             fence_before();
-            if (mine && rank == 0) {
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(O_FREE));
+            if (mine && rank == 0 && b == 0) {
                 if (whole) {
                     if (a.lse != nullptr)
-                        a.lse[((int64_t)done.r * a.m + token) * a.Hq + hq] =
+                        a.lse[((int64_t)seg.r * a.m + query.token) * a.Hq + query.hq] =
                             some ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
                 } else {
-                    __stcg((float2 *)(slot + (size_t)ROWS * VALUES) + tid, make_float2(top, sum));
+                    __stcg((float2 *)(slot + (size_t)ROWS * VALUES) + row, make_float2(top, sum));
                 }
             }
         }
-    } else if (warp < 8) {
-        // ---- loads: warp w of 4 has 8 keys of a tile ----
-        const int w = warp - 4;
+    } else if (warp < LOAD) {
+        // ---- sending: this SM's half of S to the other; and a segment's q to tensor memory ----
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        const uint32_t x_remote = remote_addr(smem0 + OFF_XBUF, rank ^ 1u) + row * 16;
+        const uint32_t bars_remote = remote_addr(bars, rank ^ 1u);
+        uint32_t it = 0;
+        bool ok = true;
+        while (ok && x < x_end) {
+            const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
+            const uint32_t n = (uint32_t)(seg.u1 - seg.u0);
+            x += n;
+            // (S of every tile so far was waited for below: no product reads the q before)
+            const Query query = query_of(seg);
+            const unsigned char *q = a.q + seg.r * a.q_request + query.token * a.q_token +
+                                     query.hq * a.q_head;
+            const unsigned char *first = q + rank * (HALF * 2), *rest = q + (VALUES + rank * REST) * 2;
+#pragma unroll 3
+            for (int k = 0; k < 9; ++k) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (query.mine) v = __ldg((const uint4 *)(k < 8 ? first + k * 64 : rest) + e);
+                    w[4 * e] = v.x, w[4 * e + 1] = v.y, w[4 * e + 2] = v.z, w[4 * e + 3] = v.w;
+                }
+                __syncwarp();
+                tm_store16(lanes + COL_Q + 16 * k, w);
+            }
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(Q_FULL));
+            for (uint32_t k = 0; k < n; ++k, ++it) {
+                const uint32_t b = it & 1, ph = (it >> 1) & 1;
+                if (!(ok = wait.all(bar(X_EMPTY + b), ph ^ 1))) break;
+                if (!(ok = wait.all(bar(S_FULL + b), ph))) break;
+                fence_after();
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t s[KT / 2];
+#pragma unroll
+                    for (int e = 0; e < KT / 32; ++e)
+                        tm_load16(s + 16 * e, lanes + COL_S + half * (KT / 2) + 16 * e);
+                    wait_ld();
+                    if (half == 1) {
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(bar(S_FREE + b));
+                    }
+#pragma unroll
+                    for (int e = 0; e < KT / 8; ++e)
+                        asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], "
+                                     "{%1, %2, %3, %4}, [%5];" ::"r"(x_remote + b * XBUF +
+                                                                     (half * (KT / 8) + e) * ROWS * 16),
+                                     "r"(s[4 * e]), "r"(s[4 * e + 1]), "r"(s[4 * e + 2]),
+                                     "r"(s[4 * e + 3]), "r"(bars_remote + 8 * (X_FULL + b))
+                                     : "memory");
+                }
+            }
+        }
+    } else if (warp < ISSUE) {
+        // ---- loads: warp w of 4 has 16 keys of a tile ----
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        const int w = warp - LOAD;
         constexpr int MINE = KT / 4;
-        static_assert(MINE == 8, "the rest of its keys is one load a warp");
-        uint32_t it = 0, bad = 0, ok = 1;
+        static_assert(MINE == 16, "a lane's half-warp number is its key");
+        uint32_t it = 0, bad = 0;
+        bool ok = true;
+        const unsigned char *src = a.plane.base;
         while (ok && x < x_end) {
             const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
             x += seg.u1 - seg.u0;
@@ -534,7 +575,6 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
                 const uint32_t stage = it % STAGES;
                 if (!(ok = wait.all(bar(K_EMPTY + stage), (it / STAGES + 1) & 1))) break;
                 const uint32_t base = smem0 + stage * STAGE;
-                const unsigned char *src = a.plane.base;
                 // values: 32 pieces of 16 bytes a key, one key at a time
 #pragma unroll
                 for (int k = 0; k < MINE; ++k) {
@@ -546,30 +586,24 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
                                  "l"(src + at), "r"(off >= 0 ? 16 : 0)
                                  : "memory");
                 }
-                // the rest: 4 pieces a key, all 8 keys at once
-                {
-                    const int64_t off = __shfl_sync(~0u, slot, lane / 4);
-                    const uint32_t row = w * MINE + lane / 4, c = lane % 4;
+                // the rest: 4 pieces a key, 8 keys at a time
+#pragma unroll
+                for (int k = 0; k < MINE; k += 8) {
+                    const int64_t off = __shfl_sync(~0u, slot, k + lane / 4);
+                    const uint32_t row = w * MINE + k + lane / 4, c = lane % 4;
                     const int64_t at = off >= 0 ? off + (VALUES + rank * REST) * 2 + c * 16 : 0;
                     const uint32_t dst = base + 4 * CHUNK + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
                                  "l"(src + at), "r"(off >= 0 ? 16 : 0)
                                  : "memory");
                 }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                if (it >= LAG) {                  // the tile LAG before this one has come
-                    asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(bar(K_FULL + (it - LAG) % STAGES));
-                }
+                // arrives when this thread's copies so far have
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                                 bar(K_FULL + stage))
+                             : "memory");
             }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0)
-            for (uint32_t i = it > LAG ? it - LAG : 0; i < it; ++i) bar_arrive(bar(K_FULL + i % STAGES));
+        asm volatile("cp.async.wait_all;" ::: "memory");
         if (bad != 0) atomicOr(a.split.flags, bad);
     } else {
         // ---- products: S two tiles ahead of O; the warp runs as one, so that operand
@@ -582,10 +616,13 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
         auto multiply_k = [&](uint32_t i) -> bool {
             const uint32_t b = i & 1, stage = i % STAGES;
             if (!wait.all(bar(K_FULL + stage), (i / STAGES) & 1)) return false;
-            if (!wait.all(bar(S_FREE + b), ((i >> 1) & 1) ^ 1)) return false;
+            // the S before, which this one goes over, has been read
+            if (i > 0 && !wait.all(bar(S_FREE + (b ^ 1)), ((i - 1) >> 1) & 1)) return false;
             fence_after();
+            // the copies came through the generic proxy; the products read through the async one
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             const uint32_t base = __shfl_sync(~0u, ring + stage * STAGE, 0);
-            const uint32_t s_col = __shfl_sync(~0u, tm + COL_S + b * KT, 0);
+            const uint32_t s_col = __shfl_sync(~0u, tm + COL_S, 0);
             if (leader) {
 #pragma unroll
             for (int k = 0; k < HALF / 16; ++k)
@@ -605,7 +642,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
             if (!wait.all(bar(P_FULL + b), (i >> 1) & 1)) return false;
             fence_after();
             const uint32_t base = __shfl_sync(~0u, ring + stage * STAGE, 0);
-            const uint32_t p_col = __shfl_sync(~0u, tm + COL_P + b * (KT / 2), 0);
+            const uint32_t p_col = __shfl_sync(~0u, tm + COL_P, 0);
             if (leader) {
 #pragma unroll
             for (int k = 0; k < KT / 16; ++k)
@@ -623,9 +660,13 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
             const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
             const uint32_t n = (uint32_t)(seg.u1 - seg.u0);
             x += n;
-            ok = wait.all(bar(Q_FULL), segments++ & 1) && multiply_k(it) && (n < 2 || multiply_k(it + 1));
+            ok = wait.all(bar(Q_FULL), segments++ & 1) && multiply_k(it) &&
+                 (n < 2 || multiply_k(it + 1));
             for (uint32_t k = 0; ok && k < n; ++k)
-                ok = (k + 2 >= n || multiply_k(it + k + 2)) && multiply_v(it + k, k == 0);
+                ok = (k + 2 >= n || multiply_k(it + k + 2)) &&
+                     // O of the segment before has been read
+                     (k > 0 || segments < 2 || wait.all(bar(O_FREE), segments & 1)) &&
+                     multiply_v(it + k, k == 0);
             it += n;
         }
         // nothing that was issued outlives the block's memory, whatever gave up above
@@ -645,7 +686,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
     fence_before();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     fence_after();
-    if (warp == 8)
+    if (warp == ISSUE)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
