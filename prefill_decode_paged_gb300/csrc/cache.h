@@ -1,6 +1,7 @@
 // cache.h -- what the decode-side cache's host code and kernels share.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -48,6 +49,8 @@ struct kvc_cache {
     int64_t span = 0;                 // bytes from a plane's base to its end
     KvrDiv block = {};
     KvcWorkspace ws = {};
+    std::vector<CUtensorMap> maps;    // latents: copy-engine maps of the planes, two a layer
+    int32_t piece = 0;                // tokens of a map's box
     int device = 0;
     int sm_count = 0;
 
@@ -103,7 +106,7 @@ inline kvr_status kvc_launch(void (*kernel)(Args), const Args &a, dim3 grid, int
 kvr_status kvc_attend_launch(const kvc_cache *c, int32_t layer, const kvc_attend *a, void *stream);
 size_t kvc_attend_partial_bytes(const kvc_desc &d, int32_t sm_count);
 size_t kvc_attend_jobs(const kvc_desc &d);
-kvr_status kvc_attend_setup(const kvc_cache *c);
+kvr_status kvc_attend_setup(kvc_cache *c);
 // cache_append.cu
 kvr_status kvc_append_launch(const kvc_cache *c, int32_t layer, const kvc_append *a, void *stream);
 

@@ -35,8 +35,8 @@ size_t kvc_attend_jobs(const kvc_desc &d) {
     return (size_t)d.max_requests * d.kv_heads * (size_t)ceil_div(M, 8);
 }
 
-kvr_status kvc_attend_setup(const kvc_cache *c) {
-    if (c->latent()) return kvc_latent_setup();
+kvr_status kvc_attend_setup(kvc_cache *c) {
+    if (c->latent()) return kvc_latent_setup(c);
     for (int32_t M : {8, 16, 32}) {
         const AttendPick p = pick(c->d, M);
         if (cudaFuncSetAttribute(p.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -21,11 +21,13 @@
 // tiles of 32 keys with two S and two P took 1.8 times as long, for the time from a tile's S to
 // its P, through the other SM and back, is nearly the same for 32 keys.
 //
-// Shared memory: a ring of 4 tiles' halves (36 KB each) that 4 warps fill by 16-byte cp.async,
-// one row after another, so that any block size and stride will do and rows of padding are
-// zeros; and two times the half of S that the other SM sends. A tile is laid out in 128-byte rows
-// of 64 elements (swizzled), which serve as the K-major operand of S and as the MN-major operand
-// of O.
+// Shared memory: a ring of 4 tiles' halves (36 KB each), and two times the half of S that the
+// other SM sends. A tile is laid out in 128-byte rows of 64 elements (swizzled), which serve as
+// the K-major operand of S and as the MN-major operand of O. Tiles come by the copy engine, in
+// boxes of a block's tokens, where blocks are multiples of 8 tokens that divide a tile or are
+// divided by it; a request's last, partial tile, and all tiles of other block sizes, come row by
+// row by 16-byte cp.async, with zeros for the rows beyond the length. (By cp.async alone the load
+// and store units were what the kernel waited for.)
 //
 // Warps: twice 4 of softmax (one thread a row; even and odd tiles), 4 that send S to the other
 // SM, 4 of loads, 1 that issues the products. With one set of softmax warps that also sent, they
@@ -38,11 +40,13 @@
 // Numbers: S, maxima, sums, O and all joins are fp32. P is rounded once to the pool's 16-bit type
 // for its product: rounding it twice as fine would cost half of the products again.
 //
-// Every wait ends: after two seconds it gives up, flags KVC_FLAG_TIMEOUT, and all warps run out
-// of their loops to the end of the kernel.
+// Every wait ends: after two seconds it gives up and flags KVC_FLAG_TIMEOUT, and its warp goes to
+// the end of the kernel, as the others do for want of it.
 #include <math.h>
 
 #include <algorithm>
+
+#include <cuda.h>
 
 #include "cache_latent.h"
 #include "cache_split.cuh"
@@ -51,32 +55,36 @@ namespace {
 
 using namespace kvc;
 
-constexpr int KT = 64;                    // keys of a tile
+constexpr int KT = 32;                    // keys of a tile
 constexpr int ROWS = 128;                 // query rows of a pass
 constexpr int HALF = 256, REST = 32;      // value elements and others of an SM
-constexpr int STAGES = 4;                 // tiles in the ring
+constexpr int STAGES = 10;                // tiles in the ring
 constexpr int CHUNK = KT * 128;           // 64 elements of each key
 constexpr int STAGE = 4 * CHUNK + KT * 64;
 constexpr int XBUF = ROWS * KT * 4;
-// warps: softmax of even tiles, of odd tiles, sending, loading (4 each), products
-constexpr int SEND = 8, LOAD = 12, ISSUE = 16, WARPS = 17, THREADS = 32 * WARPS;
+// warps: softmax of even tiles, of odd tiles, sending, loading (4 each); products of S, of O; telling
+constexpr int SEND = 8, LOAD = 12, KEYS = 16, VALS = 17, TELL = 18, WARPS = 19, THREADS = 32 * WARPS;
 constexpr int OFF_XBUF = STAGES * STAGE, OFF_BARS = OFF_XBUF + 2 * XBUF, OFF_TOPS = OFF_BARS + 512,
               OFF_PREFIX = OFF_TOPS + 6 * ROWS * 4;
-constexpr uint32_t COL_O = 0, COL_Q = 256, COL_S = 400, COL_P = COL_S + KT;
-static_assert(COL_P + KT / 2 <= 512, "tensor memory");
+constexpr uint32_t COL_O = 0, COL_Q = 256, COL_S = 400, COL_P = COL_S + 2 * KT;
+static_assert(COL_P + KT <= 512, "tensor memory");
 constexpr int VALUES = KVC_LATENT_VALUES;
 // floats of one part's results: [element / 4][row][4], then (max, sum) a row
 constexpr size_t SLOT = (size_t)ROWS * VALUES + 2 * ROWS;
 
 // barriers, in 8-byte words after OFF_BARS
+// (a wait tells a phase from the one before only; O_DONE has 4, for a tile's may be looked at while
+// those of the two before are not sure to be done)
 enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, S_FULL = K_EMPTY + STAGES, S_FREE = S_FULL + 2,
-       P_FULL = S_FREE + 2, X_FULL = P_FULL + 2, X_EMPTY = X_FULL + 2, O_DONE = X_EMPTY + 2,
-       TOP = O_DONE + 2, Q_FULL = TOP + 8, O_FREE, SUMS, DRAIN, BARS };
-constexpr int OFF_TMEM = BARS * 8, OFF_ABORT = OFF_TMEM + 4, OFF_SCRATCH = OFF_TMEM + 16;
+       P_FULL = S_FREE + 2, X_FULL = P_FULL + 2, X_EMPTY = X_FULL + 2, X_READ = X_EMPTY + 2, O_DONE = X_READ + 2,
+       TOP = O_DONE + 4, Q_FULL = TOP + 8, O_FREE, SUMS, DRAIN, BARS = DRAIN + 2 };
+constexpr int OFF_TMEM = BARS * 8, OFF_SCRATCH = OFF_TMEM + 16;
 static_assert(OFF_SCRATCH + 4 * WARPS <= 512, "the words after the barriers");
 
 struct LatentArgs {
+    CUtensorMap values, rest;  // the plane's rows in pieces of `piece` tokens (piece 0: no such map)
     KvcPlane plane;
+    int32_t piece;
     SplitArgs split;
     const unsigned char *q;
     unsigned char *out;
@@ -108,44 +116,29 @@ __device__ __forceinline__ uint32_t remote_addr(uint32_t addr, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ uint64_t now_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
+// Waits for the phase of `parity`, in turns of a microsecond and for about two seconds at most.
+__device__ __forceinline__ uint32_t wait_for(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+                 "AGAIN:\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+                 "@p bra OUT;\n\t"
+                 "add.u32 n, n, 1;\n\t"
+                 "setp.lt.u32 p, n, 2000000;\n\t"
+                 "@p bra AGAIN;\n\t"
+                 "setp.ne.u32 p, n, n;\n"
+                 "OUT:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done;
 }
-
-struct Waits {
-    volatile int32_t *abort;
-    uint32_t *flags;
-    // waits for the phase of `parity`; false after two seconds, or once another wait gave up
-    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-        uint64_t began = 0;
-        for (uint32_t n = 0;; ++n) {
-            uint32_t done;
-            asm volatile("{\n\t.reg .pred p;\n\t"
-                         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                         "selp.u32 %0, 1, 0, p;\n\t}"
-                         : "=r"(done)
-                         : "r"(bar), "r"(parity)
-                         : "memory");
-            if (done) return true;
-            if ((n & 63) == 63) {
-                if (*abort) return false;
-                const uint64_t t = now_ns();
-                if (began == 0) began = t;
-                if (t - began > 2000000000ull) {
-                    *abort = 1;
-                    atomicOr(flags, KVC_FLAG_TIMEOUT);
-                    return false;
-                }
-            }
-        }
-    }
-    // the same answer for all lanes of a warp, which go on together
-    __device__ __forceinline__ bool all(uint32_t bar, uint32_t parity) const {
-        return __all_sync(~0u, (*this)(bar, parity));
-    }
-};
+// For a warp, whose lanes go on together with the same answer: false, and a flag, if it gave up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t *flags) {
+    const bool done = __all_sync(~0u, wait_for(bar, parity));
+    if (!done) atomicOr(flags, KVC_FLAG_TIMEOUT);
+    return done;
+}
 
 // -- tensor memory and products ---------------------------------------------------
 
@@ -181,6 +174,15 @@ __device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint
 }
 __device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+// a box of the pool's plane by the copy engine; its bytes count at `bar`
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int32_t element,
+                                         int32_t token, int32_t block, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                 "l"(map), "r"(element), "r"(token), "r"(block), "r"(bar)
                  : "memory");
 }
 
@@ -238,17 +240,17 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 // -- the kernel -------------------------------------------------------------------
 
 template <bool F16>
-__global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
+__global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constant__ LatentArgs a) {
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t smem0 = smem_addr(smem), bars = smem0 + OFF_BARS;
     int32_t *prefix = (int32_t *)(smem + OFF_PREFIX);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     uint32_t rank;
     asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
-    const Waits wait = {(volatile int32_t *)(smem + OFF_BARS + OFF_ABORT), a.split.flags};
     auto bar = [&](int which) { return bars + 8 * which; };
+    auto wait = [&](uint32_t b, uint32_t parity) { return warp_wait(b, parity, a.split.flags); };
 
-    if (warp == ISSUE) {
+    if (warp == KEYS) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          bars + OFF_TMEM)
                      : "memory");
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
     }
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            bar_init(bar(K_FULL + i), 128);       // the loading threads
+            bar_init(bar(K_FULL + i), a.piece > 0 ? 1 : 32);   // the loading warp or its threads
             bar_init(bar(K_EMPTY + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -264,20 +266,22 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
             bar_init(bar(S_FREE + i), 8);         // softmax and sending warps
             bar_init(bar(P_FULL + i), 4);
             bar_init(bar(X_FULL + i), 1);         // and the bytes that the other SM stores
-            bar_init(bar(X_EMPTY + i), 4);        // its softmax warps
+            bar_init(bar(X_EMPTY + i), 1);        // its telling warp
+            bar_init(bar(X_READ + i), 4);         // the softmax warps
             bar_init(bar(O_DONE + i), 1);
+            bar_init(bar(O_DONE + 2 + i), 1);
         }
         for (int i = 0; i < 8; ++i) bar_init(bar(TOP + i), 1);
         bar_init(bar(Q_FULL), 4);
         bar_init(bar(O_FREE), 8);
         bar_init(bar(SUMS), 8);
         bar_init(bar(DRAIN), 1);
-        *wait.abort = 0;
+        bar_init(bar(DRAIN + 1), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     wait_for_previous();
     let_next_start();
-    unit_prefix<KT>(a.split, 1, prefix, (int32_t *)(smem + OFF_BARS + OFF_SCRATCH));
+    unit_prefix<KT>(a.split, KT, prefix, (int32_t *)(smem + OFF_BARS + OFF_SCRATCH));
     fence_before();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     fence_after();
@@ -305,10 +309,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
 
     if (warp < SEND) {
         // ---- softmax of every other tile ----
-        // (registers: 2 x 128 x 128 here, 128 x 72 and 128 x 56 below, 32 x 96: the 544 x 96 of the launch)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
         const uint32_t b = warp / 4;              // of even or odd tiles, and their buffers
-        const uint32_t bars_remote = remote_addr(bars, rank ^ 1u);
         const uint64_t sc2 = splat2(a.scale * 1.4426950408889634f);
         float *tops = (float *)(smem + OFF_TOPS), *sums = tops + 2 * ROWS;   // [2][ROWS], [2][2][ROWS]
         const float4 *from = (const float4 *)(smem + OFF_XBUF + b * XBUF) + row;
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
             const uint32_t n = (uint32_t)(seg.u1 - seg.u0);
             x += n;
             uint32_t bad = 0;
-            const Span sp = span_of(a.split, seg.r, 1, &bad);
+            const Span sp = span_of(a.split, seg.r, KT, &bad);
             const Query query = query_of(seg);
             const int32_t end = sp.n - a.m + query.token + 1;
             const int32_t seen_all = sp.n - a.m + 1;
@@ -330,10 +331,10 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
             for (uint32_t k = (it & 1) == b ? 0 : 1; k < n; k += 2) {
                 const uint32_t i = it + k, ph = (i >> 1) & 1;
                 uint32_t s[KT];
-                if (!(ok = wait.all(bar(S_FULL + b), ph))) break;
+                if (!(ok = wait(bar(S_FULL + b), ph))) break;
                 fence_after();
 #pragma unroll
-                for (int e = 0; e < KT / 16; ++e) tm_load16(s + 16 * e, lanes + COL_S + 16 * e);
+                for (int e = 0; e < KT / 16; ++e) tm_load16(s + 16 * e, lanes + COL_S + b * KT + 16 * e);
                 wait_ld();
                 fence_before();
                 __syncwarp();
@@ -343,7 +344,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
                                      bar(X_FULL + b)),
                                  "r"(XBUF)
                                  : "memory");
-                if (!(ok = wait.all(bar(X_FULL + b), ph))) break;
+                if (!(ok = wait(bar(X_FULL + b), ph))) break;
 #pragma unroll
                 for (int e = 0; e < KT / 4; ++e) {
                     const float4 o = from[e * ROWS];
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
                     scaled_sum(s + 4 * e + 2, o.z, o.w, sc2);
                 }
                 __syncwarp();
-                if (lane == 0) bar_arrive_remote(bars_remote + 8 * (X_EMPTY + b));
+                if (lane == 0) bar_arrive(bar(X_READ + b));
                 const int32_t j0 = sp.lo + (seg.u0 + (int32_t)k) * KT;
                 if (j0 + KT > seen_all || j0 < seen_from) {
 #pragma unroll
@@ -369,13 +370,13 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
                 // what P and O are relative to: as the tile before left it, or more
                 float top = best;                 // O starts from a segment's first tile
                 if (k > 0) {
-                    if (!(ok = wait.all(bar(TOP + (b ^ 1) * 4 + warp % 4), ((i - 1) >> 1) & 1))) break;
+                    if (!(ok = wait(bar(TOP + (b ^ 1) * 4 + warp % 4), ((i - 1) >> 1) & 1))) break;
                     top = tops[(b ^ 1) * ROWS + row];
                     if (__any_sync(~0u, best > top + 8.0f)) {
                         const float next = fmaxf(top, best);
                         const float shrink = next == top ? 1.0f : ex2(top - next);
                         top = next;
-                        if (!(ok = wait.all(bar(O_DONE + (b ^ 1)), ((i - 1) >> 1) & 1))) break;
+                        if (!(ok = wait(bar(O_DONE + ((i - 1) & 3)), ((i - 1) >> 2) & 1))) break;
                         fence_after();
 #pragma unroll 1
                         for (int c = 0; c < HALF; c += 16) {
@@ -407,10 +408,9 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
                 }
                 const float2 both = unpack2(add);
                 sum += both.x + both.y;
-                // the product before has read the P that this one's goes over
-                if (i > 0 && !(ok = wait.all(bar(O_DONE + (b ^ 1)), ((i - 1) >> 1) & 1))) break;
-                tm_store16(lanes + COL_P, p);
-                tm_store16(lanes + COL_P + 16, p + 16);
+                // the product two tiles ago has read the P that this one goes over
+                if (i >= 2 && !(ok = wait(bar(O_DONE + ((i - 2) & 3)), ((i - 2) >> 2) & 1))) break;
+                tm_store16(lanes + COL_P + b * (KT / 2), p);
                 wait_st();
                 fence_before();
                 __syncwarp();
@@ -422,18 +422,17 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
             // the segment's maximum and sum, then its O: each of the two halves of the warps has
             // half of the columns
             const uint32_t last = it - 1, lb = last & 1;
-            if (lb != b && !(ok = wait.all(bar(TOP + lb * 4 + warp % 4), (last >> 1) & 1))) break;
+            if (lb != b && !(ok = wait(bar(TOP + lb * 4 + warp % 4), (last >> 1) & 1))) break;
             const float top = tops[lb * ROWS + row];
             if (top != ref) sum *= ref == -INFINITY ? 0.0f : ex2(ref - top);
             float *mine_sum = sums + (segments & 1) * 2 * ROWS;
             mine_sum[b * ROWS + row] = sum;
             __syncwarp();
             if (lane == 0) bar_arrive(bar(SUMS));
-            if (!(ok = wait.all(bar(SUMS), segments & 1))) break;
+            if (!(ok = wait(bar(SUMS), segments & 1))) break;
             sum = mine_sum[row] + mine_sum[ROWS + row];
             ++segments;
-            if (last > 0 && !(ok = wait.all(bar(O_DONE + (lb ^ 1)), ((last - 1) >> 1) & 1))) break;
-            if (!(ok = wait.all(bar(O_DONE + lb), (last >> 1) & 1))) break;
+            if (!(ok = wait(bar(O_DONE + (last & 3)), (last >> 2) & 1))) break;
             fence_after();
 
             const bool whole = seg.u0 == 0 && seg.u1 == seg.units, mine = query.mine;
@@ -484,7 +483,6 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
         }
     } else if (warp < LOAD) {
         // ---- sending: this SM's half of S to the other; and a segment's q to tensor memory ----
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const uint32_t x_remote = remote_addr(smem0 + OFF_XBUF, rank ^ 1u) + row * 16;
         const uint32_t bars_remote = remote_addr(bars, rank ^ 1u);
         uint32_t it = 0;
@@ -516,70 +514,109 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
             if (lane == 0) bar_arrive(bar(Q_FULL));
             for (uint32_t k = 0; k < n; ++k, ++it) {
                 const uint32_t b = it & 1, ph = (it >> 1) & 1;
-                if (!(ok = wait.all(bar(X_EMPTY + b), ph ^ 1))) break;
-                if (!(ok = wait.all(bar(S_FULL + b), ph))) break;
+                if (!(ok = wait(bar(X_EMPTY + b), ph ^ 1))) break;
+                if (!(ok = wait(bar(S_FULL + b), ph))) break;
                 fence_after();
+                uint32_t s[KT];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t s[KT / 2];
+                for (int e = 0; e < KT / 16; ++e) tm_load16(s + 16 * e, lanes + COL_S + b * KT + 16 * e);
+                wait_ld();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(S_FREE + b));
 #pragma unroll
-                    for (int e = 0; e < KT / 32; ++e)
-                        tm_load16(s + 16 * e, lanes + COL_S + half * (KT / 2) + 16 * e);
-                    wait_ld();
-                    if (half == 1) {
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(bar(S_FREE + b));
-                    }
-#pragma unroll
-                    for (int e = 0; e < KT / 8; ++e)
-                        asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], "
-                                     "{%1, %2, %3, %4}, [%5];" ::"r"(x_remote + b * XBUF +
-                                                                     (half * (KT / 8) + e) * ROWS * 16),
-                                     "r"(s[4 * e]), "r"(s[4 * e + 1]), "r"(s[4 * e + 2]),
-                                     "r"(s[4 * e + 3]), "r"(bars_remote + 8 * (X_FULL + b))
-                                     : "memory");
-                }
+                for (int e = 0; e < KT / 4; ++e)
+                    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], "
+                                 "{%1, %2, %3, %4}, [%5];" ::"r"(x_remote + b * XBUF + e * ROWS * 16),
+                                 "r"(s[4 * e]), "r"(s[4 * e + 1]), "r"(s[4 * e + 2]), "r"(s[4 * e + 3]),
+                                 "r"(bars_remote + 8 * (X_FULL + b))
+                                 : "memory");
             }
         }
-    } else if (warp < ISSUE) {
-        // ---- loads: warp w of 4 has 16 keys of a tile ----
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        const int w = warp - LOAD;
-        constexpr int MINE = KT / 4;
-        static_assert(MINE == 16, "a lane's half-warp number is its key");
+    } else if (warp == TELL) {
+        // ---- telling the other SM what it may send over: its arrival takes some hundred cycles,
+        // which the softmax warps do not have ----
+        const uint32_t bars_remote = remote_addr(bars, rank ^ 1u);
+        uint32_t it = 0;
+        bool ok = true;
+        while (ok && x < x_end) {
+            const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
+            x += seg.u1 - seg.u0;
+            for (int32_t u = seg.u0; u < seg.u1; ++u, ++it) {
+                if (!(ok = wait(bar(X_READ + (it & 1)), (it >> 1) & 1))) break;
+                if (lane == 0) bar_arrive_remote(bars_remote + 8 * (X_EMPTY + (it & 1)));
+                __syncwarp();
+            }
+        }
+    } else if (warp < KEYS) {
+        // ---- loads: warp w of 4 has every fourth tile ----
+        uint32_t leader;
+        asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(leader));
+        const uint32_t w = warp - LOAD;
+        static_assert(KT == 32, "a lane's number is its key");
         uint32_t it = 0, bad = 0;
         bool ok = true;
         const unsigned char *src = a.plane.base;
         while (ok && x < x_end) {
             const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
-            x += seg.u1 - seg.u0;
-            const Span sp = span_of(a.split, seg.r, 1, &bad);
+            const uint32_t n = (uint32_t)(seg.u1 - seg.u0);
+            x += n;
+            const Span sp = span_of(a.split, seg.r, KT, &bad);
             const int32_t *table = a.split.slots.ids + (int64_t)seg.r * a.split.slots.stride;
-            auto slot_of = [&](int32_t u) -> int64_t {      // of the lane's key, -1: none
-                const int32_t j = sp.lo + u * KT + w * MINE + lane;
-                if (lane >= MINE || u >= seg.u1 || j >= sp.n) return -1;
-                const uint32_t entry = a.split.slots.block.div((uint32_t)j);
-                const int32_t id = __ldg(table + entry);
-                if (id < 0 || id >= a.split.slots.num_blocks) {
-                    bad |= KVC_FLAG_BLOCK;
-                    return -1;
-                }
-                return id * a.plane.block_stride +
-                       (int64_t)(j - (int32_t)(entry * a.split.slots.block.d)) * a.plane.token_stride;
+            // tiles that lie in the request as a whole come in boxes, if there are any
+            const int32_t whole = a.piece > 0 ? min(seg.u1, (sp.n - sp.lo) / KT) : 0;
+            const int32_t pieces = a.piece > 0 ? KT / a.piece : 0;
+            // the block id that this lane looks up for tile u: of box piece `lane`, or of its key.
+            // It is asked for a turn ahead and not looked at before.
+            auto position = [&](int32_t u) -> int32_t {
+                if (u < whole) return lane < pieces ? sp.lo + u * KT + lane * a.piece : -1;
+                const int32_t j = sp.lo + u * KT + lane;
+                return u < seg.u1 && j < sp.n ? j : -1;
             };
-            int64_t next = slot_of(seg.u0);
-            for (int32_t u = seg.u0; u < seg.u1; ++u, ++it) {
-                const int64_t slot = next;
-                next = slot_of(u + 1);
-                const uint32_t stage = it % STAGES;
-                if (!(ok = wait.all(bar(K_EMPTY + stage), (it / STAGES + 1) & 1))) break;
-                const uint32_t base = smem0 + stage * STAGE;
-                // values: 32 pieces of 16 bytes a key, one key at a time
+            auto look_up = [&](int32_t j) -> int32_t {
+                return j < 0 ? 0 : __ldg(table + a.split.slots.block.div((uint32_t)j));
+            };
+            uint32_t k = (w - it) & 3;
+            int32_t next = look_up(position(seg.u0 + (int32_t)k));
+            for (; k < n; k += 4) {
+                const int32_t u = seg.u0 + (int32_t)k;
+                const uint32_t i = it + k, stage = i % STAGES;
+                int32_t id = next;
+                next = look_up(position(u + 4));
+                if (!(ok = wait(bar(K_EMPTY + stage), (i / STAGES + 1) & 1))) break;
+                const uint32_t base = smem0 + stage * STAGE, full = bar(K_FULL + stage);
+                const int32_t j = position(u);
+                const bool there = j >= 0 && id >= 0 && id < a.split.slots.num_blocks;
+                if (j >= 0 && !there) bad |= KVC_FLAG_BLOCK;
+                const int32_t token =
+                    max(j, 0) - (int32_t)(a.split.slots.block.div((uint32_t)max(j, 0)) * a.split.slots.block.d);
+                if (u < whole) {
+                    if (!there) id = a.split.slots.num_blocks;    // past the last: zeros
+                    if (leader)
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full),
+                                     "r"(STAGE)
+                                     : "memory");
+                    for (int piece = 0; piece < pieces; ++piece) {
+                        const int32_t block = __shfl_sync(~0u, id, piece);
+                        const int32_t first = __shfl_sync(~0u, token, piece);
+                        if (leader) {
 #pragma unroll
-                for (int k = 0; k < MINE; ++k) {
-                    const int64_t off = __shfl_sync(~0u, slot, k);
-                    const uint32_t row = w * MINE + k;
+                            for (int c = 0; c < 4; ++c)
+                                load_box(base + c * CHUNK + piece * a.piece * 128, &a.values,
+                                         (int32_t)rank * HALF + c * 64, first, block, full);
+                            load_box(base + 4 * CHUNK + piece * a.piece * 64, &a.rest,
+                                     VALUES + (int32_t)rank * REST, first, block, full);
+                        }
+                    }
+                    __syncwarp();
+                    continue;
+                }
+                const int64_t slot = there ? id * a.plane.block_stride + (int64_t)token * a.plane.token_stride : -1;
+                // values: 32 pieces of 16 bytes a key, one key at a time
+#pragma unroll 8
+                for (int row = 0; row < KT; ++row) {
+                    const int64_t off = __shfl_sync(~0u, slot, row);
                     const int64_t at = off >= 0 ? off + rank * (HALF * 2) + lane * 16 : 0;
                     const uint32_t dst = base + (lane / 8) * CHUNK + row * 128 + (((lane % 8) ^ (row & 7)) << 4);
                     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst),
@@ -588,97 +625,98 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
                 }
                 // the rest: 4 pieces a key, 8 keys at a time
 #pragma unroll
-                for (int k = 0; k < MINE; k += 8) {
-                    const int64_t off = __shfl_sync(~0u, slot, k + lane / 4);
-                    const uint32_t row = w * MINE + k + lane / 4, c = lane % 4;
+                for (int r0 = 0; r0 < KT; r0 += 8) {
+                    const int64_t off = __shfl_sync(~0u, slot, r0 + lane / 4);
+                    const uint32_t row = r0 + lane / 4, c = lane % 4;
                     const int64_t at = off >= 0 ? off + (VALUES + rank * REST) * 2 + c * 16 : 0;
                     const uint32_t dst = base + 4 * CHUNK + row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
                                  "l"(src + at), "r"(off >= 0 ? 16 : 0)
                                  : "memory");
                 }
-                // arrives when this thread's copies so far have
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                                 bar(K_FULL + stage))
-                             : "memory");
+                if (a.piece > 0) {
+                    // a request's last tile
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(full);
+                } else {
+                    // arrives when this thread's copies so far have
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+                }
             }
+            it += n;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!ok)                                  // what was asked for has to come all the same
+            for (uint32_t i = 0; i < STAGES; ++i) wait_for(bar(K_FULL + i), 0), wait_for(bar(K_FULL + i), 1);
         if (bad != 0) atomicOr(a.split.flags, bad);
     } else {
-        // ---- products: S two tiles ahead of O; the warp runs as one, so that operand
-        // descriptors stay in uniform registers, and one elected lane issues ----
+        // ---- products, S by one warp and O by another, so that neither waits for what the other
+        // waits for. A warp runs as one, which keeps operand descriptors in uniform registers, and
+        // one elected lane issues ----
         uint32_t leader;
         asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                      : "=r"(leader));
         const uint32_t tm = __shfl_sync(~0u, tmem, 0), ring = __shfl_sync(~0u, smem0, 0);
         constexpr uint32_t ID_S = idesc(!F16, false, KT), ID_O = idesc(!F16, true, HALF);
-        auto multiply_k = [&](uint32_t i) -> bool {
-            const uint32_t b = i & 1, stage = i % STAGES;
-            if (!wait.all(bar(K_FULL + stage), (i / STAGES) & 1)) return false;
-            // the S before, which this one goes over, has been read
-            if (i > 0 && !wait.all(bar(S_FREE + (b ^ 1)), ((i - 1) >> 1) & 1)) return false;
-            fence_after();
-            // the copies came through the generic proxy; the products read through the async one
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            const uint32_t base = __shfl_sync(~0u, ring + stage * STAGE, 0);
-            const uint32_t s_col = __shfl_sync(~0u, tm + COL_S, 0);
-            if (leader) {
-#pragma unroll
-            for (int k = 0; k < HALF / 16; ++k)
-                product(s_col, tm + COL_Q + 8 * k,
-                        operand(base + (k / 4) * CHUNK + (k % 4) * 32, 16, 1024, 2), ID_S, k > 0);
-#pragma unroll
-            for (int k = 0; k < REST / 16; ++k)
-                product(s_col, tm + COL_Q + HALF / 2 + 8 * k,
-                        operand(base + 4 * CHUNK + k * 32, 16, 512, 4), ID_S, 1);
-            commit(bar(S_FULL + b));
-            }
-            __syncwarp();
-            return true;
-        };
-        auto multiply_v = [&](uint32_t i, bool first) -> bool {
-            const uint32_t b = i & 1, stage = i % STAGES;
-            if (!wait.all(bar(P_FULL + b), (i >> 1) & 1)) return false;
-            fence_after();
-            const uint32_t base = __shfl_sync(~0u, ring + stage * STAGE, 0);
-            const uint32_t p_col = __shfl_sync(~0u, tm + COL_P, 0);
-            if (leader) {
-#pragma unroll
-            for (int k = 0; k < KT / 16; ++k)
-                product(tm + COL_O, p_col + 8 * k,
-                        operand(base + k * 2048, CHUNK, 1024, 2), ID_O, !(first && k == 0));
-            commit(bar(K_EMPTY + stage));
-            commit(bar(O_DONE + b));
-            }
-            __syncwarp();
-            return true;
-        };
         uint32_t it = 0, segments = 0;
         bool ok = true;
         while (ok && x < x_end) {
             const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
             const uint32_t n = (uint32_t)(seg.u1 - seg.u0);
             x += n;
-            ok = wait.all(bar(Q_FULL), segments++ & 1) && multiply_k(it) &&
-                 (n < 2 || multiply_k(it + 1));
-            for (uint32_t k = 0; ok && k < n; ++k)
-                ok = (k + 2 >= n || multiply_k(it + k + 2)) &&
-                     // O of the segment before has been read
-                     (k > 0 || segments < 2 || wait.all(bar(O_FREE), segments & 1)) &&
-                     multiply_v(it + k, k == 0);
+            if (warp == KEYS) {
+                ok = wait(bar(Q_FULL), segments++ & 1);
+                for (uint32_t k = 0; ok && k < n; ++k) {
+                    const uint32_t i = it + k, b = i & 1, stage = i % STAGES;
+                    if (!(ok = wait(bar(K_FULL + stage), (i / STAGES) & 1))) break;
+                    // the S two tiles ago, which this one goes over, has been read
+                    if (i >= 2 && !(ok = wait(bar(S_FREE + b), ((i >> 1) & 1) ^ 1))) break;
+                    fence_after();
+                    // copies that came through the generic proxy; the products read through the async one
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    const uint32_t base = __shfl_sync(~0u, ring + stage * STAGE, 0);
+                    const uint32_t s_col = __shfl_sync(~0u, tm + COL_S + b * KT, 0);
+                    if (leader) {
+#pragma unroll
+                        for (int e = 0; e < HALF / 16; ++e)
+                            product(s_col, tm + COL_Q + 8 * e,
+                                    operand(base + (e / 4) * CHUNK + (e % 4) * 32, 16, 1024, 2), ID_S, e > 0);
+#pragma unroll
+                        for (int e = 0; e < REST / 16; ++e)
+                            product(s_col, tm + COL_Q + HALF / 2 + 8 * e,
+                                    operand(base + 4 * CHUNK + e * 32, 16, 512, 4), ID_S, 1);
+                        commit(bar(S_FULL + b));
+                    }
+                    __syncwarp();
+                }
+            } else {
+                for (uint32_t k = 0; ok && k < n; ++k) {
+                    const uint32_t i = it + k, b = i & 1, stage = i % STAGES;
+                    // O of the segment before has been read
+                    if (k == 0 && segments++ > 0 && !(ok = wait(bar(O_FREE), segments & 1))) break;
+                    if (!(ok = wait(bar(P_FULL + b), (i >> 1) & 1))) break;
+                    fence_after();
+                    const uint32_t base = __shfl_sync(~0u, ring + stage * STAGE, 0);
+                    const uint32_t p_col = __shfl_sync(~0u, tm + COL_P + b * (KT / 2), 0);
+                    if (leader) {
+#pragma unroll
+                        for (int e = 0; e < KT / 16; ++e)
+                            product(tm + COL_O, p_col + 8 * e, operand(base + e * 2048, CHUNK, 1024, 2),
+                                    ID_O, k > 0 || e > 0);
+                        commit(bar(K_EMPTY + stage));
+                        commit(bar(O_DONE + (i & 3)));
+                    }
+                    __syncwarp();
+                }
+            }
             it += n;
         }
         // nothing that was issued outlives the block's memory, whatever gave up above
-        if (leader) commit(bar(DRAIN));
+        if (leader) commit(bar(DRAIN + (warp - KEYS)));
         __syncwarp();
-        for (uint32_t n = 0, done = 0; !done && n < (1u << 20); ++n)
-            asm volatile("{\n\t.reg .pred p;\n\t"
-                         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0;\n\t"
-                         "selp.u32 %0, 1, 0, p;\n\t}"
-                         : "=r"(done)
-                         : "r"(bar(DRAIN))
-                         : "memory");
+        wait_for(bar(DRAIN + (warp - KEYS)), 0);
     }
 
     // both SMs stay until neither has anything under way to the other
@@ -686,7 +724,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(LatentArgs a) {
     fence_before();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     fence_after();
-    if (warp == ISSUE)
+    if (warp == KEYS)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
@@ -697,12 +735,12 @@ constexpr int JOIN_ROWS = 8, JOIN_THREADS = JOIN_ROWS * (VALUES / 8);
 // One block a job and 8 of its rows: the parts' accumulators weighted by their maxima, in the
 // order of the keys. Jobs that one part did whole are not touched.
 template <bool F16>
-__global__ void __launch_bounds__(JOIN_THREADS) latent_join(LatentArgs a) {
+__global__ void __launch_bounds__(JOIN_THREADS) latent_join(const __grid_constant__ LatentArgs a) {
     extern __shared__ int32_t join_smem[];
     int32_t *scratch = join_smem, *prefix = join_smem + 32;
     wait_for_previous();
     let_next_start();
-    unit_prefix<KT>(a.split, 1, prefix, scratch);
+    unit_prefix<KT>(a.split, KT, prefix, scratch);
     const int64_t total = (int64_t)prefix[a.split.requests] * a.chunks;
     const int64_t parts = max((int64_t)1, min((int64_t)a.parts, total / a.least));
     const int32_t groups = ROWS / JOIN_ROWS;
@@ -749,7 +787,53 @@ size_t kvc_latent_partial_bytes(int32_t sm_count) {
     return (size_t)(sm_count / 2) * 2 * SLOT * sizeof(float);
 }
 
-kvr_status kvc_latent_setup() {
+// Copy-engine maps of each layer's plane, as [block][token][element] in boxes of `piece` tokens
+// and 64 (values) or 32 elements. Where a block is no multiple of 8 tokens that divide a tile, or a
+// stride is more than a map holds, there are none and rows come by cp.async.
+static kvr_status make_maps(kvc_cache *c) {
+    const int32_t B = c->d.block_size;
+    const int32_t piece = std::min(B, KT);
+    c->piece = 0;
+    c->maps.clear();
+    if (piece < 8 || KT % piece != 0 || B % piece != 0 || c->block_stride >= (int64_t)1 << 40 ||
+        c->token_stride >= (int64_t)1 << 40)
+        return KVR_OK;
+    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, CUDART_VERSION,
+                                         cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || p == nullptr) {
+        cudaGetLastError();
+        return KVR_ERR_CUDA;
+    }
+    const Encode encode = reinterpret_cast<Encode>(p);
+    c->maps.resize(2 * (size_t)c->d.num_layers);
+    for (int32_t l = 0; l < c->d.num_layers; ++l)
+        for (int k = 0; k < 2; ++k) {
+            const cuuint64_t dims[3] = {KVC_LATENT_DIM, (cuuint64_t)B, (cuuint64_t)c->d.num_blocks};
+            // (a stride of an extent of 1 is not used, but may not be zero)
+            const cuuint64_t strides[2] = {
+                (cuuint64_t)(c->token_stride > 0 ? c->token_stride : c->row_bytes),
+                (cuuint64_t)(c->block_stride > 0 ? c->block_stride : c->row_bytes)};
+            const cuuint32_t box[3] = {k == 0 ? 64u : (cuuint32_t)REST, (cuuint32_t)piece, 1};
+            const cuuint32_t steps[3] = {1, 1, 1};
+            if (encode(&c->maps[2 * (size_t)l + k], CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
+                       (void *)(uintptr_t)c->base[l], dims, strides, box, steps,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       k == 0 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return KVR_ERR_CUDA;
+        }
+    c->piece = piece;
+    return KVR_OK;
+}
+
+kvr_status kvc_latent_setup(kvc_cache *c) {
     const int smem = OFF_PREFIX + 4 * (KVC_MAX_REQUESTS + 1);
     static_assert(OFF_PREFIX + 4 * (KVC_MAX_REQUESTS + 1) <= 227 * 1024, "");
     for (auto k : {latent_kernel<false>, latent_kernel<true>})
@@ -757,12 +841,17 @@ kvr_status kvc_latent_setup() {
             cudaGetLastError();
             return KVR_ERR_CUDA;
         }
-    return KVR_OK;
+    return make_maps(c);
 }
 
 kvr_status kvc_latent_launch(const kvc_cache *c, int32_t layer, const kvc_attend *p, void *stream) {
     LatentArgs a = {};
     a.plane = c->plane(layer, 0);
+    a.piece = c->piece;
+    if (c->piece > 0) {
+        a.values = c->maps[2 * (size_t)layer];
+        a.rest = c->maps[2 * (size_t)layer + 1];
+    }
     a.split = {c->slots(p->table), p->lengths, c->ws.flags, p->num_requests, p->num_new, p->window};
     a.q = (const unsigned char *)p->q;
     a.out = (unsigned char *)p->out;
