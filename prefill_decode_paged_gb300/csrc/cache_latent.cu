@@ -33,9 +33,9 @@
 // SM, 4 of loads, 1 that issues the products. With one set of softmax warps that also sent, they
 // were busy for 2100 cycles a tile, of which HBM wants 780. A tile's softmax needs of the one
 // before only what P is relative to, which goes through shared memory as soon as it is known.
-// O is rescaled only when a row's maximum grows by more than 2^8 over the one that its P is
-// relative to (P is then at most 2^8, fine in either 16-bit type); that happens in the first tiles
-// of a job and hardly again.
+// O is rescaled only when a row's maximum outgrows by 2^40 (f16: 2^8) the one that its P is
+// relative to, which hardly happens after the first tiles of a job: powers of two cost no
+// precision in P, O and the sums.
 //
 // Numbers: S, maxima, sums, O and all joins are fp32. P is rounded once to the pool's 16-bit type
 // for its product: rounding it twice as fine would cost half of the products again.
@@ -58,28 +58,31 @@ using namespace kvc;
 constexpr int KT = 32;                    // keys of a tile
 constexpr int ROWS = 128;                 // query rows of a pass
 constexpr int HALF = 256, REST = 32;      // value elements and others of an SM
-constexpr int STAGES = 10;                // tiles in the ring
+constexpr int STAGES = 9;                 // tiles in the ring
+constexpr int SBUF = 3;                   // halves of S at a time, own and received
 constexpr int CHUNK = KT * 128;           // 64 elements of each key
 constexpr int STAGE = 4 * CHUNK + KT * 64;
 constexpr int XBUF = ROWS * KT * 4;
-// warps: softmax of even tiles, of odd tiles, sending, loading (4 each); products of S, of O; telling
-constexpr int SEND = 8, LOAD = 12, KEYS = 16, VALS = 17, TELL = 18, WARPS = 19, THREADS = 32 * WARPS;
-constexpr int OFF_XBUF = STAGES * STAGE, OFF_BARS = OFF_XBUF + 2 * XBUF, OFF_TOPS = OFF_BARS + 512,
+// warps: softmax of even tiles, of odd tiles, sending, loading (4 each); products of S of even
+// tiles, of odd tiles, of O; telling
+constexpr int SEND = 8, LOAD = 12, KEYS = 16, VALS = 18, TELL = 19, WARPS = 20, THREADS = 32 * WARPS;
+constexpr int OFF_XBUF = STAGES * STAGE, OFF_BARS = OFF_XBUF + SBUF * XBUF, OFF_TOPS = OFF_BARS + 768,
               OFF_PREFIX = OFF_TOPS + 6 * ROWS * 4;
-constexpr uint32_t COL_O = 0, COL_Q = 256, COL_S = 400, COL_P = COL_S + 2 * KT;
-static_assert(COL_P + KT <= 512, "tensor memory");
+constexpr uint32_t COL_O = 0, COL_Q = 256, COL_S = 400, COL_P = COL_S + SBUF * KT;
+static_assert(COL_P + KT / 2 <= 512, "tensor memory");
 constexpr int VALUES = KVC_LATENT_VALUES;
 // floats of one part's results: [element / 4][row][4], then (max, sum) a row
 constexpr size_t SLOT = (size_t)ROWS * VALUES + 2 * ROWS;
 
 // barriers, in 8-byte words after OFF_BARS
-// (a wait tells a phase from the one before only; O_DONE has 4, for a tile's may be looked at while
-// those of the two before are not sure to be done)
-enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, S_FULL = K_EMPTY + STAGES, S_FREE = S_FULL + 2,
-       P_FULL = S_FREE + 2, X_FULL = P_FULL + 2, X_EMPTY = X_FULL + 2, X_READ = X_EMPTY + 2, O_DONE = X_READ + 2,
-       TOP = O_DONE + 4, Q_FULL = TOP + 8, O_FREE, SUMS, DRAIN, BARS = DRAIN + 2 };
+// (a wait tells a phase from the one before only; where more may be under way there are more
+// barriers: O_DONE has 4, and S_FREE twice as many as there are S)
+enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, S_FULL = K_EMPTY + STAGES, S_FREE = S_FULL + SBUF,
+       X_FULL = S_FREE + 2 * SBUF, X_EMPTY = X_FULL + SBUF, X_READ = X_EMPTY + SBUF,
+       P_FULL = X_READ + SBUF, O_DONE = P_FULL + 2, TOP = O_DONE + 4, Q_FULL = TOP + 8, O_FREE, SUMS,
+       DRAIN, BARS = DRAIN + 3 };
 constexpr int OFF_TMEM = BARS * 8, OFF_SCRATCH = OFF_TMEM + 16;
-static_assert(OFF_SCRATCH + 4 * WARPS <= 512, "the words after the barriers");
+static_assert(OFF_SCRATCH + 4 * WARPS <= 768, "the words after the barriers");
 
 struct LatentArgs {
     CUtensorMap values, rest;  // the plane's rows in pieces of `piece` tokens (piece 0: no such map)
@@ -239,8 +242,14 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 
 // -- the kernel -------------------------------------------------------------------
 
+// how far (as a power of two) P may exceed 1 before O is rescaled: bf16 P and fp32 sums reach
+// far, f16 P ends at 2^16
+template <bool F16>
+constexpr float GROWTH_OF = F16 ? 8.0f : 40.0f;
+
 template <bool F16>
 __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constant__ LatentArgs a) {
+    constexpr float GROWTH = GROWTH_OF<F16>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t smem0 = smem_addr(smem), bars = smem0 + OFF_BARS;
     int32_t *prefix = (int32_t *)(smem + OFF_PREFIX);
@@ -261,22 +270,23 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
             bar_init(bar(K_FULL + i), a.piece > 0 ? 1 : 32);   // the loading warp or its threads
             bar_init(bar(K_EMPTY + i), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < SBUF; ++i) {
             bar_init(bar(S_FULL + i), 1);
             bar_init(bar(S_FREE + i), 8);         // softmax and sending warps
-            bar_init(bar(P_FULL + i), 4);
-            bar_init(bar(X_FULL + i), 1);         // and the bytes that the other SM stores
+            bar_init(bar(S_FREE + SBUF + i), 8);
+            bar_init(bar(X_FULL + i), 2);         // both halves of S: the product, the other SM's bytes
             bar_init(bar(X_EMPTY + i), 1);        // its telling warp
             bar_init(bar(X_READ + i), 4);         // the softmax warps
-            bar_init(bar(O_DONE + i), 1);
-            bar_init(bar(O_DONE + 2 + i), 1);
         }
+        for (int i = 0; i < 2; ++i) bar_init(bar(P_FULL + i), 4);
+        for (int i = 0; i < 4; ++i) bar_init(bar(O_DONE + i), 1);
         for (int i = 0; i < 8; ++i) bar_init(bar(TOP + i), 1);
         bar_init(bar(Q_FULL), 4);
         bar_init(bar(O_FREE), 8);
         bar_init(bar(SUMS), 8);
         bar_init(bar(DRAIN), 1);
         bar_init(bar(DRAIN + 1), 1);
+        bar_init(bar(DRAIN + 2), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     wait_for_previous();
@@ -312,7 +322,6 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
         const uint32_t b = warp / 4;              // of even or odd tiles, and their buffers
         const uint64_t sc2 = splat2(a.scale * 1.4426950408889634f);
         float *tops = (float *)(smem + OFF_TOPS), *sums = tops + 2 * ROWS;   // [2][ROWS], [2][2][ROWS]
-        const float4 *from = (const float4 *)(smem + OFF_XBUF + b * XBUF) + row;
         uint32_t it = 0, segments = 0;            // tiles and segments so far
         bool ok = true;
         while (ok && x < x_end) {
@@ -329,30 +338,25 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
             float ref = -INFINITY, sum = 0.0f;
 
             for (uint32_t k = (it & 1) == b ? 0 : 1; k < n; k += 2) {
-                const uint32_t i = it + k, ph = (i >> 1) & 1;
+                const uint32_t i = it + k, sb = i % SBUF;
+                const float4 *from = (const float4 *)(smem + OFF_XBUF + sb * XBUF) + row;
                 uint32_t s[KT];
-                if (!(ok = wait(bar(S_FULL + b), ph))) break;
+                if (!(ok = wait(bar(X_FULL + sb), (i / SBUF) & 1))) break;
                 fence_after();
 #pragma unroll
-                for (int e = 0; e < KT / 16; ++e) tm_load16(s + 16 * e, lanes + COL_S + b * KT + 16 * e);
+                for (int e = 0; e < KT / 16; ++e) tm_load16(s + 16 * e, lanes + COL_S + sb * KT + 16 * e);
+                float4 other[KT / 4];
+#pragma unroll
+                for (int e = 0; e < KT / 4; ++e) other[e] = from[e * ROWS];
                 wait_ld();
                 fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(bar(S_FREE + b));
-                if (row == 0)
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
-                                     bar(X_FULL + b)),
-                                 "r"(XBUF)
-                                 : "memory");
-                if (!(ok = wait(bar(X_FULL + b), ph))) break;
 #pragma unroll
                 for (int e = 0; e < KT / 4; ++e) {
-                    const float4 o = from[e * ROWS];
-                    scaled_sum(s + 4 * e, o.x, o.y, sc2);
-                    scaled_sum(s + 4 * e + 2, o.z, o.w, sc2);
+                    scaled_sum(s + 4 * e, other[e].x, other[e].y, sc2);
+                    scaled_sum(s + 4 * e + 2, other[e].z, other[e].w, sc2);
                 }
                 __syncwarp();
-                if (lane == 0) bar_arrive(bar(X_READ + b));
+                if (lane < 2) bar_arrive(bar(lane == 0 ? S_FREE + i % (2 * SBUF) : X_READ + sb));
                 const int32_t j0 = sp.lo + (seg.u0 + (int32_t)k) * KT;
                 if (j0 + KT > seen_all || j0 < seen_from) {
 #pragma unroll
@@ -372,7 +376,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                 if (k > 0) {
                     if (!(ok = wait(bar(TOP + (b ^ 1) * 4 + warp % 4), ((i - 1) >> 1) & 1))) break;
                     top = tops[(b ^ 1) * ROWS + row];
-                    if (__any_sync(~0u, best > top + 8.0f)) {
+                    if (__any_sync(~0u, best > top + GROWTH)) {
                         const float next = fmaxf(top, best);
                         const float shrink = next == top ? 1.0f : ex2(top - next);
                         top = next;
@@ -408,9 +412,9 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                 }
                 const float2 both = unpack2(add);
                 sum += both.x + both.y;
-                // the product two tiles ago has read the P that this one goes over
-                if (i >= 2 && !(ok = wait(bar(O_DONE + ((i - 2) & 3)), ((i - 2) >> 2) & 1))) break;
-                tm_store16(lanes + COL_P + b * (KT / 2), p);
+                // the product before has read the P that this one goes over
+                if (i > 0 && !(ok = wait(bar(O_DONE + ((i - 1) & 3)), ((i - 1) >> 2) & 1))) break;
+                tm_store16(lanes + COL_P, p);
                 wait_st();
                 fence_before();
                 __syncwarp();
@@ -513,23 +517,23 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
             __syncwarp();
             if (lane == 0) bar_arrive(bar(Q_FULL));
             for (uint32_t k = 0; k < n; ++k, ++it) {
-                const uint32_t b = it & 1, ph = (it >> 1) & 1;
-                if (!(ok = wait(bar(X_EMPTY + b), ph ^ 1))) break;
-                if (!(ok = wait(bar(S_FULL + b), ph))) break;
+                const uint32_t sb = it % SBUF, ph = (it / SBUF) & 1;
+                if (!(ok = wait(bar(X_EMPTY + sb), ph ^ 1))) break;
+                if (!(ok = wait(bar(S_FULL + sb), ph))) break;
                 fence_after();
                 uint32_t s[KT];
 #pragma unroll
-                for (int e = 0; e < KT / 16; ++e) tm_load16(s + 16 * e, lanes + COL_S + b * KT + 16 * e);
+                for (int e = 0; e < KT / 16; ++e) tm_load16(s + 16 * e, lanes + COL_S + sb * KT + 16 * e);
                 wait_ld();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(bar(S_FREE + b));
+                if (lane == 0) bar_arrive(bar(S_FREE + it % (2 * SBUF)));
 #pragma unroll
                 for (int e = 0; e < KT / 4; ++e)
                     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], "
-                                 "{%1, %2, %3, %4}, [%5];" ::"r"(x_remote + b * XBUF + e * ROWS * 16),
+                                 "{%1, %2, %3, %4}, [%5];" ::"r"(x_remote + sb * XBUF + e * ROWS * 16),
                                  "r"(s[4 * e]), "r"(s[4 * e + 1]), "r"(s[4 * e + 2]), "r"(s[4 * e + 3]),
-                                 "r"(bars_remote + 8 * (X_FULL + b))
+                                 "r"(bars_remote + 8 * (X_FULL + sb))
                                  : "memory");
             }
         }
@@ -543,8 +547,8 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
             const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
             x += seg.u1 - seg.u0;
             for (int32_t u = seg.u0; u < seg.u1; ++u, ++it) {
-                if (!(ok = wait(bar(X_READ + (it & 1)), (it >> 1) & 1))) break;
-                if (lane == 0) bar_arrive_remote(bars_remote + 8 * (X_EMPTY + (it & 1)));
+                if (!(ok = wait(bar(X_READ + it % SBUF), (it / SBUF) & 1))) break;
+                if (lane == 0) bar_arrive_remote(bars_remote + 8 * (X_EMPTY + it % SBUF));
                 __syncwarp();
             }
         }
@@ -652,7 +656,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
             for (uint32_t i = 0; i < STAGES; ++i) wait_for(bar(K_FULL + i), 0), wait_for(bar(K_FULL + i), 1);
         if (bad != 0) atomicOr(a.split.flags, bad);
     } else {
-        // ---- products, S by one warp and O by another, so that neither waits for what the other
+        // ---- products, S by two warps and O by another, so that none waits for what another
         // waits for. A warp runs as one, which keeps operand descriptors in uniform registers, and
         // one elected lane issues ----
         uint32_t leader;
@@ -666,18 +670,20 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
             const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
             const uint32_t n = (uint32_t)(seg.u1 - seg.u0);
             x += n;
-            if (warp == KEYS) {
+            if (warp < VALS) {
                 ok = wait(bar(Q_FULL), segments++ & 1);
-                for (uint32_t k = 0; ok && k < n; ++k) {
-                    const uint32_t i = it + k, b = i & 1, stage = i % STAGES;
+                for (uint32_t k = (it ^ warp) & 1; ok && k < n; k += 2) {
+                    const uint32_t i = it + k, sb = i % SBUF, stage = i % STAGES;
                     if (!(ok = wait(bar(K_FULL + stage), (i / STAGES) & 1))) break;
-                    // the S two tiles ago, which this one goes over, has been read
-                    if (i >= 2 && !(ok = wait(bar(S_FREE + b), ((i >> 1) & 1) ^ 1))) break;
+                    // the S that this one goes over has been read
+                    const uint32_t over = i - SBUF;
+                    if (i >= SBUF && !(ok = wait(bar(S_FREE + over % (2 * SBUF)), (over / (2 * SBUF)) & 1)))
+                        break;
                     fence_after();
-                    // copies that came through the generic proxy; the products read through the async one
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    // rows that came through the generic proxy; the products read through the async one
+                    if (a.piece == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     const uint32_t base = __shfl_sync(~0u, ring + stage * STAGE, 0);
-                    const uint32_t s_col = __shfl_sync(~0u, tm + COL_S + b * KT, 0);
+                    const uint32_t s_col = __shfl_sync(~0u, tm + COL_S + sb * KT, 0);
                     if (leader) {
 #pragma unroll
                         for (int e = 0; e < HALF / 16; ++e)
@@ -687,7 +693,12 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                         for (int e = 0; e < REST / 16; ++e)
                             product(s_col, tm + COL_Q + HALF / 2 + 8 * e,
                                     operand(base + 4 * CHUNK + e * 32, 16, 512, 4), ID_S, 1);
-                        commit(bar(S_FULL + b));
+                        commit(bar(S_FULL + sb));
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
+                                         bar(X_FULL + sb)),
+                                     "r"(XBUF)
+                                     : "memory");
+                        commit(bar(X_FULL + sb));
                     }
                     __syncwarp();
                 }
@@ -699,7 +710,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                     if (!(ok = wait(bar(P_FULL + b), (i >> 1) & 1))) break;
                     fence_after();
                     const uint32_t base = __shfl_sync(~0u, ring + stage * STAGE, 0);
-                    const uint32_t p_col = __shfl_sync(~0u, tm + COL_P + b * (KT / 2), 0);
+                    const uint32_t p_col = __shfl_sync(~0u, tm + COL_P, 0);
                     if (leader) {
 #pragma unroll
                         for (int e = 0; e < KT / 16; ++e)
