@@ -29,9 +29,10 @@
 // row by 16-byte cp.async, with zeros for the rows beyond the length. (By cp.async alone the load
 // and store units were what the kernel waited for.)
 //
-// Warps: twice 4 of softmax (one thread a row; even and odd tiles), 4 that send S to the other
-// SM, 4 of loads, 1 that issues the products. With one set of softmax warps that also sent, they
-// were busy for 2100 cycles a tile, of which HBM wants 780. A tile's softmax needs of the one
+// Warps: three times 4 of softmax (one thread a row; every third tile), 4 that send S to the other
+// SM, 4 of loads, 3 that issue the products, 1 that tells the other SM what it may send over.
+// With one set of softmax warps that also sent, they were busy for 2100 cycles a tile, of which
+// HBM wants 780. A tile's softmax needs of the one
 // before only what P is relative to, which goes through shared memory as soon as it is known.
 // O is rescaled only when a row's maximum outgrows by 2^40 (f16: 2^8) the one that its P is
 // relative to, which hardly happens after the first tiles of a job: powers of two cost no
@@ -63,11 +64,13 @@ constexpr int SBUF = 3;                   // halves of S at a time, own and rece
 constexpr int CHUNK = KT * 128;           // 64 elements of each key
 constexpr int STAGE = 4 * CHUNK + KT * 64;
 constexpr int XBUF = ROWS * KT * 4;
-// warps: softmax of even tiles, of odd tiles, sending, loading (4 each); products of S of even
+// warps: softmax of every third tile (3 x 4), sending, loading (4 each); products of S of even
 // tiles, of odd tiles, of O; telling
-constexpr int SEND = 8, LOAD = 12, KEYS = 16, VALS = 18, TELL = 19, WARPS = 20, THREADS = 32 * WARPS;
+constexpr int SOFT = 2, SEND = 4 * SOFT, LOAD = SEND + 4, KEYS = LOAD + 4, VALS = KEYS + 2,
+              TELL = VALS + 1, WARPS = TELL + 1, THREADS = 32 * WARPS;
 constexpr int OFF_XBUF = STAGES * STAGE, OFF_BARS = OFF_XBUF + SBUF * XBUF, OFF_TOPS = OFF_BARS + 768,
-              OFF_PREFIX = OFF_TOPS + 6 * ROWS * 4;
+              OFF_SUMS = OFF_TOPS + SOFT * ROWS * 8,
+              OFF_PREFIX = OFF_SUMS + 2 * SOFT * ROWS * 4;
 constexpr uint32_t COL_O = 0, COL_Q = 256, COL_S = 400, COL_P = COL_S + SBUF * KT;
 static_assert(COL_P + KT / 2 <= 512, "tensor memory");
 constexpr int VALUES = KVC_LATENT_VALUES;
@@ -79,7 +82,7 @@ constexpr size_t SLOT = (size_t)ROWS * VALUES + 2 * ROWS;
 // barriers: O_DONE has 4, and S_FREE twice as many as there are S)
 enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, S_FULL = K_EMPTY + STAGES, S_FREE = S_FULL + SBUF,
        X_FULL = S_FREE + 2 * SBUF, X_EMPTY = X_FULL + SBUF, X_READ = X_EMPTY + SBUF,
-       P_FULL = X_READ + SBUF, O_DONE = P_FULL + 2, TOP = O_DONE + 4, Q_FULL = TOP + 8, O_FREE, SUMS,
+       P_FULL = X_READ + SBUF, O_DONE = P_FULL + 2, Q_FULL = O_DONE + 4, O_FREE, SUMS,
        DRAIN, BARS = DRAIN + 3 };
 constexpr int OFF_TMEM = BARS * 8, OFF_SCRATCH = OFF_TMEM + 16;
 static_assert(OFF_SCRATCH + 4 * WARPS <= 768, "the words after the barriers");
@@ -94,7 +97,7 @@ struct LatentArgs {
     float *lse;
     int64_t q_request, q_token, q_head, out_request, out_token, out_head;
     float *partial;
-    int32_t m, Hq, chunks, parts, least;
+    int32_t m, Hq, chunks, parts;
     KvrDiv heads;             // by Hq
     float scale;
 };
@@ -135,6 +138,28 @@ __device__ __forceinline__ uint32_t wait_for(uint32_t bar, uint32_t parity) {
                  : "r"(bar), "r"(parity)
                  : "memory");
     return done;
+}
+// Each lane's row's maximum after a tile, and telling it. One 64-bit word holds both, so no barrier
+// has to order two stores; a wait by barrier costs both sides ten times as much.
+__device__ __forceinline__ void tell_top(uint32_t tops, uint32_t tile, float top) {
+    const uint64_t word = (uint64_t)(tile + 1) << 32 | __float_as_uint(top);
+    asm volatile("st.volatile.shared.b64 [%0], %1;" ::"r"(tops + tile % SOFT * (ROWS * 8)), "l"(word)
+                 : "memory");
+}
+__device__ __forceinline__ bool top_after(uint32_t tops, uint32_t tile, float *top, uint32_t *flags) {
+    uint64_t word = 0;
+    for (uint32_t n = 0; n < (1u << 24); ++n) {
+        asm volatile("ld.volatile.shared.b64 %0, [%1];"
+                     : "=l"(word)
+                     : "r"(tops + tile % SOFT * (ROWS * 8))
+                     : "memory");
+        if (__all_sync(~0u, (uint32_t)(word >> 32) == tile + 1)) {
+            *top = __uint_as_float((uint32_t)word);
+            return true;
+        }
+    }
+    atomicOr(flags, KVC_FLAG_TIMEOUT);
+    return false;
 }
 // For a warp, whose lanes go on together with the same answer: false, and a flag, if it gave up.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t *flags) {
@@ -240,6 +265,12 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return d;
 }
 
+// A part has LEAST tiles at least: each costs the others a share of the join.
+constexpr int LEAST = 4;
+__device__ __forceinline__ int64_t parts_of(const LatentArgs &a, int64_t total) {
+    return max((int64_t)1, min((int64_t)a.parts, total / LEAST));
+}
+
 // -- the kernel -------------------------------------------------------------------
 
 // how far (as a power of two) P may exceed 1 before O is rescaled: bf16 P and fp32 sums reach
@@ -280,15 +311,15 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
         }
         for (int i = 0; i < 2; ++i) bar_init(bar(P_FULL + i), 4);
         for (int i = 0; i < 4; ++i) bar_init(bar(O_DONE + i), 1);
-        for (int i = 0; i < 8; ++i) bar_init(bar(TOP + i), 1);
         bar_init(bar(Q_FULL), 4);
-        bar_init(bar(O_FREE), 8);
-        bar_init(bar(SUMS), 8);
+        bar_init(bar(O_FREE), SEND);
+        bar_init(bar(SUMS), SEND);
         bar_init(bar(DRAIN), 1);
         bar_init(bar(DRAIN + 1), 1);
         bar_init(bar(DRAIN + 2), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    for (int i = tid; i < SOFT * ROWS; i += THREADS) ((uint64_t *)(smem + OFF_TOPS))[i] = 0;
     wait_for_previous();
     let_next_start();
     unit_prefix<KT>(a.split, KT, prefix, (int32_t *)(smem + OFF_BARS + OFF_SCRATCH));
@@ -298,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
     const uint32_t tmem = *(volatile uint32_t *)(smem + OFF_BARS + OFF_TMEM);
 
     const int64_t total = (int64_t)prefix[a.split.requests] * a.chunks;
-    const int64_t parts = max((int64_t)1, min((int64_t)a.parts, total / a.least));
+    const int64_t parts = parts_of(a, total);
     const int64_t part = blockIdx.x / 2;
     int64_t x = part < parts ? part * total / parts : 0;
     const int64_t x_end = part < parts ? (part + 1) * total / parts : 0;
@@ -318,10 +349,13 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
     };
 
     if (warp < SEND) {
-        // ---- softmax of every other tile ----
-        const uint32_t b = warp / 4;              // of even or odd tiles, and their buffers
+        // ---- softmax of every third tile ----
+        const uint32_t group = warp / 4;
         const uint64_t sc2 = splat2(a.scale * 1.4426950408889634f);
-        float *tops = (float *)(smem + OFF_TOPS), *sums = tops + 2 * ROWS;   // [2][ROWS], [2][2][ROWS]
+        // what a row's P is relative to after a tile: (maximum, tile + 1) by tile % 3 and row. One
+        // 64-bit word, so that whoever sees the number sees its maximum too
+        const uint32_t tops = smem0 + OFF_TOPS + row * 8;
+        float *sums = (float *)(smem + OFF_SUMS);     // [2][SOFT][ROWS]
         uint32_t it = 0, segments = 0;            // tiles and segments so far
         bool ok = true;
         while (ok && x < x_end) {
@@ -337,7 +371,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
             // the row's sum of P over these warps' tiles, relative to 2^ref
             float ref = -INFINITY, sum = 0.0f;
 
-            for (uint32_t k = (it & 1) == b ? 0 : 1; k < n; k += 2) {
+            for (uint32_t k = (group + SOFT - it % SOFT) % SOFT; k < n; k += SOFT) {
                 const uint32_t i = it + k, sb = i % SBUF;
                 const float4 *from = (const float4 *)(smem + OFF_XBUF + sb * XBUF) + row;
                 uint32_t s[KT];
@@ -350,13 +384,15 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                 for (int e = 0; e < KT / 4; ++e) other[e] = from[e * ROWS];
                 wait_ld();
                 fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(S_FREE + i % (2 * SBUF)));
 #pragma unroll
                 for (int e = 0; e < KT / 4; ++e) {
                     scaled_sum(s + 4 * e, other[e].x, other[e].y, sc2);
                     scaled_sum(s + 4 * e + 2, other[e].z, other[e].w, sc2);
                 }
                 __syncwarp();
-                if (lane < 2) bar_arrive(bar(lane == 0 ? S_FREE + i % (2 * SBUF) : X_READ + sb));
+                if (lane == 0) bar_arrive(bar(X_READ + sb));
                 const int32_t j0 = sp.lo + (seg.u0 + (int32_t)k) * KT;
                 if (j0 + KT > seen_all || j0 < seen_from) {
 #pragma unroll
@@ -374,8 +410,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                 // what P and O are relative to: as the tile before left it, or more
                 float top = best;                 // O starts from a segment's first tile
                 if (k > 0) {
-                    if (!(ok = wait(bar(TOP + (b ^ 1) * 4 + warp % 4), ((i - 1) >> 1) & 1))) break;
-                    top = tops[(b ^ 1) * ROWS + row];
+                    if (!(ok = top_after(tops, i - 1, &top, a.split.flags))) break;
                     if (__any_sync(~0u, best > top + GROWTH)) {
                         const float next = fmaxf(top, best);
                         const float shrink = next == top ? 1.0f : ex2(top - next);
@@ -395,9 +430,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                         wait_st();
                     }
                 }
-                tops[b * ROWS + row] = top;
-                __syncwarp();
-                if (lane == 0) bar_arrive(bar(TOP + b * 4 + warp % 4));
+                tell_top(tops, i, top);
                 if (top != ref) sum *= ref == -INFINITY ? 0.0f : ex2(ref - top);
                 ref = top;
                 const uint64_t minus = splat2(top == -INFINITY ? 0.0f : -top);
@@ -418,23 +451,25 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                 wait_st();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(bar(P_FULL + b));
+                if (lane == 0) bar_arrive(bar(P_FULL + (i & 1)));
             }
             if (!ok) break;
             it += n;
 
-            // the segment's maximum and sum, then its O: each of the two halves of the warps has
-            // half of the columns
-            const uint32_t last = it - 1, lb = last & 1;
-            if (lb != b && !(ok = wait(bar(TOP + lb * 4 + warp % 4), (last >> 1) & 1))) break;
-            const float top = tops[lb * ROWS + row];
+            // the segment's maximum and sum, then its O: each third of the warps has a third of the
+            // columns
+            const uint32_t last = it - 1;
+            float top;
+            if (!(ok = top_after(tops, last, &top, a.split.flags))) break;
             if (top != ref) sum *= ref == -INFINITY ? 0.0f : ex2(ref - top);
-            float *mine_sum = sums + (segments & 1) * 2 * ROWS;
-            mine_sum[b * ROWS + row] = sum;
+            float *all_sums = sums + (segments & 1) * SOFT * ROWS;
+            all_sums[group * ROWS + row] = sum;
             __syncwarp();
             if (lane == 0) bar_arrive(bar(SUMS));
             if (!(ok = wait(bar(SUMS), segments & 1))) break;
-            sum = mine_sum[row] + mine_sum[ROWS + row];
+            sum = 0.0f;
+#pragma unroll
+            for (int g = 0; g < SOFT; ++g) sum += all_sums[g * ROWS + row];
             ++segments;
             if (!(ok = wait(bar(O_DONE + (last & 3)), (last >> 2) & 1))) break;
             fence_after();
@@ -446,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
             unsigned char *out = a.out + seg.r * a.out_request + query.token * a.out_token +
                                  query.hq * a.out_head + rank * (HALF * 2);
 #pragma unroll 1
-            for (int c = b * (HALF / 2); c < (int)(b + 1) * (HALF / 2); c += 16) {
+            for (int c = group * 16; c < HALF; c += SOFT * 16) {
                 uint32_t w[16];
                 tm_load16(w, lanes + COL_O + c);
                 wait_ld();
@@ -475,7 +510,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(bar(O_FREE));
-            if (mine && rank == 0 && b == 0) {
+            if (mine && rank == 0 && group == 0) {
                 if (whole) {
                     if (a.lse != nullptr)
                         a.lse[((int64_t)seg.r * a.m + query.token) * a.Hq + query.hq] =
@@ -741,53 +776,51 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
 
 // -- joining the parts ------------------------------------------------------------
 
-constexpr int JOIN_ROWS = 8, JOIN_THREADS = JOIN_ROWS * (VALUES / 8);
+constexpr int JOIN_ROWS = 4, JOIN_COLS = 32, JOIN_THREADS = JOIN_ROWS * JOIN_COLS;
 
-// One block a job and 8 of its rows: the parts' accumulators weighted by their maxima, in the
-// order of the keys. Jobs that one part did whole are not touched.
+// One block a job, 4 of its rows and 128 of their elements: the parts' accumulators weighted by
+// their maxima, in the order of the keys. Jobs that one part did whole are not touched. (Four rows'
+// pieces of 16 bytes are two whole sectors; small blocks, so that 16 rows are still 16 blocks.)
 template <bool F16>
 __global__ void __launch_bounds__(JOIN_THREADS) latent_join(const __grid_constant__ LatentArgs a) {
     extern __shared__ int32_t join_smem[];
-    int32_t *scratch = join_smem, *prefix = join_smem + 32;
+    int32_t *scratch = join_smem, *prefix = join_smem + 4;
     wait_for_previous();
     let_next_start();
     unit_prefix<KT>(a.split, KT, prefix, scratch);
     const int64_t total = (int64_t)prefix[a.split.requests] * a.chunks;
-    const int64_t parts = max((int64_t)1, min((int64_t)a.parts, total / a.least));
-    const int32_t groups = ROWS / JOIN_ROWS;
+    const int64_t parts = parts_of(a, total);
+    const int32_t M = a.m * a.Hq, groups = (min(M, ROWS) + JOIN_ROWS - 1) / JOIN_ROWS;
     const int32_t jg = blockIdx.x / groups, r = jg / a.chunks, job = jg - r * a.chunks;
-    const int32_t M = a.m * a.Hq, row0 = job * ROWS;
     const int32_t row = (blockIdx.x % groups) * JOIN_ROWS + threadIdx.x % JOIN_ROWS;
-    const int32_t rho = row0 + row, e8 = threadIdx.x / JOIN_ROWS;    // 8 elements
-    if (rho >= M || row >= ROWS) return;
+    const int32_t rho = job * ROWS + row;
+    const int32_t e4 = blockIdx.y * JOIN_COLS + threadIdx.x / JOIN_ROWS;     // 4 elements
     const int32_t units = prefix[r + 1] - prefix[r];
     const int64_t first = (int64_t)prefix[r] * a.chunks + (int64_t)job * units;
-    const int64_t c0 = part_of(first, parts, total), c1 = part_of(first + units - 1, parts, total);
-    if (c0 == c1) return;
-    auto slot = [&](int64_t c) { return a.partial + (size_t)(2 * c + (c == c0 ? 1 : 0)) * SLOT; };
-    float m = -INFINITY, l = 0.0f, v[8] = {};
-    for (int64_t c = c0; c <= c1; ++c)
-        m = fmaxf(m, __ldcg((const float2 *)(slot(c) + (size_t)ROWS * VALUES) + row).x);
-#pragma unroll 4
-    for (int64_t c = c0; c <= c1; ++c) {
-        const float *s = slot(c);
-        const float2 ml = __ldcg((const float2 *)(s + (size_t)ROWS * VALUES) + row);
-        const float4 p0 = __ldcg((const float4 *)s + (size_t)(2 * e8) * ROWS + row);
-        const float4 p1 = __ldcg((const float4 *)s + (size_t)(2 * e8 + 1) * ROWS + row);
+    const int64_t c0 = part_of(first, parts, total);
+    const int32_t n = (int32_t)(part_of(first + units - 1, parts, total) - c0) + 1;
+    if (n == 1 || rho >= M) return;
+    auto slot = [&](int32_t c) { return a.partial + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * SLOT; };
+    auto stat = [&](int32_t c) { return __ldcg((const float2 *)(slot(c) + (size_t)ROWS * VALUES) + row); };
+    float m = -INFINITY, l = 0.0f;
+    float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+    for (int32_t c = 0; c < n; ++c) m = fmaxf(m, stat(c).x);
+#pragma unroll 8
+    for (int32_t c = 0; c < n; ++c) {
+        const float2 ml = stat(c);
+        const float4 p = __ldcg((const float4 *)slot(c) + (size_t)e4 * ROWS + row);
         if (ml.x == -INFINITY && ml.y == 0.0f) continue;
         const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
         l += f * ml.y;
-        v[0] += f * p0.x, v[1] += f * p0.y, v[2] += f * p0.z, v[3] += f * p0.w;
-        v[4] += f * p1.x, v[5] += f * p1.y, v[6] += f * p1.z, v[7] += f * p1.w;
+        v.x += f * p.x, v.y += f * p.y, v.z += f * p.z, v.w += f * p.w;
     }
     const bool some = l > 0.0f || l != l;
     const float inv = some ? 1.0f / l : 0.0f;
     const int32_t token = (int32_t)a.heads.div((uint32_t)rho), hq = rho - token * a.Hq;
-    uint4 w;
-    w.x = narrow2<F16>(v[0] * inv, v[1] * inv), w.y = narrow2<F16>(v[2] * inv, v[3] * inv);
-    w.z = narrow2<F16>(v[4] * inv, v[5] * inv), w.w = narrow2<F16>(v[6] * inv, v[7] * inv);
-    *(uint4 *)(a.out + r * a.out_request + token * a.out_token + hq * a.out_head + e8 * 16) = w;
-    if (e8 == 0 && a.lse != nullptr)
+    *(uint2 *)(a.out + r * a.out_request + token * a.out_token + hq * a.out_head + e4 * 8) =
+        make_uint2(narrow2<F16>(v.x * inv, v.y * inv), narrow2<F16>(v.z * inv, v.w * inv));
+    if (e4 == 0 && a.lse != nullptr)
         a.lse[((int64_t)r * a.m + token) * a.Hq + hq] =
             some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
@@ -878,7 +911,6 @@ kvr_status kvc_latent_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     a.chunks = (int32_t)((M + ROWS - 1) / ROWS);
     const int64_t most = ((int64_t)p->table.width * c->d.block_size + KT - 1) / KT + 1;
     if (most * p->num_requests > INT32_MAX) return KVR_ERR_UNSUPPORTED;
-    a.least = 2;
     a.parts = (int32_t)std::min<int64_t>(std::max(kvc_stream_sms(c, stream) / 2, 1),
                                          most * p->num_requests * a.chunks);
     const bool f16 = c->d.dtype == KVC_DTYPE_F16;
@@ -886,7 +918,8 @@ kvr_status kvc_latent_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     const kvr_status st = kvc_launch(f16 ? latent_kernel<true> : latent_kernel<false>, a,
                                      dim3((unsigned)(2 * a.parts)), THREADS, smem, stream, 2);
     if (st != KVR_OK) return st;
-    const int64_t blocks = (int64_t)p->num_requests * a.chunks * (ROWS / JOIN_ROWS);
-    return kvc_launch(f16 ? latent_join<true> : latent_join<false>, a, dim3((unsigned)blocks),
-                      JOIN_THREADS, 4 * (32 + (size_t)p->num_requests + 1), stream);
+    const int64_t groups = (std::min<int64_t>(M, ROWS) + JOIN_ROWS - 1) / JOIN_ROWS;
+    return kvc_launch(f16 ? latent_join<true> : latent_join<false>, a,
+                      dim3((unsigned)(p->num_requests * a.chunks * groups), VALUES / 4 / JOIN_COLS),
+                      JOIN_THREADS, 4 * (4 + (size_t)p->num_requests + 1), stream);
 }
