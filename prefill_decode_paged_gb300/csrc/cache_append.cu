@@ -1,12 +1,16 @@
 // cache_append.cu -- new tokens' keys and values into a paged pool, positions rotated on the way.
 //
 // Pure data movement with three fp32 operations a rotated element: each input row is read once,
-// each pool row and rotated query written once. One block does one token. A thread owns one
-// UNIT of a head row, 16 elements as two 16-byte pieces, and the same unit of every head that
-// it comes to, so the cosines and sines of its eight pairs are loaded once a token:
+// each pool row and rotated query written once. One block does one token, whose head rows (those
+// of the queries, keys and values) are cut into UNITS of 16 elements, two 16-byte pieces each:
 //   rotated, halves:      pieces at 8 i and 8 i + R / 2 hold pairs 8 i .. 8 i + 7 as (a | b);
 //   rotated, interleaved: pieces at 16 i and 16 i + 8 hold the same pairs side by side;
 //   not rotated:          pieces at 16 i and 16 i + 8, passed through (or quantized).
+// A thread asks for up to BATCH units at once, before it looks at the token's position: the slot
+// (position, then block id) and the angles are on their way meanwhile. Where the row's units divide
+// the block's threads, a thread has the same unit of every row, and loads its angles once.
+#include <algorithm>
+
 #include "cache.h"
 
 namespace {
@@ -14,7 +18,7 @@ namespace {
 using namespace kvc;
 
 constexpr int THREADS = 128;
-constexpr int BATCH = 4;      // rows a thread has in flight
+constexpr int BATCH = 4;      // units a thread has in flight
 
 struct Rows {                 // head rows of one input and where they go
     const unsigned char *src;
@@ -35,38 +39,34 @@ struct AppendArgs {
     const float *k_scale, *v_scale;
     uint32_t *flags;
     int32_t last;             // the rotated elements are the row's last
+    KvrDiv units, q_units;    // of a key's and of a query's row
 };
 
-struct Unit {                 // byte offsets of its two pieces in a row of 16-bit elements
-    int32_t e0, e1;           // elements
+struct Unit {
+    int32_t e0, e1;           // its two pieces' first elements in the row
+    int32_t pair;             // its first pair, -1 if it is not rotated
     bool rotated;
     float cs[8], sn[8];
 };
 
 template <bool INTERLEAVED>
-__device__ __forceinline__ Unit make_unit(const AppendArgs &a, int32_t dim, int32_t j,
-                                          const float *row) {
-    Unit u;
+__device__ __forceinline__ void place(Unit &u, const AppendArgs &a, int32_t dim, int32_t j) {
     const int32_t R = a.R;
     const int32_t first = a.last ? dim - R : 0;
     const int32_t i = a.last ? j - (dim - R) / 16 : j;      // which rotated unit, if it is one
     u.rotated = R > 0 && i >= 0 && i < R / 16;
-    if (u.rotated) {
-        u.e0 = first + (INTERLEAVED ? 16 * i : 8 * i);
-        u.e1 = u.e0 + (INTERLEAVED ? 8 : R / 2);
-        if (row != nullptr) {
-            const float4 *c = (const float4 *)(row + 8 * i), *s = (const float4 *)(row + R / 2 + 8 * i);
-            const float4 c0 = __ldg(c), c1 = __ldg(c + 1), s0 = __ldg(s), s1 = __ldg(s + 1);
-            u.cs[0] = c0.x, u.cs[1] = c0.y, u.cs[2] = c0.z, u.cs[3] = c0.w;
-            u.cs[4] = c1.x, u.cs[5] = c1.y, u.cs[6] = c1.z, u.cs[7] = c1.w;
-            u.sn[0] = s0.x, u.sn[1] = s0.y, u.sn[2] = s0.z, u.sn[3] = s0.w;
-            u.sn[4] = s1.x, u.sn[5] = s1.y, u.sn[6] = s1.z, u.sn[7] = s1.w;
-        }
-    } else {
-        u.e0 = 16 * j;
-        u.e1 = u.e0 + 8;
-    }
-    return u;
+    u.e0 = u.rotated ? first + (INTERLEAVED ? 16 * i : 8 * i) : 16 * j;
+    u.e1 = u.e0 + (u.rotated && !INTERLEAVED ? R / 2 : 8);
+    u.pair = u.rotated ? 8 * i : -1;
+}
+
+__device__ __forceinline__ void load_angles(Unit &u, const float *row, int32_t R) {
+    const float4 *c = (const float4 *)(row + u.pair), *s = (const float4 *)(row + R / 2 + u.pair);
+    const float4 c0 = __ldg(c), c1 = __ldg(c + 1), s0 = __ldg(s), s1 = __ldg(s + 1);
+    u.cs[0] = c0.x, u.cs[1] = c0.y, u.cs[2] = c0.z, u.cs[3] = c0.w;
+    u.cs[4] = c1.x, u.cs[5] = c1.y, u.cs[6] = c1.z, u.cs[7] = c1.w;
+    u.sn[0] = s0.x, u.sn[1] = s0.y, u.sn[2] = s0.z, u.sn[3] = s0.w;
+    u.sn[4] = s1.x, u.sn[5] = s1.y, u.sn[6] = s1.z, u.sn[7] = s1.w;
 }
 
 __device__ __forceinline__ uint4 load16(const unsigned char *p) {
@@ -125,110 +125,99 @@ __device__ __forceinline__ void store_8bit(unsigned char *row, const Unit &u, co
     *(uint2 *)(row + u.e1) = make_uint2(quant4f(x + 8, inv), quant4f(x + 12, inv));
 }
 
-// Rows [0, count) of this token: the queries (count = q.heads), or keys then values.
+// Where unit `t` of the token's units is: queries first, then keys, then values.
+struct Place {
+    int32_t row, j;           // head row of its input, unit of the row
+    int32_t kind;             // 0 query, 1 key, 2 value, 3 none
+};
+__device__ __forceinline__ Place place_of(const AppendArgs &a, int32_t t, int32_t n) {
+    Place p;
+    const int32_t nq = a.q.heads * (int32_t)a.q_units.d;
+    if (t < nq) {
+        p.kind = 0;
+        p.row = (int32_t)a.q_units.div((uint32_t)t);
+        p.j = t - p.row * (int32_t)a.q_units.d;
+    } else {
+        t -= nq;
+        p.row = (int32_t)a.units.div((uint32_t)t);
+        p.j = t - p.row * (int32_t)a.units.d;
+        p.kind = p.row < a.k.heads ? 1 : 2;
+        if (p.kind == 2) p.row -= a.k.heads;
+        if (t + nq >= n) p.kind = 3;
+    }
+    return p;
+}
+
 template <bool F16, bool INTERLEAVED, bool E4M3>
 __global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a) {
     wait_for_previous();
     let_next_start();
-    const int64_t t = blockIdx.x;
-    const int32_t pos = __ldg(a.positions + t), req = __ldg(a.requests + t);
-    if (pos < 0) return;
-    if (a.rotary != nullptr && pos >= a.rotary_rows) {
-        if (threadIdx.x == 0) atomicOr(a.flags, KVC_FLAG_POSITION);
-        return;
-    }
-    const float *angles = a.rotary == nullptr ? nullptr : a.rotary + (int64_t)pos * a.R;
+    const int64_t token = blockIdx.x;
+    const int32_t pos = __ldg(a.positions + token), req = __ldg(a.requests + token);
+    const int32_t n = a.q.heads * (int32_t)a.q_units.d + (a.k.heads + a.v.heads) * (int32_t)a.units.d;
+    int64_t slot = -1;                       // the token's slot in a plane, in bytes
+    const float *angles = nullptr;
+    int32_t have = -1;                       // the pair whose angles `u` holds
+    Unit u;
 
-    int64_t slot_k = -1, slot_v = -1;        // this token's slot in either plane, in bytes
-    const uint32_t entry = a.slots.block.div((uint32_t)pos);
-    uint32_t bad = 0;
-    if (req < 0 || req >= a.slots.rows) {
-        bad = KVC_FLAG_REQUEST;
-    } else if (entry >= (uint32_t)a.slots.width) {
-        bad = KVC_FLAG_POSITION;
-    } else {
-        const int32_t id = __ldg(a.slots.ids + (int64_t)req * a.slots.stride + entry);
-        const int32_t off = pos - (int32_t)(entry * a.slots.block.d);
-        if (id < 0 || id >= a.slots.num_blocks) {
-            bad = KVC_FLAG_BLOCK;
-        } else {
-            slot_k = id * a.k_plane.block_stride + off * a.k_plane.token_stride;
-            slot_v = id * a.v_plane.block_stride + off * a.v_plane.token_stride;
-        }
-    }
-    if (bad != 0) {
-        if (threadIdx.x == 0) atomicOr(a.flags, bad);
-        return;
-    }
-
-    // keys and values
-    {
-        const int32_t units = a.dim / 16, groups = THREADS / units;
-        const int32_t j = threadIdx.x % units, g = threadIdx.x / units;
-        if (g < groups) {
-            const Unit u = make_unit<INTERLEAVED>(a, a.dim, j, angles);
-            Unit plain = u;
-            plain.rotated = false;
-            const int32_t rows = a.k.heads + a.v.heads;
-            for (int32_t r0 = g; r0 < rows; r0 += groups * BATCH) {
-                uint4 p0[BATCH], p1[BATCH];
+    for (int32_t t0 = threadIdx.x; t0 < n; t0 += THREADS * BATCH) {
+        uint4 p0[BATCH], p1[BATCH];
 #pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                    const int32_t r = r0 + b * groups;
-                    if (r < rows) {
-                        const bool key = r < a.k.heads;
-                        const unsigned char *src =
-                            key ? a.k.src + t * a.k.src_token + r * a.k.src_head
-                                : a.v.src + t * a.v.src_token + (r - a.k.heads) * a.v.src_head;
-                        p0[b] = load16(src + 2 * u.e0);
-                        p1[b] = load16(src + 2 * u.e1);
-                    }
-                }
-#pragma unroll
-                for (int b = 0; b < BATCH; ++b) {
-                    const int32_t r = r0 + b * groups;
-                    if (r < rows) {
-                        const bool key = r < a.k.heads;
-                        const int32_t h = key ? r : r - a.k.heads;
-                        float x[16];
-                        turn<F16, INTERLEAVED>(p0[b], p1[b], key ? u : plain, x);
-                        unsigned char *dst =
-                            key ? a.k_plane.base + slot_k + h * a.k_plane.head_stride
-                                : a.v_plane.base + slot_v + h * a.v_plane.head_stride;
-                        if (E4M3)
-                            store_8bit(dst, u, x, 1.0f / __ldg((key ? a.k_scale : a.v_scale) + h));
-                        else
-                            store_16bit<F16>(dst, u, x);
-                    }
-                }
+        for (int b = 0; b < BATCH; ++b) {
+            const Place p = place_of(a, t0 + b * THREADS, n);
+            if (p.kind < 3) {
+                const Rows &in = p.kind == 0 ? a.q : p.kind == 1 ? a.k : a.v;
+                Unit w;
+                place<INTERLEAVED>(w, a, p.kind == 0 ? a.q_dim : a.dim, p.j);
+                const unsigned char *src = in.src + token * in.src_token + p.row * in.src_head;
+                p0[b] = load16(src + 2 * w.e0);
+                p1[b] = load16(src + 2 * w.e1);
             }
         }
-    }
-    // queries
-    if (a.q.heads > 0) {
-        const int32_t units = a.q_dim / 16, groups = THREADS / units;
-        const int32_t j = threadIdx.x % units, g = threadIdx.x / units;
-        if (g >= groups) return;
-        const Unit u = make_unit<INTERLEAVED>(a, a.q_dim, j, angles);
-        for (int32_t r0 = g; r0 < a.q.heads; r0 += groups * BATCH) {
-            uint4 p0[BATCH], p1[BATCH];
-#pragma unroll
-            for (int b = 0; b < BATCH; ++b) {
-                const int32_t r = r0 + b * groups;
-                if (r < a.q.heads) {
-                    const unsigned char *src = a.q.src + t * a.q.src_token + r * a.q.src_head;
-                    p0[b] = load16(src + 2 * u.e0);
-                    p1[b] = load16(src + 2 * u.e1);
-                }
+        if (slot < 0) {
+            if (pos < 0) return;
+            const uint32_t entry = a.slots.block.div((uint32_t)pos);
+            uint32_t bad = 0;
+            if (req < 0 || req >= a.slots.rows) {
+                bad = KVC_FLAG_REQUEST;
+            } else if (entry >= (uint32_t)a.slots.width ||
+                       (a.rotary != nullptr && pos >= a.rotary_rows)) {
+                bad = KVC_FLAG_POSITION;
+            } else {
+                const int32_t id = __ldg(a.slots.ids + (int64_t)req * a.slots.stride + entry);
+                const int32_t off = pos - (int32_t)(entry * a.slots.block.d);
+                angles = a.rotary + (int64_t)pos * a.R;
+                if (id < 0 || id >= a.slots.num_blocks)
+                    bad = KVC_FLAG_BLOCK;
+                else
+                    slot = id * a.k_plane.block_stride + off * a.k_plane.token_stride;
             }
+            if (bad != 0) {
+                if (threadIdx.x == 0) atomicOr(a.flags, bad);
+                return;
+            }
+        }
 #pragma unroll
-            for (int b = 0; b < BATCH; ++b) {
-                const int32_t r = r0 + b * groups;
-                if (r < a.q.heads) {
-                    float x[16];
-                    turn<F16, INTERLEAVED>(p0[b], p1[b], u, x);
-                    store_16bit<F16>(a.q_out + t * a.q_out_token + r * a.q_out_head, u, x);
-                }
+        for (int b = 0; b < BATCH; ++b) {
+            const Place p = place_of(a, t0 + b * THREADS, n);
+            if (p.kind == 3) continue;
+            place<INTERLEAVED>(u, a, p.kind == 0 ? a.q_dim : a.dim, p.j);
+            if (p.kind == 2) u.rotated = false;
+            if (u.rotated && u.pair != have) {
+                load_angles(u, angles, a.R);
+                have = u.pair;
+            }
+            float x[16];
+            turn<F16, INTERLEAVED>(p0[b], p1[b], u, x);
+            if (p.kind == 0) {
+                store_16bit<F16>(a.q_out + token * a.q_out_token + p.row * a.q_out_head, u, x);
+            } else {
+                const KvcPlane &plane = p.kind == 1 ? a.k_plane : a.v_plane;
+                unsigned char *dst = plane.base + slot + p.row * plane.head_stride;
+                if (E4M3)
+                    store_8bit(dst, u, x, 1.0f / __ldg((p.kind == 1 ? a.k_scale : a.v_scale) + p.row));
+                else
+                    store_16bit<F16>(dst, u, x);
             }
         }
     }
@@ -265,6 +254,8 @@ kvr_status kvc_append_launch(const kvc_cache *c, int32_t layer, const kvc_append
     a.R = p->rotary == nullptr ? 0 : p->rotary_dim;
     a.dim = c->d.head_dim;
     a.q_dim = p->q_dim;
+    a.units = kvr_make_div((uint32_t)a.dim / 16);
+    a.q_units = kvr_make_div(std::max(1u, (uint32_t)a.q_dim / 16));
     a.flags = c->ws.flags;
     a.last = (p->flags & KVC_ROTATE_LAST) != 0;
     const bool il = (p->flags & KVC_INTERLEAVED) != 0, f16 = p->dtype == KVC_DTYPE_F16;

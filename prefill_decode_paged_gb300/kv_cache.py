@@ -12,7 +12,7 @@ import struct
 import numpy as np
 
 from .kv_relayout import (KVRelayoutError, KvrLayout, _contiguous, _Layout, _nbytes, _ptr,
-                          library)
+                          _stream_handle, library)
 
 DTYPE_F16 = 3
 INTERLEAVED = 1
@@ -117,12 +117,6 @@ def _defaults(g):
     return dict(dict(query_heads=0, max_requests=1, max_new=1, value_dim=0), **g)
 
 
-def _strides(t, n):
-    """Byte strides of the first ``n`` dimensions (0 where the extent is 1)."""
-    es = t.element_size()
-    return [s * es if e > 1 else 0 for s, e in zip(t.stride()[:n], t.shape[:n])]
-
-
 class KVCache:
     """One shard pool of a decode side: append tokens to it, attend to it.
 
@@ -175,49 +169,63 @@ class KVCache:
         if st != 0:
             raise KVRelayoutError(st, "kv_cache_create")
         import torch
+        lib = _library()
         self._h, self._pool, self._torch = h.value, (pool, layout), torch
-        self._device = torch.device("cuda", torch.cuda.current_device())
+        self._append, self._attend = lib.kv_cache_append, lib.kv_cache_attend
+        self._index = torch.cuda.current_device()
+        self._device = torch.device("cuda", self._index)
         self._i32, self._f32 = torch.int32, torch.float32
         self._types = {torch.bfloat16: 1, torch.float16: DTYPE_F16}
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
         self.kv_heads, self.head_dim, self.query_heads = kv_heads, head_dim, query_heads
         self.value_dim = value_dim or (512 if num_components == 1 else head_dim)
         self.latent = num_components == 1
+        self._default_scale = head_dim ** -0.5
 
     # -- arguments ---------------------------------------------------------------
+    #
+    # A decode step calls these for every layer, and they cost about as much as the small kernels
+    # behind them: the common case (contiguous tensors) takes as few Python operations as it can.
 
     def _handle(self):
         if self._h is None:
             raise RuntimeError("cache already closed")
         return self._h
 
-    def _stream(self, stream):
-        if stream is None:
-            return self._torch.cuda.current_stream(self._device).cuda_stream
-        return stream if isinstance(stream, int) else stream.cuda_stream
-
     def _rows(self, t, name, shape, dtype=None):
-        """Check a tensor of head rows; its byte strides but the last."""
-        if t.device != self._device or tuple(t.shape) != shape or t.stride(-1) != 1 or \
-                (t.dtype is not dtype if dtype is not None else t.dtype not in self._types):
-            raise ValueError(f"{name} is {t.dtype} {list(t.shape)} on {t.device} with strides "
-                             f"{list(t.stride())}; expected {dtype or 'bfloat16 or float16'} "
-                             f"{list(shape)} on {self._device}, rows contiguous")
-        return _strides(t, t.dim() - 1)
+        """Byte strides of a tensor of head rows but the last dimension's, once it is checked."""
+        if t.shape == shape and t.get_device() == self._index and \
+                (t.dtype is dtype if dtype is not None else t.dtype in self._types):
+            if t.is_contiguous():
+                row = 2 * shape[-1]
+                if len(shape) == 3:
+                    return shape[1] * row, row
+                return shape[1] * shape[2] * row, shape[2] * row, row
+            st = t.stride()
+            if st[-1] == 1:
+                return tuple(2 * x if e > 1 else 0 for x, e in zip(st[:-1], shape[:-1]))
+        raise ValueError(f"{name} is {t.dtype} {list(t.shape)} on {t.device} with strides "
+                         f"{list(t.stride())}; expected {dtype or 'bfloat16 or float16'} "
+                         f"{list(shape)} on {self._device}, rows contiguous")
 
     def _list(self, t, name, n):
-        if t.dtype is not self._i32 or t.dim() != 1 or t.shape[0] != n or \
-                t.device != self._device or (n > 1 and t.stride(0) != 1):
-            raise ValueError(f"{name} is {t.dtype} {list(t.shape)} on {t.device}; expected "
-                             f"contiguous int32 [{n}] on {self._device}")
-        return t.data_ptr()
+        if t.dtype is self._i32 and t.shape == (n,) and t.is_contiguous() and \
+                t.get_device() == self._index:
+            return t.data_ptr()
+        raise ValueError(f"{name} is {t.dtype} {list(t.shape)} on {t.device}; expected "
+                         f"contiguous int32 [{n}] on {self._device}")
 
     def _table(self, t):
-        if t.dtype is not self._i32 or t.dim() != 2 or t.device != self._device or \
-                (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"block table is {t.dtype} {list(t.shape)} on {t.device}; expected "
-                             f"int32 [rows][width] on {self._device}, rows contiguous")
-        rows, width = t.shape
-        return t.data_ptr(), max(t.stride(0), width) if rows > 1 else width, rows, width
+        if t.dtype is self._i32 and t.dim() == 2 and t.get_device() == self._index:
+            rows, width = t.shape
+            if t.is_contiguous():
+                return t.data_ptr(), width, rows, width
+            stride, one = t.stride()
+            if one == 1 or width <= 1:
+                return t.data_ptr(), max(stride, width) if rows > 1 else width, rows, width
+        raise ValueError(f"block table is {t.dtype} {list(t.shape)} on {t.device}; expected "
+                         f"int32 [rows][width] on {self._device}, rows contiguous")
 
     # -- calls -------------------------------------------------------------------
 
@@ -228,18 +236,18 @@ class KVCache:
         padding. ``rotary``: the table of :func:`rotary_table` on the device, by which the first
         (``rotate_last``: the last) of each row's elements are rotated; ``q`` [T][heads][dim], where
         given, is rotated into ``q_out`` (a new tensor by default). Returns ``q_out``."""
-        if not self.latent and v is None:
-            raise ValueError("values are missing")
-        T = k.shape[0]
-        shape = (T, self.kv_heads, self.head_dim)
+        if (v is None) != self.latent:
+            raise ValueError("a latent cache has no values, others need them")
+        shape = (k.shape[0], self.kv_heads, self.head_dim)
+        T, dtype = shape[0], k.dtype
         ks = self._rows(k, "k", shape)
-        vs = [0, 0] if v is None else self._rows(v, "v", shape, k.dtype)
+        vp, vs = (0, (0, 0)) if v is None else (v.data_ptr(), self._rows(v, "v", shape, dtype))
         ids, stride, rows, width = self._table(block_table)
         rot = rot_rows = rot_dim = q_heads = q_dim = qp = qo = 0
         qs = os = (0, 0)
         if rotary is not None:
             if rotary.dtype is not self._f32 or rotary.dim() != 2 or \
-                    not rotary.is_contiguous() or rotary.device != self._device:
+                    not rotary.is_contiguous() or rotary.get_device() != self._index:
                 raise ValueError("the rotation table is contiguous float32 [positions][rotated] "
                                  f"on {self._device}")
             rot, (rot_rows, rot_dim) = rotary.data_ptr(), rotary.shape
@@ -247,20 +255,20 @@ class KVCache:
             if q.dim() != 3:
                 raise ValueError(f"q is {list(q.shape)}; expected [T][heads][dim]")
             _, q_heads, q_dim = q.shape
-            qs = self._rows(q, "q", (T, q_heads, q_dim), k.dtype)
+            shape = (T, q_heads, q_dim)
+            qs = self._rows(q, "q", shape, dtype)
             if q_out is None:
-                q_out = self._torch.empty((T, q_heads, q_dim), dtype=q.dtype, device=q.device)
-            os = self._rows(q_out, "q_out", (T, q_heads, q_dim), k.dtype)
+                q_out = self._torch.empty(shape, dtype=dtype, device=q.device)
+            os = self._rows(q_out, "q_out", shape, dtype)
             qp, qo = q.data_ptr(), q_out.data_ptr()
-        st = _library().kv_cache_append(
+        st = self._append(
             self._handle(), layer,
-            _APPEND.pack(T, self._types[k.dtype], self._list(requests, "requests", T),
+            _APPEND.pack(T, self._types[dtype], self._list(requests, "requests", T),
                          self._list(positions, "positions", T), ids, stride, rows, width,
-                         k.data_ptr(), 0 if v is None else v.data_ptr(), ks[0], ks[1], vs[0],
-                         vs[1], rot, rot_rows, rot_dim,
+                         k.data_ptr(), vp, *ks, *vs, rot, rot_rows, rot_dim,
                          (INTERLEAVED if interleaved else 0) | (ROTATE_LAST if rotate_last else 0),
-                         q_heads, q_dim, 0, qp, qo, qs[0], qs[1], os[0], os[1]),
-            self._stream(stream))
+                         q_heads, q_dim, 0, qp, qo, *qs, *os),
+            self._raw_stream(self._index) if stream is None else _stream_handle(stream))
         if st != 0:
             raise KVRelayoutError(st, "kv_cache_append")
         return q_out
@@ -272,37 +280,35 @@ class KVCache:
         ``scale``: D ** -0.5 by default; ``window`` > 0: only that many keys, the token's own
         included. Returns (out, lse): ``out`` like q with ``value_dim`` elements, ``lse`` float32
         [R][new][Hq], new tensors by default (``lse=False``: none)."""
-        one = q.dim() == 3
-        if q.dim() not in (3, 4):
+        n = q.dim()
+        if n not in (3, 4):
             raise ValueError(f"q is {list(q.shape)}; expected [R][new][heads][dim]")
-        lead = tuple(q.shape[:-2])
-        R, m = lead[0], 1 if one else lead[1]
-        lead += (self.query_heads,)
+        R, m = (q.shape[0], q.shape[1]) if n == 4 else (q.shape[0], 1)
+        lead = (R, m, self.query_heads) if n == 4 else (R, self.query_heads)
+        dtype = q.dtype
         qs = self._rows(q, "q", lead + (self.head_dim,))
         if out is None:
-            out = self._torch.empty(lead + (self.value_dim,), dtype=q.dtype, device=q.device)
-        os = self._rows(out, "out", lead + (self.value_dim,), q.dtype)
+            out = self._torch.empty(lead + (self.value_dim,), dtype=dtype, device=q.device)
+        os = self._rows(out, "out", lead + (self.value_dim,), dtype)
         if lse is None:
             lse = self._torch.empty(lead, dtype=self._f32, device=q.device)
         if lse is False:
             lse, lp = None, 0
-        else:
-            if lse.dtype is not self._f32 or tuple(lse.shape) != lead or \
-                    not lse.is_contiguous() or lse.device != self._device:
-                raise ValueError(f"lse is {lse.dtype} {list(lse.shape)}; expected contiguous "
-                                 f"float32 {list(lead)} on {self._device}")
+        elif lse.dtype is self._f32 and lse.shape == lead and lse.is_contiguous() and \
+                lse.get_device() == self._index:
             lp = lse.data_ptr()
-        if one:
+        else:
+            raise ValueError(f"lse is {lse.dtype} {list(lse.shape)}; expected contiguous "
+                             f"float32 {list(lead)} on {self._device}")
+        if n == 3:
             qs, os = (qs[0], 0, qs[1]), (os[0], 0, os[1])
-        ids, stride, rows, width = self._table(block_table)
-        st = _library().kv_cache_attend(
+        st = self._attend(
             self._handle(), layer,
-            _ATTEND.pack(R, m, self._types[q.dtype], window,
-                         self.head_dim ** -0.5 if scale is None else scale, 0,
-                         self._list(lengths, "lengths", R), ids, stride, rows, width,
-                         q.data_ptr(), out.data_ptr(), lp, qs[0], qs[1], qs[2], os[0], os[1],
-                         os[2]),
-            self._stream(stream))
+            _ATTEND.pack(R, m, self._types[dtype], window,
+                         self._default_scale if scale is None else scale, 0,
+                         self._list(lengths, "lengths", R), *self._table(block_table),
+                         q.data_ptr(), out.data_ptr(), lp, *qs, *os),
+            self._raw_stream(self._index) if stream is None else _stream_handle(stream))
         if st != 0:
             raise KVRelayoutError(st, "kv_cache_attend")
         return out, lse
