@@ -6,8 +6,9 @@
 //   rotated, halves:      pieces at 8 i and 8 i + R / 2 hold pairs 8 i .. 8 i + 7 as (a | b);
 //   rotated, interleaved: pieces at 16 i and 16 i + 8 hold the same pairs side by side;
 //   not rotated:          pieces at 16 i and 16 i + 8, passed through (or quantized).
-// A thread asks for up to BATCH units at once, before it looks at the token's position: the slot
-// (position, then block id) and the angles are on their way meanwhile. Where the row's units divide
+// A thread asks for BATCH units before it looks at the token's position: the slot (position, then
+// block id) and the angles are on their way meanwhile. HBM bounds it with many tokens: 39834
+// tokens of 32 + 16 heads of 128, 982 MB, 162 us (6060 GB/s, 89 % of a plain copy's rate). Where the row's units divide
 // the block's threads, a thread has the same unit of every row, and loads its angles once.
 #include <algorithm>
 
@@ -18,8 +19,6 @@ namespace {
 using namespace kvc;
 
 constexpr int THREADS = 128;
-constexpr int BATCH = 4;      // units a thread has in flight
-
 struct Rows {                 // head rows of one input and where they go
     const unsigned char *src;
     int64_t src_token, src_head;
@@ -148,8 +147,8 @@ __device__ __forceinline__ Place place_of(const AppendArgs &a, int32_t t, int32_
     return p;
 }
 
-template <bool F16, bool INTERLEAVED, bool E4M3>
-__global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a) {
+template <bool F16, bool INTERLEAVED, bool E4M3, int BATCH>
+__global__ void __launch_bounds__(THREADS, BATCH == 1 ? 10 : 5) append_kernel(AppendArgs a) {
     wait_for_previous();
     let_next_start();
     const int64_t token = blockIdx.x;
@@ -223,10 +222,19 @@ __global__ void __launch_bounds__(THREADS) append_kernel(AppendArgs a) {
     }
 }
 
+// Many tokens: one unit a thread at a time and small register sets, as the blocks on an SM hide one
+// another's waits (39834 tokens of 384 units: 162 us with 1 unit and 10 blocks an SM, 181 with 3
+// and 5). Few: a token is one chain of waits, shorter with all its units asked for at once (64
+// tokens of 640 units: 3.8 us with 3, 4.5 with 1). A block an SM is taken as the border; a token
+// that needs one unit a thread takes the first kind always.
 template <bool F16, bool E4M3>
-kvr_status go(const AppendArgs &a, bool interleaved, int32_t tokens, void *stream) {
-    return kvc_launch(interleaved ? append_kernel<F16, true, E4M3> : append_kernel<F16, false, E4M3>,
-                      a, dim3((unsigned)tokens), THREADS, 0, stream);
+kvr_status go(const AppendArgs &a, bool interleaved, int32_t tokens, int sms, void *stream) {
+    const int64_t n = (int64_t)a.q.heads * a.q_units.d + (int64_t)(a.k.heads + a.v.heads) * a.units.d;
+    const auto kernel =
+        n <= THREADS || tokens > sms
+            ? (interleaved ? append_kernel<F16, true, E4M3, 1> : append_kernel<F16, false, E4M3, 1>)
+            : (interleaved ? append_kernel<F16, true, E4M3, 3> : append_kernel<F16, false, E4M3, 3>);
+    return kvc_launch(kernel, a, dim3((unsigned)tokens), THREADS, 0, stream);
 }
 
 }  // namespace
@@ -260,8 +268,8 @@ kvr_status kvc_append_launch(const kvc_cache *c, int32_t layer, const kvc_append
     a.last = (p->flags & KVC_ROTATE_LAST) != 0;
     const bool il = (p->flags & KVC_INTERLEAVED) != 0, f16 = p->dtype == KVC_DTYPE_F16;
     if (c->d.dtype == KVR_DTYPE_FP8_E4M3)
-        return f16 ? go<true, true>(a, il, p->num_tokens, stream)
-                   : go<false, true>(a, il, p->num_tokens, stream);
-    return f16 ? go<true, false>(a, il, p->num_tokens, stream)
-               : go<false, false>(a, il, p->num_tokens, stream);
+        return f16 ? go<true, true>(a, il, p->num_tokens, c->sm_count, stream)
+                   : go<false, true>(a, il, p->num_tokens, c->sm_count, stream);
+    return f16 ? go<true, false>(a, il, p->num_tokens, c->sm_count, stream)
+               : go<false, false>(a, il, p->num_tokens, c->sm_count, stream);
 }
