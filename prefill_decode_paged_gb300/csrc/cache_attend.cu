@@ -70,13 +70,13 @@ kvr_status kvc_attend_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     const int32_t M = a.m * a.G;
     const AttendPick k = pick(c->d, M);
     a.chunks = (int32_t)ceil_div(M, k.rp);
-    // most units of a job; the kernel counts a job of every request in 32 bits
+    // most units of a job; the kernel counts those of all jobs in 32 bits
     const int64_t most = ceil_div((int64_t)p->table.width * c->d.block_size, k.unit) + 1;
-    if (most * p->num_requests > INT32_MAX) return KVR_ERR_UNSUPPORTED;
+    const int64_t all = most * p->num_requests * a.H * a.chunks;
+    if (all > INT32_MAX) return KVR_ERR_UNSUPPORTED;
     const size_t smem = k.smem(p->num_requests);
     // an SM has 228 KB, of which each block takes 1 KB for itself
     const int64_t resident = std::min<int64_t>(k.blocks, (228 << 10) / (int64_t)(smem + 1024));
-    const int64_t grid = std::min<int64_t>(resident * kvc_stream_sms(c, stream),
-                                           most * p->num_requests * a.H * a.chunks);
+    const int64_t grid = std::min<int64_t>(resident * kvc_stream_sms(c, stream), all);
     return kvc_launch(k.kernel, a, dim3((unsigned)grid), ATTEND_THREADS, smem, stream);
 }

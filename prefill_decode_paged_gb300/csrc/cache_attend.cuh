@@ -159,11 +159,11 @@ attend_kernel(AttendArgs a) {
 
     unit_prefix<C::UNIT>(a.split, KT, prefix, shared_int);
     const int32_t HJ = a.H * a.chunks;
-    const int64_t total = (int64_t)prefix[a.split.requests] * HJ;
-    const int64_t parts = gridDim.x < total ? (int64_t)gridDim.x : total;
-    if (blockIdx.x >= parts) return;
-    int64_t x = blockIdx.x * total / parts;
-    const int64_t x_end = (blockIdx.x + 1) * total / parts;
+    const int32_t total = prefix[a.split.requests] * HJ;
+    const Cut cut(total, min((int32_t)gridDim.x, total));
+    if ((int32_t)blockIdx.x >= cut.parts) return;
+    int32_t x = cut.start(blockIdx.x);
+    const int32_t x_end = cut.start(blockIdx.x + 1);
 
     const int32_t M = a.m * a.G;
     const size_t slot_floats = (size_t)RP * (a.D + 2);
@@ -214,6 +214,19 @@ attend_kernel(AttendArgs a) {
                 cp_async16(dst + KT * ROW, a.v_plane.base + at, n);
             }
         };
+        // the queries, one warp a row, asked for ahead of the keys
+        constexpr int QW = RP / ATTEND_WARPS;
+        uint4 qw[QW];
+#pragma unroll
+        for (int n = 0; n < QW; ++n) {
+            const int row = n * ATTEND_WARPS + warp;
+            const int32_t rho = row0 + row;
+            const int32_t i = (int32_t)a.group.div((uint32_t)rho), gq = rho - i * a.G;
+            const unsigned char *q = a.q + r * a.q_request + i * a.q_token +
+                                     ((int64_t)h * a.G + gq) * a.q_head;
+            qw[n] = make_uint4(0, 0, 0, 0);
+            if (row < rows && lane * 8 < a.D) qw[n] = __ldg((const uint4 *)q + lane);
+        }
         int64_t next_slot;
         {
             int64_t s[C::STAGES];
@@ -227,14 +240,11 @@ attend_kernel(AttendArgs a) {
             next_slot = s[C::STAGES - 1];
         }
 
-        // the queries: one warp a row, in the type of the products; rows beyond M are zero
-        for (int row = warp; row < RP; row += ATTEND_WARPS) {
-            const int32_t rho = row0 + row;
-            const int32_t i = (int32_t)a.group.div((uint32_t)rho), gq = rho - i * a.G;
-            const unsigned char *q = a.q + r * a.q_request + i * a.q_token +
-                                     ((int64_t)h * a.G + gq) * a.q_head;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (row < rows && lane * 8 < a.D) w = *(const uint4 *)(q + lane * 16);
+        // the queries in the type of the products; rows beyond M are zero
+#pragma unroll
+        for (int n = 0; n < QW; ++n) {
+            const int row = n * ATTEND_WARPS + warp;
+            const uint4 w = qw[n];
             float factor = a.scale * log2e * ks;
             if (POOL != KVR_DTYPE_FP8_E4M3) {
                 if (lane * 8 < DP)
@@ -483,7 +493,25 @@ attend_kernel(AttendArgs a) {
                 }
             }
         __syncthreads();
-        const int64_t job_index = (int64_t)r * HJ + job;
+        // each row's maximum and sum, and the warps' weights in place of their maxima
+        if (tid < RP) {
+            float m = -INFINITY, l = 0.0f;
+#pragma unroll
+            for (int w = 0; w < ATTEND_WARPS; ++w) m = fmaxf(m, stat[(w * RP + tid) * 2]);
+#pragma unroll
+            for (int w = 0; w < ATTEND_WARPS; ++w) {
+                const float mw = stat[(w * RP + tid) * 2], lw = stat[(w * RP + tid) * 2 + 1];
+                const float f = mw == -INFINITY ? 0.0f : ex2(mw - m);
+                // (a warp that saw no key of the row has nothing to add, whatever it multiplied)
+                const bool none = mw == -INFINITY && lw == 0.0f;
+                l += none ? 0.0f : f * lw;
+                stat[(w * RP + tid) * 2] = none ? -1.0f : f;
+            }
+            row_scale[tid] = m;
+            stat[tid * 2 + 1] = l;
+        }
+        __syncthreads();
+        const int32_t job_index = r * HJ + job;
         const bool whole = u0 == 0 && u1 == units;
         const int32_t D4 = a.D / 4;
         float *slot = a.partial + (size_t)(2 * blockIdx.x + (u0 == 0 ? 1 : 0)) * slot_floats;
@@ -492,43 +520,37 @@ attend_kernel(AttendArgs a) {
             const int32_t rho = row0 + row;
             const int32_t i = (int32_t)a.group.div((uint32_t)rho), gq = rho - i * a.G;
             const int64_t hq = (int64_t)h * a.G + gq;
-            const float inv = l > 0.0f || l != l ? vs / l : 0.0f;
+            const bool some = l > 0.0f || l != l;
+            const float inv = some ? vs / l : 0.0f;
             v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
             unsigned char *to = a.out + r * a.out_request + i * a.out_token + hq * a.out_head;
             *(uint2 *)(to + d4 * 8) = a.f16 ? narrow4<true>(v) : narrow4<false>(v);
             if (d4 == 0 && a.lse != nullptr)
                 a.lse[((int64_t)r * a.m + i) * ((int64_t)a.H * a.G) + hq] =
-                    l > 0.0f || l != l ? (m - (C::F16 ? P_SHIFT : 0.0f) + log2f(l)) * 0.6931471805599453f
-                                       : -INFINITY;
+                    some ? (m - (C::F16 ? P_SHIFT : 0.0f) + log2f(l)) * 0.6931471805599453f : -INFINITY;
         };
-        for (int k = tid; k < rows * D4; k += ATTEND_THREADS) {
-            const int row = k / D4, d4 = k - row * D4;
-            float m = -INFINITY, l = 0.0f;
+        for (int row = warp; row < rows; row += ATTEND_WARPS)
+            for (int d4 = lane; d4 < D4; d4 += 32) {
+                float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll
-            for (int w = 0; w < ATTEND_WARPS; ++w) m = fmaxf(m, stat[(w * RP + row) * 2]);
-            float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll
-            for (int w = 0; w < ATTEND_WARPS; ++w) {
-                const float mw = stat[(w * RP + row) * 2];
-                const float f = mw == -INFINITY ? 0.0f : ex2(mw - m);
-                const float4 p = *(const float4 *)(acc + (w * RP + row) * C::PITCH + d4 * 4);
-                if (mw == -INFINITY && stat[(w * RP + row) * 2 + 1] == 0.0f) continue;
-                l += f * stat[(w * RP + row) * 2 + 1];
-                v.x += f * p.x, v.y += f * p.y, v.z += f * p.z, v.w += f * p.w;
+                for (int w = 0; w < ATTEND_WARPS; ++w) {
+                    const float f = stat[(w * RP + row) * 2];
+                    const float4 p = *(const float4 *)(acc + (w * RP + row) * C::PITCH + d4 * 4);
+                    if (f < 0.0f) continue;
+                    v.x += f * p.x, v.y += f * p.y, v.z += f * p.z, v.w += f * p.w;
+                }
+                const float m = row_scale[row], l = stat[row * 2 + 1];
+                if (whole) {
+                    finish(row, d4, v, m, l);
+                } else {
+                    __stcg((float4 *)(slot + (size_t)row * a.D) + d4, v);
+                    if (d4 == 0) __stcg((float2 *)(slot + (size_t)RP * a.D) + row, make_float2(m, l));
+                }
             }
-            if (whole) {
-                finish(row, d4, v, m, l);
-            } else {
-                __stcg((float4 *)(slot + (size_t)row * a.D) + d4, v);
-                if (d4 == 0)
-                    __stcg((float2 *)(slot + (size_t)RP * a.D) + row, make_float2(m, l));
-            }
-        }
         if (!whole) {
             // the job's parts: the blocks that hold its first and its last unit, and all between
-            const int64_t c0 = part_of(seg.job_first, parts, total);
-            const int64_t c1 = part_of(seg.job_first + units - 1, parts, total);
-            const int32_t n = (int32_t)(c1 - c0 + 1);
+            const int32_t c0 = cut.part_of(seg.job_first);
+            const int32_t n = cut.part_of(seg.job_first + units - 1) - c0 + 1;
             __threadfence();
             __syncthreads();
             if (tid == 0) {
@@ -538,44 +560,57 @@ attend_kernel(AttendArgs a) {
             }
             __syncthreads();
             if (shared_int[0]) {
+                // the last to come joins them, in the order of the keys, with the running maximum;
+                // each lane has two rows' pieces of 8 parts on their way at once
                 __threadfence();
-                auto part = [&](int32_t k) {
-                    return a.partial + (size_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * slot_floats;
-                };
-                // weights of the parts, row by row: [n][RP], in the ring's memory
-                float *weight = (float *)smem;
-                for (int row = warp; row < rows; row += ATTEND_WARPS) {
-                    float m = -INFINITY;
-                    for (int k = lane; k < n; k += 32)
-                        m = fmaxf(m, __ldcg((const float2 *)(part(k) + (size_t)RP * a.D) + row).x);
+                constexpr int AHEAD = 8, PAIR = 2;
+                for (int row0_ = warp; row0_ < rows; row0_ += PAIR * ATTEND_WARPS)
+                    for (int d4 = lane; d4 < D4; d4 += 32) {
+                        float m[PAIR], l[PAIR];
+                        float4 v[PAIR];
 #pragma unroll
-                    for (int w = 16; w > 0; w /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, w));
-                    float l = 0.0f;
-                    for (int k = lane; k < n; k += 32) {
-                        const float2 p = __ldcg((const float2 *)(part(k) + (size_t)RP * a.D) + row);
-                        const float f = p.x == -INFINITY ? 0.0f : ex2(p.x - m);
-                        weight[k * RP + row] = f;
-                        if (p.x != -INFINITY || p.y != 0.0f) l += f * p.y;
-                    }
+                        for (int e = 0; e < PAIR; ++e) {
+                            m[e] = -INFINITY, l[e] = 0.0f;
+                            v[e] = make_float4(0, 0, 0, 0);
+                        }
+                        for (int32_t k0 = 0; k0 < n; k0 += AHEAD) {
+                            float2 ml[PAIR][AHEAD];
+                            float4 p[PAIR][AHEAD];
 #pragma unroll
-                    for (int w = 16; w > 0; w /= 2) l += __shfl_xor_sync(~0u, l, w);
-                    if (lane == 0) {
-                        stat[row * 2] = m;
-                        stat[row * 2 + 1] = l;
+                            for (int k = 0; k < AHEAD; ++k) {
+                                const int32_t c = min(k0 + k, n - 1);
+                                const float *s = a.partial + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * slot_floats;
+#pragma unroll
+                                for (int e = 0; e < PAIR; ++e) {
+                                    const int row = min(row0_ + e * ATTEND_WARPS, rows - 1);
+                                    ml[e][k] = __ldcg((const float2 *)(s + (size_t)RP * a.D) + row);
+                                    p[e][k] = __ldcg((const float4 *)(s + (size_t)row * a.D) + d4);
+                                }
+                            }
+#pragma unroll
+                            for (int e = 0; e < PAIR; ++e) {
+                                float top = m[e];
+#pragma unroll
+                                for (int k = 0; k < AHEAD; ++k) top = fmaxf(top, ml[e][k].x);
+                                const float old = m[e] == -INFINITY ? 0.0f : ex2(m[e] - top);
+                                m[e] = top;
+                                l[e] *= old;
+                                v[e].x *= old, v[e].y *= old, v[e].z *= old, v[e].w *= old;
+#pragma unroll
+                                for (int k = 0; k < AHEAD; ++k) {
+                                    const float2 q = ml[e][k];
+                                    if (k0 + k >= n || (q.x == -INFINITY && q.y == 0.0f)) continue;
+                                    const float f = q.x == -INFINITY ? 0.0f : ex2(q.x - top);
+                                    l[e] += f * q.y;
+                                    v[e].x += f * p[e][k].x, v[e].y += f * p[e][k].y;
+                                    v[e].z += f * p[e][k].z, v[e].w += f * p[e][k].w;
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < PAIR; ++e)
+                            if (row0_ + e * ATTEND_WARPS < rows) finish(row0_ + e * ATTEND_WARPS, d4, v[e], m[e], l[e]);
                     }
-                }
-                __syncthreads();
-                for (int k = tid; k < rows * D4; k += ATTEND_THREADS) {
-                    const int row = k / D4, d4 = k - row * D4;
-                    float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-                    for (int32_t c = 0; c < n; ++c) {
-                        const float f = weight[c * RP + row];
-                        const float4 p = __ldcg((const float4 *)(part(c) + (size_t)row * a.D) + d4);
-                        v.x += f * p.x, v.y += f * p.y, v.z += f * p.z, v.w += f * p.w;
-                    }
-                    finish(row, d4, v, stat[row * 2], stat[row * 2 + 1]);
-                }
             }
         }
         __syncthreads();

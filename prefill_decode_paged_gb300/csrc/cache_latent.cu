@@ -267,8 +267,8 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
 
 // A part has LEAST tiles at least: each costs the others a share of the join.
 constexpr int LEAST = 4;
-__device__ __forceinline__ int64_t parts_of(const LatentArgs &a, int64_t total) {
-    return max((int64_t)1, min((int64_t)a.parts, total / LEAST));
+__device__ __forceinline__ int32_t parts_of(const LatentArgs &a, int32_t total) {
+    return max(1, min(a.parts, total / LEAST));
 }
 
 // -- the kernel -------------------------------------------------------------------
@@ -328,11 +328,11 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
     fence_after();
     const uint32_t tmem = *(volatile uint32_t *)(smem + OFF_BARS + OFF_TMEM);
 
-    const int64_t total = (int64_t)prefix[a.split.requests] * a.chunks;
-    const int64_t parts = parts_of(a, total);
-    const int64_t part = blockIdx.x / 2;
-    int64_t x = part < parts ? part * total / parts : 0;
-    const int64_t x_end = part < parts ? (part + 1) * total / parts : 0;
+    const int32_t total = prefix[a.split.requests] * a.chunks;
+    const Cut cut(total, parts_of(a, total));
+    const int32_t part = blockIdx.x / 2;
+    int32_t x = part < cut.parts ? cut.start(part) : 0;
+    const int32_t x_end = part < cut.parts ? cut.start(part + 1) : 0;
     const int32_t M = a.m * a.Hq;
 
     // a thread's query row in a segment: lane of tensor memory, row of the pass
@@ -788,17 +788,16 @@ __global__ void __launch_bounds__(JOIN_THREADS) latent_join(const __grid_constan
     wait_for_previous();
     let_next_start();
     unit_prefix<KT>(a.split, KT, prefix, scratch);
-    const int64_t total = (int64_t)prefix[a.split.requests] * a.chunks;
-    const int64_t parts = parts_of(a, total);
+    const int32_t total = prefix[a.split.requests] * a.chunks;
+    const Cut cut(total, parts_of(a, total));
     const int32_t M = a.m * a.Hq, groups = (min(M, ROWS) + JOIN_ROWS - 1) / JOIN_ROWS;
     const int32_t jg = blockIdx.x / groups, r = jg / a.chunks, job = jg - r * a.chunks;
     const int32_t row = (blockIdx.x % groups) * JOIN_ROWS + threadIdx.x % JOIN_ROWS;
     const int32_t rho = job * ROWS + row;
     const int32_t e4 = blockIdx.y * JOIN_COLS + threadIdx.x / JOIN_ROWS;     // 4 elements
     const int32_t units = prefix[r + 1] - prefix[r];
-    const int64_t first = (int64_t)prefix[r] * a.chunks + (int64_t)job * units;
-    const int64_t c0 = part_of(first, parts, total);
-    const int32_t n = (int32_t)(part_of(first + units - 1, parts, total) - c0) + 1;
+    const int32_t first = prefix[r] * a.chunks + job * units;
+    const int32_t c0 = cut.part_of(first), n = cut.part_of(first + units - 1) - c0 + 1;
     if (n == 1 || rho >= M) return;
     auto slot = [&](int32_t c) { return a.partial + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * SLOT; };
     auto stat = [&](int32_t c) { return __ldcg((const float2 *)(slot(c) + (size_t)ROWS * VALUES) + row); };
@@ -910,7 +909,7 @@ kvr_status kvc_latent_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     const int64_t M = (int64_t)a.m * a.Hq;
     a.chunks = (int32_t)((M + ROWS - 1) / ROWS);
     const int64_t most = ((int64_t)p->table.width * c->d.block_size + KT - 1) / KT + 1;
-    if (most * p->num_requests > INT32_MAX) return KVR_ERR_UNSUPPORTED;
+    if (most * p->num_requests * a.chunks > INT32_MAX) return KVR_ERR_UNSUPPORTED;
     a.parts = (int32_t)std::min<int64_t>(std::max(kvc_stream_sms(c, stream) / 2, 1),
                                          most * p->num_requests * a.chunks);
     const bool f16 = c->d.dtype == KVC_DTYPE_F16;

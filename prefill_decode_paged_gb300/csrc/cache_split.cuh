@@ -67,32 +67,45 @@ __device__ __forceinline__ void unit_prefix(const SplitArgs &a, int32_t align, i
     __syncthreads();
 }
 
-// The part that holds unit x of `total`, when part c holds [c total / parts, (c + 1) total / parts).
-__device__ __forceinline__ int64_t part_of(int64_t x, int64_t parts, int64_t total) {
-    return ((x + 1) * parts - 1) / total;
-}
+// The line's cut into parts: the first `more` have one unit more than the others.
+struct Cut {
+    int32_t total, parts, each, more;
+
+    __device__ __forceinline__ Cut(int32_t total_, int32_t parts_) : total(total_), parts(parts_) {
+        each = (int32_t)((uint32_t)total / (uint32_t)parts);
+        more = total - each * parts;
+    }
+    __device__ __forceinline__ int32_t start(int32_t c) const { return c * each + min(c, more); }
+    // the part that holds unit x
+    __device__ __forceinline__ int32_t part_of(int32_t x) const {
+        const int32_t edge = more * (each + 1);
+        return x < edge ? (int32_t)((uint32_t)x / (uint32_t)(each + 1))
+                        : more + (int32_t)((uint32_t)(x - edge) / (uint32_t)max(each, 1));
+    }
+};
 
 // What of the line a part does next: units [u0, u1) of job `job` (of `units`) of request r.
 struct Segment {
     int32_t r, job, u0, u1, units;
-    int64_t job_first;        // the job's first unit in the line
+    int32_t job_first;        // the job's first unit in the line
 };
-__device__ __forceinline__ Segment segment_at(int64_t x, int64_t x_end, const int32_t *prefix,
+__device__ __forceinline__ Segment segment_at(int32_t x, int32_t x_end, const int32_t *prefix,
                                               int32_t requests, int32_t jobs) {
     Segment s;
     int32_t lo = 0, hi = requests - 1;
-    const int32_t xj = (int32_t)(x / jobs);
+    const int32_t xj = (int32_t)((uint32_t)x / (uint32_t)jobs);
     while (lo < hi) {
         const int32_t mid = (lo + hi + 1) / 2;
         if (prefix[mid] <= xj) lo = mid; else hi = mid - 1;
     }
     s.r = lo;
-    s.units = prefix[lo + 1] - prefix[lo];
-    const int64_t start = (int64_t)prefix[lo] * jobs;
-    s.job = (int32_t)((x - start) / s.units);
-    s.job_first = start + (int64_t)s.job * s.units;
-    s.u0 = (int32_t)(x - s.job_first);
-    s.u1 = (int32_t)min((int64_t)s.units, s.u0 + (x_end - x));
+    const int32_t first = prefix[lo];
+    s.units = prefix[lo + 1] - first;
+    const int32_t start = first * jobs;
+    s.job = (int32_t)((uint32_t)(x - start) / (uint32_t)s.units);
+    s.job_first = start + s.job * s.units;
+    s.u0 = x - s.job_first;
+    s.u1 = min(s.units, s.u0 + (x_end - x));
     return s;
 }
 
