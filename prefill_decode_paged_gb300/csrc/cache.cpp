@@ -193,6 +193,37 @@ bool type_fits(const kvc_cache *c, int32_t dtype) {
 
 }  // namespace
 
+bool kvc_make_map(CUtensorMap *map, int es, int rank, uint64_t base, int64_t row_bytes,
+                  const uint64_t *dims, const int64_t *strides, const uint32_t *box, int line) {
+    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, CUDART_VERSION,
+                                         cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || p == nullptr) {
+        cudaGetLastError();
+        return false;
+    }
+    cuuint64_t extents[5], steps[4];
+    cuuint32_t boxes[5], ones[5];
+    for (int i = 0; i < rank; ++i) {
+        extents[i] = dims[i];
+        boxes[i] = box[i];
+        ones[i] = 1;
+        // (a stride of an extent of 1 is not used, but may not be zero)
+        if (i > 0) steps[i - 1] = (cuuint64_t)(strides[i - 1] > 0 ? strides[i - 1] : row_bytes);
+    }
+    return reinterpret_cast<Encode>(p)(
+               map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+               (cuuint32_t)rank, (void *)(uintptr_t)base, extents, steps, boxes, ones,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 extern "C" kvr_status kv_cache_workspace_bytes(const kvc_desc *desc, int32_t sm_count,
                                                int64_t *bytes) {
     if (bytes == nullptr || sm_count < 1) return KVR_ERR_INVALID_ARG;

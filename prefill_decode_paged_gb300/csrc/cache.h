@@ -49,8 +49,8 @@ struct kvc_cache {
     int64_t span = 0;                 // bytes from a plane's base to its end
     KvrDiv block = {};
     KvcWorkspace ws = {};
-    std::vector<CUtensorMap> maps;    // latents: copy-engine maps of the planes, two a layer
-    int32_t piece = 0;                // tokens of a map's box
+    std::vector<CUtensorMap> maps;    // copy-engine maps of the planes, two a layer
+    int32_t piece = 0;                // tokens of a map's box; 0: there are no maps
     int device = 0;
     int sm_count = 0;
 
@@ -100,6 +100,12 @@ inline kvr_status kvc_launch(void (*kernel)(Args), const Args &a, dim3 grid, int
     cudaGetLastError();
     return KVR_ERR_CUDA;
 }
+
+// cache.cpp: a copy-engine map of a plane of `es`-byte elements, `dims` from the innermost on,
+// byte strides of the others (0 where the extent is 1), swizzled in lines of 128 or 64 bytes.
+// False if the driver has none for it.
+bool kvc_make_map(CUtensorMap *map, int es, int rank, uint64_t base, int64_t row_bytes,
+                  const uint64_t *dims, const int64_t *strides, const uint32_t *box, int line);
 
 // cache_attend.cu, cache_latent.cu: the launches behind kv_cache_attend(), and what they want
 // of the workspace. (`setup` runs once a cache: shared memory limits of the kernels.)

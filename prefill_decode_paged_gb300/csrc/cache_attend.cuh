@@ -75,8 +75,9 @@ struct Attend {
     static constexpr int BLOCKS = STAGE > 8192 ? 1 : 2;          // resident on an SM
     static constexpr int Q_BYTES = RP * DP * 2;
     static_assert(ATTEND_WARPS * RP * PITCH * 4 <= RING, "the join reuses the ring");
-    // ring, queries, then floats: row scales [RP], per-warp statistics [4][RP][2]; then prefix
-    static constexpr int FIXED = RING + Q_BYTES + 4 * RP + 4 * ATTEND_WARPS * RP * 2 + 16;
+    // ring, queries, a barrier, then floats: row scales [RP], per-warp statistics [4][RP][2]; 4 ints;
+    // then prefix
+    static constexpr int FIXED = RING + Q_BYTES + 16 + 4 * RP + 4 * ATTEND_WARPS * RP * 2 + 16;
     static constexpr size_t smem(int32_t requests) { return FIXED + 4 * (size_t)(requests + 1); }
 };
 
@@ -134,6 +135,38 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) {
     return r * ROW + ((c ^ ((r >> 1) & 3)) << 4);       // 64-byte rows: two share 128 bytes
 }
 
+// -- the barrier that a join's copies count at ------------------------------------------
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+// Waits for the phase of `parity`, in turns of a microsecond and for about two seconds at most.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+                 "AGAIN:\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+                 "@p bra OUT;\n\t"
+                 "add.u32 n, n, 1;\n\t"
+                 "setp.lt.u32 p, n, 2000000;\n\t"
+                 "@p bra AGAIN;\n\t"
+                 "setp.ne.u32 p, n, n;\n"
+                 "OUT:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ void load_bytes(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // out (16-bit), four elements of one row, from floats
 template <bool F16>
 __device__ __forceinline__ uint2 narrow4(float4 v) {
@@ -148,12 +181,18 @@ attend_kernel(AttendArgs a) {
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t smem0 = (uint32_t)__cvta_generic_to_shared(smem);
     unsigned char *q_smem = smem + C::RING;
-    float *row_scale = (float *)(q_smem + C::Q_BYTES);
+    const uint32_t join_bar = smem0 + C::RING + C::Q_BYTES;
+    float *row_scale = (float *)(q_smem + C::Q_BYTES + 16);
     float *stat = row_scale + RP;                       // [warp][RP][max, sum]
     int32_t *shared_int = (int32_t *)(stat + ATTEND_WARPS * RP * 2);   // [4]
     int32_t *prefix = shared_int + 4;                   // [requests + 1], in units of one job
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
 
+    if (tid == 0) {
+        bar_init(join_bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    uint32_t join_phase = 0;
     wait_for_previous();
     let_next_start();
 
@@ -166,7 +205,7 @@ attend_kernel(AttendArgs a) {
     const int32_t x_end = cut.start(blockIdx.x + 1);
 
     const int32_t M = a.m * a.G;
-    const size_t slot_floats = (size_t)RP * (a.D + 2);
+    const int32_t slot_floats = RP * (a.D + 2);
     const uint32_t ring = smem0 + (uint32_t)(warp * C::STAGES * C::STAGE);
     const float log2e = 1.4426950408889634f;
 
@@ -514,7 +553,7 @@ attend_kernel(AttendArgs a) {
         const int32_t job_index = r * HJ + job;
         const bool whole = u0 == 0 && u1 == units;
         const int32_t D4 = a.D / 4;
-        float *slot = a.partial + (size_t)(2 * blockIdx.x + (u0 == 0 ? 1 : 0)) * slot_floats;
+        float *slot = a.partial + (size_t)(2 * blockIdx.x + (u0 == 0 ? 1 : 0)) * (size_t)slot_floats;
         const float vs = POOL == KVR_DTYPE_FP8_E4M3 ? a.v_scale[h] : 1.0f;
         auto finish = [&](int row, int d4, float4 v, float m, float l) {
             const int32_t rho = row0 + row;
@@ -560,57 +599,86 @@ attend_kernel(AttendArgs a) {
             }
             __syncthreads();
             if (shared_int[0]) {
-                // the last to come joins them, in the order of the keys, with the running maximum;
-                // each lane has two rows' pieces of 8 parts on their way at once
+                // the last to come joins them, in the order of the keys: as many parts at a time as
+                // the ring holds, each one copy; their weights, then the weighted sums
                 __threadfence();
-                constexpr int AHEAD = 8, PAIR = 2;
-                for (int row0_ = warp; row0_ < rows; row0_ += PAIR * ATTEND_WARPS)
-                    for (int d4 = lane; d4 < D4; d4 += 32) {
-                        float m[PAIR], l[PAIR];
-                        float4 v[PAIR];
+                constexpr int COLS = DP / 4, ITEMS = RP * COLS / ATTEND_THREADS;
+                static_assert(RP * COLS % ATTEND_THREADS == 0 && RP <= ATTEND_THREADS, "");
+                const int32_t slot_bytes = slot_floats * 4;
+                const int32_t batch = C::RING / slot_bytes;
+                float m = -INFINITY, l = 0.0f;          // of row tid / LANES
+                float4 v[ITEMS];
 #pragma unroll
-                        for (int e = 0; e < PAIR; ++e) {
-                            m[e] = -INFINITY, l[e] = 0.0f;
-                            v[e] = make_float4(0, 0, 0, 0);
+                for (int e = 0; e < ITEMS; ++e) v[e] = make_float4(0, 0, 0, 0);
+                for (int32_t k0 = 0; k0 < n; k0 += batch) {
+                    const int32_t here = min(batch, n - k0);
+                    // (what is here was read and written by threads, there written by others')
+                    asm volatile("fence.proxy.async;" ::: "memory");
+                    __syncthreads();
+                    if (warp == 0) {
+                        if (lane == 0) bar_expect(join_bar, here * slot_bytes);
+                        __syncwarp();
+                        for (int32_t k = lane; k < here; k += 32) {
+                            const int32_t c = k0 + k;
+                            load_bytes(smem0 + k * slot_bytes,
+                                       a.partial + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * (size_t)slot_floats,
+                                       slot_bytes, join_bar);
                         }
-                        for (int32_t k0 = 0; k0 < n; k0 += AHEAD) {
-                            float2 ml[PAIR][AHEAD];
-                            float4 p[PAIR][AHEAD];
-#pragma unroll
-                            for (int k = 0; k < AHEAD; ++k) {
-                                const int32_t c = min(k0 + k, n - 1);
-                                const float *s = a.partial + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * slot_floats;
-#pragma unroll
-                                for (int e = 0; e < PAIR; ++e) {
-                                    const int row = min(row0_ + e * ATTEND_WARPS, rows - 1);
-                                    ml[e][k] = __ldcg((const float2 *)(s + (size_t)RP * a.D) + row);
-                                    p[e][k] = __ldcg((const float4 *)(s + (size_t)row * a.D) + d4);
-                                }
-                            }
-#pragma unroll
-                            for (int e = 0; e < PAIR; ++e) {
-                                float top = m[e];
-#pragma unroll
-                                for (int k = 0; k < AHEAD; ++k) top = fmaxf(top, ml[e][k].x);
-                                const float old = m[e] == -INFINITY ? 0.0f : ex2(m[e] - top);
-                                m[e] = top;
-                                l[e] *= old;
-                                v[e].x *= old, v[e].y *= old, v[e].z *= old, v[e].w *= old;
-#pragma unroll
-                                for (int k = 0; k < AHEAD; ++k) {
-                                    const float2 q = ml[e][k];
-                                    if (k0 + k >= n || (q.x == -INFINITY && q.y == 0.0f)) continue;
-                                    const float f = q.x == -INFINITY ? 0.0f : ex2(q.x - top);
-                                    l[e] += f * q.y;
-                                    v[e].x += f * p[e][k].x, v[e].y += f * p[e][k].y;
-                                    v[e].z += f * p[e][k].z, v[e].w += f * p[e][k].w;
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int e = 0; e < PAIR; ++e)
-                            if (row0_ + e * ATTEND_WARPS < rows) finish(row0_ + e * ATTEND_WARPS, d4, v[e], m[e], l[e]);
                     }
+                    if (!bar_wait(join_bar, join_phase)) atomicOr(a.split.flags, KVC_FLAG_TIMEOUT);
+                    join_phase ^= 1;
+                    {
+                        // LANES threads a row
+                        constexpr int LANES = ATTEND_THREADS / RP;
+                        const int row = tid / LANES, at = tid % LANES;
+                        float2 *ml = (float2 *)(acc + RP * a.D) + row;
+                        float top = m;
+                        for (int32_t k = at; k < here; k += LANES)
+                            top = fmaxf(top, ml[k * (slot_floats / 2)].x);
+#pragma unroll
+                        for (int w = 1; w < LANES; w *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
+                        const float old = m == -INFINITY ? 0.0f : ex2(m - top);
+                        m = top;
+                        float add = 0.0f;
+                        for (int32_t k = at; k < here; k += LANES) {
+                            const float2 q = ml[k * (slot_floats / 2)];
+                            const bool none = q.x == -INFINITY && q.y == 0.0f;
+                            const float f = q.x == -INFINITY ? 0.0f : ex2(q.x - top);
+                            if (!none) add += f * q.y;
+                            ml[k * (slot_floats / 2)].x = none ? -1.0f : f;
+                        }
+#pragma unroll
+                        for (int w = 1; w < LANES; w *= 2) add += __shfl_xor_sync(~0u, add, w);
+                        l = l * old + add;
+                        if (at == 0) {
+                            row_scale[row] = m;
+                            stat[row * 2] = old;
+                            stat[row * 2 + 1] = l;
+                        }
+                    }
+                    __syncthreads();
+#pragma unroll
+                    for (int e = 0; e < ITEMS; ++e) {
+                        const int item = e * ATTEND_THREADS + tid, row = item / COLS, d4 = item % COLS;
+                        if (row >= rows || d4 >= D4) continue;
+                        const float old = stat[row * 2];
+                        v[e].x *= old, v[e].y *= old, v[e].z *= old, v[e].w *= old;
+                        const float *part = acc;
+#pragma unroll 8
+                        for (int32_t k = 0; k < here; ++k, part += slot_floats) {
+                            const float f = part[RP * a.D + 2 * row];
+                            const float4 p = *(const float4 *)(part + row * a.D + 4 * d4);
+                            if (f < 0.0f) continue;
+                            v[e].x += f * p.x, v[e].y += f * p.y, v[e].z += f * p.z, v[e].w += f * p.w;
+                        }
+                    }
+                    __syncthreads();
+                }
+#pragma unroll
+                for (int e = 0; e < ITEMS; ++e) {
+                    const int item = e * ATTEND_THREADS + tid, row = item / COLS, d4 = item % COLS;
+                    if (row < rows && d4 < D4) finish(row, d4, v[e], row_scale[row], stat[row * 2 + 1]);
+                }
             }
         }
         __syncthreads();

@@ -831,46 +831,23 @@ size_t kvc_latent_partial_bytes(int32_t sm_count) {
 }
 
 // Copy-engine maps of each layer's plane, as [block][token][element] in boxes of `piece` tokens
-// and 64 (values) or 32 elements. Where a block is no multiple of 8 tokens that divide a tile, or a
-// stride is more than a map holds, there are none and rows come by cp.async.
+// and 64 (values) or 32 elements. Where blocks are no multiples of 8 tokens that divide a tile, or a
+// map cannot be had, there are none and rows come by cp.async.
 static kvr_status make_maps(kvc_cache *c) {
     const int32_t B = c->d.block_size;
     const int32_t piece = std::min(B, KT);
     c->piece = 0;
     c->maps.clear();
-    if (piece < 8 || KT % piece != 0 || B % piece != 0 || c->block_stride >= (int64_t)1 << 40 ||
-        c->token_stride >= (int64_t)1 << 40)
-        return KVR_OK;
-    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, CUDART_VERSION,
-                                         cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || p == nullptr) {
-        cudaGetLastError();
-        return KVR_ERR_CUDA;
-    }
-    const Encode encode = reinterpret_cast<Encode>(p);
+    if (piece < 8 || KT % piece != 0 || B % piece != 0) return KVR_OK;
     c->maps.resize(2 * (size_t)c->d.num_layers);
     for (int32_t l = 0; l < c->d.num_layers; ++l)
         for (int k = 0; k < 2; ++k) {
-            const cuuint64_t dims[3] = {KVC_LATENT_DIM, (cuuint64_t)B, (cuuint64_t)c->d.num_blocks};
-            // (a stride of an extent of 1 is not used, but may not be zero)
-            const cuuint64_t strides[2] = {
-                (cuuint64_t)(c->token_stride > 0 ? c->token_stride : c->row_bytes),
-                (cuuint64_t)(c->block_stride > 0 ? c->block_stride : c->row_bytes)};
-            const cuuint32_t box[3] = {k == 0 ? 64u : (cuuint32_t)REST, (cuuint32_t)piece, 1};
-            const cuuint32_t steps[3] = {1, 1, 1};
-            if (encode(&c->maps[2 * (size_t)l + k], CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
-                       (void *)(uintptr_t)c->base[l], dims, strides, box, steps,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       k == 0 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-                return KVR_ERR_CUDA;
+            const uint64_t dims[3] = {KVC_LATENT_DIM, (uint64_t)B, (uint64_t)c->d.num_blocks};
+            const int64_t strides[2] = {c->token_stride, c->block_stride};
+            const uint32_t box[3] = {k == 0 ? 64u : (uint32_t)REST, (uint32_t)piece, 1};
+            if (!kvc_make_map(&c->maps[2 * (size_t)l + k], 2, 3, c->base[l], c->row_bytes, dims, strides,
+                              box, k == 0 ? 128 : 64))
+                return KVR_OK;
         }
     c->piece = piece;
     return KVR_OK;
