@@ -149,6 +149,7 @@ kvr_status kv_cache_append(const kvc_cache *cache, int32_t layer, const kvc_appe
  * A query that sees nothing (p < 0) gives out = 0 and lse = -infinity. What the cache holds at
  * places that no query of the request sees is never used, NaN included; a NaN or an infinity
  * in a value at a place that only some of a request's newest tokens see may reach the others.
+ * Weights below 2^-24 of a row's largest count as zero where the cache holds f16 or E4M3.
  * Requirements: q and out of `dtype` (the pool's type if that has 16 bits), rows contiguous,
  * every address and stride a multiple of 16 bytes; lse NULL or [R][num_new][Hq], contiguous.
  */

@@ -23,7 +23,7 @@
 // in registers by movmatrix.
 //
 // Numbers. S, the running maximum and sum, and O are fp32. P enters its product as two 16-bit
-// numbers (rounded, and the rest), so 16 bits of it count: one rounding of P alone would be as
+// numbers (the one next below, and the rest), so 15 bits of it count: one rounding of P alone would be as
 // large as that of the output. With an E4M3 cache the codes become f16 (exact), Q is scaled per
 // row by a power of two to f16 (exact but for elements 2^-14 of the row's largest), P is f16
 // alone: 11 bits against the output's rounding and the codes' 4 bits. P is scaled by 2^10 in f16
@@ -165,6 +165,17 @@ __device__ __forceinline__ void load_bytes(uint32_t dst, const void *src, uint32
     asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
+}
+
+// Two weights (>= 0) as the 16-bit numbers next below them: the rests are positive wherever the
+// weights are, so an infinite value times both parts is one infinity, not two that cancel.
+template <bool F16>
+__device__ __forceinline__ uint32_t below2(float lo, float hi) {
+    const uint32_t a = max(__float_as_uint(lo), 1u) - 1u, b = max(__float_as_uint(hi), 1u) - 1u;
+    if (!F16) return __byte_perm(a, b, 0x7632);
+    uint32_t w;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(__uint_as_float(b)), "f"(__uint_as_float(a)));
+    return w;
 }
 
 // out (16-bit), four elements of one row, from floats
@@ -465,11 +476,13 @@ attend_kernel(AttendArgs a) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const float p0 = s[k][n][2 * u], p1 = s[k][n][2 * u + 1];
-                        const uint32_t w = narrow2<C::F16>(p0, p1);
-                        ph[k][n][u] = movmatrix(w);
                         if (C::SPLIT) {
+                            const uint32_t w = below2<C::F16>(p0, p1);
                             const float2 f = widen2<C::F16>(w);
+                            ph[k][n][u] = movmatrix(w);
                             pl[k][n][u] = movmatrix(narrow2<C::F16>(p0 - f.x, p1 - f.y));
+                        } else {
+                            ph[k][n][u] = movmatrix(narrow2<C::F16>(p0, p1));
                         }
                     }
 #pragma unroll
