@@ -97,6 +97,7 @@ struct LatentArgs {
     float *lse;
     int64_t q_request, q_token, q_head, out_request, out_token, out_head;
     float *partial;
+    int32_t *prefix;          // [requests + 1], what the first block counted, for the join
     int32_t m, Hq, chunks, parts;
     KvrDiv heads;             // by Hq
     float scale;
@@ -328,6 +329,8 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
     fence_after();
     const uint32_t tmem = *(volatile uint32_t *)(smem + OFF_BARS + OFF_TMEM);
 
+    if (blockIdx.x == 0)
+        for (int32_t r = tid; r <= a.split.requests; r += THREADS) a.prefix[r] = prefix[r];
     const int32_t total = prefix[a.split.requests] * a.chunks;
     const Cut cut(total, parts_of(a, total));
     const int32_t part = blockIdx.x / 2;
@@ -783,20 +786,17 @@ constexpr int JOIN_ROWS = 4, JOIN_COLS = 32, JOIN_THREADS = JOIN_ROWS * JOIN_COL
 // pieces of 16 bytes are two whole sectors; small blocks, so that 16 rows are still 16 blocks.)
 template <bool F16>
 __global__ void __launch_bounds__(JOIN_THREADS) latent_join(const __grid_constant__ LatentArgs a) {
-    extern __shared__ int32_t join_smem[];
-    int32_t *scratch = join_smem, *prefix = join_smem + 4;
     wait_for_previous();
     let_next_start();
-    unit_prefix<KT>(a.split, KT, prefix, scratch);
-    const int32_t total = prefix[a.split.requests] * a.chunks;
+    const int32_t total = a.prefix[a.split.requests] * a.chunks;
     const Cut cut(total, parts_of(a, total));
     const int32_t M = a.m * a.Hq, groups = (min(M, ROWS) + JOIN_ROWS - 1) / JOIN_ROWS;
     const int32_t jg = blockIdx.x / groups, r = jg / a.chunks, job = jg - r * a.chunks;
     const int32_t row = (blockIdx.x % groups) * JOIN_ROWS + threadIdx.x % JOIN_ROWS;
     const int32_t rho = job * ROWS + row;
     const int32_t e4 = blockIdx.y * JOIN_COLS + threadIdx.x / JOIN_ROWS;     // 4 elements
-    const int32_t units = prefix[r + 1] - prefix[r];
-    const int32_t first = prefix[r] * a.chunks + job * units;
+    const int32_t before = a.prefix[r], units = a.prefix[r + 1] - before;
+    const int32_t first = before * a.chunks + job * units;
     const int32_t c0 = cut.part_of(first), n = cut.part_of(first + units - 1) - c0 + 1;
     if (n == 1 || rho >= M) return;
     auto slot = [&](int32_t c) { return a.partial + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * SLOT; };
@@ -880,6 +880,7 @@ kvr_status kvc_latent_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     a.out_request = p->out_request_stride, a.out_token = p->out_token_stride;
     a.out_head = p->out_head_stride;
     a.partial = c->ws.partial;
+    a.prefix = (int32_t *)c->ws.arrived;
     a.m = p->num_new, a.Hq = c->d.query_heads;
     a.heads = kvr_make_div((uint32_t)a.Hq);
     a.scale = p->scale;
@@ -897,5 +898,5 @@ kvr_status kvc_latent_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     const int64_t groups = (std::min<int64_t>(M, ROWS) + JOIN_ROWS - 1) / JOIN_ROWS;
     return kvc_launch(f16 ? latent_join<true> : latent_join<false>, a,
                       dim3((unsigned)(p->num_requests * a.chunks * groups), VALUES / 4 / JOIN_COLS),
-                      JOIN_THREADS, 4 * (4 + (size_t)p->num_requests + 1), stream);
+                      JOIN_THREADS, 0, stream);
 }
