@@ -545,8 +545,30 @@ attend_kernel(AttendArgs a) {
                 }
             }
         __syncthreads();
+        const int32_t job_index = r * HJ + job;
+        const bool whole = u0 == 0 && u1 == units;
+        const int32_t D4 = a.D / 4;
+        float *slot = a.partial + (size_t)(2 * blockIdx.x + (u0 == 0 ? 1 : 0)) * (size_t)slot_floats;
+        const float vs = POOL == KVR_DTYPE_FP8_E4M3 ? a.v_scale[h] : 1.0f;
+        // a row's maximum and sum are final: its lse, and what its accumulators are multiplied with
+        auto settle = [&](int row, float m, float l) -> float {
+            const bool some = l > 0.0f || l != l;
+            if (a.lse != nullptr) {
+                const int32_t rho = row0 + row, i = (int32_t)a.group.div((uint32_t)rho);
+                a.lse[((int64_t)r * a.m + i) * ((int64_t)a.H * a.G) + (int64_t)h * a.G + (rho - i * a.G)] =
+                    some ? (m - (C::F16 ? P_SHIFT : 0.0f) + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            }
+            return some ? vs / l : 0.0f;
+        };
+        auto finish = [&](int row, int d4, float4 v, float inv) {
+            const int32_t rho = row0 + row, i = (int32_t)a.group.div((uint32_t)rho);
+            v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+            unsigned char *to = a.out + r * a.out_request + i * a.out_token +
+                                ((int64_t)h * a.G + (rho - i * a.G)) * a.out_head;
+            *(uint2 *)(to + d4 * 8) = a.f16 ? narrow4<true>(v) : narrow4<false>(v);
+        };
         // each row's maximum and sum, and the warps' weights in place of their maxima
-        if (tid < RP) {
+        if (tid < rows) {
             float m = -INFINITY, l = 0.0f;
 #pragma unroll
             for (int w = 0; w < ATTEND_WARPS; ++w) m = fmaxf(m, stat[(w * RP + tid) * 2]);
@@ -559,28 +581,13 @@ attend_kernel(AttendArgs a) {
                 l += none ? 0.0f : f * lw;
                 stat[(w * RP + tid) * 2] = none ? -1.0f : f;
             }
-            row_scale[tid] = m;
-            stat[tid * 2 + 1] = l;
+            if (whole)
+                row_scale[tid] = settle(tid, m, l);
+            else
+                __stcg((float2 *)(slot + RP * a.D) + tid, make_float2(m, l));
         }
         __syncthreads();
-        const int32_t job_index = r * HJ + job;
-        const bool whole = u0 == 0 && u1 == units;
-        const int32_t D4 = a.D / 4;
-        float *slot = a.partial + (size_t)(2 * blockIdx.x + (u0 == 0 ? 1 : 0)) * (size_t)slot_floats;
-        const float vs = POOL == KVR_DTYPE_FP8_E4M3 ? a.v_scale[h] : 1.0f;
-        auto finish = [&](int row, int d4, float4 v, float m, float l) {
-            const int32_t rho = row0 + row;
-            const int32_t i = (int32_t)a.group.div((uint32_t)rho), gq = rho - i * a.G;
-            const int64_t hq = (int64_t)h * a.G + gq;
-            const bool some = l > 0.0f || l != l;
-            const float inv = some ? vs / l : 0.0f;
-            v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-            unsigned char *to = a.out + r * a.out_request + i * a.out_token + hq * a.out_head;
-            *(uint2 *)(to + d4 * 8) = a.f16 ? narrow4<true>(v) : narrow4<false>(v);
-            if (d4 == 0 && a.lse != nullptr)
-                a.lse[((int64_t)r * a.m + i) * ((int64_t)a.H * a.G) + hq] =
-                    some ? (m - (C::F16 ? P_SHIFT : 0.0f) + log2f(l)) * 0.6931471805599453f : -INFINITY;
-        };
+#pragma unroll 2
         for (int row = warp; row < rows; row += ATTEND_WARPS)
             for (int d4 = lane; d4 < D4; d4 += 32) {
                 float4 v = make_float4(0, 0, 0, 0);
@@ -591,30 +598,28 @@ attend_kernel(AttendArgs a) {
                     if (f < 0.0f) continue;
                     v.x += f * p.x, v.y += f * p.y, v.z += f * p.z, v.w += f * p.w;
                 }
-                const float m = row_scale[row], l = stat[row * 2 + 1];
-                if (whole) {
-                    finish(row, d4, v, m, l);
-                } else {
-                    __stcg((float4 *)(slot + (size_t)row * a.D) + d4, v);
-                    if (d4 == 0) __stcg((float2 *)(slot + (size_t)RP * a.D) + row, make_float2(m, l));
-                }
+                if (whole)
+                    finish(row, d4, v, row_scale[row]);
+                else
+                    __stcg((float4 *)(slot + row * a.D) + d4, v);
             }
         if (!whole) {
             // the job's parts: the blocks that hold its first and its last unit, and all between
             const int32_t c0 = cut.part_of(seg.job_first);
             const int32_t n = cut.part_of(seg.job_first + units - 1) - c0 + 1;
-            __threadfence();
             __syncthreads();
             if (tid == 0) {
+                // (fences by one thread cover what the barriers order before and after it)
+                __threadfence();
                 const uint32_t before = atomicAdd(a.arrived + job_index, 1u);
                 shared_int[0] = before == (uint32_t)(n - 1);
                 if (before == (uint32_t)(n - 1)) a.arrived[job_index] = 0;
+                __threadfence();
             }
             __syncthreads();
             if (shared_int[0]) {
                 // the last to come joins them, in the order of the keys: as many parts at a time as
                 // the ring holds, each one copy; their weights, then the weighted sums
-                __threadfence();
                 constexpr int COLS = DP / 4, ITEMS = RP * COLS / ATTEND_THREADS;
                 static_assert(RP * COLS % ATTEND_THREADS == 0 && RP <= ATTEND_THREADS, "");
                 const int32_t slot_bytes = slot_floats * 4;
@@ -664,9 +669,8 @@ attend_kernel(AttendArgs a) {
                         for (int w = 1; w < LANES; w *= 2) add += __shfl_xor_sync(~0u, add, w);
                         l = l * old + add;
                         if (at == 0) {
-                            row_scale[row] = m;
                             stat[row * 2] = old;
-                            stat[row * 2 + 1] = l;
+                            if (k0 + batch >= n && row < rows) row_scale[row] = settle(row, m, l);
                         }
                     }
                     __syncthreads();
@@ -690,7 +694,7 @@ attend_kernel(AttendArgs a) {
 #pragma unroll
                 for (int e = 0; e < ITEMS; ++e) {
                     const int item = e * ATTEND_THREADS + tid, row = item / COLS, d4 = item % COLS;
-                    if (row < rows && d4 < D4) finish(row, d4, v[e], row_scale[row], stat[row * 2 + 1]);
+                    if (row < rows && d4 < D4) finish(row, d4, v[e], row_scale[row]);
                 }
             }
         }
