@@ -55,6 +55,11 @@ struct AttendArgs {
 
 constexpr int ATTEND_WARPS = 4;
 constexpr int ATTEND_THREADS = 32 * ATTEND_WARPS;
+// A part has LEAST units at least, but in jobs that have fewer: each part costs its job a share of
+// the join. Parts of 1, 2, 4 and 8 units (us): one request of 4096 keys, 8 heads of 8 queries,
+// 15.7, 12.7, 11.6, 14.0; its 4 newest tokens 62, 39, 31, 32; 16 requests of 512 keys 15.8, 15.5,
+// 12.7, 11.8; one of 1024 keys 8.0, 8.1, 9.4, 11.8.
+constexpr int LEAST = 4;
 constexpr float P_SHIFT = 10.0f;      // log2 of P's scale in f16
 
 template <int DP, int POOL, int NT>
@@ -210,7 +215,7 @@ attend_kernel(AttendArgs a) {
     unit_prefix<C::UNIT>(a.split, KT, prefix, shared_int);
     const int32_t HJ = a.H * a.chunks;
     const int32_t total = prefix[a.split.requests] * HJ;
-    const Cut cut(total, min((int32_t)gridDim.x, total));
+    const Cut cut(total, min((int32_t)gridDim.x, max(total / LEAST, a.split.requests * HJ)));
     if ((int32_t)blockIdx.x >= cut.parts) return;
     int32_t x = cut.start(blockIdx.x);
     const int32_t x_end = cut.start(blockIdx.x + 1);
