@@ -5,16 +5,17 @@
 // and 16-bit elements there are 8 flops a byte of cache, 1/30 of what the card can do.
 //
 // Split. The keys of all (request, head) JOBS, in UNITS of 4 KT keys, form one line that is cut
-// into equal parts, one a resident block, whatever the lengths are; each block works the prefix
-// sums of the lengths out by itself, so that the lengths can stay on the device. A part of a
-// job that is not the whole of it leaves (max, sum, accumulator) in the workspace, and the last
-// of the job's blocks to arrive joins them, in the order of the keys: results do not depend on
-// who is last.
+// into equal parts, one a resident block, whatever the lengths are (two and three times as many
+// parts: 71 and 75 us where one takes 52, as each part begins with an empty ring and ends with a
+// share of a join); each block works the prefix sums of the lengths out by itself, so that the
+// lengths can stay on the device. A part of a job that is not the whole of it leaves (max, sum,
+// accumulator) in the workspace, and the last of the job's blocks to arrive copies all of them
+// into its ring and joins them, in the order of the keys: results do not depend on who is last.
 //
 // Inside a block each of 4 warps takes every fourth tile of KT keys and keeps its own ring of
-// STAGES tiles filled by 16-byte cp.async: nothing in the loop waits for another warp. Rows of
-// padding (beyond the length, or beyond D) are written as zeros, so that what the pool holds
-// there never meets the arithmetic.
+// STAGES tiles filled by 16-byte cp.async: nothing in the loop waits for another warp. (The copy
+// engine's boxes took 57 us where these take 53.) Rows of padding (beyond the length, or beyond
+// D) are written as zeros, so that what the pool holds there never meets the arithmetic.
 //
 // Products. S^T = K Q^T and O^T += V^T P^T by mma.sync m16n8k16 with keys (then head elements)
 // as the 16 rows and the queries as the 8 columns: with M = 8 nothing is padded, where 128-row
@@ -28,6 +29,12 @@
 // row by a power of two to f16 (exact but for elements 2^-14 of the row's largest), P is f16
 // alone: 11 bits against the output's rounding and the codes' 4 bits. P is scaled by 2^10 in f16
 // so that weights down to 2^-24 of the largest are normal numbers.
+//
+// Measured, 8 key heads of 128 under 64 queries: one request of 65536 keys, bf16 (268 MB) 52.5 us,
+// 5.1 TB/s; 131072 keys in E4M3 (268 MB) 58 to 61 us; 64 requests of 8192 keys (2.1 GB) 6.5 TB/s,
+// 95 % of a plain copy's rate. What is lost below that is fixed: 7 us from the launch to the first
+// keys (lengths, block ids, keys, each after the one before), 6 to 9 us from the first block's end
+// to the last's, as not all SMs are as near to all of HBM, and 3 to 8 us of joining.
 #pragma once
 
 #include <math.h>

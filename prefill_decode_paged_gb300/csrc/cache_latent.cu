@@ -10,18 +10,19 @@
 // leaves no room for S. So two SMs share a tile of KT keys, each with HALF OF THE ELEMENTS (256
 // of the value and 32 of the rest): each loads its half of every latent, and nothing twice; each
 // computes the partial S = Q K^T of its half and sends it to the other through distributed
-// shared memory (32 KB a tile); each adds the two halves in the same way, so both hold the same
+// shared memory (16 KB a tile); each adds the two halves in the same way, so both hold the same
 // softmax, and multiplies P with its 256 value elements. No product and no load is done twice;
 // the exponentials are.
 //
 // Tensor memory: O [128 x 256] fp32 in columns 0-255; Q, 288 16-bit elements a row, in 144
 // columns, where the products read it as operand A (from shared memory it would take 72 KB of it
-// and cost more of its bandwidth than all of K); S of KT = 64 columns, and P of 32. That is 496
-// of 512. One S is enough, as S of the next tile is computed once this tile's is in registers;
-// tiles of 32 keys with two S and two P took 1.8 times as long, for the time from a tile's S to
-// its P, through the other SM and back, is nearly the same for 32 keys.
+// and cost more of its bandwidth than all of K); three S of KT = 32 columns, and one P of 16:
+// all 512. What a tile waits for is the way from its S to its P, through the other SM and
+// back, so the number of S under way counts for more than their size: tiles of 64 keys, which
+// leave room for one S, took 210 us where these take 165; 48 keys with P over S 540; a second P,
+// with part of Q in shared memory instead, 181.
 //
-// Shared memory: a ring of 4 tiles' halves (36 KB each), and two times the half of S that the
+// Shared memory: a ring of 9 tiles' halves (18 KB each), and three times the half of S that the
 // other SM sends. A tile is laid out in 128-byte rows of 64 elements (swizzled), which serve as
 // the K-major operand of S and as the MN-major operand of O. Tiles come by the copy engine, in
 // boxes of a block's tokens, where blocks are multiples of 8 tokens that divide a tile or are
@@ -29,20 +30,27 @@
 // row by 16-byte cp.async, with zeros for the rows beyond the length. (By cp.async alone the load
 // and store units were what the kernel waited for.)
 //
-// Warps: three times 4 of softmax (one thread a row; every third tile), 4 that send S to the other
-// SM, 4 of loads, 3 that issue the products, 1 that tells the other SM what it may send over.
-// With one set of softmax warps that also sent, they were busy for 2100 cycles a tile, of which
-// HBM wants 780. A tile's softmax needs of the one
-// before only what P is relative to, which goes through shared memory as soon as it is known.
-// O is rescaled only when a row's maximum outgrows by 2^40 (f16: 2^8) the one that its P is
-// relative to, which hardly happens after the first tiles of a job: powers of two cost no
-// precision in P, O and the sums.
+// Warps: two times 4 of softmax (one thread a row; every second tile), 4 that send S to the other
+// SM, 4 of loads, 2 that issue the products of S and 1 those of O, 1 that tells the other SM what
+// it may send over. One tile's softmax takes its 4 warps about 1700 cycles, and HBM wants a tile
+// in 780, so one set is too few; a third (177 us) only shares the SM's issue slots with the
+// others. A tile's softmax needs of the one before only what P is relative to, which goes through
+// shared memory as soon as it is known. O is rescaled only when a row's maximum outgrows by 2^40
+// (f16: 2^8) the one that its P is relative to, which hardly happens after the first tiles of a
+// job: powers of two cost no precision in P, O and the sums.
 //
 // Numbers: S, maxima, sums, O and all joins are fp32. P is rounded once to the pool's 16-bit type
 // for its product: rounding it twice as fine would cost half of the products again.
 //
 // Every wait ends: after two seconds it gives up and flags KVC_FLAG_TIMEOUT, and its warp goes to
 // the end of the kernel, as the others do for want of it.
+//
+// Measured, with the join: 64 requests of 1024 to 16384 latents, 128 heads, bf16 (528,481
+// latents, 627 MB and 147 GFLOP): 165 us, 3.8 TB/s and 0.89 PFLOP/s, 56 % of what HBM alone would
+// allow. A tile of 32 keys comes through in about 1000 cycles, which is the softmax and the way
+// of S through the other SM; each change of job costs about 8 us of 262 KB of partial results and
+// an empty pipe, and the join 8 us. One request of 4096 latents with 16 heads: 13.8 us, its fill,
+// four tiles and the join one after another.
 #include <math.h>
 
 #include <algorithm>
@@ -64,7 +72,7 @@ constexpr int SBUF = 3;                   // halves of S at a time, own and rece
 constexpr int CHUNK = KT * 128;           // 64 elements of each key
 constexpr int STAGE = 4 * CHUNK + KT * 64;
 constexpr int XBUF = ROWS * KT * 4;
-// warps: softmax of every third tile (3 x 4), sending, loading (4 each); products of S of even
+// warps: softmax of every second tile (2 x 4), sending, loading (4 each); products of S of even
 // tiles, of odd tiles, of O; telling
 constexpr int SOFT = 2, SEND = 4 * SOFT, LOAD = SEND + 4, KEYS = LOAD + 4, VALS = KEYS + 2,
               TELL = VALS + 1, WARPS = TELL + 1, THREADS = 32 * WARPS;
@@ -352,10 +360,10 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
     };
 
     if (warp < SEND) {
-        // ---- softmax of every third tile ----
+        // ---- softmax of every second tile ----
         const uint32_t group = warp / 4;
         const uint64_t sc2 = splat2(a.scale * 1.4426950408889634f);
-        // what a row's P is relative to after a tile: (maximum, tile + 1) by tile % 3 and row. One
+        // what a row's P is relative to after a tile: (maximum, tile + 1) by tile % SOFT and row. One
         // 64-bit word, so that whoever sees the number sees its maximum too
         const uint32_t tops = smem0 + OFF_TOPS + row * 8;
         float *sums = (float *)(smem + OFF_SUMS);     // [2][SOFT][ROWS]
@@ -459,7 +467,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
             if (!ok) break;
             it += n;
 
-            // the segment's maximum and sum, then its O: each third of the warps has a third of the
+            // the segment's maximum and sum, then its O: each set of warps has its share of the
             // columns
             const uint32_t last = it - 1;
             float top;
@@ -779,41 +787,104 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
 
 // -- joining the parts ------------------------------------------------------------
 
-constexpr int JOIN_ROWS = 4, JOIN_COLS = 32, JOIN_THREADS = JOIN_ROWS * JOIN_COLS;
+constexpr int JOIN_ROWS = 4, JOIN_COLS = 32, JOIN_SET = JOIN_ROWS * JOIN_COLS;
+constexpr int JOIN_GRID = VALUES / 4 / JOIN_COLS, JOIN_RESIDENT = 1024;   // of an SM's threads
+constexpr int PARTS_MOST = 128;           // clusters of the attention kernel
 
 // One block a job, 4 of its rows and 128 of their elements: the parts' accumulators weighted by
-// their maxima, in the order of the keys. Jobs that one part did whole are not touched. (Four rows'
-// pieces of 16 bytes are two whole sectors; small blocks, so that 16 rows are still 16 blocks.)
-template <bool F16>
-__global__ void __launch_bounds__(JOIN_THREADS) latent_join(const __grid_constant__ LatentArgs a) {
+// their maxima, in an order that depends on the lengths alone. Jobs that one part did whole are
+// not touched. (Four rows' pieces of 16 bytes are two whole sectors; small blocks, so that 16 rows
+// are still 16 blocks.) It is the latency of few loads that it waits for, so the statistics of
+// all parts are asked for at once, the first accumulators before they are there, and SETS sets of
+// threads take every SETS-th part: as many as the SMs hold at once, and as have two parts each.
+// With 1, 2, 4 and 8 sets the whole attention took (us, * the choice) 20.8, 17.0, 14.6, 13.8* for
+// one request of 4096 latents and 16 heads; 59.7, 46.2, 39.0, 36.1* for one of 65536 and 128
+// heads; 57.6, 54.8*, 55.7, 63.1 for 4 of 32768; 41.9*, 45.1, 53.9, 78.5 for 16 of 4096.
+template <bool F16, int SETS>
+__global__ void __launch_bounds__(JOIN_SET * SETS) latent_join(const __grid_constant__ LatentArgs a) {
+    constexpr int AHEAD = SETS == 1 ? 4 : 8;           // parts that a thread asks for at a time
+    __shared__ float weights[PARTS_MOST][JOIN_ROWS];   // a part's share of a row; below 0: has none
+    __shared__ float2 warp_stat[JOIN_SET * SETS / 32][JOIN_ROWS];
+    __shared__ float4 sums[SETS > 1 ? SETS - 1 : 1][JOIN_SET];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, set = tid / JOIN_SET;
+    const int jr = tid % JOIN_ROWS;
     wait_for_previous();
     let_next_start();
     const int32_t total = a.prefix[a.split.requests] * a.chunks;
     const Cut cut(total, parts_of(a, total));
     const int32_t M = a.m * a.Hq, groups = (min(M, ROWS) + JOIN_ROWS - 1) / JOIN_ROWS;
     const int32_t jg = blockIdx.x / groups, r = jg / a.chunks, job = jg - r * a.chunks;
-    const int32_t row = (blockIdx.x % groups) * JOIN_ROWS + threadIdx.x % JOIN_ROWS;
+    const int32_t row = (blockIdx.x % groups) * JOIN_ROWS + jr;
     const int32_t rho = job * ROWS + row;
-    const int32_t e4 = blockIdx.y * JOIN_COLS + threadIdx.x / JOIN_ROWS;     // 4 elements
+    const int32_t e4 = blockIdx.y * JOIN_COLS + tid % JOIN_SET / JOIN_ROWS;     // 4 elements
     const int32_t before = a.prefix[r], units = a.prefix[r + 1] - before;
     const int32_t first = before * a.chunks + job * units;
     const int32_t c0 = cut.part_of(first), n = cut.part_of(first + units - 1) - c0 + 1;
-    if (n == 1 || rho >= M) return;
+    if (n == 1) return;
+    const bool mine = rho < M;
     auto slot = [&](int32_t c) { return a.partial + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * SLOT; };
-    auto stat = [&](int32_t c) { return __ldcg((const float2 *)(slot(c) + (size_t)ROWS * VALUES) + row); };
-    float m = -INFINITY, l = 0.0f;
-    float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-    for (int32_t c = 0; c < n; ++c) m = fmaxf(m, stat(c).x);
-#pragma unroll 8
-    for (int32_t c = 0; c < n; ++c) {
-        const float2 ml = stat(c);
-        const float4 p = __ldcg((const float4 *)slot(c) + (size_t)e4 * ROWS + row);
-        if (ml.x == -INFINITY && ml.y == 0.0f) continue;
-        const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
-        l += f * ml.y;
-        v.x += f * p.x, v.y += f * p.y, v.z += f * p.z, v.w += f * p.w;
+
+    float4 p[AHEAD];
+    auto ask = [&](int32_t c1) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (mine && c1 + k * SETS < n)
+                p[k] = __ldcg((const float4 *)slot(c1 + k * SETS) + (size_t)e4 * ROWS + row);
+    };
+    // one part and row a thread: (max, sum), then the rows' maxima and sums over all parts
+    constexpr int TURN = JOIN_SET * SETS / JOIN_ROWS, TURNS = (PARTS_MOST + TURN - 1) / TURN;
+    float2 ml[TURNS];
+#pragma unroll
+    for (int k = 0; k < TURNS; ++k) {
+        const int32_t c = tid / JOIN_ROWS + k * TURN;
+        ml[k] = make_float2(-INFINITY, 0.0f);
+        if (mine && c < n) ml[k] = __ldcg((const float2 *)(slot(c) + (size_t)ROWS * VALUES) + row);
     }
+    ask(set);
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < TURNS; ++k) m = fmaxf(m, ml[k].x);
+#pragma unroll
+    for (int o = JOIN_ROWS; o < 32; o *= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    if (lane < JOIN_ROWS) warp_stat[warp][jr].x = m;
+    __syncthreads();
+    for (int w = 0; w < JOIN_SET * SETS / 32; ++w) m = fmaxf(m, warp_stat[w][jr].x);
+#pragma unroll
+    for (int k = 0; k < TURNS; ++k) {
+        const int32_t c = tid / JOIN_ROWS + k * TURN;
+        const bool some = !(ml[k].x == -INFINITY && ml[k].y == 0.0f);
+        const float f = ml[k].x == -INFINITY ? 0.0f : ex2(ml[k].x - m);
+        if (some) l += f * ml[k].y;
+        if (c < n) weights[c][jr] = some ? f : -1.0f;
+    }
+#pragma unroll
+    for (int o = JOIN_ROWS; o < 32; o *= 2) l += __shfl_xor_sync(~0u, l, o);
+    if (lane < JOIN_ROWS) warp_stat[warp][jr].y = l;
+    __syncthreads();
+
+    float4 v = make_float4(0, 0, 0, 0);
+    for (int32_t c1 = set; c1 < n; c1 += AHEAD * SETS) {
+        if (c1 != set) ask(c1);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int32_t c = c1 + k * SETS;
+            const float f = c < n && mine ? weights[c][jr] : -1.0f;
+            if (f < 0.0f) continue;
+            v.x += f * p[k].x, v.y += f * p[k].y, v.z += f * p[k].z, v.w += f * p[k].w;
+        }
+    }
+    if (SETS > 1) {
+        if (set > 0) sums[set - 1][tid % JOIN_SET] = v;
+        __syncthreads();
+        if (set > 0) return;
+        for (int k = 0; k < SETS - 1; ++k) {
+            const float4 w = sums[k][tid];
+            v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+        }
+    }
+    if (!mine) return;
+    l = 0.0f;
+    for (int w = 0; w < JOIN_SET * SETS / 32; ++w) l += warp_stat[w][jr].y;
     const bool some = l > 0.0f || l != l;
     const float inv = some ? 1.0f / l : 0.0f;
     const int32_t token = (int32_t)a.heads.div((uint32_t)rho), hq = rho - token * a.Hq;
@@ -823,6 +894,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) latent_join(const __grid_constan
         a.lse[((int64_t)r * a.m + token) * a.Hq + hq] =
             some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
+
+constexpr void (*JOINS[2][4])(LatentArgs) = {
+    {latent_join<false, 1>, latent_join<false, 2>, latent_join<false, 4>, latent_join<false, 8>},
+    {latent_join<true, 1>, latent_join<true, 2>, latent_join<true, 4>, latent_join<true, 8>}};
 
 }  // namespace
 
@@ -861,6 +936,13 @@ kvr_status kvc_latent_setup(kvc_cache *c) {
             cudaGetLastError();
             return KVR_ERR_CUDA;
         }
+    cudaFuncAttributes loaded;            // now, and not while a stream is captured
+    for (const auto &of_type : JOINS)
+        for (auto k : of_type)
+            if (cudaFuncGetAttributes(&loaded, k) != cudaSuccess) {
+                cudaGetLastError();
+                return KVR_ERR_CUDA;
+            }
     return make_maps(c);
 }
 
@@ -888,7 +970,8 @@ kvr_status kvc_latent_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     a.chunks = (int32_t)((M + ROWS - 1) / ROWS);
     const int64_t most = ((int64_t)p->table.width * c->d.block_size + KT - 1) / KT + 1;
     if (most * p->num_requests * a.chunks > INT32_MAX) return KVR_ERR_UNSUPPORTED;
-    a.parts = (int32_t)std::min<int64_t>(std::max(kvc_stream_sms(c, stream) / 2, 1),
+    const int32_t sms = kvc_stream_sms(c, stream);
+    a.parts = (int32_t)std::min<int64_t>(std::clamp(sms / 2, 1, PARTS_MOST),
                                          most * p->num_requests * a.chunks);
     const bool f16 = c->d.dtype == KVC_DTYPE_F16;
     const size_t smem = OFF_PREFIX + 4 * (size_t)(p->num_requests + 1);
@@ -896,7 +979,10 @@ kvr_status kvc_latent_launch(const kvc_cache *c, int32_t layer, const kvc_attend
                                      dim3((unsigned)(2 * a.parts)), THREADS, smem, stream, 2);
     if (st != KVR_OK) return st;
     const int64_t groups = (std::min<int64_t>(M, ROWS) + JOIN_ROWS - 1) / JOIN_ROWS;
-    return kvc_launch(f16 ? latent_join<true> : latent_join<false>, a,
-                      dim3((unsigned)(p->num_requests * a.chunks * groups), VALUES / 4 / JOIN_COLS),
-                      JOIN_THREADS, 0, stream);
+    const int64_t jobs = (int64_t)p->num_requests * a.chunks, blocks = jobs * groups * JOIN_GRID;
+    // parts of a job, on average at most: lengths are known on the device alone
+    const int64_t parts = std::min<int64_t>(a.parts, most * jobs / LEAST) / jobs;
+    int k = 0;
+    while (k < 3 && (4 << k) <= parts && (blocks * JOIN_SET * 2 << k) <= (int64_t)sms * JOIN_RESIDENT) ++k;
+    return kvc_launch(JOINS[f16][k], a, dim3((unsigned)(jobs * groups), JOIN_GRID), JOIN_SET << k, 0, stream);
 }
