@@ -37,7 +37,7 @@ struct KvcWorkspace {
     float *scales;            // [L][C][H] (E4M3 pools)
     float *partial;           // attend: accumulators of key ranges that another part finishes
     uint32_t *arrived;        // attend: parts of a job that are done, zero between launches; latents:
-                              // units before each request, from the products to the join
+                              // units and parts before each request, from the products to the join
     uint32_t *flags;          // KVC_FLAG_* found by the kernels
 };
 

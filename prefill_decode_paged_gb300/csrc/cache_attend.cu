@@ -30,7 +30,7 @@ size_t kvc_attend_partial_bytes(const kvc_desc &d, int32_t sm_count) {
 }
 
 size_t kvc_attend_jobs(const kvc_desc &d) {
-    if (d.num_components == 1) return (size_t)d.max_requests + 1;   // latents: the units before each request
+    if (d.num_components == 1) return 2 * ((size_t)d.max_requests + 1);   // latents: units and parts before each request
     const int64_t M = (int64_t)d.max_new * (d.query_heads / d.kv_heads);
     return (size_t)d.max_requests * d.kv_heads * (size_t)ceil_div(M, 8);
 }

@@ -62,11 +62,13 @@ struct AttendArgs {
 
 constexpr int ATTEND_WARPS = 4;
 constexpr int ATTEND_THREADS = 32 * ATTEND_WARPS;
-// A part has LEAST units at least, but in jobs that have fewer: each part costs its job a share of
-// the join. Parts of 1, 2, 4 and 8 units (us): one request of 4096 keys, 8 heads of 8 queries,
+// Units that a part has at least, and that a change of job costs (cache_split.cuh). Parts of 1, 2, 4 and 8 units (us): one request of 4096 keys, 8 heads of 8 queries,
 // 15.7, 12.7, 11.6, 14.0; its 4 newest tokens 62, 39, 31, 32; 16 requests of 512 keys 15.8, 15.5,
-// 12.7, 11.8; one of 1024 keys 8.0, 8.1, 9.4, 11.8.
-constexpr int LEAST = 4;
+// 12.7, 11.8; one of 1024 keys 8.0, 8.1, 9.4, 11.8. Parts within jobs took 49.1 where equal ones took
+// 52.1 (4 requests of 32768 keys, 4 heads), 27.4 for 33.3 (8 of 16 to 8192, 8 heads), 23.8 for 26.7
+// (48 of a window of 1024, 32 rows), and with a group 5 above the equal parts' 48.6 for 51.5 (8 of
+// 8192, 8 heads); where nothing was to be gained 0.3 to 0.8 more.
+constexpr int LEAST = 4, SLACK = 8;
 constexpr float P_SHIFT = 10.0f;      // log2 of P's scale in f16
 
 template <int DP, int POOL, int NT>
@@ -88,8 +90,9 @@ struct Attend {
     static constexpr int Q_BYTES = RP * DP * 2;
     static_assert(ATTEND_WARPS * RP * PITCH * 4 <= RING, "the join reuses the ring");
     // ring, queries, a barrier, then floats: row scales [RP], per-warp statistics [4][RP][2]; 4 ints;
-    // then prefix
-    static constexpr int FIXED = RING + Q_BYTES + 16 + 4 * RP + 4 * ATTEND_WARPS * RP * 2 + 16;
+    // then ahead and prefix
+    static constexpr int FIXED = RING + Q_BYTES + 16 + 4 * RP + 4 * ATTEND_WARPS * RP * 2 + 16 +
+                                 4 * (AHEAD_MOST + 4);
     static constexpr size_t smem(int32_t requests) { return FIXED + 4 * (size_t)(requests + 1); }
 };
 
@@ -208,7 +211,8 @@ attend_kernel(AttendArgs a) {
     float *row_scale = (float *)(q_smem + C::Q_BYTES + 16);
     float *stat = row_scale + RP;                       // [warp][RP][max, sum]
     int32_t *shared_int = (int32_t *)(stat + ATTEND_WARPS * RP * 2);   // [4]
-    int32_t *prefix = shared_int + 4;                   // [requests + 1], in units of one job
+    int32_t *ahead = shared_int + 4;                    // [AHEAD_MOST + 1]
+    int32_t *prefix = ahead + AHEAD_MOST + 4;           // [requests + 1], in units of one job
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
 
     if (tid == 0) {
@@ -222,10 +226,13 @@ attend_kernel(AttendArgs a) {
     unit_prefix<C::UNIT>(a.split, KT, prefix, shared_int);
     const int32_t HJ = a.H * a.chunks;
     const int32_t total = prefix[a.split.requests] * HJ;
-    const Cut cut(total, min((int32_t)gridDim.x, max(total / LEAST, a.split.requests * HJ)));
-    if ((int32_t)blockIdx.x >= cut.parts) return;
-    int32_t x = cut.start(blockIdx.x);
-    const int32_t x_end = cut.start(blockIdx.x + 1);
+    const Cut cut(total, a.split.requests, HJ, (int32_t)gridDim.x, LEAST, SLACK);
+    if (cut.group > 0) {
+        if (warp == 0) cut.count(prefix, a.split.requests, ahead);
+        __syncthreads();
+    }
+    int32_t x, x_end;
+    cut.units_of(blockIdx.x, prefix, ahead, a.split.requests, HJ, &x, &x_end);
 
     const int32_t M = a.m * a.G;
     const int32_t slot_floats = RP * (a.D + 2);
@@ -617,8 +624,8 @@ attend_kernel(AttendArgs a) {
             }
         if (!whole) {
             // the job's parts: the blocks that hold its first and its last unit, and all between
-            const int32_t c0 = cut.part_of(seg.job_first);
-            const int32_t n = cut.part_of(seg.job_first + units - 1) - c0 + 1;
+            int32_t c0, n;
+            cut.parts_of(r, job, seg.job_first, units, ahead, HJ, &c0, &n);
             __syncthreads();
             if (tid == 0) {
                 // (fences by one thread cover what the barriers order before and after it)

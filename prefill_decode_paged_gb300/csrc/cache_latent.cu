@@ -78,7 +78,8 @@ constexpr int SOFT = 2, SEND = 4 * SOFT, LOAD = SEND + 4, KEYS = LOAD + 4, VALS 
               TELL = VALS + 1, WARPS = TELL + 1, THREADS = 32 * WARPS;
 constexpr int OFF_XBUF = STAGES * STAGE, OFF_BARS = OFF_XBUF + SBUF * XBUF, OFF_TOPS = OFF_BARS + 768,
               OFF_SUMS = OFF_TOPS + SOFT * ROWS * 8,
-              OFF_PREFIX = OFF_SUMS + 2 * SOFT * ROWS * 4;
+              OFF_AHEAD = OFF_SUMS + 2 * SOFT * ROWS * 4,
+              OFF_PREFIX = OFF_AHEAD + 4 * (AHEAD_MOST + 4);
 constexpr uint32_t COL_O = 0, COL_Q = 256, COL_S = 400, COL_P = COL_S + SBUF * KT;
 static_assert(COL_P + KT / 2 <= 512, "tensor memory");
 constexpr int VALUES = KVC_LATENT_VALUES;
@@ -105,7 +106,7 @@ struct LatentArgs {
     float *lse;
     int64_t q_request, q_token, q_head, out_request, out_token, out_head;
     float *partial;
-    int32_t *prefix;          // [requests + 1], what the first block counted, for the join
+    int32_t *prefix, *ahead;  // [requests + 1], what the first block counted, for the join
     int32_t m, Hq, chunks, parts;
     KvrDiv heads;             // by Hq
     float scale;
@@ -274,10 +275,13 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return d;
 }
 
-// A part has LEAST tiles at least: each costs the others a share of the join.
-constexpr int LEAST = 4;
-__device__ __forceinline__ int32_t parts_of(const LatentArgs &a, int32_t total) {
-    return max(1, min(a.parts, total / LEAST));
+// Units (tiles) that a part has at least, and that a change of job costs (cache_split.cuh). Parts
+// within jobs took (us) 37.6 where equal ones took 41.7 (8 requests of 8192 latents, 128 heads), 25.3
+// for 28.8 (2 of 8192), 21.3 for 23.0 (9 of up to 6001, 32 rows); groups 10 above the equal parts 39.9
+// for 34.7 (19 of 4096, 64 heads).
+constexpr int LEAST = 4, SLACK = 8;
+__device__ __forceinline__ Cut cut_of(const LatentArgs &a, const int32_t *prefix) {
+    return Cut(prefix[a.split.requests] * a.chunks, a.split.requests, a.chunks, a.parts, LEAST, SLACK);
 }
 
 // -- the kernel -------------------------------------------------------------------
@@ -292,7 +296,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
     constexpr float GROWTH = GROWTH_OF<F16>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t smem0 = smem_addr(smem), bars = smem0 + OFF_BARS;
-    int32_t *prefix = (int32_t *)(smem + OFF_PREFIX);
+    int32_t *prefix = (int32_t *)(smem + OFF_PREFIX), *ahead = (int32_t *)(smem + OFF_AHEAD);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     uint32_t rank;
     asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
@@ -332,18 +336,22 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
     wait_for_previous();
     let_next_start();
     unit_prefix<KT>(a.split, KT, prefix, (int32_t *)(smem + OFF_BARS + OFF_SCRATCH));
+    const Cut cut = cut_of(a, prefix);
+    if (warp == KEYS && cut.group > 0) cut.count(prefix, a.split.requests, ahead);
+    __syncwarp();
     fence_before();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     fence_after();
     const uint32_t tmem = *(volatile uint32_t *)(smem + OFF_BARS + OFF_TMEM);
 
     if (blockIdx.x == 0)
-        for (int32_t r = tid; r <= a.split.requests; r += THREADS) a.prefix[r] = prefix[r];
-    const int32_t total = prefix[a.split.requests] * a.chunks;
-    const Cut cut(total, parts_of(a, total));
+        for (int32_t r = tid; r <= a.split.requests; r += THREADS) {
+            a.prefix[r] = prefix[r];
+            if (cut.group > 0) a.ahead[r] = ahead[r];
+        }
     const int32_t part = blockIdx.x / 2;
-    int32_t x = part < cut.parts ? cut.start(part) : 0;
-    const int32_t x_end = part < cut.parts ? cut.start(part + 1) : 0;
+    int32_t x, x_end;
+    cut.units_of(part, prefix, ahead, a.split.requests, a.chunks, &x, &x_end);
     const int32_t M = a.m * a.Hq;
 
     // a thread's query row in a segment: lane of tensor memory, row of the pass
@@ -810,8 +818,7 @@ __global__ void __launch_bounds__(JOIN_SET * SETS) latent_join(const __grid_cons
     const int jr = tid % JOIN_ROWS;
     wait_for_previous();
     let_next_start();
-    const int32_t total = a.prefix[a.split.requests] * a.chunks;
-    const Cut cut(total, parts_of(a, total));
+    const Cut cut = cut_of(a, a.prefix);
     const int32_t M = a.m * a.Hq, groups = (min(M, ROWS) + JOIN_ROWS - 1) / JOIN_ROWS;
     const int32_t jg = blockIdx.x / groups, r = jg / a.chunks, job = jg - r * a.chunks;
     const int32_t row = (blockIdx.x % groups) * JOIN_ROWS + jr;
@@ -819,7 +826,8 @@ __global__ void __launch_bounds__(JOIN_SET * SETS) latent_join(const __grid_cons
     const int32_t e4 = blockIdx.y * JOIN_COLS + tid % JOIN_SET / JOIN_ROWS;     // 4 elements
     const int32_t before = a.prefix[r], units = a.prefix[r + 1] - before;
     const int32_t first = before * a.chunks + job * units;
-    const int32_t c0 = cut.part_of(first), n = cut.part_of(first + units - 1) - c0 + 1;
+    int32_t c0, n;
+    cut.parts_of(r, job, first, units, a.ahead, a.chunks, &c0, &n);
     if (n == 1) return;
     const bool mine = rho < M;
     auto slot = [&](int32_t c) { return a.partial + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * SLOT; };
@@ -963,6 +971,7 @@ kvr_status kvc_latent_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     a.out_head = p->out_head_stride;
     a.partial = c->ws.partial;
     a.prefix = (int32_t *)c->ws.arrived;
+    a.ahead = a.prefix + p->num_requests + 1;
     a.m = p->num_new, a.Hq = c->d.query_heads;
     a.heads = kvr_make_div((uint32_t)a.Hq);
     a.scale = p->scale;

@@ -2,7 +2,8 @@
 //
 // The units (a fixed number of keys) of all jobs form one line: request by request, job by job of
 // a request (key heads, or passes of query rows), units of a job in the order of its keys. It is
-// cut into equal parts, one a block or cluster.
+// cut into parts, one a block or cluster: equal ones, which may end within a job and go on in the
+// next; or, where that makes the longest part hardly longer, parts within jobs.
 #pragma once
 
 #include "cache.h"
@@ -67,20 +68,106 @@ __device__ __forceinline__ void unit_prefix(const SplitArgs &a, int32_t align, i
     __syncthreads();
 }
 
-// The line's cut into parts: the first `more` have one unit more than the others.
-struct Cut {
-    int32_t total, parts, each, more;
+// The line's cut into parts. A part has `least` units at least, but in jobs that have fewer, as
+// each costs its job a share of the join.
+//
+// Equal parts (group 0): the first `more` have one unit more than the others. Parts within jobs:
+// a job of u units is cut into ceil(u / group) equal ones, with the smallest group that at most
+// `most` parts come of whatever the lengths are: sum ceil(u / group) <= (total + jobs (group - 1)) /
+// group <= most. (With room for more, the fewer that have `least` units.) A change of job within a
+// part costs the part a new start, as long as `slack` units take.
+constexpr int32_t AHEAD_MOST = 128;       // requests up to which parts may be within jobs
 
-    __device__ __forceinline__ Cut(int32_t total_, int32_t parts_) : total(total_), parts(parts_) {
+struct Cut {
+    int32_t total, parts, each, more, group, least;
+
+    // `of_request`: jobs of a request. The parts are counted later where group > 0.
+    __device__ __forceinline__ Cut(int32_t total_, int32_t requests, int32_t of_request, int32_t most,
+                                   int32_t least_, int32_t slack)
+        : total(total_), least(least_) {
+        const int32_t jobs = requests * of_request;
+        parts = min(most, max(total / least, jobs));
         each = (int32_t)((uint32_t)total / (uint32_t)parts);
         more = total - each * parts;
+        group = 0;
+        if (jobs > 1 && jobs < most && requests <= AHEAD_MOST && total > jobs * least) {
+            const int32_t g =
+                max(least, (int32_t)((uint32_t)(total - jobs + most - jobs - 1) / (uint32_t)(most - jobs)));
+            if (g <= each + slack) group = g;
+        }
     }
+    // parts that a job of so many units has
+    __device__ __forceinline__ int32_t of_job(int32_t units) const {
+        return group == least ? max(1, (int32_t)((uint32_t)units / (uint32_t)least))
+                              : (int32_t)((uint32_t)(units + group - 1) / (uint32_t)group);
+    }
+    // equal parts: where part c begins, and the part that holds unit x
     __device__ __forceinline__ int32_t start(int32_t c) const { return c * each + min(c, more); }
-    // the part that holds unit x
     __device__ __forceinline__ int32_t part_of(int32_t x) const {
         const int32_t edge = more * (each + 1);
         return x < edge ? (int32_t)((uint32_t)x / (uint32_t)(each + 1))
                         : more + (int32_t)((uint32_t)(x - edge) / (uint32_t)max(each, 1));
+    }
+    // ahead[r]: parts of one job of each of the requests before r. By one warp; needs a barrier.
+    __device__ __forceinline__ void count(const int32_t *prefix, int32_t requests, int32_t *ahead) const {
+        const int lane = threadIdx.x % 32;
+        constexpr int PER = AHEAD_MOST / 32;
+        int32_t own[PER], sum = 0;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int32_t r = lane * PER + k;
+            own[k] = r < requests ? of_job(prefix[r + 1] - prefix[r]) : 0;
+            sum += own[k];
+        }
+        int32_t incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int32_t y = __shfl_up_sync(~0u, incl, o);
+            if (lane >= o) incl += y;
+        }
+        int32_t before = incl - sum;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int32_t r = lane * PER + k;
+            if (r <= requests) ahead[r] = before;
+            before += own[k];
+        }
+        if (lane == 31 && requests == AHEAD_MOST) ahead[requests] = before;
+    }
+    // units [x, x_end) of part c, none if there is no such part
+    __device__ __forceinline__ void units_of(int32_t c, const int32_t *prefix, const int32_t *ahead,
+                                             int32_t requests, int32_t of_request, int32_t *x,
+                                             int32_t *x_end) const {
+        *x = *x_end = 0;
+        if (group == 0) {
+            if (c < parts) *x = start(c), *x_end = start(c + 1);
+        } else if (c < ahead[requests] * of_request) {
+            int32_t lo = 0, hi = requests - 1;
+            const int32_t cj = (int32_t)((uint32_t)c / (uint32_t)of_request);
+            while (lo < hi) {
+                const int32_t mid = (lo + hi + 1) / 2;
+                if (ahead[mid] <= cj) lo = mid; else hi = mid - 1;
+            }
+            const int32_t units = prefix[lo + 1] - prefix[lo], n = ahead[lo + 1] - ahead[lo];
+            const int32_t at = c - ahead[lo] * of_request;
+            const int32_t job = (int32_t)((uint32_t)at / (uint32_t)n), k = at - job * n;
+            const int32_t size = (int32_t)((uint32_t)units / (uint32_t)n), rest = units - size * n;
+            *x = prefix[lo] * of_request + job * units + k * size + min(k, rest);
+            *x_end = *x + size + (k < rest ? 1 : 0);
+        }
+    }
+    // job `job` of request r, whose first unit and number of units are these: its first part, and
+    // how many it has
+    __device__ __forceinline__ void parts_of(int32_t r, int32_t job, int32_t first, int32_t units,
+                                             const int32_t *ahead, int32_t of_request, int32_t *c0,
+                                             int32_t *n) const {
+        if (group == 0) {
+            *c0 = part_of(first);
+            *n = part_of(first + units - 1) - *c0 + 1;
+        } else {
+            *n = of_job(units);
+            *c0 = ahead[r] * of_request + job * *n;
+        }
     }
 };
 
