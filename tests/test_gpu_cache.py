@@ -184,6 +184,45 @@ def test_many_parts_of_one_request_are_joined():
     Case(6, [3000, 1, 0, 2000, 17, 900], dim=576, queries=16, new=2).attend(scale=0.07)
 
 
+DIVIDED = [
+    ([2000] * 9, dict(heads=2, queries=4, dim=64)),
+    ([4100, 3, 0, 900, 2048], dict(heads=2, queries=8, dim=128, new=2)),
+    ([60000, 1, 30000], dict(heads=1, queries=2, dim=64, pool="f16", block=64)),
+    ([97 * k % 701 for k in range(128)], dict(heads=1, queries=2, dim=64)),
+    ([97 * k % 701 for k in range(129)], dict(heads=1, queries=2, dim=64)),
+    ([97 * k % 701 for k in range(128)], dict(heads=3, queries=3, dim=64)),
+    ([0] * 20 + [5000], dict(heads=2, queries=4, dim=64)),
+    ([1300, 0, 40, 2500, 7, 1280], dict(dim=576, queries=16)),
+    ([640] * 19, dict(dim=576, queries=16, block=64)),
+    ([97 * k % 301 for k in range(75)], dict(dim=576, queries=4)),
+    ([97 * k % 301 for k in range(130)], dict(dim=576, queries=4)),
+    ([2100, 700], dict(dim=576, queries=100, new=2, pool="f16")),
+]
+
+
+@pytest.mark.parametrize("lengths, kw", DIVIDED)
+def test_jobs_of_all_sizes_are_divided_and_joined(lengths, kw):
+    """Few long jobs and many short ones: parts that end with jobs, and parts that do not."""
+    Case(61, lengths, **kw).attend()
+
+
+@pytest.mark.parametrize("kw", [dict(heads=2, queries=8, dim=64), dict(dim=576, queries=16)])
+def test_the_first_call_may_be_captured(kw):
+    """Nothing is left for a first launch that a graph's capture would not allow."""
+    import torch
+    case = Case(67, [700, 33, 2100], **kw)
+    scale = case.D ** -0.5
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = case.cache.attend(0, case.q, case.dlen, case.dtable, scale=scale)
+        one = case.cache.attend(0, case.q[:1], case.dlen[:1], case.dtable[:1], scale=scale)
+    graph.replay()
+    case.cache.check()
+    case.check(out, lse, scale, 0)
+    case.check(one[0], one[1], scale, 0, first=1)
+
+
 def test_most_requests_of_one_call():
     import torch
     lengths = [(7 * r) % 5 for r in range(2048)]
