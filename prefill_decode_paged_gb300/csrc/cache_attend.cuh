@@ -70,6 +70,10 @@ constexpr int ATTEND_THREADS = 32 * ATTEND_WARPS;
 // 8192, 8 heads); where nothing was to be gained 0.3 to 0.8 more.
 constexpr int LEAST = 4, SLACK = 8;
 constexpr float P_SHIFT = 10.0f;      // log2 of P's scale in f16
+// how far (as a power of two) P may exceed its scale before a new maximum is taken: bf16 and the fp32
+// sums reach far, f16 P ends at 2^16
+template <bool F16>
+constexpr float GROWTH_OF = F16 ? 5.0f : 40.0f;
 
 template <int DP, int POOL, int NT>
 struct Attend {
@@ -203,6 +207,7 @@ template <int DP, int POOL, int NT>
 __global__ void __launch_bounds__(ATTEND_THREADS, (Attend<DP, POOL, NT>::BLOCKS))
 attend_kernel(AttendArgs a) {
     using C = Attend<DP, POOL, NT>;
+    constexpr float GROWTH = GROWTH_OF<C::F16>;
     constexpr int KT = C::KT, KS = C::KS, RP = C::RP, MT = C::MT, ROW = C::ROW;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t smem0 = (uint32_t)__cvta_generic_to_shared(smem);
@@ -254,18 +259,19 @@ attend_kernel(AttendArgs a) {
         const int32_t t_begin = u0 * ATTEND_WARPS + warp, t_end = min(u1 * ATTEND_WARPS, tiles);
         const int32_t *table = a.split.slots.ids + (int64_t)r * a.split.slots.stride;
         const int64_t head_off = (int64_t)h * a.k_plane.head_stride;
-        auto slot_of = [&](int32_t t) -> int64_t {      // byte offset in a plane, -1: no key
+        // its block, which is looked at a tile later than it is asked for; its byte offset in a plane
+        auto block_of = [&](int32_t t) -> int32_t {
             const int32_t j = sp.lo + t * KT + (lane & (KT - 1));
-            if (t >= t_end || j >= sp.n) return -1;
-            const uint32_t entry = a.split.slots.block.div((uint32_t)j);
-            const int32_t id = __ldg(table + entry);
-            if (id < 0 || id >= a.split.slots.num_blocks) {
-                bad = KVC_FLAG_BLOCK;
-                return -1;
-            }
-            return id * a.k_plane.block_stride +
-                   (int64_t)(j - (int32_t)(entry * a.split.slots.block.d)) * a.k_plane.token_stride +
-                   head_off;
+            int32_t id = 0;
+            if (t < t_end && j < sp.n) id = __ldg(table + a.split.slots.block.div((uint32_t)j));
+            return id;
+        };
+        auto slot_of = [&](int32_t t, int32_t id) -> int64_t {         // -1: no key
+            const int32_t j = sp.lo + t * KT + (lane & (KT - 1));
+            const int32_t in = j - (int32_t)(a.split.slots.block.div((uint32_t)j) * a.split.slots.block.d);
+            const bool key = t < t_end && j < sp.n, known = id >= 0 && id < a.split.slots.num_blocks;
+            if (key && !known) bad = KVC_FLAG_BLOCK;
+            return key && known ? id * a.k_plane.block_stride + in * a.k_plane.token_stride + head_off : -1;
         };
         auto issue = [&](int32_t stage, int64_t slot) {
             constexpr int CPR = ROW / 16, RPI = 32 / CPR;   // chunks of a row, rows at a time
@@ -296,17 +302,18 @@ attend_kernel(AttendArgs a) {
             qw[n] = make_uint4(0, 0, 0, 0);
             if (row < rows && lane * 8 < a.D) qw[n] = __ldg((const uint4 *)q + lane);
         }
-        int64_t next_slot;
+        int32_t next_block;
         {
-            int64_t s[C::STAGES];
+            int32_t ids[C::STAGES];
 #pragma unroll
-            for (int k = 0; k < C::STAGES; ++k) s[k] = slot_of(t_begin + k * ATTEND_WARPS);
+            for (int k = 0; k < C::STAGES; ++k) ids[k] = block_of(t_begin + k * ATTEND_WARPS);
 #pragma unroll
             for (int k = 0; k < C::STAGES - 1; ++k) {
-                if (t_begin + k * ATTEND_WARPS < t_end) issue(k, s[k]);
+                const int32_t t = t_begin + k * ATTEND_WARPS;
+                if (t < t_end) issue(k, slot_of(t, ids[k]));
                 cp_async_commit();
             }
-            next_slot = s[C::STAGES - 1];
+            next_block = ids[C::STAGES - 1];
         }
 
         // the queries in the type of the products; rows beyond M are zero
@@ -382,9 +389,9 @@ attend_kernel(AttendArgs a) {
             {
                 const int32_t tn = t + (C::STAGES - 1) * ATTEND_WARPS;
                 const int into = stage == 0 ? C::STAGES - 1 : stage - 1;
-                if (tn < t_end) issue(into, next_slot);
+                if (tn < t_end) issue(into, slot_of(tn, next_block));
                 cp_async_commit();
-                next_slot = slot_of(tn + ATTEND_WARPS);
+                next_block = block_of(tn + ATTEND_WARPS);
             }
             const uint32_t kbase = ring + (uint32_t)(stage * C::STAGE), vbase = kbase + KT * ROW;
             stage = stage == C::STAGES - 1 ? 0 : stage + 1;
@@ -434,16 +441,17 @@ attend_kernel(AttendArgs a) {
                 }
             }
 
-            // softmax over the tile's keys, one pass with the running maximum
+            // softmax over the tile's keys, relative to the maximum of those before; a new maximum is
+            // looked for only where it is outgrown (16 cycles a shuffle, three a row and tile)
             const int32_t j0 = sp.lo + t * KT;
             const bool mixed = j0 + KT > seen_all || j0 < seen_from;
-            float shrink[NT][2];
-            bool changed = false;
+            bool outgrown = false;
+            float best[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float best = -INFINITY;
+                    best[n][e] = -INFINITY;
 #pragma unroll
                     for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -456,35 +464,40 @@ attend_kernel(AttendArgs a) {
                                     (a.split.window > 0 && j < end[n][e] - a.split.window))
                                     v = -INFINITY;
                             }
-                            best = fmaxf(best, v);
+                            best[n][e] = fmaxf(best[n][e], v);
                         }
+                    outgrown |= best[n][e] > top[n][e] + GROWTH;
+                }
+            if (__any_sync(~0u, outgrown)) {
 #pragma unroll
-                    for (int w = 4; w < 32; w *= 2)
-                        best = fmaxf(best, __shfl_xor_sync(~0u, best, w));
-                    const float next = fmaxf(top[n][e], best);
-                    const float at = (next == -INFINITY ? 0.0f : next) - (C::F16 ? P_SHIFT : 0.0f);
-                    shrink[n][e] = next == top[n][e] ? 1.0f : ex2(top[n][e] - next);
-                    changed |= next != top[n][e];
-                    top[n][e] = next;
-                    float add = 0.0f;
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int w = 4; w < 32; w *= 2)
+                            best[n][e] = fmaxf(best[n][e], __shfl_xor_sync(~0u, best[n][e], w));
+                        const float next = fmaxf(top[n][e], best[n][e]);
+                        const float shrink = next == top[n][e] ? 1.0f : ex2(top[n][e] - next);
+                        top[n][e] = next;
+                        sum[n][e] *= shrink;
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) o[i][n][e] *= shrink, o[i][n][2 + e] *= shrink;
+                    }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float at = (top[n][e] == -INFINITY ? 0.0f : top[n][e]) - (C::F16 ? P_SHIFT : 0.0f);
 #pragma unroll
                     for (int k = 0; k < KS; ++k)
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             float &v = s[k][n][2 * u + e];
                             v = ex2(v - at);
-                            add += v;
+                            sum[n][e] += v;
                         }
-                    sum[n][e] = sum[n][e] * shrink[n][e] + add;
                 }
-            if (__any_sync(~0u, changed)) {
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[i][n][e] *= shrink[n][e & 1];
-            }
 
             // O^T += V^T P^T
             uint32_t ph[KS][NT][2], pl[KS][NT][2];
