@@ -46,10 +46,10 @@
 // the end of the kernel, as the others do for want of it.
 //
 // Measured, with the join: 64 requests of 1024 to 16384 latents, 128 heads, bf16 (528,481
-// latents, 627 MB and 147 GFLOP): 165 us, 3.8 TB/s and 0.89 PFLOP/s, 56 % of what HBM alone would
-// allow. A tile of 32 keys comes through in about 1000 cycles, which is the softmax and the way
-// of S through the other SM; each change of job costs about 8 us of 262 KB of partial results and
-// an empty pipe, and the join 8 us. One request of 4096 latents with 16 heads: 13.8 us, its fill,
+// latents, 627 MB and 147 GFLOP): 163 us, 3.85 TB/s and 0.90 PFLOP/s, 57 % of what HBM alone would
+// allow; 64 of 8192 (622 MB) 150 us. A tile of 32 keys comes through in about 1000 cycles, which is the
+// softmax and the way of S through the other SM; each change of job costs about 8 us of 262 KB of
+// partial results and an empty pipe, and the join 5 us. One request of 4096 latents with 16 heads: 13.8 us, its fill,
 // four tiles and the join one after another.
 #include <math.h>
 
@@ -808,12 +808,19 @@ constexpr int PARTS_MOST = 128;           // clusters of the attention kernel
 // With 1, 2, 4 and 8 sets the whole attention took (us, * the choice) 20.8, 17.0, 14.6, 13.8* for
 // one request of 4096 latents and 16 heads; 59.7, 46.2, 39.0, 36.1* for one of 65536 and 128
 // heads; 57.6, 54.8*, 55.7, 63.1 for 4 of 32768; 41.9*, 45.1, 53.9, 78.5 for 16 of 4096.
-template <bool F16, int SETS>
+//
+// With many jobs of few parts each it is bound by its instructions (77 % of the issue slots), most of
+// which come before the first product. So where at most 3 parts are to be expected and the
+// blocks are still 4 an SM, one takes all 512 elements (ALL): 166.8 -> 162.9 us for 64 requests of 1024 to
+// 16384 latents, 60.6 -> 59.2 for 32 of 4096 (with 9 parts a job it would be 37.5 -> 43.9).
+template <bool F16, int SETS, bool ALL>
 __global__ void __launch_bounds__(JOIN_SET * SETS) latent_join(const __grid_constant__ LatentArgs a) {
-    constexpr int AHEAD = SETS == 1 ? 4 : 8;           // parts that a thread asks for at a time
+    // parts and 4-element columns that a thread asks for at a time
+    constexpr int AHEAD = ALL ? 2 : SETS == 1 ? 4 : 8, PIECES = ALL ? JOIN_GRID : 1;
+    static_assert(!ALL || SETS == 1, "");
     __shared__ float weights[PARTS_MOST][JOIN_ROWS];   // a part's share of a row; below 0: has none
     __shared__ float2 warp_stat[JOIN_SET * SETS / 32][JOIN_ROWS];
-    __shared__ float4 sums[SETS > 1 ? SETS - 1 : 1][JOIN_SET];
+    __shared__ float4 sums[SETS > 1 ? SETS - 1 : 1][JOIN_SET];   // (PIECES is 1)
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, set = tid / JOIN_SET;
     const int jr = tid % JOIN_ROWS;
     wait_for_previous();
@@ -832,12 +839,15 @@ __global__ void __launch_bounds__(JOIN_SET * SETS) latent_join(const __grid_cons
     const bool mine = rho < M;
     auto slot = [&](int32_t c) { return a.partial + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * SLOT; };
 
-    float4 p[AHEAD];
+    float4 p[AHEAD][PIECES];
     auto ask = [&](int32_t c1) {
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k)
-            if (mine && c1 + k * SETS < n)
-                p[k] = __ldcg((const float4 *)slot(c1 + k * SETS) + (size_t)e4 * ROWS + row);
+            if (mine && c1 + k * SETS < n) {
+                const float4 *from = (const float4 *)slot(c1 + k * SETS) + (size_t)e4 * ROWS + row;
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i) p[k][i] = __ldcg(from + i * JOIN_COLS * ROWS);
+            }
     };
     // one part and row a thread: (max, sum), then the rows' maxima and sums over all parts
     constexpr int TURN = JOIN_SET * SETS / JOIN_ROWS, TURNS = (PARTS_MOST + TURN - 1) / TURN;
@@ -870,7 +880,9 @@ __global__ void __launch_bounds__(JOIN_SET * SETS) latent_join(const __grid_cons
     if (lane < JOIN_ROWS) warp_stat[warp][jr].y = l;
     __syncthreads();
 
-    float4 v = make_float4(0, 0, 0, 0);
+    float4 v[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) v[i] = make_float4(0, 0, 0, 0);
     for (int32_t c1 = set; c1 < n; c1 += AHEAD * SETS) {
         if (c1 != set) ask(c1);
 #pragma unroll
@@ -878,16 +890,20 @@ __global__ void __launch_bounds__(JOIN_SET * SETS) latent_join(const __grid_cons
             const int32_t c = c1 + k * SETS;
             const float f = c < n && mine ? weights[c][jr] : -1.0f;
             if (f < 0.0f) continue;
-            v.x += f * p[k].x, v.y += f * p[k].y, v.z += f * p[k].z, v.w += f * p[k].w;
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                v[i].x += f * p[k][i].x, v[i].y += f * p[k][i].y;
+                v[i].z += f * p[k][i].z, v[i].w += f * p[k][i].w;
+            }
         }
     }
     if (SETS > 1) {
-        if (set > 0) sums[set - 1][tid % JOIN_SET] = v;
+        if (set > 0) sums[set - 1][tid % JOIN_SET] = v[0];
         __syncthreads();
         if (set > 0) return;
         for (int k = 0; k < SETS - 1; ++k) {
             const float4 w = sums[k][tid];
-            v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+            v[0].x += w.x, v[0].y += w.y, v[0].z += w.z, v[0].w += w.w;
         }
     }
     if (!mine) return;
@@ -896,16 +912,20 @@ __global__ void __launch_bounds__(JOIN_SET * SETS) latent_join(const __grid_cons
     const bool some = l > 0.0f || l != l;
     const float inv = some ? 1.0f / l : 0.0f;
     const int32_t token = (int32_t)a.heads.div((uint32_t)rho), hq = rho - token * a.Hq;
-    *(uint2 *)(a.out + r * a.out_request + token * a.out_token + hq * a.out_head + e4 * 8) =
-        make_uint2(narrow2<F16>(v.x * inv, v.y * inv), narrow2<F16>(v.z * inv, v.w * inv));
+    unsigned char *out = a.out + r * a.out_request + token * a.out_token + hq * a.out_head + e4 * 8;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+        *(uint2 *)(out + i * JOIN_COLS * 8) = make_uint2(narrow2<F16>(v[i].x * inv, v[i].y * inv),
+                                                         narrow2<F16>(v[i].z * inv, v[i].w * inv));
     if (e4 == 0 && a.lse != nullptr)
         a.lse[((int64_t)r * a.m + token) * a.Hq + hq] =
             some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-constexpr void (*JOINS[2][4])(LatentArgs) = {
-    {latent_join<false, 1>, latent_join<false, 2>, latent_join<false, 4>, latent_join<false, 8>},
-    {latent_join<true, 1>, latent_join<true, 2>, latent_join<true, 4>, latent_join<true, 8>}};
+template <bool F16>
+constexpr void (*JOINS_OF[5])(LatentArgs) = {latent_join<F16, 1, false>, latent_join<F16, 2, false>,
+                                             latent_join<F16, 4, false>, latent_join<F16, 8, false>,
+                                             latent_join<F16, 1, true>};
 
 }  // namespace
 
@@ -945,9 +965,9 @@ kvr_status kvc_latent_setup(kvc_cache *c) {
             return KVR_ERR_CUDA;
         }
     cudaFuncAttributes loaded;            // now, and not while a stream is captured
-    for (const auto &of_type : JOINS)
-        for (auto k : of_type)
-            if (cudaFuncGetAttributes(&loaded, k) != cudaSuccess) {
+    for (const auto &of_type : {JOINS_OF<false>, JOINS_OF<true>})
+        for (int k = 0; k < 5; ++k)
+            if (cudaFuncGetAttributes(&loaded, of_type[k]) != cudaSuccess) {
                 cudaGetLastError();
                 return KVR_ERR_CUDA;
             }
@@ -993,5 +1013,7 @@ kvr_status kvc_latent_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     const int64_t parts = std::min<int64_t>(a.parts, most * jobs / LEAST) / jobs;
     int k = 0;
     while (k < 3 && (4 << k) <= parts && (blocks * JOIN_SET * 2 << k) <= (int64_t)sms * JOIN_RESIDENT) ++k;
-    return kvc_launch(JOINS[f16][k], a, dim3((unsigned)(jobs * groups), JOIN_GRID), JOIN_SET << k, 0, stream);
+    const bool all = parts <= 3 && jobs * groups >= 4 * (int64_t)sms;
+    return kvc_launch((f16 ? JOINS_OF<true> : JOINS_OF<false>)[all ? 4 : k], a,
+                      dim3((unsigned)(jobs * groups), all ? 1 : JOIN_GRID), JOIN_SET << k, 0, stream);
 }

@@ -197,6 +197,7 @@ DIVIDED = [
     ([97 * k % 301 for k in range(75)], dict(dim=576, queries=4)),
     ([97 * k % 301 for k in range(130)], dict(dim=576, queries=4)),
     ([2100, 700], dict(dim=576, queries=100, new=2, pool="f16")),
+    ([97 * k % 601 for k in range(40)], dict(dim=576, queries=64)),
 ]
 
 
