@@ -202,11 +202,27 @@ __device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t v[16]) 
                  "r"(v[14]), "r"(v[15])
                  : "memory");
 }
-// D (+)= A B with A in tensor memory, B in shared memory
-__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+// D (+)= A B with A in tensor memory, B in shared memory: two steps of 16 elements, A's 8 columns
+// apart, B's `step` times 16 bytes; four such. (One statement, so that an operand is one addition.)
+__device__ __forceinline__ void product2(uint32_t d, uint32_t a, uint64_t b, uint32_t step, uint32_t idesc,
+                                         uint32_t add) {
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 b1;\n\t.reg .b32 a1;\n\t"
+                 "setp.ne.u32 p, %5, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
+                 "add.u32 a1, %1, 8;\n\tadd.u64 b1, %2, %3;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, q;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "l"((uint64_t)step), "r"(idesc), "r"(add)
+                 : "memory");
+}
+__device__ __forceinline__ void product4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+                 "setp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
+                 "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+                 "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n\t}" ::"r"(d),
                  "r"(a), "l"(b), "r"(idesc), "r"(add)
                  : "memory");
 }
@@ -739,14 +755,12 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                     const uint32_t base = __shfl_sync(~0u, ring + stage * STAGE, 0);
                     const uint32_t s_col = __shfl_sync(~0u, tm + COL_S + sb * KT, 0);
                     if (leader) {
+                        const uint64_t first = operand(base, 16, 1024, 2);
 #pragma unroll
-                        for (int e = 0; e < HALF / 16; ++e)
-                            product(s_col, tm + COL_Q + 8 * e,
-                                    operand(base + (e / 4) * CHUNK + (e % 4) * 32, 16, 1024, 2), ID_S, e > 0);
-#pragma unroll
-                        for (int e = 0; e < REST / 16; ++e)
-                            product(s_col, tm + COL_Q + HALF / 2 + 8 * e,
-                                    operand(base + 4 * CHUNK + e * 32, 16, 512, 4), ID_S, 1);
+                        for (int e = 0; e < HALF / 64; ++e)
+                            product4(s_col, tm + COL_Q + 32 * e, first + e * (CHUNK / 16), ID_S, e > 0);
+                        static_assert(REST == 32, "");
+                        product2(s_col, tm + COL_Q + HALF / 2, operand(base + 4 * CHUNK, 16, 512, 4), 2, ID_S, 1);
                         commit(bar(S_FULL + sb));
                         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
                                          bar(X_FULL + sb)),
@@ -766,10 +780,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                     const uint32_t base = __shfl_sync(~0u, ring + stage * STAGE, 0);
                     const uint32_t p_col = __shfl_sync(~0u, tm + COL_P, 0);
                     if (leader) {
-#pragma unroll
-                        for (int e = 0; e < KT / 16; ++e)
-                            product(tm + COL_O, p_col + 8 * e, operand(base + e * 2048, CHUNK, 1024, 2),
-                                    ID_O, k > 0 || e > 0);
+                        product2(tm + COL_O, p_col, operand(base, CHUNK, 1024, 2), 2048 / 16, ID_O, k > 0);
                         commit(bar(K_EMPTY + stage));
                         commit(bar(O_DONE + (i & 3)));
                     }
