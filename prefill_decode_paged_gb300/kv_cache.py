@@ -182,11 +182,13 @@ class KVCache:
         self.value_dim = value_dim or (512 if num_components == 1 else head_dim)
         self.latent = num_components == 1
         self._default_scale = head_dim ** -0.5
+        self._row_bytes = (2 * kv_heads * head_dim, 2 * head_dim)
 
     # -- arguments ---------------------------------------------------------------
     #
     # A decode step calls these for every layer, and they cost about as much as the small kernels
-    # behind them: the common case (contiguous tensors) takes as few Python operations as it can.
+    # behind them: contiguous tensors are looked at where they are used, in as few Python operations
+    # as that takes, and only others (and wrong ones) reach the methods below.
 
     def _handle(self):
         if self._h is None:
@@ -238,37 +240,51 @@ class KVCache:
         given, is rotated into ``q_out`` (a new tensor by default). Returns ``q_out``."""
         if (v is None) != self.latent:
             raise ValueError("a latent cache has no values, others need them")
-        shape = (k.shape[0], self.kv_heads, self.head_dim)
-        T, dtype = shape[0], k.dtype
-        ks = self._rows(k, "k", shape)
-        vp, vs = (0, (0, 0)) if v is None else (v.data_ptr(), self._rows(v, "v", shape, dtype))
+        index, i32, dtype = self._index, self._i32, k.dtype
+        T = k.shape[0]
+        shape, line = (T, self.kv_heads, self.head_dim), (T,)
+        code = self._types.get(dtype)
+        ks = self._row_bytes if code is not None and k.shape == shape and k.is_contiguous() and \
+            k.get_device() == index else self._rows(k, "k", shape)
+        if v is None:
+            vp, vs = 0, (0, 0)
+        else:
+            vp, vs = v.data_ptr(), self._row_bytes
+            if not (v.dtype is dtype and v.shape == shape and v.is_contiguous() and
+                    v.get_device() == index):
+                vs = self._rows(v, "v", shape, dtype)
         ids, stride, rows, width = self._table(block_table)
         rot = rot_rows = rot_dim = q_heads = q_dim = qp = qo = 0
         qs = os = (0, 0)
         if rotary is not None:
             if rotary.dtype is not self._f32 or rotary.dim() != 2 or \
-                    not rotary.is_contiguous() or rotary.get_device() != self._index:
+                    not rotary.is_contiguous() or rotary.get_device() != index:
                 raise ValueError("the rotation table is contiguous float32 [positions][rotated] "
                                  f"on {self._device}")
             rot, (rot_rows, rot_dim) = rotary.data_ptr(), rotary.shape
         if q is not None:
-            if q.dim() != 3:
-                raise ValueError(f"q is {list(q.shape)}; expected [T][heads][dim]")
-            _, q_heads, q_dim = q.shape
-            shape = (T, q_heads, q_dim)
-            qs = self._rows(q, "q", shape, dtype)
+            shape = q.shape
+            if len(shape) != 3 or shape[0] != T:
+                raise ValueError(f"q is {list(shape)}; expected [{T}][heads][dim]")
+            _, q_heads, q_dim = shape
+            plain = (2 * q_heads * q_dim, 2 * q_dim)
+            qs = plain if q.dtype is dtype and q.is_contiguous() and q.get_device() == index else \
+                self._rows(q, "q", shape, dtype)
             if q_out is None:
                 q_out = self._torch.empty(shape, dtype=dtype, device=q.device)
-            os = self._rows(q_out, "q_out", shape, dtype)
+            os = plain if q_out.dtype is dtype and q_out.shape == shape and q_out.is_contiguous() and \
+                q_out.get_device() == index else self._rows(q_out, "q_out", shape, dtype)
             qp, qo = q.data_ptr(), q_out.data_ptr()
+        for t, name in ((requests, "requests"), (positions, "positions")):
+            if not (t.dtype is i32 and t.shape == line and t.is_contiguous() and t.get_device() == index):
+                self._list(t, name, T)
         st = self._append(
             self._handle(), layer,
-            _APPEND.pack(T, self._types[dtype], self._list(requests, "requests", T),
-                         self._list(positions, "positions", T), ids, stride, rows, width,
+            _APPEND.pack(T, code, requests.data_ptr(), positions.data_ptr(), ids, stride, rows, width,
                          k.data_ptr(), vp, *ks, *vs, rot, rot_rows, rot_dim,
                          (INTERLEAVED if interleaved else 0) | (ROTATE_LAST if rotate_last else 0),
                          q_heads, q_dim, 0, qp, qo, *qs, *os),
-            self._raw_stream(self._index) if stream is None else _stream_handle(stream))
+            self._raw_stream(index) if stream is None else _stream_handle(stream))
         if st != 0:
             raise KVRelayoutError(st, "kv_cache_append")
         return q_out
@@ -280,35 +296,51 @@ class KVCache:
         ``scale``: D ** -0.5 by default; ``window`` > 0: only that many keys, the token's own
         included. Returns (out, lse): ``out`` like q with ``value_dim`` elements, ``lse`` float32
         [R][new][Hq], new tensors by default (``lse=False``: none)."""
-        n = q.dim()
-        if n not in (3, 4):
-            raise ValueError(f"q is {list(q.shape)}; expected [R][new][heads][dim]")
-        R, m = (q.shape[0], q.shape[1]) if n == 4 else (q.shape[0], 1)
-        lead = (R, m, self.query_heads) if n == 4 else (R, self.query_heads)
-        dtype = q.dtype
-        qs = self._rows(q, "q", lead + (self.head_dim,))
+        index, dtype, shape, heads = self._index, q.dtype, q.shape, self.query_heads
+        n = len(shape)
+        if n == 4:
+            R, m = shape[0], shape[1]
+            rows = (R, m, heads)
+        elif n == 3:
+            R, m = shape[0], 1
+            rows = (R, heads)
+        else:
+            raise ValueError(f"q is {list(shape)}; expected [R][new][heads][dim]")
+        q_row, out_row = 2 * self.head_dim, 2 * self.value_dim
+        code = self._types.get(dtype)
+        if code is not None and shape == rows + (self.head_dim,) and q.is_contiguous() and \
+                q.get_device() == index:
+            qs = m * heads * q_row, heads * q_row, q_row
+        else:
+            qs = self._rows(q, "q", rows + (self.head_dim,))
+            qs = qs if n == 4 else (qs[0], 0, qs[1])
+        line = rows + (self.value_dim,)
         if out is None:
-            out = self._torch.empty(lead + (self.value_dim,), dtype=dtype, device=q.device)
-        os = self._rows(out, "out", lead + (self.value_dim,), dtype)
+            out = self._torch.empty(line, dtype=dtype, device=q.device)
+        if out.dtype is dtype and out.shape == line and out.is_contiguous() and out.get_device() == index:
+            os = m * heads * out_row, heads * out_row, out_row
+        else:
+            os = self._rows(out, "out", line, dtype)
+            os = os if n == 4 else (os[0], 0, os[1])
         if lse is None:
-            lse = self._torch.empty(lead, dtype=self._f32, device=q.device)
+            lse = self._torch.empty(rows, dtype=self._f32, device=q.device)
         if lse is False:
             lse, lp = None, 0
-        elif lse.dtype is self._f32 and lse.shape == lead and lse.is_contiguous() and \
-                lse.get_device() == self._index:
+        elif lse.dtype is self._f32 and lse.shape == rows and lse.is_contiguous() and \
+                lse.get_device() == index:
             lp = lse.data_ptr()
         else:
             raise ValueError(f"lse is {lse.dtype} {list(lse.shape)}; expected contiguous "
-                             f"float32 {list(lead)} on {self._device}")
-        if n == 3:
-            qs, os = (qs[0], 0, qs[1]), (os[0], 0, os[1])
+                             f"float32 {list(rows)} on {self._device}")
+        if not (lengths.dtype is self._i32 and lengths.shape == (R,) and lengths.is_contiguous() and
+                lengths.get_device() == index):
+            self._list(lengths, "lengths", R)
         st = self._attend(
             self._handle(), layer,
-            _ATTEND.pack(R, m, self._types[dtype], window,
-                         self._default_scale if scale is None else scale, 0,
-                         self._list(lengths, "lengths", R), *self._table(block_table),
+            _ATTEND.pack(R, m, code, window, self._default_scale if scale is None else scale, 0,
+                         lengths.data_ptr(), *self._table(block_table),
                          q.data_ptr(), out.data_ptr(), lp, *qs, *os),
-            self._raw_stream(self._index) if stream is None else _stream_handle(stream))
+            self._raw_stream(index) if stream is None else _stream_handle(stream))
         if st != 0:
             raise KVRelayoutError(st, "kv_cache_attend")
         return out, lse
