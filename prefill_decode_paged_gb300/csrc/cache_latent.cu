@@ -35,7 +35,7 @@
 // it may send over. One tile's softmax takes its 4 warps about 1700 cycles, and HBM wants a tile
 // in 780, so one set is too few; a third (177 us) only shares the SM's issue slots with the
 // others. A tile's softmax needs of the one before only what P is relative to, which goes through
-// shared memory as soon as it is known. O is rescaled only when a row's maximum outgrows by 2^40
+// shared memory as soon as it is known. O is rescaled only when a row's maximum outgrows by 2^20
 // (f16: 2^8) the one that its P is relative to, which hardly happens after the first tiles of a
 // job: powers of two cost no precision in P, O and the sums.
 //
@@ -46,9 +46,11 @@
 // the end of the kernel, as the others do for want of it.
 //
 // Measured, with the join: 64 requests of 1024 to 16384 latents, 128 heads, bf16 (528,481
-// latents, 627 MB and 147 GFLOP): 163 us, 3.85 TB/s and 0.90 PFLOP/s, 57 % of what HBM alone would
-// allow; 64 of 8192 (622 MB) 150 us. A tile of 32 keys comes through in about 1000 cycles, which is the
-// softmax and the way of S through the other SM; each change of job costs about 8 us of 262 KB of
+// latents, 627 MB and 147 GFLOP): 162 us, 3.9 TB/s and 0.91 PFLOP/s, 57 % of what HBM alone would
+// allow; 64 of 8192 (622 MB) 149 us. A tile of 32 keys comes through in about 1000 cycles. No unit is
+// busy for all of them (tensor cores 40 %, shared memory about 75 %: 85 KB of boxes, operands and S a
+// tile); from S to P's product a tile is under way for some 5000, most of it in the products, where
+// S of two tiles and O of a third take turns, and in the exchange. Each change of job costs about 8 us of 262 KB of
 // partial results and an empty pipe, and the join 5 us. One request of 4096 latents with 16 heads: 13.8 us, its fill,
 // four tiles and the join one after another.
 #include <math.h>
@@ -302,10 +304,11 @@ __device__ __forceinline__ Cut cut_of(const LatentArgs &a, const int32_t *prefix
 
 // -- the kernel -------------------------------------------------------------------
 
-// how far (as a power of two) P may exceed 1 before O is rescaled: bf16 P and fp32 sums reach
-// far, f16 P ends at 2^16
+// How far (as a power of two) P may exceed 1 before O is rescaled. bf16 P and fp32 sums reach further
+// than is of use: with logits of 5 (in powers of two) standard deviation 8 takes 186 us where 16 to
+// 40 take 162, and O of values up to 2^100 has to stay finite. f16 P ends at 2^16.
 template <bool F16>
-constexpr float GROWTH_OF = F16 ? 8.0f : 40.0f;
+constexpr float GROWTH_OF = F16 ? 8.0f : 20.0f;
 
 template <bool F16>
 __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constant__ LatentArgs a) {

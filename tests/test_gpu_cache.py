@@ -274,6 +274,24 @@ def test_infinite_logits_and_nan_keys_reach_their_own_rows_only():
     assert torch.isinf(out[0, 0, :2].float()).all() and torch.isfinite(lse).all()
 
 
+@pytest.mark.parametrize("kw, size", [(dict(heads=2, queries=8, dim=64), 2.0 ** 105),
+                                      (dict(dim=576, queries=16), 2.0 ** 95)])
+def test_values_near_the_largest_stay_finite(kw, size):
+    """Sums over keys may run ahead of the last maximum, but not beyond fp32."""
+    import torch
+    case = Case(71, [700, 2000], **kw)
+    small = size ** -0.5 if case.latent else 1.0         # a latent is its own key
+    dev = case.dev.double()
+    dev = dev * size if case.latent else torch.stack([dev[:, 0], dev[:, 1] * size], 1)
+    case.dev.copy_(dev.to(torch.bfloat16))
+    case.wide = case.dev.double().cpu().numpy()
+    case.q.copy_((case.q.double() * small).to(torch.bfloat16))
+    scale = case.D ** -0.5 * (small if case.latent else 1.0)
+    out, lse = case.cache.attend(0, case.q, case.dlen, case.dtable, scale=scale)
+    case.cache.check()
+    case.check(out, lse, scale, 0)
+
+
 def _padded(case):
     """Rows 48 bytes apart from each other's ends, heads before tokens, layers in tensors of their own."""
     import torch
