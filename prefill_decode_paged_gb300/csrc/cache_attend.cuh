@@ -32,7 +32,7 @@
 //
 // Measured, 8 queries a key head of 128: 4 requests of 32768 keys, 4 heads, bf16 (268 MB) 48.7 us,
 // 5.5 TB/s; one of 131072, 8 heads, E4M3 (268 MB) 54 us, 5.0 TB/s; 64 of 8192, 8 heads, bf16 (2.1 GB)
-// 323 us, 6.65 TB/s, and with 4 newest tokens, 32 rows, 381 us. What is lost below a plain copy's
+// 322 us, 6.68 TB/s, and with 4 newest tokens, 32 rows, 381 us. What is lost below a plain copy's
 // rate is fixed: 5 us from the launch to the first keys (lengths, block ids, keys, each after the one
 // before), 6 us from the first block's end to the last's, as not all SMs are as near to all of
 // HBM, and 3 to 6 us of joining.
