@@ -7,9 +7,10 @@
 //   rotated, interleaved: pieces at 16 i and 16 i + 8 hold the same pairs side by side;
 //   not rotated:          pieces at 16 i and 16 i + 8, passed through (or quantized).
 // A thread asks for BATCH units before it looks at the token's position: the slot (position, then
-// block id) and the angles are on their way meanwhile. HBM bounds it with many tokens: 39834
-// tokens of 32 + 16 heads of 128, 982 MB, 162 us (6060 GB/s, 89 % of a plain copy's rate). Where the row's units divide
-// the block's threads, a thread has the same unit of every row, and loads its angles once.
+// block id) and the angles are on their way meanwhile. Where the row's units divide the block's
+// threads, a thread has the same unit of every row, and loads its angles once. HBM bounds it with
+// many tokens: 39834 tokens of 32 + 16 heads of 128, 982 MB, 152 us (6440 GB/s, 95 % of a plain
+// copy's rate).
 #include <algorithm>
 
 #include "cache.h"
@@ -18,7 +19,11 @@ namespace {
 
 using namespace kvc;
 
-constexpr int THREADS = 128;
+constexpr int BORDER = 2;     // tokens an SM, above which they are many
+// MB written above which the stores do not ask L2 to keep them: half of it. Prompts' 486 MB take 152
+// us instead of 161 so; 60 MB would take 22 instead of 24, but what reads them next finds them there.
+constexpr int AWAY = 64;
+constexpr int MANY_THREADS = 128, FEW_THREADS = 512;
 struct Rows {                 // head rows of one input and where they go
     const unsigned char *src;
     int64_t src_token, src_head;
@@ -38,6 +43,7 @@ struct AppendArgs {
     const float *k_scale, *v_scale;
     uint32_t *flags;
     int32_t last;             // the rotated elements are the row's last
+    int32_t away;             // what is written need not stay in L2
     KvrDiv units, q_units;    // of a key's and of a query's row
 };
 
@@ -96,15 +102,24 @@ __device__ __forceinline__ void turn(const uint4 &p0, const uint4 &p1, const Uni
     }
 }
 
+template <typename T>
+__device__ __forceinline__ void store(unsigned char *to, T v, bool away) {
+    if (away)
+        __stcs((T *)to, v);
+    else
+        *(T *)to = v;
+}
+
 template <bool F16>
-__device__ __forceinline__ void store_16bit(unsigned char *row, const Unit &u, const float x[16]) {
+__device__ __forceinline__ void store_16bit(unsigned char *row, const Unit &u, const float x[16],
+                                            bool away) {
     uint4 o0, o1;
     o0.x = narrow2<F16>(x[0], x[1]), o0.y = narrow2<F16>(x[2], x[3]);
     o0.z = narrow2<F16>(x[4], x[5]), o0.w = narrow2<F16>(x[6], x[7]);
     o1.x = narrow2<F16>(x[8], x[9]), o1.y = narrow2<F16>(x[10], x[11]);
     o1.z = narrow2<F16>(x[12], x[13]), o1.w = narrow2<F16>(x[14], x[15]);
-    *(uint4 *)(row + 2 * u.e0) = o0;
-    *(uint4 *)(row + 2 * u.e1) = o1;
+    store(row + 2 * u.e0, o0, away);
+    store(row + 2 * u.e1, o1, away);
 }
 
 // Four E4M3 codes of x * inv, nearest-even, saturated; every code gets its value's sign bit (a
@@ -119,9 +134,9 @@ __device__ __forceinline__ uint32_t quant4f(const float *x, float inv) {
 }
 
 __device__ __forceinline__ void store_8bit(unsigned char *row, const Unit &u, const float x[16],
-                                           float inv) {
-    *(uint2 *)(row + u.e0) = make_uint2(quant4f(x, inv), quant4f(x + 4, inv));
-    *(uint2 *)(row + u.e1) = make_uint2(quant4f(x + 8, inv), quant4f(x + 12, inv));
+                                           float inv, bool away) {
+    store(row + u.e0, make_uint2(quant4f(x, inv), quant4f(x + 4, inv)), away);
+    store(row + u.e1, make_uint2(quant4f(x + 8, inv), quant4f(x + 12, inv)), away);
 }
 
 // Where unit `t` of the token's units is: queries first, then keys, then values.
@@ -147,8 +162,11 @@ __device__ __forceinline__ Place place_of(const AppendArgs &a, int32_t t, int32_
     return p;
 }
 
-template <bool F16, bool INTERLEAVED, bool E4M3, int BATCH>
-__global__ void __launch_bounds__(THREADS, BATCH == 1 ? 10 : 5) append_kernel(AppendArgs a) {
+template <bool F16, bool INTERLEAVED, bool E4M3, bool MANY>
+__global__ void __launch_bounds__(MANY ? MANY_THREADS : FEW_THREADS, MANY ? 10 : 2)
+append_kernel(AppendArgs a) {
+    constexpr int BATCH = MANY ? 1 : 2;
+    const int32_t THREADS = MANY ? MANY_THREADS : (int32_t)blockDim.x;
     wait_for_previous();
     let_next_start();
     const int64_t token = blockIdx.x;
@@ -209,32 +227,37 @@ __global__ void __launch_bounds__(THREADS, BATCH == 1 ? 10 : 5) append_kernel(Ap
             float x[16];
             turn<F16, INTERLEAVED>(p0[b], p1[b], u, x);
             if (p.kind == 0) {
-                store_16bit<F16>(a.q_out + token * a.q_out_token + p.row * a.q_out_head, u, x);
+                store_16bit<F16>(a.q_out + token * a.q_out_token + p.row * a.q_out_head, u, x,
+                                 MANY && a.away);
             } else {
                 const KvcPlane &plane = p.kind == 1 ? a.k_plane : a.v_plane;
                 unsigned char *dst = plane.base + slot + p.row * plane.head_stride;
                 if (E4M3)
-                    store_8bit(dst, u, x, 1.0f / __ldg((p.kind == 1 ? a.k_scale : a.v_scale) + p.row));
+                    store_8bit(dst, u, x, 1.0f / __ldg((p.kind == 1 ? a.k_scale : a.v_scale) + p.row),
+                               MANY && a.away);
                 else
-                    store_16bit<F16>(dst, u, x);
+                    store_16bit<F16>(dst, u, x, MANY && a.away);
             }
         }
     }
 }
 
-// Many tokens: one unit a thread at a time and small register sets, as the blocks on an SM hide one
-// another's waits (39834 tokens of 384 units: 162 us with 1 unit and 10 blocks an SM, 181 with 3
-// and 5). Few: a token is one chain of waits, shorter with all its units asked for at once (64
-// tokens of 640 units: 3.8 us with 3, 4.5 with 1). A block an SM is taken as the border; a token
-// that needs one unit a thread takes the first kind always.
+// Many tokens: blocks of 128 threads, one unit a thread at a time and small register sets, as the blocks
+// on an SM hide one another's waits. Few: a token is one chain of waits, so each unit has a thread of
+// its own, up to 512 and two units a thread. Few and many took (us) 3.0 and 4.0 for 64 tokens of 640
+// units, 4.2 and 5.6 for 256; 2.9 and 3.1 for 300 of 384, 4.9 and 3.8 for 600; and with blocks of 192,
+// 256 and 384 threads 39834 tokens took 186, 190 and 216 where those of 128 took 162.
 template <bool F16, bool E4M3>
-kvr_status go(const AppendArgs &a, bool interleaved, int32_t tokens, int sms, void *stream) {
+kvr_status go(AppendArgs &a, bool interleaved, int32_t tokens, int sms, void *stream) {
     const int64_t n = (int64_t)a.q.heads * a.q_units.d + (int64_t)(a.k.heads + a.v.heads) * a.units.d;
+    const bool many = tokens > BORDER * sms;
+    const int64_t rounds = (n + FEW_THREADS - 1) / FEW_THREADS;
+    const int threads = many ? MANY_THREADS : (int)((n + 32 * rounds - 1) / (32 * rounds)) * 32;
+    a.away = tokens * n * 16 * 2 > (int64_t)AWAY << 20;
     const auto kernel =
-        n <= THREADS || tokens > sms
-            ? (interleaved ? append_kernel<F16, true, E4M3, 1> : append_kernel<F16, false, E4M3, 1>)
-            : (interleaved ? append_kernel<F16, true, E4M3, 3> : append_kernel<F16, false, E4M3, 3>);
-    return kvc_launch(kernel, a, dim3((unsigned)tokens), THREADS, 0, stream);
+        many ? (interleaved ? append_kernel<F16, true, E4M3, true> : append_kernel<F16, false, E4M3, true>)
+             : (interleaved ? append_kernel<F16, true, E4M3, false> : append_kernel<F16, false, E4M3, false>);
+    return kvc_launch(kernel, a, dim3((unsigned)tokens), threads, 0, stream);
 }
 
 }  // namespace

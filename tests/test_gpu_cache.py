@@ -566,6 +566,48 @@ def test_append(H, Q, D, QD, rot, il, last, pool, dtype, B, tokens):
         assert again is q and torch.equal(q[torch.from_numpy(live)], out[torch.from_numpy(live)])
 
 
+@pytest.mark.parametrize("H, Q, D, QD, rot, il, last, pool, dtype, B, tokens",
+                         [c + (1100,) for c in APPEND] +
+                         [APPEND[0] + (6000,), (8, 32, 128, 128, 64, True, False, "e4m3", "f16", 32, 6000)])
+def test_append_of_many_tokens_is_that_of_few(H, Q, D, QD, rot, il, last, pool, dtype, B, tokens):
+    """Bit for bit: what one call writes, calls of 150 of its tokens write."""
+    import torch
+    from prefill_decode_paged_gb300 import KVCache, rotary_table
+    C, R = (1 if D == 576 else 2), 4
+    each = tokens // R
+    width = each // B + 1
+    gen = torch.Generator("cuda").manual_seed(tokens + D)
+    order = torch.randperm(R * width, device="cuda", generator=gen).int()
+    table = order.view(R, width)
+    req = torch.arange(R, device="cuda").repeat_interleave(each).int()
+    pos = torch.arange(each, device="cuda").repeat(R).int()
+    mixed = torch.randperm(R * each, device="cuda", generator=gen)
+    req, pos = req[mixed].contiguous(), pos[mixed].contiguous()
+    pos[::17] = -1
+    T, tt = R * each, torch_type(dtype)
+    k, v, q = (torch.randn(T, h, d, device="cuda", generator=gen).to(tt) for h, d in ((H, D), (H, D), (Q, QD)))
+    angles = torch.from_numpy(rotary_table(each, rot, 10000.0)).cuda() if rot else None
+    kw = dict(rotary=angles, interleaved=il, rotate_last=last)
+    results = []
+    for step in (T, 150):
+        shape = (1, C, R * width, B, H, D)
+        dev = torch.full(shape, 7, dtype=torch.uint8, device="cuda") if pool == "e4m3" else \
+            torch.full(shape, 7.0, dtype=torch_type(pool), device="cuda")
+        out = torch.full_like(q, 5.0) if Q else None
+        with KVCache(dev, num_layers=1, num_components=C, kv_heads=H, head_dim=D, block=B,
+                     num_blocks=R * width, dtype=TYPES[pool],
+                     scales=np.full((1, C), 0.02, np.float32) if pool == "e4m3" else None) as cache:
+            for a in range(0, T, step):
+                b = min(T, a + step)
+                cache.append(0, k[a:b], v[a:b] if C == 2 else None, req[a:b], pos[a:b], table,
+                             q=q[a:b] if Q else None, q_out=out[a:b] if Q else None, **kw)
+            cache.check()
+        results.append((dev, out))
+    assert torch.equal(results[0][0].view(torch.uint8), results[1][0].view(torch.uint8))
+    if Q:
+        assert torch.equal(results[0][1].view(torch.uint8), results[1][1].view(torch.uint8))
+
+
 def test_append_nan_and_saturation_in_eight_bits():
     import torch
     from prefill_decode_paged_gb300 import KVCache
