@@ -82,7 +82,7 @@ struct Cut {
     int32_t total, parts, each, more, group, least;
 
     // `of_request`: jobs of a request. The parts are counted later where group > 0.
-    __device__ __forceinline__ Cut(int32_t total_, int32_t requests, int32_t of_request, int32_t most,
+    __host__ __device__ __forceinline__ Cut(int32_t total_, int32_t requests, int32_t of_request, int32_t most,
                                    int32_t least_, int32_t slack)
         : total(total_), least(least_) {
         const int32_t jobs = requests * of_request;
@@ -97,13 +97,13 @@ struct Cut {
         }
     }
     // parts that a job of so many units has
-    __device__ __forceinline__ int32_t of_job(int32_t units) const {
+    __host__ __device__ __forceinline__ int32_t of_job(int32_t units) const {
         return group == least ? max(1, (int32_t)((uint32_t)units / (uint32_t)least))
                               : (int32_t)((uint32_t)(units + group - 1) / (uint32_t)group);
     }
     // equal parts: where part c begins, and the part that holds unit x
-    __device__ __forceinline__ int32_t start(int32_t c) const { return c * each + min(c, more); }
-    __device__ __forceinline__ int32_t part_of(int32_t x) const {
+    __host__ __device__ __forceinline__ int32_t start(int32_t c) const { return c * each + min(c, more); }
+    __host__ __device__ __forceinline__ int32_t part_of(int32_t x) const {
         const int32_t edge = more * (each + 1);
         return x < edge ? (int32_t)((uint32_t)x / (uint32_t)(each + 1))
                         : more + (int32_t)((uint32_t)(x - edge) / (uint32_t)max(each, 1));
@@ -135,7 +135,7 @@ struct Cut {
         if (lane == 31 && requests == AHEAD_MOST) ahead[requests] = before;
     }
     // units [x, x_end) of part c, none if there is no such part
-    __device__ __forceinline__ void units_of(int32_t c, const int32_t *prefix, const int32_t *ahead,
+    __host__ __device__ __forceinline__ void units_of(int32_t c, const int32_t *prefix, const int32_t *ahead,
                                              int32_t requests, int32_t of_request, int32_t *x,
                                              int32_t *x_end) const {
         *x = *x_end = 0;
@@ -158,7 +158,7 @@ struct Cut {
     }
     // job `job` of request r, whose first unit and number of units are these: its first part, and
     // how many it has
-    __device__ __forceinline__ void parts_of(int32_t r, int32_t job, int32_t first, int32_t units,
+    __host__ __device__ __forceinline__ void parts_of(int32_t r, int32_t job, int32_t first, int32_t units,
                                              const int32_t *ahead, int32_t of_request, int32_t *c0,
                                              int32_t *n) const {
         if (group == 0) {
@@ -176,7 +176,7 @@ struct Segment {
     int32_t r, job, u0, u1, units;
     int32_t job_first;        // the job's first unit in the line
 };
-__device__ __forceinline__ Segment segment_at(int32_t x, int32_t x_end, const int32_t *prefix,
+__host__ __device__ __forceinline__ Segment segment_at(int32_t x, int32_t x_end, const int32_t *prefix,
                                               int32_t requests, int32_t jobs) {
     Segment s;
     int32_t lo = 0, hi = requests - 1;
