@@ -78,5 +78,7 @@ kvr_status kvc_attend_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     // an SM has 228 KB, of which each block takes 1 KB for itself
     const int64_t resident = std::min<int64_t>(k.blocks, (228 << 10) / (int64_t)(smem + 1024));
     const int64_t grid = std::min<int64_t>(resident * kvc_stream_sms(c, stream), all);
+    a.by_chunks = kvr_make_div((uint32_t)a.chunks);
+    a.shape = make_cut_shape(p->num_requests, a.H * a.chunks, (int32_t)grid, SLACK);
     return kvc_launch(k.kernel, a, dim3((unsigned)grid), ATTEND_THREADS, smem, stream);
 }

@@ -57,19 +57,20 @@ struct AttendArgs {
     uint32_t *arrived;
     int32_t m, H, G, D, f16;
     int32_t chunks;           // passes over a job's keys, RP rows each
-    KvrDiv group;             // by G
+    KvrDiv group, by_chunks;  // by G, chunks
+    CutShape shape;
     float scale;
 };
 
 constexpr int ATTEND_WARPS = 4;
 constexpr int ATTEND_THREADS = 32 * ATTEND_WARPS;
-// Units that a part has at least, and that a change of job costs (cache_split.cuh). Parts of 1, 2, 4 and 8 units (us): one request of 4096 keys, 8 heads of 8 queries,
+// Units that a change of job costs (cache_split.cuh). Parts with at least 1, 2, 4 and 8 units (us): one request of 4096 keys, 8 heads of 8 queries,
 // 15.7, 12.7, 11.6, 14.0; its 4 newest tokens 62, 39, 31, 32; 16 requests of 512 keys 15.8, 15.5,
 // 12.7, 11.8; one of 1024 keys 8.0, 8.1, 9.4, 11.8. Parts within jobs took 49.1 where equal ones took
 // 52.1 (4 requests of 32768 keys, 4 heads), 27.4 for 33.3 (8 of 16 to 8192, 8 heads), 23.8 for 26.7
 // (48 of a window of 1024, 32 rows), and with a group 5 above the equal parts' 48.6 for 51.5 (8 of
 // 8192, 8 heads); where nothing was to be gained 0.3 to 0.8 more.
-constexpr int LEAST = 4, SLACK = 8;
+constexpr int SLACK = 8;
 constexpr float P_SHIFT = 10.0f;      // log2 of P's scale in f16
 // how far (as a power of two) P may exceed its scale before a new maximum is taken: f16 P ends at
 // 2^16; bf16 reaches further, but 40 was no faster, and O of values up to 2^110 has to stay finite
@@ -232,13 +233,13 @@ attend_kernel(AttendArgs a) {
     unit_prefix<C::UNIT>(a.split, KT, prefix, shared_int);
     const int32_t HJ = a.H * a.chunks;
     const int32_t total = prefix[a.split.requests] * HJ;
-    const Cut cut(total, a.split.requests, HJ, (int32_t)gridDim.x, LEAST, SLACK);
+    const Cut cut(total, a.shape);
     if (cut.group > 0) {
         if (warp == 0) cut.count(prefix, a.split.requests, ahead);
         __syncthreads();
     }
     int32_t x, x_end;
-    cut.units_of(blockIdx.x, prefix, ahead, a.split.requests, HJ, &x, &x_end);
+    int32_t known = cut.units_of(blockIdx.x, prefix, ahead, a.shape, &x, &x_end);
 
     const int32_t M = a.m * a.G;
     const int32_t slot_floats = RP * (a.D + 2);
@@ -246,10 +247,11 @@ attend_kernel(AttendArgs a) {
     const float log2e = 1.4426950408889634f;
 
     while (x < x_end) {
-        const Segment seg = segment_at(x, x_end, prefix, a.split.requests, HJ);
+        const Segment seg = segment_at(x, x_end, prefix, a.shape, known);
+        known = -1;
         const int32_t r = seg.r, job = seg.job, u0 = seg.u0, u1 = seg.u1, units = seg.units;
         x += u1 - u0;
-        const int32_t h = job / a.chunks, row0 = (job - h * a.chunks) * RP;
+        const int32_t h = (int32_t)a.by_chunks.div((uint32_t)job), row0 = (job - h * a.chunks) * RP;
         const int32_t rows = min(RP, M - row0);
         uint32_t bad = 0;
         const Span sp = span_of(a.split, r, KT, &bad);
@@ -641,7 +643,7 @@ attend_kernel(AttendArgs a) {
         if (!whole) {
             // the job's parts: the blocks that hold its first and its last unit, and all between
             int32_t c0, n;
-            cut.parts_of(r, job, seg.job_first, units, ahead, HJ, &c0, &n);
+            cut.parts_of(r, job, seg.job_first, units, ahead, a.shape, &c0, &n);
             __syncthreads();
             if (tid == 0) {
                 // (fences by one thread cover what the barriers order before and after it)

@@ -111,6 +111,7 @@ struct LatentArgs {
     int32_t *prefix, *ahead;  // [requests + 1], what the first block counted, for the join
     int32_t m, Hq, chunks, parts;
     KvrDiv heads;             // by Hq
+    CutShape shape;
     float scale;
 };
 
@@ -293,13 +294,13 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return d;
 }
 
-// Units (tiles) that a part has at least, and that a change of job costs (cache_split.cuh). Parts
+// Units (tiles) that a change of job costs (cache_split.cuh). Parts
 // within jobs took (us) 37.6 where equal ones took 41.7 (8 requests of 8192 latents, 128 heads), 25.3
 // for 28.8 (2 of 8192), 21.3 for 23.0 (9 of up to 6001, 32 rows); groups 10 above the equal parts 39.9
 // for 34.7 (19 of 4096, 64 heads).
-constexpr int LEAST = 4, SLACK = 8;
+constexpr int SLACK = 8;
 __device__ __forceinline__ Cut cut_of(const LatentArgs &a, const int32_t *prefix) {
-    return Cut(prefix[a.split.requests] * a.chunks, a.split.requests, a.chunks, a.parts, LEAST, SLACK);
+    return Cut(prefix[a.split.requests] * a.chunks, a.shape);
 }
 
 // -- the kernel -------------------------------------------------------------------
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
         }
     const int32_t part = blockIdx.x / 2;
     int32_t x, x_end;
-    cut.units_of(part, prefix, ahead, a.split.requests, a.chunks, &x, &x_end);
+    int32_t known = cut.units_of(part, prefix, ahead, a.shape, &x, &x_end);
     const int32_t M = a.m * a.Hq;
 
     // a thread's query row in a segment: lane of tensor memory, row of the pass
@@ -401,7 +402,8 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
         uint32_t it = 0, segments = 0;            // tiles and segments so far
         bool ok = true;
         while (ok && x < x_end) {
-            const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
+            const Segment seg = segment_at(x, x_end, prefix, a.shape, known);
+            known = -1;
             const uint32_t n = (uint32_t)(seg.u1 - seg.u0);
             x += n;
             uint32_t bad = 0;
@@ -576,7 +578,8 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
         uint32_t it = 0;
         bool ok = true;
         while (ok && x < x_end) {
-            const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
+            const Segment seg = segment_at(x, x_end, prefix, a.shape, known);
+            known = -1;
             const uint32_t n = (uint32_t)(seg.u1 - seg.u0);
             x += n;
             // (S of every tile so far was waited for below: no product reads the q before)
@@ -633,7 +636,8 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
         uint32_t it = 0;
         bool ok = true;
         while (ok && x < x_end) {
-            const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
+            const Segment seg = segment_at(x, x_end, prefix, a.shape, known);
+            known = -1;
             x += seg.u1 - seg.u0;
             for (int32_t u = seg.u0; u < seg.u1; ++u, ++it) {
                 if (!(ok = wait(bar(X_READ + it % SBUF), (it / SBUF) & 1))) break;
@@ -652,7 +656,8 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
         bool ok = true;
         const unsigned char *src = a.plane.base;
         while (ok && x < x_end) {
-            const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
+            const Segment seg = segment_at(x, x_end, prefix, a.shape, known);
+            known = -1;
             const uint32_t n = (uint32_t)(seg.u1 - seg.u0);
             x += n;
             const Span sp = span_of(a.split, seg.r, KT, &bad);
@@ -756,7 +761,8 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
         uint32_t it = 0, segments = 0;
         bool ok = true;
         while (ok && x < x_end) {
-            const Segment seg = segment_at(x, x_end, prefix, a.split.requests, a.chunks);
+            const Segment seg = segment_at(x, x_end, prefix, a.shape, known);
+            known = -1;
             const uint32_t n = (uint32_t)(seg.u1 - seg.u0);
             x += n;
             if (warp < VALS) {
@@ -864,7 +870,7 @@ __global__ void __launch_bounds__(JOIN_SET * SETS) latent_join(const __grid_cons
     const int32_t before = a.prefix[r], units = a.prefix[r + 1] - before;
     const int32_t first = before * a.chunks + job * units;
     int32_t c0, n;
-    cut.parts_of(r, job, first, units, a.ahead, a.chunks, &c0, &n);
+    cut.parts_of(r, job, first, units, a.ahead, a.shape, &c0, &n);
     if (n == 1) return;
     const bool mine = rho < M;
     auto slot = [&](int32_t c) { return a.partial + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * SLOT; };
@@ -1032,6 +1038,7 @@ kvr_status kvc_latent_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     const int32_t sms = kvc_stream_sms(c, stream);
     a.parts = (int32_t)std::min<int64_t>(std::clamp(sms / 2, 1, PARTS_MOST),
                                          most * p->num_requests * a.chunks);
+    a.shape = make_cut_shape(p->num_requests, a.chunks, a.parts, SLACK);
     const bool f16 = c->d.dtype == KVC_DTYPE_F16;
     const size_t smem = OFF_PREFIX + 4 * (size_t)(p->num_requests + 1);
     const kvr_status st = kvc_launch(f16 ? latent_kernel<true> : latent_kernel<false>, a,

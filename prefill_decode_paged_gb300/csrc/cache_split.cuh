@@ -68,37 +68,50 @@ __device__ __forceinline__ void unit_prefix(const SplitArgs &a, int32_t align, i
     __syncthreads();
 }
 
-// The line's cut into parts. A part has `least` units at least, but in jobs that have fewer, as
+// The line's cut into parts. A part has LEAST units at least, but in jobs that have fewer, as
 // each costs its job a share of the join.
 //
 // Equal parts (group 0): the first `more` have one unit more than the others. Parts within jobs:
 // a job of u units is cut into ceil(u / group) equal ones, with the smallest group that at most
 // `most` parts come of whatever the lengths are: sum ceil(u / group) <= (total + jobs (group - 1)) /
-// group <= most. (With room for more, the fewer that have `least` units.) A change of job within a
+// group <= most. (With room for more, the fewer that have LEAST units.) A change of job within a
 // part costs the part a new start, as long as `slack` units take.
+//
+// (What the host knows of the divisors comes as multipliers: all this lies before a block's first
+// load, and a division takes a hundred cycles.)
+constexpr int32_t LEAST = 4;
 constexpr int32_t AHEAD_MOST = 128;       // requests up to which parts may be within jobs
 
-struct Cut {
-    int32_t total, parts, each, more, group, least;
+struct CutShape {
+    int32_t requests, of_request, most, slack;   // of_request: jobs of a request
+    KvrDiv by_jobs, by_most, by_rest;            // by of_request, most, and most - jobs
+};
+inline CutShape make_cut_shape(int32_t requests, int32_t of_request, int32_t most, int32_t slack) {
+    const int64_t jobs = (int64_t)requests * of_request;
+    return {requests, of_request, most, slack, kvr_make_div((uint32_t)of_request),
+            kvr_make_div((uint32_t)most), kvr_make_div(jobs < most ? (uint32_t)(most - jobs) : 1u)};
+}
 
-    // `of_request`: jobs of a request. The parts are counted later where group > 0.
-    __host__ __device__ __forceinline__ Cut(int32_t total_, int32_t requests, int32_t of_request, int32_t most,
-                                   int32_t least_, int32_t slack)
-        : total(total_), least(least_) {
-        const int32_t jobs = requests * of_request;
-        parts = min(most, max(total / least, jobs));
-        each = (int32_t)((uint32_t)total / (uint32_t)parts);
+struct Cut {
+    int32_t total, parts, each, more, group;
+
+    // The parts are counted later where group > 0.
+    __host__ __device__ __forceinline__ Cut(int32_t total_, const CutShape &s) : total(total_) {
+        const int32_t jobs = s.requests * s.of_request;
+        parts = min(s.most, max(total / LEAST, jobs));
+        each = parts == s.most ? (int32_t)s.by_most.div((uint32_t)total)
+                               : (int32_t)((uint32_t)total / (uint32_t)parts);
         more = total - each * parts;
         group = 0;
-        if (jobs > 1 && jobs < most && requests <= AHEAD_MOST && total > jobs * least) {
+        if (jobs > 1 && jobs < s.most && s.requests <= AHEAD_MOST && total > jobs * LEAST) {
             const int32_t g =
-                max(least, (int32_t)((uint32_t)(total - jobs + most - jobs - 1) / (uint32_t)(most - jobs)));
-            if (g <= each + slack) group = g;
+                max(LEAST, (int32_t)s.by_rest.div((uint32_t)(total - jobs + s.most - jobs - 1)));
+            if (g <= each + s.slack) group = g;
         }
     }
     // parts that a job of so many units has
     __host__ __device__ __forceinline__ int32_t of_job(int32_t units) const {
-        return group == least ? max(1, (int32_t)((uint32_t)units / (uint32_t)least))
+        return group == LEAST ? max(1, units / LEAST)
                               : (int32_t)((uint32_t)(units + group - 1) / (uint32_t)group);
     }
     // equal parts: where part c begins, and the part that holds unit x
@@ -134,39 +147,41 @@ struct Cut {
         }
         if (lane == 31 && requests == AHEAD_MOST) ahead[requests] = before;
     }
-    // units [x, x_end) of part c, none if there is no such part
-    __host__ __device__ __forceinline__ void units_of(int32_t c, const int32_t *prefix, const int32_t *ahead,
-                                             int32_t requests, int32_t of_request, int32_t *x,
-                                             int32_t *x_end) const {
+    // units [x, x_end) of part c, none if there is no such part; the request of x, or -1: unknown
+    __host__ __device__ __forceinline__ int32_t units_of(int32_t c, const int32_t *prefix,
+                                                         const int32_t *ahead, const CutShape &s,
+                                                         int32_t *x, int32_t *x_end) const {
         *x = *x_end = 0;
         if (group == 0) {
             if (c < parts) *x = start(c), *x_end = start(c + 1);
-        } else if (c < ahead[requests] * of_request) {
-            int32_t lo = 0, hi = requests - 1;
-            const int32_t cj = (int32_t)((uint32_t)c / (uint32_t)of_request);
-            while (lo < hi) {
-                const int32_t mid = (lo + hi + 1) / 2;
-                if (ahead[mid] <= cj) lo = mid; else hi = mid - 1;
-            }
-            const int32_t units = prefix[lo + 1] - prefix[lo], n = ahead[lo + 1] - ahead[lo];
-            const int32_t at = c - ahead[lo] * of_request;
-            const int32_t job = (int32_t)((uint32_t)at / (uint32_t)n), k = at - job * n;
-            const int32_t size = (int32_t)((uint32_t)units / (uint32_t)n), rest = units - size * n;
-            *x = prefix[lo] * of_request + job * units + k * size + min(k, rest);
-            *x_end = *x + size + (k < rest ? 1 : 0);
+            return -1;
         }
+        if (c >= ahead[s.requests] * s.of_request) return -1;
+        int32_t lo = 0, hi = s.requests - 1;
+        const int32_t cj = (int32_t)s.by_jobs.div((uint32_t)c);
+        while (lo < hi) {
+            const int32_t mid = (lo + hi + 1) / 2;
+            if (ahead[mid] <= cj) lo = mid; else hi = mid - 1;
+        }
+        const int32_t units = prefix[lo + 1] - prefix[lo], n = ahead[lo + 1] - ahead[lo];
+        const int32_t at = c - ahead[lo] * s.of_request;
+        const int32_t job = (int32_t)((uint32_t)at / (uint32_t)n), k = at - job * n;
+        const int32_t size = (int32_t)((uint32_t)units / (uint32_t)n), rest = units - size * n;
+        *x = prefix[lo] * s.of_request + job * units + k * size + min(k, rest);
+        *x_end = *x + size + (k < rest ? 1 : 0);
+        return lo;
     }
     // job `job` of request r, whose first unit and number of units are these: its first part, and
     // how many it has
     __host__ __device__ __forceinline__ void parts_of(int32_t r, int32_t job, int32_t first, int32_t units,
-                                             const int32_t *ahead, int32_t of_request, int32_t *c0,
+                                             const int32_t *ahead, const CutShape &s, int32_t *c0,
                                              int32_t *n) const {
         if (group == 0) {
             *c0 = part_of(first);
             *n = part_of(first + units - 1) - *c0 + 1;
         } else {
             *n = of_job(units);
-            *c0 = ahead[r] * of_request + job * *n;
+            *c0 = ahead[r] * s.of_request + job * *n;
         }
     }
 };
@@ -176,11 +191,12 @@ struct Segment {
     int32_t r, job, u0, u1, units;
     int32_t job_first;        // the job's first unit in the line
 };
+// `known`: the request of x, or -1.
 __host__ __device__ __forceinline__ Segment segment_at(int32_t x, int32_t x_end, const int32_t *prefix,
-                                              int32_t requests, int32_t jobs) {
+                                                       const CutShape &shape, int32_t known = -1) {
     Segment s;
-    int32_t lo = 0, hi = requests - 1;
-    const int32_t xj = (int32_t)((uint32_t)x / (uint32_t)jobs);
+    int32_t lo = known < 0 ? 0 : known, hi = known < 0 ? shape.requests - 1 : known;
+    const int32_t jobs = shape.of_request, xj = (int32_t)shape.by_jobs.div((uint32_t)x);
     while (lo < hi) {
         const int32_t mid = (lo + hi + 1) / 2;
         if (prefix[mid] <= xj) lo = mid; else hi = mid - 1;

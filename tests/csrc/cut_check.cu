@@ -17,8 +17,8 @@ using namespace kvc;
 #define REQUIRE(x)                                                              \
     do {                                                                        \
         if (!(x)) {                                                             \
-            printf("%s: %d requests, %d jobs, %d blocks, least %d, slack %d\n", #x, \
-                   requests, jobs, most, least, slack);                         \
+            printf("%s: %d requests, %d jobs, %d blocks, slack %d\n", #x, requests, \
+                   jobs, most, slack);                                          \
             return 1;                                                           \
         }                                                                       \
     } while (0)
@@ -30,11 +30,12 @@ int main() {
     for (int trial = 0; trial < 4000; ++trial) {
         const int requests = trial % 5 == 0 ? pick({1, 127, 128, 129}) : 1 + (int)(rng() % 140);
         const int jobs = pick({1, 2, 3, 8}), most = pick({1, 2, 76, 152, 304});
-        const int least = pick({1, 4}), slack = pick({0, 8, 50}), longest = pick({1, 3, 20, 200, 3000});
+        const int slack = pick({0, 8, 50}), longest = pick({1, 3, 20, 200, 3000});
         std::vector<int32_t> prefix(requests + 1, 0), ahead(requests + 1, 0);
         for (int r = 0; r < requests; ++r) prefix[r + 1] = prefix[r] + 1 + (int)(rng() % longest);
         const int32_t total = prefix[requests] * jobs;
-        const Cut cut(total, requests, jobs, most, least, slack);
+        const CutShape shape = make_cut_shape(requests, jobs, most, slack);
+        const Cut cut(total, shape);
         (cut.group > 0 ? within : across) += 1;
         if (cut.group > 0)
             for (int r = 0; r < requests; ++r) ahead[r + 1] = ahead[r] + cut.of_job(prefix[r + 1] - prefix[r]);
@@ -45,11 +46,12 @@ int main() {
         int32_t at = 0;
         for (int32_t c = 0; c < most; ++c) {
             int32_t x, x_end;
-            cut.units_of(c, prefix.data(), ahead.data(), requests, jobs, &x, &x_end);
+            int32_t known = cut.units_of(c, prefix.data(), ahead.data(), shape, &x, &x_end);
             REQUIRE(x == at || x == x_end);
             int segments = 0;
             while (x < x_end) {
-                const Segment s = segment_at(x, x_end, prefix.data(), requests, jobs);
+                const Segment s = segment_at(x, x_end, prefix.data(), shape, known);
+                known = -1;
                 REQUIRE(s.r >= 0 && s.r < requests && s.job >= 0 && s.job < jobs);
                 REQUIRE(s.units == prefix[s.r + 1] - prefix[s.r]);
                 REQUIRE(s.job_first == prefix[s.r] * jobs + s.job * s.units && s.job_first + s.u0 == x);
@@ -67,7 +69,7 @@ int main() {
             for (int j = 0; j < jobs; ++j) {
                 const int32_t units = prefix[r + 1] - prefix[r];
                 int32_t c0, n;
-                cut.parts_of(r, j, prefix[r] * jobs + j * units, units, ahead.data(), jobs, &c0, &n);
+                cut.parts_of(r, j, prefix[r] * jobs + j * units, units, ahead.data(), shape, &c0, &n);
                 const std::vector<int32_t> &p = parts[(size_t)r * jobs + j];
                 REQUIRE((int32_t)p.size() == n);
                 for (int k = 0; k < n; ++k) REQUIRE(p[k] == c0 + k);
