@@ -30,8 +30,8 @@
 // alone: 11 bits against the output's rounding and the codes' 4 bits. P is scaled by 2^10 in f16
 // so that weights down to 2^-24 of the largest are normal numbers.
 //
-// Measured, 8 queries a key head of 128: 4 requests of 32768 keys, 4 heads, bf16 (268 MB) 48.7 us,
-// 5.5 TB/s; one of 131072, 8 heads, E4M3 (268 MB) 54 us, 5.0 TB/s; 64 of 8192, 8 heads, bf16 (2.1 GB)
+// Measured, 8 queries a key head of 128: 4 requests of 32768 keys, 4 heads, bf16 (268 MB) 48 us,
+// 5.6 TB/s; one of 131072, 8 heads, E4M3 (268 MB) 53 us, 5.1 TB/s; 64 of 8192, 8 heads, bf16 (2.1 GB)
 // 322 us, 6.68 TB/s, and with 4 newest tokens, 32 rows, 381 us. What is lost below a plain copy's
 // rate is fixed: 5 us from the launch to the first keys (lengths, block ids, keys, each after the one
 // before), 6 us from the first block's end to the last's, as not all SMs are as near to all of
