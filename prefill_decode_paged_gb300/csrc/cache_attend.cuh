@@ -465,7 +465,7 @@ attend_kernel(AttendArgs a) {
                             if (mixed) {
                                 const int32_t j = j0 + k * 16 + u * 8 + g;
                                 if (j >= end[n][e] ||
-                                    (a.split.window > 0 && j < end[n][e] - a.split.window))
+                                    (a.split.window > 0 && j < window_from(end[n][e], a.split.window)))
                                     v = -INFINITY;
                             }
                             best[n][e] = fmaxf(best[n][e], v);

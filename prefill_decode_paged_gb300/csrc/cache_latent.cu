@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                 if (j0 + KT > seen_all || j0 < seen_from) {
 #pragma unroll
                     for (int e = 0; e < KT; ++e)
-                        if (j0 + e >= end || (a.split.window > 0 && j0 + e < end - a.split.window))
+                        if (j0 + e >= end || (a.split.window > 0 && j0 + e < window_from(end, a.split.window)))
                             s[e] = 0xFF800000u;   // -infinity
                 }
                 float best = -INFINITY, more = -INFINITY;

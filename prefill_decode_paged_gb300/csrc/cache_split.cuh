@@ -22,18 +22,28 @@ struct SplitArgs {
     int32_t requests, m, window;
 };
 
-// `align`: lo is a multiple of it. A length out of range counts as the nearest in range.
+// The first key that a query which sees the keys below `end` sees. (A window may be any positive
+// int32 and `end` negative, for a token before a short request's first: their difference may not
+// be taken as it is.)
+__host__ __device__ __forceinline__ int32_t window_from(int32_t end, int32_t window) {
+    return max(end, 0) - window;
+}
+
+// The keys of a request of n tokens, of which the newest m attend; `lo` is a multiple of `align`.
+__host__ __device__ __forceinline__ Span span_of(int32_t n, int32_t m, int32_t window, int32_t align) {
+    return {n, window > 0 ? max(0, window_from(n - m + 1, window)) / align * align : 0};
+}
+
+// Request r's. A length out of range counts as the nearest in range.
 __device__ __forceinline__ Span span_of(const SplitArgs &a, int32_t r, int32_t align,
                                         uint32_t *bad) {
-    Span s;
-    s.n = __ldg(a.lengths + r);
+    int32_t n = __ldg(a.lengths + r);
     const int32_t most = a.slots.width * (int32_t)a.slots.block.d;
-    if (s.n < 0 || s.n > most) {
+    if (n < 0 || n > most) {
         *bad = KVC_FLAG_LENGTH;
-        s.n = s.n < 0 ? 0 : most;
+        n = n < 0 ? 0 : most;
     }
-    s.lo = a.window > 0 ? max(0, s.n - a.m + 1 - a.window) / align * align : 0;
-    return s;
+    return span_of(n, a.m, a.window, align);
 }
 
 // prefix[r] = units of one job of each of the requests before r (at least one a request, so that
