@@ -147,8 +147,10 @@ kvr_status kv_cache_append(const kvc_cache *cache, int32_t layer, const kvc_appe
  * g / (Hq / H). With x_j = scale * q . k_j over the keys it sees,
  *   out = sum_j exp(x_j - lse) v_j,   lse = log sum_j exp(x_j)   (natural logarithm).
  * A query that sees nothing (p < 0) gives out = 0 and lse = -infinity. What the cache holds at
- * places that no query of the request sees is never used, NaN included; a NaN or an infinity
- * in a value at a place that only some of a request's newest tokens see may reach the others.
+ * places that no query of the request sees (beyond its length, or below its newest tokens'
+ * windows) is never used, NaN included, and table entries of blocks that hold such places only
+ * are not looked at; a NaN or an infinity in a value at a place that only some of a request's
+ * newest tokens see may reach the others.
  * Weights below 2^-24 of a row's largest count as zero where the cache holds f16 or E4M3.
  * Requirements: q and out of `dtype` (the pool's type if that has 16 bits), rows contiguous,
  * every address and stride a multiple of 16 bytes; lse NULL or [R][num_new][Hq], contiguous.

@@ -230,7 +230,7 @@ attend_kernel(AttendArgs a) {
     wait_for_previous();
     let_next_start();
 
-    unit_prefix<C::UNIT>(a.split, KT, prefix, shared_int);
+    unit_prefix<C::UNIT>(a.split, 1, prefix, shared_int);
     const int32_t HJ = a.H * a.chunks;
     const int32_t total = prefix[a.split.requests] * HJ;
     const Cut cut(total, a.shape);
@@ -254,7 +254,7 @@ attend_kernel(AttendArgs a) {
         const int32_t h = (int32_t)a.by_chunks.div((uint32_t)job), row0 = (job - h * a.chunks) * RP;
         const int32_t rows = min(RP, M - row0);
         uint32_t bad = 0;
-        const Span sp = span_of(a.split, r, KT, &bad);
+        const Span sp = span_of(a.split, r, 1, &bad);   // tiles begin at the first key
         const float ks = POOL == KVR_DTYPE_FP8_E4M3 ? a.k_scale[h] : 1.0f;
 
         // this warp's tiles; the lane's key of a tile (lane < KT) and its slot

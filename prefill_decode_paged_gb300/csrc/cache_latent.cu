@@ -26,8 +26,8 @@
 // other SM sends. A tile is laid out in 128-byte rows of 64 elements (swizzled), which serve as
 // the K-major operand of S and as the MN-major operand of O. Tiles come by the copy engine, in
 // boxes of a block's tokens, where blocks are multiples of 8 tokens that divide a tile or are
-// divided by it; a request's last, partial tile, and all tiles of other block sizes, come row by
-// row by 16-byte cp.async, with zeros for the rows beyond the length. (By cp.async alone the load
+// divided by it; a request's last, partial tile, a window's first, and all tiles of other block sizes,
+// come row by row by 16-byte cp.async, with zeros for the rows that no query sees. (By cp.async alone the load
 // and store units were what the kernel waited for.)
 //
 // Warps: two times 4 of softmax (one thread a row; every second tile), 4 that send S to the other
@@ -662,15 +662,17 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
             x += n;
             const Span sp = span_of(a.split, seg.r, KT, &bad);
             const int32_t *table = a.split.slots.ids + (int64_t)seg.r * a.split.slots.stride;
-            // tiles that lie in the request as a whole come in boxes, if there are any
+            // tiles of which all keys are seen come in boxes, if there are any: [full, whole)
+            const int32_t full = sp.first > sp.lo ? 1 : 0;
             const int32_t whole = a.piece > 0 ? min(seg.u1, (sp.n - sp.lo) / KT) : 0;
+            auto boxed = [&](int32_t u) { return u >= full && u < whole; };
             const int32_t pieces = a.piece > 0 ? KT / a.piece : 0;
             // the block id that this lane looks up for tile u: of box piece `lane`, or of its key.
             // It is asked for a turn ahead and not looked at before.
             auto position = [&](int32_t u) -> int32_t {
-                if (u < whole) return lane < pieces ? sp.lo + u * KT + lane * a.piece : -1;
+                if (boxed(u)) return lane < pieces ? sp.lo + u * KT + lane * a.piece : -1;
                 const int32_t j = sp.lo + u * KT + lane;
-                return u < seg.u1 && j < sp.n ? j : -1;
+                return u < seg.u1 && j >= sp.first && j < sp.n ? j : -1;
             };
             auto look_up = [&](int32_t j) -> int32_t {
                 return j < 0 ? 0 : __ldg(table + a.split.slots.block.div((uint32_t)j));
@@ -683,16 +685,16 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                 int32_t id = next;
                 next = look_up(position(u + 4));
                 if (!(ok = wait(bar(K_EMPTY + stage), (i / STAGES + 1) & 1))) break;
-                const uint32_t base = smem0 + stage * STAGE, full = bar(K_FULL + stage);
+                const uint32_t base = smem0 + stage * STAGE, filled = bar(K_FULL + stage);
                 const int32_t j = position(u);
                 const bool there = j >= 0 && id >= 0 && id < a.split.slots.num_blocks;
                 if (j >= 0 && !there) bad |= KVC_FLAG_BLOCK;
                 const int32_t token =
                     max(j, 0) - (int32_t)(a.split.slots.block.div((uint32_t)max(j, 0)) * a.split.slots.block.d);
-                if (u < whole) {
+                if (boxed(u)) {
                     if (!there) id = a.split.slots.num_blocks;    // past the last: zeros
                     if (leader)
-                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full),
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(filled),
                                      "r"(STAGE)
                                      : "memory");
                     for (int piece = 0; piece < pieces; ++piece) {
@@ -702,9 +704,9 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
 #pragma unroll
                             for (int c = 0; c < 4; ++c)
                                 load_box(base + c * CHUNK + piece * a.piece * 128, &a.values,
-                                         (int32_t)rank * HALF + c * 64, first, block, full);
+                                         (int32_t)rank * HALF + c * 64, first, block, filled);
                             load_box(base + 4 * CHUNK + piece * a.piece * 64, &a.rest,
-                                     VALUES + (int32_t)rank * REST, first, block, full);
+                                     VALUES + (int32_t)rank * REST, first, block, filled);
                         }
                     }
                     __syncwarp();
@@ -733,14 +735,14 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                                  : "memory");
                 }
                 if (a.piece > 0) {
-                    // a request's last tile
+                    // a request's last tile, or a window's first
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0) bar_arrive(full);
+                    if (lane == 0) bar_arrive(filled);
                 } else {
                     // arrives when this thread's copies so far have
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(filled) : "memory");
                 }
             }
             it += n;

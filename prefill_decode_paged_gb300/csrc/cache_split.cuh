@@ -10,9 +10,10 @@
 
 namespace kvc {
 
-// A request's keys that some of its newest tokens see: [lo, n).
+// A request's keys that some of its newest tokens see: [first, n). What lies below is not read, and
+// its block may be gone from the table. Tiles begin at `lo`, which may be a little before `first`.
 struct Span {
-    int32_t n, lo;
+    int32_t n, lo, first;
 };
 
 struct SplitArgs {
@@ -29,9 +30,11 @@ __host__ __device__ __forceinline__ int32_t window_from(int32_t end, int32_t win
     return max(end, 0) - window;
 }
 
-// The keys of a request of n tokens, of which the newest m attend; `lo` is a multiple of `align`.
+// The keys of a request of n tokens, of which the newest m attend; `lo` is the multiple of `align`
+// next below (1: the first key itself).
 __host__ __device__ __forceinline__ Span span_of(int32_t n, int32_t m, int32_t window, int32_t align) {
-    return {n, window > 0 ? max(0, window_from(n - m + 1, window)) / align * align : 0};
+    const int32_t first = window > 0 ? max(0, window_from(n - m + 1, window)) : 0;
+    return {n, first / align * align, first};
 }
 
 // Request r's. A length out of range counts as the nearest in range.

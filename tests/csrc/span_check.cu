@@ -28,7 +28,7 @@ int main() {
                 for (int64_t align : {1, 16, 32}) {
                     const int64_t first = std::max<int64_t>(0, n - m + 1 - w);
                     const Span s = span_of((int32_t)n, (int32_t)m, (int32_t)w, (int32_t)align);
-                    bool good = s.n == n && s.lo == first / align * align;
+                    bool good = s.n == n && s.first == first && s.lo == first / align * align;
                     // a query that sees a key: where its window begins
                     for (int64_t i = 0; i < m; i += m > 9 ? 511 : 1) {
                         const int64_t end = n - m + i + 1;
@@ -44,7 +44,7 @@ int main() {
                 }
     for (int64_t n : lengths) {
         const Span s = span_of((int32_t)n, 4, 0, 32);
-        if (s.n != n || s.lo != 0) return 1;
+        if (s.n != n || s.lo != 0 || s.first != 0) return 1;
     }
     printf("%d\n", checked);
     return 0;
