@@ -84,7 +84,8 @@ kvr_status kv_cache_workspace_bytes(const kvc_desc *desc, int32_t sm_count, int6
  * its tokens [k * B, (k + 1) * B). */
 typedef struct kvc_table {
     const int32_t *ids;        /* device [rows][width] */
-    int64_t stride;            /* entries between rows, >= width */
+    int64_t stride;            /* entries between rows, >= 0 (rows may overlap: one row for all
+                                  requests has a stride of 0) */
     int32_t rows;
     int32_t width;
 } kvc_table;

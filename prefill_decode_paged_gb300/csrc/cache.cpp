@@ -176,7 +176,7 @@ bool on_device(const kvc_cache *c) {
 }
 
 bool ok_table(const kvc_table &t) {
-    return t.rows >= 0 && t.width >= 0 && t.stride >= t.width &&
+    return t.rows >= 0 && t.width >= 0 && t.stride >= 0 &&
            (t.ids != nullptr || t.rows == 0 || t.width == 0) && (uintptr_t)t.ids % 4 == 0;
 }
 

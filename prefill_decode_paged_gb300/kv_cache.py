@@ -225,7 +225,7 @@ class KVCache:
                 return t.data_ptr(), width, rows, width
             stride, one = t.stride()
             if one == 1 or width <= 1:
-                return t.data_ptr(), max(stride, width) if rows > 1 else width, rows, width
+                return t.data_ptr(), stride, rows, width     # (rows may overlap: they are only read)
         raise ValueError(f"block table is {t.dtype} {list(t.shape)} on {t.device}; expected "
                          f"int32 [rows][width] on {self._device}, rows contiguous")
 
