@@ -130,6 +130,10 @@ class KVCache:
     the workspace of the attention calls; calls on different streams that share a cache must
     be ordered. Tensors that the calls do not hold for are ValueErrors, what the C library
     refuses is a KVRelayoutError.
+
+    Calls run on torch's current stream, or on ``stream`` (a torch stream or a handle). Results that a
+    call makes belong to that stream, as those of torch's own operations do: used on another one,
+    they need its order and ``record_stream``; and so do inputs of another stream.
     """
 
     def __init__(self, pool, *, num_layers, num_components, kv_heads, head_dim, block,
@@ -194,6 +198,17 @@ class KVCache:
         if self._h is None:
             raise RuntimeError("cache already closed")
         return self._h
+
+    def _new(self, shape, dtype, stream):
+        """A result's memory, from the allocator's share of the stream that the kernel writes it on: memory
+        of torch's current stream may still be in use by what is queued there."""
+        if stream is None:
+            return self._torch.empty(shape, dtype=dtype, device=self._device)
+        cuda, handle = self._torch.cuda, _stream_handle(stream) or 0
+        on = cuda.ExternalStream(handle, device=self._device) if handle > 1 else \
+            cuda.default_stream(self._device)              # (0 and 1: the legacy default stream)
+        with cuda.stream(on):
+            return self._torch.empty(shape, dtype=dtype, device=self._device)
 
     def _rows(self, t, name, shape, dtype=None):
         """Byte strides of a tensor of head rows but the last dimension's, once it is checked."""
@@ -271,7 +286,7 @@ class KVCache:
             qs = plain if q.dtype is dtype and q.is_contiguous() and q.get_device() == index else \
                 self._rows(q, "q", shape, dtype)
             if q_out is None:
-                q_out = self._torch.empty(shape, dtype=dtype, device=q.device)
+                q_out = self._new(shape, dtype, stream)
             os = plain if q_out.dtype is dtype and q_out.shape == shape and q_out.is_contiguous() and \
                 q_out.get_device() == index else self._rows(q_out, "q_out", shape, dtype)
             qp, qo = q.data_ptr(), q_out.data_ptr()
@@ -316,14 +331,14 @@ class KVCache:
             qs = qs if n == 4 else (qs[0], 0, qs[1])
         line = rows + (self.value_dim,)
         if out is None:
-            out = self._torch.empty(line, dtype=dtype, device=q.device)
+            out = self._new(line, dtype, stream)
         if out.dtype is dtype and out.shape == line and out.is_contiguous() and out.get_device() == index:
             os = m * heads * out_row, heads * out_row, out_row
         else:
             os = self._rows(out, "out", line, dtype)
             os = os if n == 4 else (os[0], 0, os[1])
         if lse is None:
-            lse = self._torch.empty(rows, dtype=self._f32, device=q.device)
+            lse = self._new(rows, self._f32, stream)
         if lse is False:
             lse, lp = None, 0
         elif lse.dtype is self._f32 and lse.shape == rows and lse.is_contiguous() and \
