@@ -74,6 +74,7 @@ typedef struct kvc_cache kvc_cache;
  * NULL on failure.
  */
 kvr_status kv_cache_create(const kvc_desc *desc, kvc_cache **out);
+/* Frees the workspace like cudaFree(); allowed while a stream is being captured. */
 void kv_cache_destroy(kvc_cache *cache);
 
 /* Bytes of the device workspace that kv_cache_create() allocates (host only, no CUDA call;

@@ -336,7 +336,8 @@ kvr_status kv_relayout_plan_launch_shape(const kvr_plan *plan, int64_t *grid_all
 
 /* Free the plan and its device buffer (NULL is a no-op). Synchronizes the
  * device buffer's release like cudaFree: call it after the launches that use
- * the plan have been ordered before any reuse of that memory. */
+ * the plan have been ordered before any reuse of that memory. Allowed while a
+ * stream is being captured. */
 void kv_relayout_plan_destroy(kvr_plan *plan);
 
 /* Static, human-readable name of a status. */

@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "cache.h"
+#include "device_free.h"
 
 namespace {
 
@@ -292,7 +293,7 @@ extern "C" kvr_status kv_cache_create(const kvc_desc *desc, kvc_cache **out) {
 
 extern "C" void kv_cache_destroy(kvc_cache *cache) {
     if (cache == nullptr) return;
-    if (cache->ws.mem != nullptr) cudaFree(cache->ws.mem);
+    kvr_device_free(cache->ws.mem);
     delete cache;
 }
 

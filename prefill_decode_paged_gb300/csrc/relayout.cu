@@ -28,6 +28,7 @@
 #include <algorithm>
 #include <new>
 
+#include "device_free.h"
 #include "kv_relayout.h"
 #include "kvr_convert.cuh"
 #include "kvr_index.h"
@@ -883,9 +884,9 @@ extern "C" kvr_status kv_relayout_plan_launch_shape(const kvr_plan *plan, int64_
 
 extern "C" void kv_relayout_plan_destroy(kvr_plan *plan) {
     if (plan == nullptr) return;
-    if (plan->dev_meta != nullptr) cudaFree(plan->dev_meta);
+    kvr_device_free(plan->dev_meta);
 #ifdef KVR_DEVICE_CHECKS
-    if (plan->dev_regions != nullptr) cudaFree(plan->dev_regions);
+    kvr_device_free(plan->dev_regions);
 #endif
     delete plan;
 }
