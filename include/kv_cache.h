@@ -19,7 +19,8 @@
  * allocate nothing, never synchronize, and report launch errors only. The current device must
  * be the cache's device (KVR_ERR_INVALID_ARG otherwise). The attention calls of one cache share
  * its workspace: calls on different streams must be ordered by the caller (or use a second
- * cache of the same pool). Every launch is ordered after the work before it on `stream`.
+ * cache of the same pool). Host threads may call with one cache at once: what a call enqueues
+ * stays together. Every launch is ordered after the work before it on `stream`.
  * No C++ exception crosses this ABI.
  */
 #ifndef KV_CACHE_H_

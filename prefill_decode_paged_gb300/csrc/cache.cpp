@@ -366,7 +366,15 @@ extern "C" kvr_status kv_cache_attend(const kvc_cache *c, int32_t layer, const k
         return KVR_ERR_ALIGNMENT;
     if (!on_device(c)) return KVR_ERR_INVALID_ARG;
     if (a->num_requests == 0) return KVR_OK;
-    return kvc_attend_launch(c, layer, a, stream);
+    try {
+        // Latents take two launches that hand the workspace over: another host thread's must not
+        // come between them on the stream.
+        std::unique_lock<std::mutex> lock(c->use, std::defer_lock);
+        if (c->latent()) lock.lock();
+        return kvc_attend_launch(c, layer, a, stream);
+    } catch (...) {
+        return KVR_ERR_NOMEM;
+    }
 }
 
 extern "C" kvr_status kv_cache_status(const kvc_cache *cache, uint32_t *flags) {

@@ -6,6 +6,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
 #include <vector>
 
 #include "kv_cache.h"
@@ -54,6 +55,7 @@ struct kvc_cache {
     int32_t piece = 0;                // tokens of a map's box; 0: there are no maps
     int device = 0;
     int sm_count = 0;
+    mutable std::mutex use;           // held over the two launches of an attention over latents
 
     KvcPlane plane(int32_t layer, int32_t comp) const {
         return {(unsigned char *)(uintptr_t)base[(size_t)layer * d.num_components + comp],
