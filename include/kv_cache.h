@@ -177,7 +177,8 @@ typedef struct kvc_attend {
 kvr_status kv_cache_attend(const kvc_cache *cache, int32_t layer, const kvc_attend *args,
                            void *stream);
 
-/* Waits for the device, reads and clears the flags of what the kernels found out of range:
+/* Waits for the cache's device (which need not be the current one), reads and clears the flags
+ * of what the kernels found out of range:
  * KVR_OK with *flags = 0, or KVR_ERR_DEVICE_BOUNDS with the KVC_FLAG_* bits. */
 kvr_status kv_cache_status(const kvc_cache *cache, uint32_t *flags);
 

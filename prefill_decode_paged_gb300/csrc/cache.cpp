@@ -380,14 +380,22 @@ extern "C" kvr_status kv_cache_attend(const kvc_cache *c, int32_t layer, const k
 extern "C" kvr_status kv_cache_status(const kvc_cache *cache, uint32_t *flags) {
     if (flags != nullptr) *flags = 0;
     if (cache == nullptr) return KVR_ERR_INVALID_ARG;
-    uint32_t word = 0;
-    if (cudaDeviceSynchronize() != cudaSuccess ||
-        cudaMemcpy(&word, cache->ws.flags, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess ||
-        cudaMemset(cache->ws.flags, 0, sizeof(word)) != cudaSuccess ||
-        cudaDeviceSynchronize() != cudaSuccess) {
+    // the cache's device is waited for, whichever is current
+    int current = -1;
+    if (cudaGetDevice(&current) != cudaSuccess ||
+        (current != cache->device && cudaSetDevice(cache->device) != cudaSuccess)) {
         cudaGetLastError();
         return KVR_ERR_CUDA;
     }
+    uint32_t word = 0;
+    const bool ok =
+        cudaDeviceSynchronize() == cudaSuccess &&
+        cudaMemcpy(&word, cache->ws.flags, sizeof(word), cudaMemcpyDeviceToHost) == cudaSuccess &&
+        cudaMemset(cache->ws.flags, 0, sizeof(word)) == cudaSuccess &&
+        cudaDeviceSynchronize() == cudaSuccess;
+    if (!ok) cudaGetLastError();
+    if (current != cache->device) cudaSetDevice(current);
+    if (!ok) return KVR_ERR_CUDA;
     if (flags != nullptr) *flags = word;
     return word != 0 ? KVR_ERR_DEVICE_BOUNDS : KVR_OK;
 }

@@ -101,7 +101,29 @@ static int threads() {
     return 0;
 }
 
+// Status under another current device: the cache's own is waited for, the current one stays.
+static int device() {
+    kvc_cache *c;
+    REQUIRE(latent_cache(&c) == KVR_OK);
+    for (int now : {0, 1, 3}) {
+        current = now;
+        flags_word = KVC_FLAG_LENGTH | KVC_FLAG_BLOCK, synced = -1, failing = 0;
+        uint32_t flags = 7;
+        REQUIRE(kv_cache_status(c, &flags) == KVR_ERR_DEVICE_BOUNDS);
+        REQUIRE(flags == (KVC_FLAG_LENGTH | KVC_FLAG_BLOCK) && flags_word == 0);
+        REQUIRE(synced == 0 && current == now);
+        REQUIRE(kv_cache_status(c, nullptr) == KVR_OK && current == now);
+        flags_word = KVC_FLAG_POSITION, failing = 1, flags = 7;
+        REQUIRE(kv_cache_status(c, &flags) == KVR_ERR_CUDA);
+        REQUIRE(flags == 0 && flags_word == KVC_FLAG_POSITION && current == now);
+    }
+    current = 0;
+    kv_cache_destroy(c);
+    return 0;
+}
+
 int main(int argc, char **argv) {
     if (argc > 1 && strcmp(argv[1], "threads") == 0) return threads();
+    if (argc > 1 && strcmp(argv[1], "device") == 0) return device();
     return 2;
 }

@@ -1,4 +1,4 @@
-"""The decode cache's host code on stand-ins for the CUDA runtime: host threads."""
+"""The decode cache's host code on stand-ins for the CUDA runtime: host threads, devices."""
 import os
 import subprocess
 
@@ -25,3 +25,7 @@ def play(harness, what):
 
 def test_calls_of_host_threads_do_not_mix(harness):
     play(harness, "threads")
+
+
+def test_status_is_of_the_caches_device(harness):
+    play(harness, "device")
