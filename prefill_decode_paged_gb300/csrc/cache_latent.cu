@@ -629,6 +629,10 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                                  : "memory");
             }
         }
+        // Nothing is on its way to an SM that may leave: what this warp sent last has been read. (A warp
+        // that gave up has waited for two seconds since it sent anything.)
+        for (uint32_t i = it > SBUF ? it - SBUF : 0; ok && i < it; ++i)
+            ok = wait(bar(X_EMPTY + i % SBUF), (i / SBUF) & 1);
     } else if (warp == TELL) {
         // ---- telling the other SM what it may send over: its arrival takes some hundred cycles,
         // which the softmax warps do not have ----
@@ -822,7 +826,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
         wait_for(bar(DRAIN + (warp - KEYS)), 0);
     }
 
-    // both SMs stay until neither has anything under way to the other
+    // both SMs stay until neither has anything under way to the other (S that was sent: above)
     __syncwarp();
     fence_before();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
