@@ -752,7 +752,11 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
             it += n;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if (!ok)                                  // what was asked for has to come all the same
+        // What was asked for has to come, whatever the other warps gave up: the last tiles here (no
+        // later one has gone over them); where this warp gave up itself, whatever is under way.
+        for (uint32_t i = it > STAGES ? it - STAGES : 0; ok && i < it; ++i)
+            if ((i & 3) == w) wait_for(bar(K_FULL + i % STAGES), (i / STAGES) & 1);
+        if (!ok)
             for (uint32_t i = 0; i < STAGES; ++i) wait_for(bar(K_FULL + i), 0), wait_for(bar(K_FULL + i), 1);
         if (bad != 0) atomicOr(a.split.flags, bad);
     } else {
