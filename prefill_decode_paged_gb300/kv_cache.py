@@ -133,7 +133,8 @@ class KVCache:
 
     Calls run on torch's current stream, or on ``stream`` (a torch stream or a handle). Results that a
     call makes belong to that stream, as those of torch's own operations do: used on another one,
-    they need its order and ``record_stream``; and so do inputs of another stream.
+    they need its order and ``record_stream``; and so do inputs of another stream. There is no
+    backward pass: where gradients are recorded, tensors that require one are refused.
     """
 
     def __init__(self, pool, *, num_layers, num_components, kv_heads, head_dim, block,
@@ -199,6 +200,12 @@ class KVCache:
             raise RuntimeError("cache already closed")
         return self._h
 
+    def _refuse_gradients(self):
+        """For tensors of which one requires a gradient: the results would silently have none."""
+        if self._torch.is_grad_enabled():
+            raise ValueError("a tensor here requires a gradient, and these calls have none: "
+                             "call them under torch.no_grad() or detach it")
+
     def _new(self, shape, dtype, stream):
         """A result's memory, from the allocator's share of the stream that the kernel writes it on: memory
         of torch's current stream may still be in use by what is queued there."""
@@ -255,6 +262,8 @@ class KVCache:
         given, is rotated into ``q_out`` (a new tensor by default). Returns ``q_out``."""
         if (v is None) != self.latent:
             raise ValueError("a latent cache has no values, others need them")
+        if k.requires_grad or (v is not None and v.requires_grad) or (q is not None and q.requires_grad):
+            self._refuse_gradients()
         index, i32, dtype = self._index, self._i32, k.dtype
         T = k.shape[0]
         shape, line = (T, self.kv_heads, self.head_dim), (T,)
@@ -311,6 +320,8 @@ class KVCache:
         ``scale``: D ** -0.5 by default; ``window`` > 0: only that many keys, the token's own
         included. Returns (out, lse): ``out`` like q with ``value_dim`` elements, ``lse`` float32
         [R][new][Hq], new tensors by default (``lse=False``: none)."""
+        if q.requires_grad:
+            self._refuse_gradients()
         index, dtype, shape, heads = self._index, q.dtype, q.shape, self.query_heads
         n = len(shape)
         if n == 4:
