@@ -188,17 +188,6 @@ __device__ __forceinline__ void load_bytes(uint32_t dst, const void *src, uint32
                  : "memory");
 }
 
-// Two weights (>= 0) as the 16-bit numbers next below them: the rests are positive wherever the
-// weights are, so an infinite value times both parts is one infinity, not two that cancel.
-template <bool F16>
-__device__ __forceinline__ uint32_t below2(float lo, float hi) {
-    const uint32_t a = max(__float_as_uint(lo), 1u) - 1u, b = max(__float_as_uint(hi), 1u) - 1u;
-    if (!F16) return __byte_perm(a, b, 0x7632);
-    uint32_t w;
-    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(__uint_as_float(b)), "f"(__uint_as_float(a)));
-    return w;
-}
-
 // out (16-bit), four elements of one row, from floats
 template <bool F16>
 __device__ __forceinline__ uint2 narrow4(float4 v) {

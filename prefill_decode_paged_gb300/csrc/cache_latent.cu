@@ -39,8 +39,17 @@
 // (f16: 2^8) the one that its P is relative to, which hardly happens after the first tiles of a
 // job: powers of two cost no precision in P, O and the sums.
 //
-// Numbers: S, maxima, sums, O and all joins are fp32. P is rounded once to the pool's 16-bit type
-// for its product: rounding it twice as fine would cost half of the products again.
+// Numbers: S, maxima, sums, O and all joins are fp32. With more than 32 rows P is rounded once to the
+// pool's 16-bit type for its product: a second product for what is left of it reads V again, and its
+// columns of tensor memory leave room for two S instead of three (181 -> 221 us for 64 requests of 1024 to
+// 16384 latents under 128 heads, L2 cold). Up to 32 rows (FINE) most of the 128 rows are free, and 32 of
+// them take what is left: rows r and r + 32 hold the same query, so both get the same S, maxima and P, bit
+// for bit; one enters the 16-bit number next below P into the product, the other the rest, and their O are
+// added at the end: 15 bits of P count over bf16. Errors against 64 bits (2-norm, relative) are 0.0016 to 0.0017
+// then, those of 32-bit sums rounded to bf16, instead of 0.0019 to 0.0026 (f16 0.00021, 0.00022 to 0.00026).
+// It costs a second warp of softmax and of sending, and the way of O from one warp to the other: one
+// request of 4096, 16 heads 13.9 -> 14.8 us; 9 of 5 to 6001, 32 rows 20.0 -> 21.5; L2 cold, 4 of 32768, 16
+// heads 51.7 -> 53.8, 64 of 8192 126 -> 134. (The second product instead: 14.6, 21.5, 53.8, 146.)
 //
 // Every wait ends: after two seconds it gives up and flags KVC_FLAG_TIMEOUT, and its warp goes to
 // the end of the kernel, as the others do for want of it.
@@ -71,6 +80,7 @@ constexpr int ROWS = 128;                 // query rows of a pass
 constexpr int HALF = 256, REST = 32;      // value elements and others of an SM
 constexpr int STAGES = 9;                 // tiles in the ring
 constexpr int SBUF = 3;                   // halves of S at a time, own and received
+constexpr int FINE_ROWS = 32;             // query rows up to which P is two numbers: a warp's
 constexpr int CHUNK = KT * 128;           // 64 elements of each key
 constexpr int STAGE = 4 * CHUNK + KT * 64;
 constexpr int XBUF = ROWS * KT * 4;
@@ -94,7 +104,7 @@ constexpr size_t SLOT = (size_t)ROWS * VALUES + 2 * ROWS;
 enum { K_FULL = 0, K_EMPTY = K_FULL + STAGES, S_FULL = K_EMPTY + STAGES, S_FREE = S_FULL + SBUF,
        X_FULL = S_FREE + 2 * SBUF, X_EMPTY = X_FULL + SBUF, X_READ = X_EMPTY + SBUF,
        P_FULL = X_READ + SBUF, O_DONE = P_FULL + 2, Q_FULL = O_DONE + 4, O_FREE, SUMS,
-       DRAIN, BARS = DRAIN + 3 };
+       DRAIN, REST_FULL = DRAIN + 3, REST_READ = REST_FULL + 2 * SOFT, BARS = REST_READ + 2 * SOFT };
 constexpr int OFF_TMEM = BARS * 8, OFF_SCRATCH = OFF_TMEM + 16;
 static_assert(OFF_SCRATCH + 4 * WARPS <= 768, "the words after the barriers");
 
@@ -311,7 +321,9 @@ __device__ __forceinline__ Cut cut_of(const LatentArgs &a, const int32_t *prefix
 template <bool F16>
 constexpr float GROWTH_OF = F16 ? 8.0f : 20.0f;
 
-template <bool F16>
+// FINE: rows r and r + 32 of the products are the same query; P of the first is the 16-bit number next
+// below the weight, P of the second what is left of it, and O of the two is added.
+template <bool F16, bool FINE>
 __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constant__ LatentArgs a) {
     constexpr float GROWTH = GROWTH_OF<F16>;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -350,6 +362,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
         bar_init(bar(DRAIN), 1);
         bar_init(bar(DRAIN + 1), 1);
         bar_init(bar(DRAIN + 2), 1);
+        for (int i = 0; i < 2 * SOFT; ++i) bar_init(bar(REST_FULL + i), 1), bar_init(bar(REST_READ + i), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     for (int i = tid; i < SOFT * ROWS; i += THREADS) ((uint64_t *)(smem + OFF_TOPS))[i] = 0;
@@ -382,14 +395,17 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
         bool mine;
     };
     auto query_of = [&](const Segment &seg) -> Query {
-        const int32_t rho = seg.job * ROWS + row;
+        const int32_t rho = seg.job * ROWS + (FINE ? row % FINE_ROWS : row);
         const int32_t token = (int32_t)a.heads.div((uint32_t)rho);
         return {token, rho - token * a.Hq, rho < M};
     };
     // Warps of 32 rows that a segment has rows for. The others of softmax and sending only keep
     // step: what lies in their lanes of tensor memory is read by nobody. (4 requests of 32768
     // latents, 16 heads: 39.5 us, and 45.5 with all at work.)
-    auto live_warps = [&](const Segment &seg) { return min(ROWS / 32, (M - seg.job * ROWS + 31) / 32); };
+    auto live_warps = [&](const Segment &seg) {
+        return FINE ? 2 : min(ROWS / 32, (M - seg.job * ROWS + 31) / 32);
+    };
+    const bool second = FINE && warp % 4 == 1;       // rows of what is left of P
 
     if (warp < SEND) {
         // ---- softmax of every second tile ----
@@ -400,6 +416,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
         const uint32_t tops = smem0 + OFF_TOPS + row * 8;
         float *sums = (float *)(smem + OFF_SUMS);     // [2][SOFT][ROWS]
         uint32_t it = 0, segments = 0;            // tiles and segments so far
+        uint32_t handed = 0;                      // pieces of O from second rows to first ones
         bool ok = true;
         while (ok && x < x_end) {
             const Segment seg = segment_at(x, x_end, prefix, a.shape, known);
@@ -492,7 +509,13 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                     const float2 d = unpack2(add2(pack2(s[2 * e], s[2 * e + 1]), minus));
                     const float p0 = ex2(d.x), p1 = ex2(d.y);
                     add = add2(add, pack2(__float_as_uint(p0), __float_as_uint(p1)));
-                    p[e] = narrow2<F16>(p0, p1);
+                    if (FINE) {
+                        p[e] = below2<F16>(p0, p1);
+                        const float2 f = widen2<F16>(p[e]);
+                        if (second) p[e] = narrow2<F16>(p0 - f.x, p1 - f.y);
+                    } else {
+                        p[e] = narrow2<F16>(p0, p1);
+                    }
                 }
                 const float2 both = unpack2(add);
                 sum += both.x + both.y;
@@ -525,25 +548,53 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
             if (!(ok = wait(bar(O_DONE + (last & 3)), (last >> 2) & 1))) break;
             fence_after();
 
-            const bool whole = seg.u0 == 0 && seg.u1 == seg.units, mine = query.mine;
+            const bool whole = seg.u0 == 0 && seg.u1 == seg.units, mine = query.mine && !second;
             const bool some = sum > 0.0f || sum != sum;
             const float inv = some ? 1.0f / sum : 0.0f;
             float *slot = a.partial + (size_t)(2 * part + (seg.u0 == 0 ? 1 : 0)) * SLOT;
             unsigned char *out = a.out + seg.r * a.out_request + query.token * a.out_token +
                                  query.hq * a.out_head + rank * (HALF * 2);
+            constexpr int PIECE = FINE ? 32 : 16;      // columns at a time
 #pragma unroll 1
-            for (int c = group * 16; live && c < HALF; c += SOFT * 16) {
-                uint32_t w[16];
-                tm_load16(w, lanes + COL_O + c);
+            for (int c = group * PIECE; live && c < HALF; c += SOFT * PIECE) {
+                uint32_t w[PIECE];
+#pragma unroll
+                for (int e = 0; e < PIECE; e += 16) tm_load16(w + e, lanes + COL_O + c + e);
                 wait_ld();
+                if (FINE) {
+                    // the second rows' O to the first's, through where rows 64 to 127 of S would come
+                    const uint32_t buf = 2 * group + handed % 2, turn = handed / 2;
+                    float4 *at = (float4 *)(smem + OFF_XBUF + group * XBUF) + 64 + handed % 2 * 32 + lane;
+                    ++handed;
+                    if (second) {
+                        if (turn > 0 && !(ok = wait(bar(REST_READ + buf), (turn - 1) & 1))) break;
+#pragma unroll
+                        for (int e = 0; e < PIECE / 4; ++e)
+                            at[e * ROWS] = *(const float4 *)((const float *)w + 4 * e);
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(bar(REST_FULL + buf));
+                        continue;
+                    }
+                    if (!(ok = wait(bar(REST_FULL + buf), turn & 1))) break;
+#pragma unroll
+                    for (int e = 0; e < PIECE / 4; ++e) {
+                        const float4 v = at[e * ROWS];
+                        w[4 * e] = __float_as_uint(__uint_as_float(w[4 * e]) + v.x);
+                        w[4 * e + 1] = __float_as_uint(__uint_as_float(w[4 * e + 1]) + v.y);
+                        w[4 * e + 2] = __float_as_uint(__uint_as_float(w[4 * e + 2]) + v.z);
+                        w[4 * e + 3] = __float_as_uint(__uint_as_float(w[4 * e + 3]) + v.w);
+                    }
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(bar(REST_READ + buf));
+                }
                 if (mine && whole) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int e = 0; e < PIECE; ++e) {
                         const float v = __uint_as_float(w[e]);
                         w[e] = some ? __float_as_uint(v * inv) : 0u;
                     }
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = 0; e < PIECE / 8; ++e) {
                         uint4 v;
                         const float *f = (const float *)w + 8 * e;
                         v.x = narrow2<F16>(f[0], f[1]), v.y = narrow2<F16>(f[2], f[3]);
@@ -553,11 +604,12 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                 } else if (mine) {
                     float4 *to = (float4 *)slot + (size_t)((rank * HALF + c) / 4) * ROWS + row;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < PIECE / 4; ++e)
                         __stcg(to + e * ROWS, *(const float4 *)((const float *)w + 4 * e));
                 }
                 __syncwarp();
             }
+            if (FINE && !ok) break;
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(bar(O_FREE));
@@ -1005,7 +1057,8 @@ static kvr_status make_maps(kvc_cache *c) {
 kvr_status kvc_latent_setup(kvc_cache *c) {
     const int smem = OFF_PREFIX + 4 * (KVC_MAX_REQUESTS + 1);
     static_assert(OFF_PREFIX + 4 * (KVC_MAX_REQUESTS + 1) <= 227 * 1024, "");
-    for (auto k : {latent_kernel<false>, latent_kernel<true>})
+    for (auto k : {latent_kernel<false, false>, latent_kernel<false, true>, latent_kernel<true, false>,
+                   latent_kernel<true, true>})
         if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
             cudaGetLastError();
             return KVR_ERR_CUDA;
@@ -1051,8 +1104,11 @@ kvr_status kvc_latent_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     a.shape = make_cut_shape(p->num_requests, a.chunks, a.parts, SLACK);
     const bool f16 = c->d.dtype == KVC_DTYPE_F16;
     const size_t smem = OFF_PREFIX + 4 * (size_t)(p->num_requests + 1);
-    const kvr_status st = kvc_launch(f16 ? latent_kernel<true> : latent_kernel<false>, a,
-                                     dim3((unsigned)(2 * a.parts)), THREADS, smem, stream, 2);
+    const auto kernel = M <= FINE_ROWS
+                            ? (f16 ? latent_kernel<true, true> : latent_kernel<false, true>)
+                            : (f16 ? latent_kernel<true, false> : latent_kernel<false, false>);
+    const kvr_status st =
+        kvc_launch(kernel, a, dim3((unsigned)(2 * a.parts)), THREADS, smem, stream, 2);
     if (st != KVR_OK) return st;
     const int64_t groups = (std::min<int64_t>(M, ROWS) + JOIN_ROWS - 1) / JOIN_ROWS;
     const int64_t jobs = (int64_t)p->num_requests * a.chunks, blocks = jobs * groups * JOIN_GRID;
