@@ -42,14 +42,16 @@
 // Numbers: S, maxima, sums, O and all joins are fp32. With more than 32 rows P is rounded once to the
 // pool's 16-bit type for its product: a second product for what is left of it reads V again, and its
 // columns of tensor memory leave room for two S instead of three (181 -> 221 us for 64 requests of 1024 to
-// 16384 latents under 128 heads, L2 cold). Up to 32 rows (FINE) most of the 128 rows are free, and 32 of
-// them take what is left: rows r and r + 32 hold the same query, so both get the same S, maxima and P, bit
-// for bit; one enters the 16-bit number next below P into the product, the other the rest, and their O are
-// added at the end: 15 bits of P count over bf16. Errors against 64 bits (2-norm, relative) are 0.0016 to 0.0017
-// then, those of 32-bit sums rounded to bf16, instead of 0.0019 to 0.0026 (f16 0.00021, 0.00022 to 0.00026).
-// It costs a second warp of softmax and of sending, and the way of O from one warp to the other: one
-// request of 4096, 16 heads 13.9 -> 14.8 us; 9 of 5 to 6001, 32 rows 20.0 -> 21.5; L2 cold, 4 of 32768, 16
-// heads 51.7 -> 53.8, 64 of 8192 126 -> 134. (The second product instead: 14.6, 21.5, 53.8, 146.)
+// 16384 latents under 128 heads, L2 cold). Up to 32 rows (FINE) most of the 128 are free, and as many of
+// them take what is left: rows r and r + FINE hold the same query, so both get the same S, maxima and P, bit
+// for bit; one enters P cut to 16 bits into the product, the other the rest, and their O are added at the
+// end: 15 bits of P count over bf16. Errors against 64 bits (2-norm, relative) are 0.0016 to 0.0017 then, those
+// of 32-bit sums rounded to bf16, instead of 0.0019 to 0.0026 (f16 0.00021, 0.00022 to 0.00026). Up to 16 rows
+// both are a warp's, and it costs the cutting and 16 shuffles a piece of O; up to 32, a second warp of
+// softmax and of sending, and O's way from one warp to the other: one request of 4096, 16 heads 14.0 ->
+// 14.6 us, 4 of 32768 40.7 -> 41.9, 64 of 8192 112 -> 116; 32 rows: 9 of 5 to 6001 19.9 -> 21.1, 64 of 8192 117 ->
+// 122. (By a second product 64 of 8192 under 16 heads took 15 % more. 33 to 64 rows could be done the same way,
+// but would then keep all four warps busy, as 128 do: 53.4 instead of 44 us for 4 of 32768.)
 //
 // Every wait ends: after two seconds it gives up and flags KVC_FLAG_TIMEOUT, and its warp goes to
 // the end of the kernel, as the others do for want of it.
@@ -60,7 +62,7 @@
 // busy for all of them (tensor cores 40 %, shared memory about 75 %: 85 KB of boxes, operands and S a
 // tile); from S to P's product a tile is under way for some 5000, most of it in the products, where
 // S of two tiles and O of a third take turns, and in the exchange. Each change of job costs about 8 us of 262 KB of
-// partial results and an empty pipe, and the join 5 us. One request of 4096 latents with 16 heads: 13.4 us, its fill,
+// partial results and an empty pipe, and the join 5 us. One request of 4096 latents with 16 heads: 14.6 us, its fill,
 // four tiles and the join one after another.
 #include <math.h>
 
@@ -80,7 +82,6 @@ constexpr int ROWS = 128;                 // query rows of a pass
 constexpr int HALF = 256, REST = 32;      // value elements and others of an SM
 constexpr int STAGES = 9;                 // tiles in the ring
 constexpr int SBUF = 3;                   // halves of S at a time, own and received
-constexpr int FINE_ROWS = 32;             // query rows up to which P is two numbers: a warp's
 constexpr int CHUNK = KT * 128;           // 64 elements of each key
 constexpr int STAGE = 4 * CHUNK + KT * 64;
 constexpr int XBUF = ROWS * KT * 4;
@@ -304,6 +305,33 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return d;
 }
 
+// Two weights cut to 16 bits, or what that leaves of them, cut: less is -1 in both halves for the rest, else
+// 0. (That the rest may be zero, which an infinite value would not stand, is no matter for latents: a row
+// with an infinite value has an infinite key.)
+template <bool F16>
+__device__ __forceinline__ uint32_t first_or_rest2(float lo, float hi, uint64_t less) {
+    uint64_t cut;
+    if (F16) {
+        uint32_t w;
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+        const float2 f = widen2<true>(w);
+        cut = pack2(__float_as_uint(f.x), __float_as_uint(f.y));
+    } else {
+        cut = pack2(__float_as_uint(lo) & 0xFFFF0000u, __float_as_uint(hi) & 0xFFFF0000u);
+    }
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(cut), "l"(less), "l"(pack2(__float_as_uint(lo), __float_as_uint(hi))));
+    const float2 f = unpack2(d);
+    uint32_t w;
+    if (F16)
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(f.y), "f"(f.x));
+    else
+        asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(f.y), "f"(f.x));
+    return w;
+}
+
 // Units (tiles) that a change of job costs (cache_split.cuh). Parts
 // within jobs took (us) 37.6 where equal ones took 41.7 (8 requests of 8192 latents, 128 heads), 25.3
 // for 28.8 (2 of 8192), 21.3 for 23.0 (9 of up to 6001, 32 rows); groups 10 above the equal parts 39.9
@@ -321,9 +349,9 @@ __device__ __forceinline__ Cut cut_of(const LatentArgs &a, const int32_t *prefix
 template <bool F16>
 constexpr float GROWTH_OF = F16 ? 8.0f : 20.0f;
 
-// FINE: rows r and r + 32 of the products are the same query; P of the first is the 16-bit number next
-// below the weight, P of the second what is left of it, and O of the two is added.
-template <bool F16, bool FINE>
+// FINE (16 or 32, 0: not so): rows r and r + FINE of the products are the same query; P of the first is
+// the 16-bit number next below the weight, P of the second what is left of it, and O of the two is added.
+template <bool F16, int FINE>
 __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constant__ LatentArgs a) {
     constexpr float GROWTH = GROWTH_OF<F16>;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -395,22 +423,23 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
         bool mine;
     };
     auto query_of = [&](const Segment &seg) -> Query {
-        const int32_t rho = seg.job * ROWS + (FINE ? row % FINE_ROWS : row);
+        const int32_t rho = seg.job * ROWS + (FINE > 0 ? row % (FINE > 0 ? FINE : 1) : row);
         const int32_t token = (int32_t)a.heads.div((uint32_t)rho);
         return {token, rho - token * a.Hq, rho < M};
     };
     // Warps of 32 rows that a segment has rows for. The others of softmax and sending only keep
     // step: what lies in their lanes of tensor memory is read by nobody. (4 requests of 32768
-    // latents, 16 heads: 39.5 us, and 45.5 with all at work.)
+    // latents, 16 heads: 40.7 us, and 45.5 with all at work.)
     auto live_warps = [&](const Segment &seg) {
-        return FINE ? 2 : min(ROWS / 32, (M - seg.job * ROWS + 31) / 32);
+        return FINE > 0 ? FINE / 16 : min(ROWS / 32, (M - seg.job * ROWS + 31) / 32);
     };
-    const bool second = FINE && warp % 4 == 1;       // rows of what is left of P
+    const bool second = FINE > 0 && (row / (FINE > 0 ? FINE : 1)) % 2 == 1;      // of what is left of P
 
     if (warp < SEND) {
         // ---- softmax of every second tile ----
         const uint32_t group = warp / 4;
         const uint64_t sc2 = splat2(a.scale * 1.4426950408889634f);
+        const uint64_t less = splat2(second ? -1.0f : 0.0f);
         // what a row's P is relative to after a tile: (maximum, tile + 1) by tile % SOFT and row. One
         // 64-bit word, so that whoever sees the number sees its maximum too
         const uint32_t tops = smem0 + OFF_TOPS + row * 8;
@@ -509,13 +538,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                     const float2 d = unpack2(add2(pack2(s[2 * e], s[2 * e + 1]), minus));
                     const float p0 = ex2(d.x), p1 = ex2(d.y);
                     add = add2(add, pack2(__float_as_uint(p0), __float_as_uint(p1)));
-                    if (FINE) {
-                        p[e] = below2<F16>(p0, p1);
-                        const float2 f = widen2<F16>(p[e]);
-                        if (second) p[e] = narrow2<F16>(p0 - f.x, p1 - f.y);
-                    } else {
-                        p[e] = narrow2<F16>(p0, p1);
-                    }
+                    p[e] = FINE > 0 ? first_or_rest2<F16>(p0, p1, less) : narrow2<F16>(p0, p1);
                 }
                 const float2 both = unpack2(add);
                 sum += both.x + both.y;
@@ -554,14 +577,19 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
             float *slot = a.partial + (size_t)(2 * part + (seg.u0 == 0 ? 1 : 0)) * SLOT;
             unsigned char *out = a.out + seg.r * a.out_request + query.token * a.out_token +
                                  query.hq * a.out_head + rank * (HALF * 2);
-            constexpr int PIECE = FINE ? 32 : 16;      // columns at a time
+            constexpr int PIECE = FINE == 32 ? 32 : 16;      // columns at a time
 #pragma unroll 1
             for (int c = group * PIECE; live && c < HALF; c += SOFT * PIECE) {
                 uint32_t w[PIECE];
 #pragma unroll
                 for (int e = 0; e < PIECE; e += 16) tm_load16(w + e, lanes + COL_O + c + e);
                 wait_ld();
-                if (FINE) {
+                if (FINE == 16)                       // the second rows' O to the first's, 16 lanes away
+#pragma unroll
+                    for (int e = 0; e < PIECE; ++e)
+                        w[e] = __float_as_uint(__uint_as_float(w[e]) +
+                                               __uint_as_float(__shfl_xor_sync(~0u, w[e], 16)));
+                if (FINE == 32) {
                     // the second rows' O to the first's, through where rows 64 to 127 of S would come
                     const uint32_t buf = 2 * group + handed % 2, turn = handed / 2;
                     float4 *at = (float4 *)(smem + OFF_XBUF + group * XBUF) + 64 + handed % 2 * 32 + lane;
@@ -609,7 +637,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_kernel(const __grid_constan
                 }
                 __syncwarp();
             }
-            if (FINE && !ok) break;
+            if (FINE == 32 && !ok) break;
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(bar(O_FREE));
@@ -1020,6 +1048,12 @@ __global__ void __launch_bounds__(JOIN_SET * SETS) latent_join(const __grid_cons
             some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
+// the instance for M query rows
+template <bool F16>
+auto kernel_of(int64_t M) {
+    return M <= 16 ? latent_kernel<F16, 16> : M <= 32 ? latent_kernel<F16, 32> : latent_kernel<F16, 0>;
+}
+
 template <bool F16>
 constexpr void (*JOINS_OF[5])(LatentArgs) = {latent_join<F16, 1, false>, latent_join<F16, 2, false>,
                                              latent_join<F16, 4, false>, latent_join<F16, 8, false>,
@@ -1057,8 +1091,8 @@ static kvr_status make_maps(kvc_cache *c) {
 kvr_status kvc_latent_setup(kvc_cache *c) {
     const int smem = OFF_PREFIX + 4 * (KVC_MAX_REQUESTS + 1);
     static_assert(OFF_PREFIX + 4 * (KVC_MAX_REQUESTS + 1) <= 227 * 1024, "");
-    for (auto k : {latent_kernel<false, false>, latent_kernel<false, true>, latent_kernel<true, false>,
-                   latent_kernel<true, true>})
+    for (auto k : {kernel_of<false>(1), kernel_of<false>(17), kernel_of<false>(33), kernel_of<true>(1),
+                   kernel_of<true>(17), kernel_of<true>(33)})
         if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
             cudaGetLastError();
             return KVR_ERR_CUDA;
@@ -1104,11 +1138,8 @@ kvr_status kvc_latent_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     a.shape = make_cut_shape(p->num_requests, a.chunks, a.parts, SLACK);
     const bool f16 = c->d.dtype == KVC_DTYPE_F16;
     const size_t smem = OFF_PREFIX + 4 * (size_t)(p->num_requests + 1);
-    const auto kernel = M <= FINE_ROWS
-                            ? (f16 ? latent_kernel<true, true> : latent_kernel<false, true>)
-                            : (f16 ? latent_kernel<true, false> : latent_kernel<false, false>);
     const kvr_status st =
-        kvc_launch(kernel, a, dim3((unsigned)(2 * a.parts)), THREADS, smem, stream, 2);
+        kvc_launch(f16 ? kernel_of<true>(M) : kernel_of<false>(M), a, dim3((unsigned)(2 * a.parts)), THREADS, smem, stream, 2);
     if (st != KVR_OK) return st;
     const int64_t groups = (std::min<int64_t>(M, ROWS) + JOIN_ROWS - 1) / JOIN_ROWS;
     const int64_t jobs = (int64_t)p->num_requests * a.chunks, blocks = jobs * groups * JOIN_GRID;
