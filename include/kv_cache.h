@@ -72,7 +72,9 @@ typedef struct kvc_cache kvc_cache;
  * Validate *desc (KVR_ERR_INVALID_ARG, _UNSUPPORTED, _ALIGNMENT, _POOL_OVERLAP for a layout
  * whose slots overlap), check that the pool is memory the current device can access
  * (_POOL_ADDRESS), and allocate the device workspace of its calls. *out is the new cache, or
- * NULL on failure.
+ * NULL on failure. The workspace (kv_cache_workspace_bytes()) is 256 bytes where query_heads is 0; for
+ * attention on 152 SMs it is 40 MB over latents and 5 to 10 MB over keys and values, whatever the pool's
+ * size and layers: caches of many shards on one device that only append need not reserve it.
  */
 kvr_status kv_cache_create(const kvc_desc *desc, kvc_cache **out);
 /* Frees the workspace like cudaFree(); allowed while a stream is being captured. */
@@ -113,8 +115,7 @@ typedef struct kvc_table {
  * The queries, where given, are rotated into q_out (which may be q itself).
  * Requirements: k, v, q of `dtype` (the pool's type if that has 16 bits), rows contiguous,
  * every address and stride a multiple of 16 bytes; rotary_dim a multiple of 16, at most both
- * row lengths; q_dim a multiple of 8, and of 16 where that is what remains beside the rotated
- * part. Two tokens of one call must not have the same slot; k, v and q must not overlap the
+ * row lengths; q_dim a multiple of 16, at most 576. Two tokens of one call must not have the same slot; k, v and q must not overlap the
  * pool.
  */
 typedef struct kvc_append {
@@ -154,7 +155,10 @@ kvr_status kv_cache_append(const kvc_cache *cache, int32_t layer, const kvc_appe
  * windows) is never used, NaN included, and table entries of blocks that hold such places only
  * are not looked at; a NaN or an infinity in a value at a place that only some of a request's
  * newest tokens see may reach the others.
- * Weights below 2^-24 of a row's largest count as zero where the cache holds f16 or E4M3.
+ * Weights below 2^-24 of a row's largest count as zero where the cache holds f16 or E4M3. Before they
+ * meet the values, weights count with 15 bits or more over bf16 and f16 keys and values and under at most
+ * 32 rows (num_new Hq) of latents, with those of an f16 over E4M3, and with those of the pool's type
+ * under more rows of latents; sums are fp32.
  * Requirements: q and out of `dtype` (the pool's type if that has 16 bits), rows contiguous,
  * every address and stride a multiple of 16 bytes; lse NULL or [R][num_new][Hq], contiguous.
  */

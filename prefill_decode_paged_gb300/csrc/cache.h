@@ -156,17 +156,6 @@ __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
     return w;
 }
 
-// Two weights (>= 0) as the 16-bit numbers next below them: the rests are positive wherever the
-// weights are, so an infinite value times both parts is one infinity, not two that cancel.
-template <bool F16>
-__device__ __forceinline__ uint32_t below2(float lo, float hi) {
-    const uint32_t a = max(__float_as_uint(lo), 1u) - 1u, b = max(__float_as_uint(hi), 1u) - 1u;
-    if (!F16) return __byte_perm(a, b, 0x7632);
-    uint32_t w;
-    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(__uint_as_float(b)), "f"(__uint_as_float(a)));
-    return w;
-}
-
 // Two E4M3 codes (the low one first) as f16x2: exact, a NaN code gives a NaN.
 __device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t two_codes) {
     uint32_t h2;

@@ -20,7 +20,8 @@ namespace {
 using namespace kvc;
 
 constexpr int BORDER = 2;     // tokens an SM, above which they are many
-// MB written above which the stores do not ask L2 to keep them: half of it. Prompts' 486 MB take 152
+// MB of rows (those of E4M3 pools counted as they are read, in 16 bits) above which the stores do not ask
+// L2 to keep what they write: half of it. Prompts' 486 MB take 152
 // us instead of 161 so; 60 MB would take 22 instead of 24, but what reads them next finds them there.
 constexpr int AWAY = 64;
 constexpr int MANY_THREADS = 128, FEW_THREADS = 512;
@@ -246,7 +247,8 @@ append_kernel(AppendArgs a) {
 // on an SM hide one another's waits. Few: a token is one chain of waits, so each unit has a thread of
 // its own, up to 512 and two units a thread. Few and many took (us) 3.0 and 4.0 for 64 tokens of 640
 // units, 4.2 and 5.6 for 256; 2.9 and 3.1 for 300 of 384, 4.9 and 3.8 for 600; and with blocks of 192,
-// 256 and 384 threads 39834 tokens took 186, 190 and 216 where those of 128 took 162.
+// 256 and 384 threads 39834 tokens took 186, 190 and 216 where those of 128 took 162. (The register limits, 48
+// for many and 64 for few, make the compiler spill 12 to 64 bytes a thread; looser ones have not been tried.)
 template <bool F16, bool E4M3>
 kvr_status go(AppendArgs &a, bool interleaved, int32_t tokens, int sms, void *stream) {
     const int64_t n = (int64_t)a.q.heads * a.q_units.d + (int64_t)(a.k.heads + a.v.heads) * a.units.d;

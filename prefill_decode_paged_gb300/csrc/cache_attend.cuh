@@ -4,24 +4,27 @@
 // meet the same keys, so one pass over the cache serves them all. It is bound by HBM: at G = 8
 // and 16-bit elements there are 8 flops a byte of cache, 1/30 of what the card can do.
 //
-// Split. The keys of all (request, head) JOBS, in UNITS of 4 KT keys, form one line that is cut
-// into equal parts, one a resident block, whatever the lengths are (two and three times as many
-// parts: 71 and 75 us where one takes 52, as each part begins with an empty ring and ends with a
-// share of a join); each block works the prefix sums of the lengths out by itself, so that the
-// lengths can stay on the device. A part of a job that is not the whole of it leaves (max, sum,
+// Split. The keys of all (request, head) JOBS, in UNITS of 4 KT keys, form one line that is cut into
+// parts, at most one a resident block: equal ones whatever the lengths are, or parts within jobs where
+// that makes the longest hardly longer (cache_split.cuh). (Two and three times as many parts: 71 and
+// 75 us where one takes 52, as each begins with an empty ring and ends with a share of a join.) Each
+// block works the prefix sums of the lengths out by itself, so that the lengths can stay on the device. A part of a job that is not the whole of it leaves (max, sum,
 // accumulator) in the workspace, and the last of the job's blocks to arrive copies all of them
 // into its ring and joins them, in the order of the keys: results do not depend on who is last.
 //
 // Inside a block each of 4 warps takes every fourth tile of KT keys and keeps its own ring of
 // STAGES tiles filled by 16-byte cp.async: nothing in the loop waits for another warp. (The copy
-// engine's boxes took 57 us where these take 53.) Rows of padding (beyond the length, or beyond
-// D) are written as zeros, so that what the pool holds there never meets the arithmetic.
+// engine's boxes took 57 us where these take 53.) A window's first tile begins at its first key. Rows of
+// padding (beyond the length, or beyond D) are written as zeros, so that what the pool holds there never
+// meets the arithmetic.
 //
 // Products. S^T = K Q^T and O^T += V^T P^T by mma.sync m16n8k16 with keys (then head elements)
-// as the 16 rows and the queries as the 8 columns: with M = 8 nothing is padded, where 128-row
-// tcgen05 tiles would be 15/16 empty; the tensor work is far below the loads at any M here. K
-// and V^T fragments come by ldmatrix (.trans for V), P^T is P's accumulator fragment transposed
-// in registers by movmatrix.
+// as the 16 rows and the queries as the 8 columns: with M = 8 nothing is padded, and each warp goes its
+// own way with tiles of 16 or 32 keys and its accumulators in registers. tcgen05 products could take
+// 128 keys (then head elements) as their rows in the same way; that has not been built. With 8 rows
+// nothing could be gained, HBM bounds them; with 32 (a chain of 1.3 us a tile, the tensor pipe at 8 %) and
+// over E4M3 (instructions) it might be. K and V^T fragments come by ldmatrix (.trans for V), P^T is
+// P's accumulator fragment transposed in registers by movmatrix.
 //
 // Numbers. S, the running maximum and sum, and O are fp32. P enters its product as two 16-bit
 // numbers (the one next below, and the rest), so 15 bits of it count: one rounding of P alone would be as
@@ -64,9 +67,7 @@ struct AttendArgs {
 
 constexpr int ATTEND_WARPS = 4;
 constexpr int ATTEND_THREADS = 32 * ATTEND_WARPS;
-// Units that a change of job costs (cache_split.cuh). Parts with at least 1, 2, 4 and 8 units (us): one request of 4096 keys, 8 heads of 8 queries,
-// 15.7, 12.7, 11.6, 14.0; its 4 newest tokens 62, 39, 31, 32; 16 requests of 512 keys 15.8, 15.5,
-// 12.7, 11.8; one of 1024 keys 8.0, 8.1, 9.4, 11.8. Parts within jobs took 49.1 where equal ones took
+// Units that a change of job costs (cache_split.cuh). Parts within jobs took 49.1 where equal ones took
 // 52.1 (4 requests of 32768 keys, 4 heads), 27.4 for 33.3 (8 of 16 to 8192, 8 heads), 23.8 for 26.7
 // (48 of a window of 1024, 32 rows), and with a group 5 above the equal parts' 48.6 for 51.5 (8 of
 // 8192, 8 heads); where nothing was to be gained 0.3 to 0.8 more.
@@ -186,6 +187,17 @@ __device__ __forceinline__ void load_bytes(uint32_t dst, const void *src, uint32
     asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
+}
+
+// Two weights (>= 0) as the 16-bit numbers next below them: the rests are positive wherever the
+// weights are, so an infinite value times both parts is one infinity, not two that cancel.
+template <bool F16>
+__device__ __forceinline__ uint32_t below2(float lo, float hi) {
+    const uint32_t a = max(__float_as_uint(lo), 1u) - 1u, b = max(__float_as_uint(hi), 1u) - 1u;
+    if (!F16) return __byte_perm(a, b, 0x7632);
+    uint32_t w;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(__uint_as_float(b)), "f"(__uint_as_float(a)));
+    return w;
 }
 
 // out (16-bit), four elements of one row, from floats

@@ -127,8 +127,9 @@ class KVCache:
     [L][C][H]) as the relayout's conversion takes them. Two components hold keys and values
     (head_dim a multiple of 16, at most 256), one a latent (head_dim 576, of which the first
     512 are the values). ``query_heads`` (0: append only), ``max_requests`` and ``max_new`` size
-    the workspace of the attention calls; calls on different streams that share a cache must
-    be ordered. Tensors that the calls do not hold for are ValueErrors, what the C library
+    the workspace of the attention calls (:func:`workspace_bytes`: 40 MB for latents, 5 to 10 MB for
+    keys and values, whatever the pool's size); calls on different streams that share a cache must
+    be ordered, host threads need not be. Tensors that the calls do not hold for are ValueErrors, what the C library
     refuses is a KVRelayoutError.
 
     Calls run on torch's current stream, or on ``stream`` (a torch stream or a handle). Results that a
