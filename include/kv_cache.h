@@ -34,16 +34,28 @@
 extern "C" {
 #endif
 
-/* Element types: kvr_dtype's KVR_DTYPE_BF16 (1) and KVR_DTYPE_FP8_E4M3 (2), and IEEE half. */
+/* Element types: kvr_dtype's KVR_DTYPE_BF16 (1) and KVR_DTYPE_FP8_E4M3 (2), IEEE half, and 4 bits. */
 #define KVC_DTYPE_F16 3
+
+/*
+ * A 4-bit pool's row of D elements is D / 2 bytes of E2M1 codes (element 2 i in the low half of byte i) and
+ * D / 16 bytes of block scales, E4M3 numbers, each for 16 neighbours. An element stands for
+ *   E2M1(code) * E4M3(block scale) * s,    s: the plane's or head's (kvc_desc.scales, 1 without).
+ * The pool is [num_layers][2][num_blocks][block_size][kv_heads][D / 2] bytes of codes and right behind
+ * them [num_layers][2][num_blocks][block_size][kv_heads][D / 16] bytes of block scales. With a layout,
+ * bases has 2 L C entries, those of the codes' planes and then those of the block scales', whose strides are
+ * an eighth of the codes'. Keys and values only; D a multiple of 64; code strides multiples of 32 bytes,
+ * of 64 where D is a multiple of 128.
+ */
+#define KVC_DTYPE_E2M1 5
 
 /* Most requests of one attention call. */
 #define KVC_MAX_REQUESTS 2048
 
 /* Flags of kv_cache_status(). */
-#define KVC_FLAG_REQUEST 1u    /* append: a request index outside the block table's rows */
-#define KVC_FLAG_POSITION 2u   /* append: a position beyond the block table or the rotation table */
-#define KVC_FLAG_LENGTH 4u     /* attend: a negative length, or one beyond the block table */
+#define KVC_FLAG_REQUEST 1u    /* append, read: a request index outside the block table's rows */
+#define KVC_FLAG_POSITION 2u   /* append, read: a position beyond the block table or the rotation table */
+#define KVC_FLAG_LENGTH 4u     /* a negative length, or one beyond the block table or the weights */
 #define KVC_FLAG_BLOCK 8u      /* a block id outside [0, num_blocks) */
 #define KVC_FLAG_TIMEOUT 16u   /* a wait inside a kernel gave up (a defect of the library) */
 
@@ -59,7 +71,7 @@ typedef struct kvc_desc {
     int64_t num_blocks;        /* N >= 1 */
     void *pool;                /* device, 16-byte aligned (ignored with a layout) */
     const kvr_layout *layout;  /* NULL: the standard layout; else bases [L * C], byte strides */
-    const float *scales;       /* host [L][C] or [L][C][H], E4M3 pools only (required there):
+    const float *scales;       /* host [L][C] or [L][C][H], E4M3 (required there) and E2M1 pools only:
                                   positive, finite; copied */
     int32_t query_heads;       /* Hq: a multiple of H (0: this cache only appends) */
     int32_t max_requests;      /* most requests of an attention call, 1..KVC_MAX_REQUESTS */
@@ -111,7 +123,11 @@ typedef struct kvc_table {
  * negative position marks padding: nothing of that token is written. Keys (or latents)
  * are rotated, values are not; rows are stored in the pool's type. An E4M3 pool stores
  * E4M3(x * fl32(1 / s)), nearest-even, saturating at +-448, of the rotated fp32 value x (a NaN
- * gives a NaN code).
+ * gives a NaN code). A 4-bit pool stores, of each group of 16 elements y = fl32(x * fl32(1 / s)),
+ *   b = max(2^-9, E4M3(fl32(max |y| * fl32(1 / 6)))),   codes E2M1(fl32(y * fl32(1 / b))),
+ * nearest-even, saturating at 448 and at +-6; a NaN makes b, and so its group, NaN. For this pool the two products
+ * of a rotated element and their sum are rounded one by one (a value next to a border of its codes goes the same
+ * way wherever it is worked out), and rotary_dim and q_dim are multiples of 32.
  * The queries, where given, are rotated into q_out (which may be q itself).
  * Requirements: k, v, q of `dtype` (the pool's type if that has 16 bits), rows contiguous,
  * every address and stride a multiple of 16 bytes; rotary_dim a multiple of 16, at most both
@@ -143,6 +159,32 @@ typedef struct kvc_append {
 kvr_status kv_cache_append(const kvc_cache *cache, int32_t layer, const kvc_append *args,
                            void *stream);
 
+/* The same, with keys and queries rotated by angles[t] (device [num_tokens]; NULL: positions[t]), so that a
+ * token may be stored at another place than its own: behind what an eviction has left. An angle below zero, or
+ * beyond the rotation table, is KVC_FLAG_POSITION and nothing of that token is written. */
+kvr_status kv_cache_append_at(const kvc_cache *cache, int32_t layer, const kvc_append *args,
+                              const int32_t *angles, void *stream);
+
+/*
+ * Read tokens back: row t of k and v gets what the pool holds for token positions[t] of request requests[t],
+ * as numbers of `dtype` (the pool's type if that has 16 bits; others are decoded, scaled in fp32 and
+ * rounded once, nearest-even). Padding (a negative position) and tokens whose request, position or block is out of range
+ * (flagged) give zeros. Requirements as for kv_cache_append.
+ */
+typedef struct kvc_read {
+    int32_t num_tokens;        /* >= 0 */
+    int32_t dtype;             /* KVR_DTYPE_BF16 or KVC_DTYPE_F16: type of k, v */
+    const int32_t *requests;   /* device [num_tokens] */
+    const int32_t *positions;  /* device [num_tokens] */
+    kvc_table table;
+    void *k;                   /* device [num_tokens][H][D] */
+    void *v;                   /* device [num_tokens][H][D]; NULL for a latent */
+    int64_t k_token_stride, k_head_stride;     /* bytes */
+    int64_t v_token_stride, v_head_stride;
+} kvc_read;
+
+kvr_status kv_cache_read(const kvc_cache *cache, int32_t layer, const kvc_read *args, void *stream);
+
 /*
  * Attention of the newest `num_new` tokens of each request over layer `layer`. lengths[r]
  * counts the request's cached tokens, the newest included (append them first). Query i of
@@ -155,9 +197,9 @@ kvr_status kv_cache_append(const kvc_cache *cache, int32_t layer, const kvc_appe
  * windows) is never used, NaN included, and table entries of blocks that hold such places only
  * are not looked at; a NaN or an infinity in a value at a place that only some of a request's
  * newest tokens see may reach the others.
- * Weights below 2^-24 of a row's largest count as zero where the cache holds f16 or E4M3. Before they
+ * Weights below 2^-24 of a row's largest count as zero where the cache holds f16, E4M3 or E2M1. Before they
  * meet the values, weights count with 15 bits or more over bf16 and f16 keys and values and under at most
- * 32 rows (num_new Hq) of latents, with those of an f16 over E4M3, and with those of the pool's type
+ * 32 rows (num_new Hq) of latents, with those of an f16 over E4M3 and E2M1, and with those of the pool's type
  * under more rows of latents; sums are fp32.
  * Requirements: q and out of `dtype` (the pool's type if that has 16 bits), rows contiguous,
  * every address and stride a multiple of 16 bytes; lse NULL or [R][num_new][Hq], contiguous.

@@ -24,4 +24,4 @@ Public API (see ``include/kv_relayout.h`` for the C ABI it binds):
 from .kv_relayout import (KVRelayoutError, RelayoutPlan, desc_bytes, library,  # noqa: F401
                           LIB_PATH, STATUS, EXPORTS, relayout_all_prealloc, layout_of_views,
                           pack_plan, unpack_plan, SmStream, DTYPE_BF16, DTYPE_FP8_E4M3)
-from .kv_cache import KVCache, rotary_table, DTYPE_F16  # noqa: F401
+from .kv_cache import KVCache, rotary_table, DTYPE_F16, DTYPE_FP4_E2M1  # noqa: F401

@@ -46,8 +46,11 @@ kvr_status build(const kvc_desc *desc, kvc_cache *c) {
     if (L < 1 || (C != 1 && C != 2) || H < 1 || D < 1 || d.block_size < 1 || d.num_blocks < 1 ||
         d.value_dim < 0 || (d.per_head != 0 && d.per_head != 1) || d.query_heads < 0)
         return KVR_ERR_INVALID_ARG;
-    if (d.dtype != KVR_DTYPE_BF16 && d.dtype != KVC_DTYPE_F16 && d.dtype != KVR_DTYPE_FP8_E4M3)
+    if (d.dtype != KVR_DTYPE_BF16 && d.dtype != KVC_DTYPE_F16 && d.dtype != KVR_DTYPE_FP8_E4M3 &&
+        d.dtype != KVC_DTYPE_E2M1)
         return KVR_ERR_UNSUPPORTED;
+    const bool four = d.dtype == KVC_DTYPE_E2M1;
+    if (four && (C != 2 || D % 64 != 0)) return KVR_ERR_UNSUPPORTED;
     if (d.num_blocks > INT32_MAX || (int64_t)L * C > (int64_t)1 << 26) return KVR_ERR_UNSUPPORTED;
     if (d.value_dim == 0) d.value_dim = C == 1 ? KVC_LATENT_VALUES : D;
     if (C == 1) {
@@ -63,16 +66,16 @@ kvr_status build(const kvc_desc *desc, kvc_cache *c) {
         if (d.max_requests > KVC_MAX_REQUESTS || d.query_heads > 4096 || d.max_new > 4096)
             return KVR_ERR_UNSUPPORTED;
     }
-    const int64_t row = (int64_t)D * kvc_elem_bytes(d.dtype);
+    const int64_t row = kvc_row_bytes(d.dtype, D);
     c->row_bytes = row;
     c->block = kvr_make_div((uint32_t)d.block_size);
 
     c->scales.clear();
-    if (d.dtype == KVR_DTYPE_FP8_E4M3) {
-        if (d.scales == nullptr) return KVR_ERR_INVALID_ARG;
+    if (d.dtype == KVR_DTYPE_FP8_E4M3 || four) {
+        if (d.scales == nullptr && !four) return KVR_ERR_INVALID_ARG;
         for (int64_t v = 0; v < (int64_t)L * C; ++v)
             for (int32_t h = 0; h < H; ++h) {
-                const float s = d.scales[d.per_head ? v * H + h : v];
+                const float s = d.scales == nullptr ? 1.0f : d.scales[d.per_head ? v * H + h : v];
                 if (!(s > 0.0f) || !std::isfinite(s)) return KVR_ERR_INVALID_ARG;
                 c->scales.push_back(s);
             }
@@ -93,6 +96,14 @@ kvr_status build(const kvc_desc *desc, kvc_cache *c) {
         c->span = plane;
         for (size_t v = 0; v < c->base.size(); ++v)
             c->base[v] = (uint64_t)(uintptr_t)d.pool + v * (uint64_t)plane;
+        if (four) {
+            if (total > INT64_MAX - total / 8 ||
+                (uint64_t)(uintptr_t)d.pool > UINT64_MAX - (uint64_t)(total + total / 8))
+                return KVR_ERR_UNSUPPORTED;
+            for (size_t v = 0; v < c->base.size(); ++v)
+                c->block_scale_base.push_back((uint64_t)(uintptr_t)d.pool + (uint64_t)total +
+                                              v * (uint64_t)(plane / 8));
+        }
     } else {
         const kvr_layout &lay = *d.layout;
         if (lay.bases == nullptr || lay.block_stride < 0 || lay.token_stride < 0 ||
@@ -102,7 +113,8 @@ kvr_status build(const kvc_desc *desc, kvc_cache *c) {
         c->block_stride = d.num_blocks > 1 ? lay.block_stride : 0;
         c->token_stride = d.block_size > 1 ? lay.token_stride : 0;
         c->head_stride = H > 1 ? lay.head_stride : 0;
-        if (c->block_stride % 16 != 0 || c->token_stride % 16 != 0 || c->head_stride % 16 != 0)
+        const int64_t step = four ? (D % 128 == 0 ? 64 : 32) : 16;
+        if (c->block_stride % step != 0 || c->token_stride % step != 0 || c->head_stride % step != 0)
             return KVR_ERR_ALIGNMENT;
         int64_t a = 0, b = 0, h = 0;
         if (!mul_fits({d.num_blocks - 1, c->block_stride}, &a) ||
@@ -116,12 +128,19 @@ kvr_status build(const kvc_desc *desc, kvc_cache *c) {
             if ((uintptr_t)lay.bases[v] % 16 != 0) return KVR_ERR_ALIGNMENT;
             c->base[v] = (uint64_t)(uintptr_t)lay.bases[v];
         }
+        for (size_t v = c->base.size(); four && v < 2 * c->base.size(); ++v) {
+            if (lay.bases[v] == nullptr) return KVR_ERR_INVALID_ARG;
+            if ((uintptr_t)lay.bases[v] % 16 != 0) return KVR_ERR_ALIGNMENT;
+            c->block_scale_base.push_back((uint64_t)(uintptr_t)lay.bases[v]);
+        }
         if (!slots_are_disjoint(d.num_blocks, c->block_stride, d.block_size, c->token_stride, H,
                                 c->head_stride, row))
             return KVR_ERR_POOL_OVERLAP;
     }
     for (uint64_t b : c->base)
         if (b > UINT64_MAX - (uint64_t)c->span) return KVR_ERR_UNSUPPORTED;
+    for (uint64_t b : c->block_scale_base)
+        if (b > UINT64_MAX - (uint64_t)(c->span / 8)) return KVR_ERR_UNSUPPORTED;
     // host pointers of the caller's that are not needed any more
     d.layout = nullptr;
     d.scales = nullptr;
@@ -171,28 +190,29 @@ kvr_status check_plane(uint64_t base, int64_t span, int dev) {
     return KVR_OK;
 }
 
-bool on_device(const kvc_cache *c) {
-    int dev = -1;
-    return cudaGetDevice(&dev) == cudaSuccess && dev == c->device;
-}
-
-bool ok_table(const kvc_table &t) {
-    return t.rows >= 0 && t.width >= 0 && t.stride >= 0 &&
-           (t.ids != nullptr || t.rows == 0 || t.width == 0) && (uintptr_t)t.ids % 4 == 0;
-}
-
 bool aligned16(std::initializer_list<int64_t> xs) {
     for (int64_t x : xs)
         if (x % 16 != 0) return false;
     return true;
 }
 
-bool type_fits(const kvc_cache *c, int32_t dtype) {
-    return c->d.dtype == KVR_DTYPE_FP8_E4M3 ? dtype == KVR_DTYPE_BF16 || dtype == KVC_DTYPE_F16
-                                            : dtype == c->d.dtype;
+}  // namespace
+
+bool kvc_on_device(const kvc_cache *c) {
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == c->device;
 }
 
-}  // namespace
+bool kvc_ok_table(const kvc_table &t) {
+    return t.rows >= 0 && t.width >= 0 && t.stride >= 0 &&
+           (t.ids != nullptr || t.rows == 0 || t.width == 0) && (uintptr_t)t.ids % 4 == 0;
+}
+
+bool kvc_type_fits(const kvc_cache *c, int32_t dtype) {
+    return c->d.dtype == KVR_DTYPE_FP8_E4M3 || c->d.dtype == KVC_DTYPE_E2M1
+               ? dtype == KVR_DTYPE_BF16 || dtype == KVC_DTYPE_F16
+               : dtype == c->d.dtype;
+}
 
 bool kvc_make_map(CUtensorMap *map, int es, int rank, uint64_t base, int64_t row_bytes,
                   const uint64_t *dims, const int64_t *strides, const uint32_t *box, int line) {
@@ -256,6 +276,8 @@ extern "C" kvr_status kv_cache_create(const kvc_desc *desc, kvc_cache **out) {
         }
         for (size_t v = 0; st == KVR_OK && v < c->base.size(); ++v)
             st = check_plane(c->base[v], c->span, c->device);
+        for (size_t v = 0; st == KVR_OK && v < c->block_scale_base.size(); ++v)
+            st = check_plane(c->block_scale_base[v], c->span / 8, c->device);
         if (st == KVR_OK && c->d.query_heads > 0) st = kvc_attend_setup(c);
         if (st == KVR_OK) {
             const size_t bytes = place(*c, c->sm_count, nullptr, nullptr);
@@ -297,18 +319,17 @@ extern "C" void kv_cache_destroy(kvc_cache *cache) {
     delete cache;
 }
 
-extern "C" kvr_status kv_cache_append(const kvc_cache *c, int32_t layer, const kvc_append *a,
-                                      void *stream) {
+kvr_status kvc_check_append(const kvc_cache *c, int32_t layer, const kvc_append *a) {
     if (c == nullptr || a == nullptr) return KVR_ERR_INVALID_ARG;
     const kvc_desc &d = c->d;
     if (layer < 0 || layer >= d.num_layers) return KVR_ERR_LAYER_RANGE;
-    if (a->num_tokens < 0 || a->reserved != 0 || a->q_heads < 0 || !ok_table(a->table) ||
+    if (a->num_tokens < 0 || a->reserved != 0 || a->q_heads < 0 || !kvc_ok_table(a->table) ||
         (a->flags & ~(KVC_INTERLEAVED | KVC_ROTATE_LAST)) != 0)
         return KVR_ERR_INVALID_ARG;
     if (a->num_tokens > 0 && (a->requests == nullptr || a->positions == nullptr ||
                               a->k == nullptr || (a->v == nullptr) != c->latent()))
         return KVR_ERR_INVALID_ARG;
-    if (!type_fits(c, a->dtype)) return KVR_ERR_UNSUPPORTED;
+    if (!kvc_type_fits(c, a->dtype)) return KVR_ERR_UNSUPPORTED;
     if ((uintptr_t)a->requests % 4 != 0 || (uintptr_t)a->positions % 4 != 0 ||
         !aligned16({(int64_t)(uintptr_t)a->k, (int64_t)(uintptr_t)a->v, a->k_token_stride,
                     a->k_head_stride, a->v_token_stride, a->v_head_stride}))
@@ -335,22 +356,32 @@ extern "C" kvr_status kv_cache_append(const kvc_cache *c, int32_t layer, const k
                         a->q_head_stride, a->q_out_token_stride, a->q_out_head_stride}))
             return KVR_ERR_ALIGNMENT;
     }
-    if (!on_device(c)) return KVR_ERR_INVALID_ARG;
+    // (a thread of the 4-bit pool's kernel takes 32 elements)
+    if (d.dtype == KVC_DTYPE_E2M1 && ((a->rotary != nullptr && a->rotary_dim % 32 != 0) ||
+                                      (a->q_heads > 0 && a->q_dim % 32 != 0)))
+        return KVR_ERR_UNSUPPORTED;
+    return KVR_OK;
+}
+
+extern "C" kvr_status kv_cache_append(const kvc_cache *c, int32_t layer, const kvc_append *a,
+                                      void *stream) {
+    const kvr_status st = kvc_check_append(c, layer, a);
+    if (st != KVR_OK) return st;
+    if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
     if (a->num_tokens == 0) return KVR_OK;
     return kvc_append_launch(c, layer, a, stream);
 }
 
-extern "C" kvr_status kv_cache_attend(const kvc_cache *c, int32_t layer, const kvc_attend *a,
-                                      void *stream) {
+kvr_status kvc_check_attend(const kvc_cache *c, int32_t layer, const kvc_attend *a) {
     if (c == nullptr || a == nullptr) return KVR_ERR_INVALID_ARG;
     const kvc_desc &d = c->d;
     if (layer < 0 || layer >= d.num_layers) return KVR_ERR_LAYER_RANGE;
     if (d.query_heads < 1) return KVR_ERR_UNSUPPORTED;
     if (a->num_requests < 0 || a->num_requests > d.max_requests || a->num_new < 1 ||
         a->num_new > d.max_new || a->window < 0 || a->reserved != 0 || !std::isfinite(a->scale) ||
-        !ok_table(a->table) || a->table.rows < a->num_requests)
+        !kvc_ok_table(a->table) || a->table.rows < a->num_requests)
         return KVR_ERR_INVALID_ARG;
-    if (!type_fits(c, a->dtype)) return KVR_ERR_UNSUPPORTED;
+    if (!kvc_type_fits(c, a->dtype)) return KVR_ERR_UNSUPPORTED;
     // positions are 32-bit: a table row must not describe more of them
     if ((int64_t)a->table.width * d.block_size > (int64_t)INT32_MAX - KVC_MAX_REQUESTS)
         return KVR_ERR_UNSUPPORTED;
@@ -364,7 +395,14 @@ extern "C" kvr_status kv_cache_attend(const kvc_cache *c, int32_t layer, const k
                     a->q_token_stride, a->q_head_stride, a->out_request_stride,
                     a->out_token_stride, a->out_head_stride}))
         return KVR_ERR_ALIGNMENT;
-    if (!on_device(c)) return KVR_ERR_INVALID_ARG;
+    return KVR_OK;
+}
+
+extern "C" kvr_status kv_cache_attend(const kvc_cache *c, int32_t layer, const kvc_attend *a,
+                                      void *stream) {
+    const kvr_status st = kvc_check_attend(c, layer, a);
+    if (st != KVR_OK) return st;
+    if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
     if (a->num_requests == 0) return KVR_OK;
     try {
         // Latents take two launches that hand the workspace over: another host thread's must not

@@ -35,7 +35,7 @@ struct KvcSlots {
 struct KvcWorkspace {
     unsigned char *mem;       // one allocation
     size_t bytes;
-    float *scales;            // [L][C][H] (E4M3 pools)
+    float *scales;            // [L][C][H] (E4M3 and E2M1 pools)
     float *partial;           // attend: accumulators of key ranges that another part finishes
     uint32_t *arrived;        // attend: parts of a job that are done, zero between launches; latents:
                               // units and parts before each request, from the products to the join
@@ -45,6 +45,7 @@ struct KvcWorkspace {
 struct kvc_cache {
     kvc_desc d = {};
     std::vector<uint64_t> base;       // [L][C]
+    std::vector<uint64_t> block_scale_base;   // [L][C] (4-bit pools): strides are an eighth of the codes'
     std::vector<float> scales;        // [L][C][H]
     int64_t block_stride = 0, token_stride = 0, head_stride = 0;
     int64_t row_bytes = 0;
@@ -61,6 +62,11 @@ struct kvc_cache {
         return {(unsigned char *)(uintptr_t)base[(size_t)layer * d.num_components + comp],
                 block_stride, token_stride, head_stride};
     }
+    unsigned char *block_scales(int32_t layer, int32_t comp) const {
+        return block_scale_base.empty()
+                   ? nullptr
+                   : (unsigned char *)(uintptr_t)block_scale_base[(size_t)layer * d.num_components + comp];
+    }
     KvcSlots slots(const kvc_table &t) const {
         return {t.ids, t.stride, t.rows, t.width, (int32_t)d.num_blocks, block};
     }
@@ -72,7 +78,10 @@ struct kvc_cache {
     bool latent() const { return d.num_components == 1; }
 };
 
-inline int kvc_elem_bytes(int32_t dtype) { return dtype == KVR_DTYPE_FP8_E4M3 ? 1 : 2; }
+// Bytes of a row of D elements (a 4-bit pool's codes).
+inline int64_t kvc_row_bytes(int32_t dtype, int32_t D) {
+    return dtype == KVC_DTYPE_E2M1 ? D / 2 : dtype == KVR_DTYPE_FP8_E4M3 ? D : 2 * (int64_t)D;
+}
 
 // SMs that a launch on `stream` may use (sm_stream.cpp tells a green context's).
 int32_t kvr_stream_green_sms(void *stream);
@@ -110,14 +119,26 @@ inline kvr_status kvc_launch(void (*kernel)(Args), const Args &a, dim3 grid, int
 bool kvc_make_map(CUtensorMap *map, int es, int rank, uint64_t base, int64_t row_bytes,
                   const uint64_t *dims, const int64_t *strides, const uint32_t *box, int line);
 
+// cache.cpp: whether a call's arguments hold (KVR_OK), but for the current device.
+kvr_status kvc_check_append(const kvc_cache *c, int32_t layer, const kvc_append *a);
+kvr_status kvc_check_attend(const kvc_cache *c, int32_t layer, const kvc_attend *a);
+bool kvc_ok_table(const kvc_table &t);
+bool kvc_type_fits(const kvc_cache *c, int32_t dtype);
+bool kvc_on_device(const kvc_cache *c);
+
 // cache_attend.cu, cache_latent.cu: the launches behind kv_cache_attend(), and what they want
 // of the workspace. (`setup` runs once a cache: shared memory limits of the kernels.)
 kvr_status kvc_attend_launch(const kvc_cache *c, int32_t layer, const kvc_attend *a, void *stream);
 size_t kvc_attend_partial_bytes(const kvc_desc &d, int32_t sm_count);
 size_t kvc_attend_jobs(const kvc_desc &d);
 kvr_status kvc_attend_setup(kvc_cache *c);
-// cache_append.cu
+// cache_append.cu, cache_append_e2m1.cu (`angles`: NULL for the positions), cache_read.cu
 kvr_status kvc_append_launch(const kvc_cache *c, int32_t layer, const kvc_append *a, void *stream);
+kvr_status kvc_append_at_launch(const kvc_cache *c, int32_t layer, const kvc_append *a,
+                                const int32_t *angles, void *stream);
+kvr_status kvc_append_e2m1_launch(const kvc_cache *c, int32_t layer, const kvc_append *a,
+                                  const int32_t *angles, void *stream);
+kvr_status kvc_read_launch(const kvc_cache *c, int32_t layer, const kvc_read *a, void *stream);
 
 #if defined(__CUDACC__)
 
@@ -163,6 +184,15 @@ __device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t two_codes) {
         : "=r"(h2)
         : "r"(two_codes));
     return h2;
+}
+
+// Four pairs of E2M1 codes (low half first), one a byte, as f16x2: exact.
+__device__ __forceinline__ void e2m1_to_f16x2(uint32_t w, uint32_t h[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
 }
 
 }  // namespace kvc

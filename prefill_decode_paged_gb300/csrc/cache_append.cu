@@ -37,6 +37,7 @@ struct AppendArgs {
     unsigned char *q_out;
     int64_t q_out_token, q_out_head;
     const int32_t *requests, *positions;
+    const int32_t *angles;    // positions of rotation, NULL: `positions`
     KvcSlots slots;
     const float *rotary;      // [rows][R]
     int32_t rotary_rows, R;
@@ -172,6 +173,7 @@ append_kernel(AppendArgs a) {
     let_next_start();
     const int64_t token = blockIdx.x;
     const int32_t pos = __ldg(a.positions + token), req = __ldg(a.requests + token);
+    const int32_t turned = a.angles != nullptr ? __ldg(a.angles + token) : pos;
     const int32_t n = a.q.heads * (int32_t)a.q_units.d + (a.k.heads + a.v.heads) * (int32_t)a.units.d;
     int64_t slot = -1;                       // the token's slot in a plane, in bytes
     const float *angles = nullptr;
@@ -199,12 +201,12 @@ append_kernel(AppendArgs a) {
             if (req < 0 || req >= a.slots.rows) {
                 bad = KVC_FLAG_REQUEST;
             } else if (entry >= (uint32_t)a.slots.width ||
-                       (a.rotary != nullptr && pos >= a.rotary_rows)) {
+                       (a.rotary != nullptr && (turned < 0 || turned >= a.rotary_rows))) {
                 bad = KVC_FLAG_POSITION;
             } else {
                 const int32_t id = __ldg(a.slots.ids + (int64_t)req * a.slots.stride + entry);
                 const int32_t off = pos - (int32_t)(entry * a.slots.block.d);
-                angles = a.rotary + (int64_t)pos * a.R;
+                angles = a.rotary + (int64_t)turned * a.R;
                 if (id < 0 || id >= a.slots.num_blocks)
                     bad = KVC_FLAG_BLOCK;
                 else
@@ -265,6 +267,12 @@ kvr_status go(AppendArgs &a, bool interleaved, int32_t tokens, int sms, void *st
 }  // namespace
 
 kvr_status kvc_append_launch(const kvc_cache *c, int32_t layer, const kvc_append *p, void *stream) {
+    return kvc_append_at_launch(c, layer, p, nullptr, stream);
+}
+
+kvr_status kvc_append_at_launch(const kvc_cache *c, int32_t layer, const kvc_append *p, const int32_t *angles,
+                                void *stream) {
+    if (c->d.dtype == KVC_DTYPE_E2M1) return kvc_append_e2m1_launch(c, layer, p, angles, stream);
     AppendArgs a = {};
     const int32_t H = c->d.kv_heads;
     a.k = {(const unsigned char *)p->k, p->k_token_stride, p->k_head_stride, H};
@@ -281,6 +289,7 @@ kvr_status kvc_append_launch(const kvc_cache *c, int32_t layer, const kvc_append
     a.q_out_head = p->q_out_head_stride;
     a.requests = p->requests;
     a.positions = p->positions;
+    a.angles = angles;
     a.slots = c->slots(p->table);
     a.rotary = p->rotary;
     a.rotary_rows = p->rotary_rows;

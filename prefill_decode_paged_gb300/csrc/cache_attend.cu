@@ -13,6 +13,7 @@ using namespace kvc;
 
 AttendPick pick(const kvc_desc &d, int32_t M) {
     return d.dtype == KVR_DTYPE_FP8_E4M3 ? attend_pick_e4m3(d.head_dim, M)
+           : d.dtype == KVC_DTYPE_E2M1   ? attend_pick_e2m1(d.head_dim, M)
            : d.dtype == KVC_DTYPE_F16    ? attend_pick_f16(d.head_dim, M)
                                          : attend_pick_bf16(d.head_dim, M);
 }
@@ -25,8 +26,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t kvc_attend_partial_bytes(const kvc_desc &d, int32_t sm_count) {
     if (d.num_components == 1) return kvc_latent_partial_bytes(sm_count);
     size_t rows = 0;
-    for (int32_t M : {8, 16, 32}) rows = std::max(rows, (size_t)pick(d, M).rp);
-    return (size_t)sm_count * 2 * 2 * rows * (size_t)(d.head_dim + 2) * sizeof(float);
+    for (int32_t M : {8, 16, 32})
+        rows = std::max(rows, (size_t)std::max(2, pick(d, M).blocks) * (size_t)pick(d, M).rp);
+    return (size_t)sm_count * 2 * rows * (size_t)(d.head_dim + 2) * sizeof(float);
 }
 
 size_t kvc_attend_jobs(const kvc_desc &d) {
@@ -55,6 +57,8 @@ kvr_status kvc_attend_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     a.v_plane = c->plane(layer, 1);
     a.k_scale = c->scale_of(layer, 0);
     a.v_scale = c->scale_of(layer, 1);
+    a.k_block_scales = c->block_scales(layer, 0);
+    a.v_block_scales = c->block_scales(layer, 1);
     a.split = {c->slots(p->table), p->lengths, c->ws.flags, p->num_requests, p->num_new, p->window};
     a.q = (const unsigned char *)p->q;
     a.out = (unsigned char *)p->out;

@@ -56,6 +56,7 @@ struct AttendArgs {
     float *lse;
     int64_t q_request, q_token, q_head, out_request, out_token, out_head;
     const float *k_scale, *v_scale;
+    const unsigned char *k_block_scales, *v_block_scales;   // 4-bit pools: an eighth of a row's offset on
     float *partial;
     uint32_t *arrived;
     int32_t m, H, G, D, f16;
@@ -80,20 +81,22 @@ constexpr float GROWTH_OF = F16 ? 5.0f : 8.0f;
 
 template <int DP, int POOL, int NT>
 struct Attend {
-    static constexpr int ES = POOL == KVR_DTYPE_FP8_E4M3 ? 1 : 2;
+    static constexpr bool E4 = POOL == KVR_DTYPE_FP8_E4M3, E2 = POOL == KVC_DTYPE_E2M1;
     static constexpr bool F16 = POOL != KVR_DTYPE_BF16;          // type of the products
-    static constexpr bool SPLIT = POOL != KVR_DTYPE_FP8_E4M3;    // P as two numbers
-    static constexpr int ROW = DP * ES;                          // bytes of a row in the ring
+    static constexpr bool CODES = E4 || E2;                      // elements that become f16 on the way
+    static constexpr bool SPLIT = !CODES;                        // P as two numbers
+    static constexpr int ROW = E2 ? DP / 2 : E4 ? DP : DP * 2;   // bytes of a row in the ring
+    static constexpr int SROW = E2 ? DP / 16 : 0;                // and of its block scales
     static constexpr int KT = 2 * 16 * ROW >= 8192 ? 16 : 32;    // keys of a tile
     static constexpr int KS = KT / 16;
-    static constexpr int STAGE = 2 * KT * ROW;
-    static constexpr int STAGES = STAGE >= 8192 ? 3 : 6;
+    static constexpr int STAGE = 2 * KT * (ROW + SROW);          // keys, values, then their block scales
+    static constexpr int BLOCKS = E2 ? (DP > 128 || NT > 1 ? 2 : 4) : STAGE > 8192 ? 1 : 2;   // resident on an SM
+    static constexpr int STAGES = E2 ? (BLOCKS == 4 && DP == 128 ? 3 : DP > 128 ? 3 : 5) : STAGE >= 8192 ? 3 : 6;
     static constexpr int RING = ATTEND_WARPS * STAGES * STAGE;
     static constexpr int UNIT = ATTEND_WARPS * KT;               // keys of a unit
     static constexpr int RP = 8 * NT;
     static constexpr int MT = DP / 16;
     static constexpr int PITCH = DP + 4;                         // floats of a row to be joined
-    static constexpr int BLOCKS = STAGE > 8192 ? 1 : 2;          // resident on an SM
     static constexpr int Q_BYTES = RP * DP * 2;
     static_assert(ATTEND_WARPS * RP * PITCH * 4 <= RING, "the join reuses the ring");
     // ring, queries, a barrier, then floats: row scales [RP], per-warp statistics [4][RP][2]; 4 ints;
@@ -111,6 +114,11 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(bytes)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_few(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -135,6 +143,11 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
 template <bool F16>
 __device__ __forceinline__ void mma(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
     if (F16)
@@ -154,7 +167,8 @@ __device__ __forceinline__ void mma(float c[4], const uint32_t a[4], uint32_t b0
 template <int ROW>
 __device__ __forceinline__ uint32_t swizzled(uint32_t r, uint32_t c) {
     if (ROW >= 128) return r * ROW + ((c ^ (r & 7)) << 4);
-    return r * ROW + ((c ^ ((r >> 1) & 3)) << 4);       // 64-byte rows: two share 128 bytes
+    if (ROW >= 64) return r * ROW + ((c ^ ((r >> 1) & 3)) << 4);   // two rows share 128 bytes
+    return r * ROW + ((c ^ ((r >> 2) & 1)) << 4);                  // four do
 }
 
 // -- the barrier that a join's copies count at ------------------------------------------
@@ -187,6 +201,94 @@ __device__ __forceinline__ void load_bytes(uint32_t dst, const void *src, uint32
     asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
+}
+
+// -- 4-bit codes ---------------------------------------------------------------------------
+//
+// An 8 x 8 matrix of ldmatrix is 8 rows of 32 codes here. As it is, a lane gets 8 codes of one row, pairs for
+// the steps of two products; transposed, 4 neighbouring codes of each of two rows, whose odd ones change
+// places so that each byte holds two rows' codes of one element. A code times its block scale is exact in f16: at
+// most 6 bits, from 2^-10 to 2688.
+
+// Keys by rows: s += the products of a tile's KT keys and the queries.
+template <int DP, int KT, int NT>
+__device__ __forceinline__ void scores_e2m1(float (&s)[KT / 16][NT][4], uint32_t kbase, uint32_t q_base,
+                                            const unsigned char *scales) {
+    constexpr int ROW = DP / 2, SROW = DP / 16;
+    const int lane = threadIdx.x % 32, g = lane / 4, t4 = lane % 4;
+    const uint32_t pick = t4 < 2 ? 0x2200 : 0x3311;     // a lane's codes lie within one group of 16
+#pragma unroll
+    for (int k = 0; k < KT / 16; ++k) {
+        uint32_t sc[2][SROW / 4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int p = 0; p < SROW / 4; ++p)
+                sc[u][p] = *(const uint32_t *)(scales + (k * 16 + u * 8 + g) * SROW + 4 * p);
+#pragma unroll
+        for (int p = 0; p < DP / 64; ++p) {             // 64 elements: a word of block scales
+            uint32_t w[4];                              // rows g, g + 8 of the 1st, 2nd 32 elements
+            ldmatrix4(w, kbase + swizzled<ROW>(k * 16 + lane % 16, p * 2 + lane / 16));
+            const uint32_t lo = __byte_perm(sc[0][p], 0, pick), hi = __byte_perm(sc[1][p], 0, pick);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const uint32_t slo = e4m3_to_f16x2(c == 0 ? lo : lo >> 16);
+                const uint32_t shi = e4m3_to_f16x2(c == 0 ? hi : hi >> 16);
+                uint32_t x[4], y[4];
+                e2m1_to_f16x2(w[2 * c], x);
+                e2m1_to_f16x2(w[2 * c + 1], y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = mul_f16x2(x[e], slo), y[e] = mul_f16x2(y[e], shi);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    uint32_t b[4];                      // [step][half]
+                    ldmatrix4(b, q_base + swizzled<DP * 2>(n * 8 + lane % 8, (p * 2 + c) * 4 + lane / 8));
+                    const uint32_t f0[4] = {x[0], y[0], x[1], y[1]}, f1[4] = {x[2], y[2], x[3], y[3]};
+                    mma<true>(s[k][n], f0, b[0], b[1]);
+                    mma<true>(s[k][n], f1, b[2], b[3]);
+                }
+            }
+        }
+    }
+}
+
+// Elements by rows: o += the products of the values of 16 keys (the k-th of the tile) and their weights. Rows g
+// and g + 8 of o[i] are elements 4 g + 2 (i % 2) and the next of the 32 from 32 (i / 2) on.
+template <int DP, int KT, int NT>
+__device__ __forceinline__ void values_e2m1(float (&o)[DP / 16][NT][4], const uint32_t (&ph)[NT][2], int k,
+                                            uint32_t vbase, const unsigned char *scales) {
+    constexpr int ROW = DP / 2, SROW = DP / 16;
+    const int lane = threadIdx.x % 32, g = lane / 4, t4 = lane % 4;
+    const uint32_t pick = g < 4 ? 0x6240 : 0x7351;      // a lane's 4 elements lie within one group of 16
+#pragma unroll
+    for (int p = 0; p < DP / 64; ++p) {
+        uint32_t sc[2];                                 // keys 2 t4, 2 t4 + 1 of the 1st, 2nd 8
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const unsigned char *at = scales + (k * 16 + u * 8 + 2 * t4) * SROW + 4 * p;
+            sc[u] = __byte_perm(*(const uint32_t *)at, *(const uint32_t *)(at + SROW), pick);
+        }
+        uint32_t w[4];                                  // keys 0-7, 8-15 of the 1st, 2nd 32 elements
+        ldmatrix4t(w, vbase + swizzled<ROW>(k * 16 + lane % 16, p * 2 + lane / 16));
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t x[2][4];                           // elements 0, 2, 1, 3 of the lane's 4
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint32_t v = w[2 * c + u], odd = (v ^ (v >> 12)) & 0x0000F0F0u;
+                e2m1_to_f16x2(v ^ odd ^ (odd << 12), x[u]);
+                const uint32_t by = e4m3_to_f16x2(c == 0 ? sc[u] : sc[u] >> 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[u][e] = mul_f16x2(x[u][e], by);
+            }
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                const uint32_t f[4] = {x[0][st], x[0][st + 2], x[1][st], x[1][st + 2]};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma<true>(o[2 * (2 * p + c) + st][n], f, ph[n][0], ph[n][1]);
+            }
+        }
+    }
 }
 
 // Two weights (>= 0) as the 16-bit numbers next below them: the rests are positive wherever the
@@ -256,7 +358,7 @@ attend_kernel(AttendArgs a) {
         const int32_t rows = min(RP, M - row0);
         uint32_t bad = 0;
         const Span sp = span_of(a.split, r, 1, &bad);   // tiles begin at the first key
-        const float ks = POOL == KVR_DTYPE_FP8_E4M3 ? a.k_scale[h] : 1.0f;
+        const float ks = C::CODES ? a.k_scale[h] : 1.0f;
 
         // this warp's tiles; the lane's key of a tile (lane < KT) and its slot
         const int32_t tiles = (sp.n - sp.lo + KT - 1) / KT;
@@ -281,7 +383,7 @@ attend_kernel(AttendArgs a) {
             constexpr int CPR = ROW / 16, RPI = 32 / CPR;   // chunks of a row, rows at a time
             const uint32_t base = ring + (uint32_t)(stage * C::STAGE);
             const int c = lane % CPR;
-            const bool in_row = c * 16 < a.D * C::ES;
+            const bool in_row = C::E2 ? c * 32 < a.D : C::E4 ? c * 16 < a.D : c * 8 < a.D;
 #pragma unroll
             for (int i = 0; i < KT / RPI; ++i) {
                 const int row = i * RPI + lane / CPR;
@@ -291,6 +393,17 @@ attend_kernel(AttendArgs a) {
                 const uint32_t dst = base + swizzled<ROW>(row, c), n = there ? 16 : 0;
                 cp_async16(dst, a.k_plane.base + at, n);
                 cp_async16(dst + KT * ROW, a.v_plane.base + at, n);
+            }
+            if (C::E2) {                                // each lane its own key's block scales
+                constexpr int PIECE = DP == 128 ? 8 : 4;
+#pragma unroll
+                for (int p = 0; p < C::SROW / PIECE; ++p) {
+                    const bool there = slot >= 0 && p * PIECE * 16 < a.D;
+                    const int64_t at = there ? slot / 8 + p * PIECE : 0;
+                    const uint32_t dst = base + 2 * KT * ROW + lane * C::SROW + p * PIECE, n = there ? PIECE : 0;
+                    cp_async_few<PIECE>(dst, a.k_block_scales + at, n);
+                    cp_async_few<PIECE>(dst + KT * C::SROW, a.v_block_scales + at, n);
+                }
             }
         };
         // the queries, one warp a row, asked for ahead of the keys
@@ -326,7 +439,7 @@ attend_kernel(AttendArgs a) {
             const int row = n * ATTEND_WARPS + warp;
             const uint4 w = qw[n];
             float factor = a.scale * log2e * ks;
-            if (POOL != KVR_DTYPE_FP8_E4M3) {
+            if (!C::CODES) {
                 if (lane * 8 < DP)
                     *(uint4 *)(q_smem + swizzled<DP * 2>(row, lane)) = w;
             } else {
@@ -345,9 +458,17 @@ attend_kernel(AttendArgs a) {
                 e = e < 2 || e > 252 ? 127 : e;
                 const float down = __uint_as_float((254 - e) << 23);
                 factor *= __uint_as_float(e << 23);
-                // element d = 4 t + x of 16 is at 2 t + x (x < 2) or 8 + 2 t + x - 2: where the
-                // codes of four neighbours land when two 8-bit elements load as one 16-bit one
-                if (lane * 8 < DP) {
+                // 8 bits: element d = 4 t + x of 16 is at 2 t + x (x < 2) or 8 + 2 t + x - 2: where the
+                // codes of four neighbours land when two 8-bit elements load as one 16-bit one.
+                // 4 bits: pair y of elements 8 t + 2 y, 8 t + 2 y + 1 of 32 is at 8 y + 2 t: a lane's 8
+                // codes of a row are two pairs each for two steps of 16 elements
+                if (C::E2) {
+                    if (lane * 8 < DP)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *(uint32_t *)(q_smem + swizzled<DP * 2>(row, (lane / 4) * 4 + k) + (lane % 4) * 4) =
+                                narrow2<true>(f[2 * k] * down, f[2 * k + 1] * down);
+                } else if (lane * 8 < DP) {
                     const int grp = lane / 2, half = lane % 2;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -409,15 +530,17 @@ attend_kernel(AttendArgs a) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[k][n][e] = 0.0f;
             const uint32_t q_base = smem0 + C::RING;
+            if constexpr (C::E2)
+                scores_e2m1<DP, KT, NT>(s, kbase, q_base, smem + (vbase - smem0) + KT * ROW);
 #pragma unroll
-            for (int d2 = 0; d2 < DP / 32; ++d2) {      // two steps of 16 elements
+            for (int d2 = 0; d2 < (C::E2 ? 0 : DP / 32); ++d2) {      // two steps of 16 elements
                 uint32_t b[NT][4];                      // [row tile][step][half]
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     ldmatrix4(b[n], q_base + swizzled<DP * 2>(n * 8 + lane % 8, d2 * 4 + lane / 8));
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    if (C::ES == 2) {
+                    if (!C::CODES) {
 #pragma unroll
                         for (int st = 0; st < 2; ++st) {
                             uint32_t f[4];
@@ -524,7 +647,9 @@ attend_kernel(AttendArgs a) {
                     }
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                if (C::ES == 2) {
+                if constexpr (C::E2) {
+                    values_e2m1<DP, KT, NT>(o, ph[k], k, vbase, smem + (vbase - smem0) + KT * (ROW + C::SROW));
+                } else if (!C::CODES) {
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
                         uint32_t f[4];
@@ -577,8 +702,9 @@ attend_kernel(AttendArgs a) {
                 float *to = acc + (warp * RP + row) * C::PITCH;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
-                    to[i * 16 + (C::ES == 2 ? g : 2 * g)] = o[i][n][e];
-                    to[i * 16 + (C::ES == 2 ? g + 8 : 2 * g + 1)] = o[i][n][2 + e];
+                    const int at = C::E2 ? i / 2 * 32 + 4 * g + i % 2 * 2 : i * 16 + (C::E4 ? 2 * g : g);
+                    to[at] = o[i][n][e];
+                    to[at + (C::CODES ? 1 : 8)] = o[i][n][2 + e];
                 }
             }
         __syncthreads();
@@ -586,7 +712,7 @@ attend_kernel(AttendArgs a) {
         const bool whole = u0 == 0 && u1 == units;
         const int32_t D4 = a.D / 4;
         float *slot = a.partial + (size_t)(2 * blockIdx.x + (u0 == 0 ? 1 : 0)) * (size_t)slot_floats;
-        const float vs = POOL == KVR_DTYPE_FP8_E4M3 ? a.v_scale[h] : 1.0f;
+        const float vs = C::CODES ? a.v_scale[h] : 1.0f;
         // a row's maximum and sum are final: its lse, and what its accumulators are multiplied with
         auto settle = [&](int row, float m, float l) -> float {
             const bool some = l > 0.0f || l != l;
@@ -775,5 +901,6 @@ inline AttendPick attend_pick(int32_t D, int32_t M) {
 AttendPick attend_pick_bf16(int32_t D, int32_t M);   // one translation unit each
 AttendPick attend_pick_f16(int32_t D, int32_t M);
 AttendPick attend_pick_e4m3(int32_t D, int32_t M);
+AttendPick attend_pick_e2m1(int32_t D, int32_t M);
 
 }  // namespace kvc

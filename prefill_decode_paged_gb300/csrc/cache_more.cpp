@@ -1,0 +1,51 @@
+// cache_more.cpp -- host side of the decode cache's further calls: validation ahead of their launches.
+#include <math.h>
+
+#include <initializer_list>
+
+#include "cache.h"
+
+namespace {
+
+bool multiples(int64_t of, std::initializer_list<int64_t> xs) {
+    for (int64_t x : xs)
+        if (x % of != 0) return false;
+    return true;
+}
+bool negative(std::initializer_list<int64_t> xs) {
+    for (int64_t x : xs)
+        if (x < 0) return true;
+    return false;
+}
+int64_t address(const void *p) { return (int64_t)(uintptr_t)p; }
+
+}  // namespace
+
+extern "C" kvr_status kv_cache_append_at(const kvc_cache *c, int32_t layer, const kvc_append *a,
+                                         const int32_t *angles, void *stream) {
+    const kvr_status st = kvc_check_append(c, layer, a);
+    if (st != KVR_OK) return st;
+    if (address(angles) % 4 != 0) return KVR_ERR_ALIGNMENT;
+    if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
+    if (a->num_tokens == 0) return KVR_OK;
+    return kvc_append_at_launch(c, layer, a, angles, stream);
+}
+
+extern "C" kvr_status kv_cache_read(const kvc_cache *c, int32_t layer, const kvc_read *a, void *stream) {
+    if (c == nullptr || a == nullptr) return KVR_ERR_INVALID_ARG;
+    if (layer < 0 || layer >= c->d.num_layers) return KVR_ERR_LAYER_RANGE;
+    if (a->num_tokens < 0 || !kvc_ok_table(a->table)) return KVR_ERR_INVALID_ARG;
+    if (a->num_tokens > 0 && (a->requests == nullptr || a->positions == nullptr || a->k == nullptr ||
+                              (a->v == nullptr) != c->latent()))
+        return KVR_ERR_INVALID_ARG;
+    if (!kvc_type_fits(c, a->dtype)) return KVR_ERR_UNSUPPORTED;
+    if (negative({a->k_token_stride, a->k_head_stride, a->v_token_stride, a->v_head_stride}))
+        return KVR_ERR_INVALID_ARG;
+    if (!multiples(4, {address(a->requests), address(a->positions)}) ||
+        !multiples(16, {address(a->k), address(a->v), a->k_token_stride, a->k_head_stride,
+                        a->v_token_stride, a->v_head_stride}))
+        return KVR_ERR_ALIGNMENT;
+    if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
+    if (a->num_tokens == 0) return KVR_OK;
+    return kvc_read_launch(c, layer, a, stream);
+}

@@ -15,17 +15,19 @@ from .kv_relayout import (KVRelayoutError, KvrLayout, _contiguous, _Layout, _nby
                           _stream_handle, library)
 
 DTYPE_F16 = 3
+DTYPE_FP4_E2M1 = 5
 INTERLEAVED = 1
 ROTATE_LAST = 2
 FLAGS = {1: "request index", 2: "position", 4: "length", 8: "block id", 16: "wait"}
 SCALINGS = {"linear": 1, "base": 2, "ramp": 3, "bands": 4}
 CACHE_EXPORTS = ("kv_cache_create", "kv_cache_destroy", "kv_cache_workspace_bytes",
                  "kv_cache_append", "kv_cache_attend", "kv_cache_status",
-                 "kv_cache_rotary_table")
+                 "kv_cache_rotary_table", "kv_cache_append_at", "kv_cache_read")
 
-# kvc_append and kvc_attend as the C header lays them out (no padding between their fields)
+# kvc_append, kvc_attend and kvc_read as the C header lays them out (no padding between their fields)
 _APPEND = struct.Struct("=iiQQQqiiQQqqqqQiiIiiiQQqqqq")
 _ATTEND = struct.Struct("=iiiifiQQqiiQQQqqqqqq")
+_READ = struct.Struct("=iiQQQqiiQQqqqq")
 
 
 class KvcDesc(ctypes.Structure):
@@ -55,6 +57,7 @@ def _library() -> ctypes.CDLL:
         for name, args in (("kv_cache_create", [p, p]),
                            ("kv_cache_workspace_bytes", [p, i32, p]),
                            ("kv_cache_append", [p, i32, p, p]),
+                           ("kv_cache_append_at", [p, i32, p, p, p]), ("kv_cache_read", [p, i32, p, p]),
                            ("kv_cache_attend", [p, i32, p, p]), ("kv_cache_status", [p, p]),
                            ("kv_cache_rotary_table", [p, i32, i32, ctypes.c_double, p])):
             fn = getattr(lib, name)
@@ -88,9 +91,11 @@ def rotary_table(rows, rotary_dim, base=10000.0, scaling=None):
     return out
 
 
-def _desc(pool, layout, scales, per_head, geometry):
+def _desc(pool, layout, scales, per_head, geometry, block_scales=None):
     """The C descriptor and the host objects that it points to."""
     d = KvcDesc()
+    if layout is not None and block_scales is not None:
+        layout = dict(layout, bases=list(layout["bases"]) + list(block_scales))
     lay = None if layout is None else _Layout(**layout)
     sc = None if scales is None else np.ascontiguousarray(scales, dtype=np.float32)
     for name in ("num_layers", "num_components", "kv_heads", "head_dim", "dtype", "num_blocks",
@@ -103,9 +108,10 @@ def _desc(pool, layout, scales, per_head, geometry):
     return d, (lay, sc)
 
 
-def workspace_bytes(sm_count, pool=1 << 40, layout=None, scales=None, per_head=False, **geometry):
+def workspace_bytes(sm_count, pool=1 << 40, layout=None, scales=None, per_head=False, block_scales=None,
+                    **geometry):
     """Validate a cache's geometry on the host; the device bytes of its workspace."""
-    d, keep = _desc(pool, layout, scales, per_head, _defaults(geometry))
+    d, keep = _desc(pool, layout, scales, per_head, _defaults(geometry), block_scales)
     out = ctypes.c_int64()
     st = _library().kv_cache_workspace_bytes(ctypes.byref(d), int(sm_count), ctypes.byref(out))
     if st != 0:
@@ -124,7 +130,10 @@ class KVCache:
     [kv_heads][head_dim] -- the decode pool that a :class:`RelayoutPlan` wrote -- with ``kv_heads``
     the shard's heads; or ``layout=layout_of_views([views])`` for any strided one. ``dtype``:
     DTYPE_BF16, DTYPE_F16 or DTYPE_FP8_E4M3, the last with ``scales`` [L][C] (``per_head``:
-    [L][C][H]) as the relayout's conversion takes them. Two components hold keys and values
+    [L][C][H]) as the relayout's conversion takes them; or DTYPE_FP4_E2M1, whose pool is one byte tensor (the
+    codes of all planes, then their block scales: 9/16 byte an element, head_dim a multiple of 64, ``scales`` 1 by
+    default) or ``layout`` of the codes' views [block][token][head][head_dim / 2] with ``block_scales``, a list of
+    L * C views [block][token][head][head_dim / 16] in the order of the codes' and an eighth of their strides. Two components hold keys and values
     (head_dim a multiple of 16, at most 256), one a latent (head_dim 576, of which the first
     512 are the values). ``query_heads`` (0: append only), ``max_requests`` and ``max_new`` size
     the workspace of the attention calls (:func:`workspace_bytes`: 40 MB for latents, 5 to 10 MB for
@@ -140,16 +149,19 @@ class KVCache:
 
     def __init__(self, pool, *, num_layers, num_components, kv_heads, head_dim, block,
                  num_blocks, dtype, scales=None, per_head=False, layout=None, query_heads=0,
-                 max_requests=1, max_new=1, value_dim=0):
+                 max_requests=1, max_new=1, value_dim=0, block_scales=None):
         self._h = None
         g = dict(num_layers=num_layers, num_components=num_components, kv_heads=kv_heads,
                  head_dim=head_dim, block=block, num_blocks=num_blocks, dtype=dtype,
                  query_heads=query_heads, max_requests=max_requests, max_new=max_new,
                  value_dim=value_dim)
-        es = 1 if dtype == 2 else 2
+        four = dtype == DTYPE_FP4_E2M1
+        es = 1 if dtype == 2 or four else 2
+        if (block_scales is not None) != (four and layout is not None):
+            raise ValueError("block scales of their own go with a layout of a 4-bit pool, and it needs them")
         if layout is not None:
             shape, elem = layout.get("shape"), layout.get("elem_bytes")
-            need = (num_blocks, block, kv_heads, head_dim)
+            need = (num_blocks, block, kv_heads, head_dim // 2 if four else head_dim)
             if elem is not None and elem != es:
                 raise ValueError(f"views hold {elem}-byte elements; the cache holds {es}-byte ones")
             if shape is not None and any(h < n for h, n in zip(shape, need)):
@@ -158,10 +170,14 @@ class KVCache:
             if len(layout["bases"]) != num_layers * num_components:
                 raise ValueError(f"{len(layout['bases'])} views; the geometry has "
                                  f"{num_layers} layers of {num_components} components")
+            if four:
+                self._check_block_scales(block_scales, layout, num_layers * num_components, need)
         elif pool is not None:
             if not _contiguous(pool):
                 raise ValueError("pool is not contiguous: describe it with a layout")
             need = num_layers * num_components * num_blocks * block * kv_heads * head_dim * es
+            if four:
+                need = need * 9 // 16
             have = _nbytes(pool)
             if have is not None and have < need:
                 raise ValueError(f"pool holds {have} bytes; the geometry addresses {need}")
@@ -169,19 +185,21 @@ class KVCache:
             n = num_layers * num_components * (kv_heads if per_head else 1)
             if np.size(scales) != n:
                 raise ValueError(f"{np.size(scales)} scales; {n} expected")
-        d, _ = _desc(pool, layout, scales, per_head, g)
+        d, _ = _desc(pool, layout, scales, per_head, g, block_scales)
         h = ctypes.c_void_p()
         st = _library().kv_cache_create(ctypes.byref(d), ctypes.byref(h))
         if st != 0:
             raise KVRelayoutError(st, "kv_cache_create")
         import torch
         lib = _library()
-        self._h, self._pool, self._torch = h.value, (pool, layout), torch
+        self._h, self._pool, self._torch = h.value, (pool, layout, block_scales), torch
         self._append, self._attend = lib.kv_cache_append, lib.kv_cache_attend
+        self._append_at, self._read = lib.kv_cache_append_at, lib.kv_cache_read
         self._index = torch.cuda.current_device()
         self._device = torch.device("cuda", self._index)
         self._i32, self._f32 = torch.int32, torch.float32
         self._types = {torch.bfloat16: 1, torch.float16: DTYPE_F16}
+        self._default_dtype = torch.float16 if dtype == DTYPE_F16 else torch.bfloat16
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
         self.kv_heads, self.head_dim, self.query_heads = kv_heads, head_dim, query_heads
@@ -189,6 +207,23 @@ class KVCache:
         self.latent = num_components == 1
         self._default_scale = head_dim ** -0.5
         self._row_bytes = (2 * kv_heads * head_dim, 2 * head_dim)
+
+    @staticmethod
+    def _check_block_scales(views, layout, planes, need):
+        """Tensors among the views are looked at; addresses are taken as they are."""
+        if len(views) != planes:
+            raise ValueError(f"{len(views)} views of block scales; the geometry has {planes} planes")
+        for v in views:
+            if not hasattr(v, "stride"):
+                continue
+            es = v.element_size()
+            st = tuple(x * es for x in v.stride())
+            shape = need[:3] + (need[3] // 8,)
+            want = [layout[n] for n in ("block_stride", "token_stride", "head_stride")]
+            if v.dim() != 4 or es != 1 or any(h < n for h, n in zip(v.shape, shape)) or st[3] != 1 or \
+                    any(8 * s != w for s, w, n in zip(st, want, shape) if n > 1):
+                raise ValueError(f"block scales are {v.dtype} {list(v.shape)} with strides {list(st)}; expected "
+                                 f"bytes {list(shape)}, contiguous rows and an eighth of the codes' strides")
 
     # -- arguments ---------------------------------------------------------------
     #
@@ -255,12 +290,14 @@ class KVCache:
     # -- calls -------------------------------------------------------------------
 
     def append(self, layer, k, v, requests, positions, block_table, *, rotary=None,
-               interleaved=False, rotate_last=False, q=None, q_out=None, stream=None):
+               interleaved=False, rotate_last=False, q=None, q_out=None, stream=None, angles=None):
         """Append tokens to ``layer``: ``k`` and ``v`` [T][H][D] (``v`` None for latents), token t
         of request ``requests[t]`` (a row of ``block_table``) at ``positions[t]``, negative for
         padding. ``rotary``: the table of :func:`rotary_table` on the device, by which the first
         (``rotate_last``: the last) of each row's elements are rotated; ``q`` [T][heads][dim], where
-        given, is rotated into ``q_out`` (a new tensor by default). Returns ``q_out``."""
+        given, is rotated into ``q_out`` (a new tensor by default). ``angles`` int32 [T]: positions to
+        rotate by, where they are others than the places that ``positions`` name (after an eviction).
+        Returns ``q_out``."""
         if (v is None) != self.latent:
             raise ValueError("a latent cache has no values, others need them")
         if k.requires_grad or (v is not None and v.requires_grad) or (q is not None and q.requires_grad):
@@ -303,16 +340,45 @@ class KVCache:
         for t, name in ((requests, "requests"), (positions, "positions")):
             if not (t.dtype is i32 and t.shape == line and t.is_contiguous() and t.get_device() == index):
                 self._list(t, name, T)
-        st = self._append(
-            self._handle(), layer,
-            _APPEND.pack(T, code, requests.data_ptr(), positions.data_ptr(), ids, stride, rows, width,
-                         k.data_ptr(), vp, *ks, *vs, rot, rot_rows, rot_dim,
-                         (INTERLEAVED if interleaved else 0) | (ROTATE_LAST if rotate_last else 0),
-                         q_heads, q_dim, 0, qp, qo, *qs, *os),
-            self._raw_stream(index) if stream is None else _stream_handle(stream))
+        args = _APPEND.pack(T, code, requests.data_ptr(), positions.data_ptr(), ids, stride, rows, width,
+                            k.data_ptr(), vp, *ks, *vs, rot, rot_rows, rot_dim,
+                            (INTERLEAVED if interleaved else 0) | (ROTATE_LAST if rotate_last else 0),
+                            q_heads, q_dim, 0, qp, qo, *qs, *os)
+        on = self._raw_stream(index) if stream is None else _stream_handle(stream)
+        if angles is None:
+            st = self._append(self._handle(), layer, args, on)
+        else:
+            st = self._append_at(self._handle(), layer, args, self._list(angles, "angles", T), on)
         if st != 0:
             raise KVRelayoutError(st, "kv_cache_append")
         return q_out
+
+    def read(self, layer, requests, positions, block_table, *, k=None, v=None, dtype=None, stream=None):
+        """Tokens' rows out of ``layer``, the inverse of :meth:`append`: (k, v) [T][H][D] (v None for latents),
+        new tensors by default, of ``dtype`` (torch.bfloat16 by default, the pool's type if that has 16 bits).
+        Padding (a negative position) and tokens out of range give zeros."""
+        T = positions.shape[0] if positions.dim() == 1 else -1
+        shape = (T, self.kv_heads, self.head_dim)
+        if k is None:
+            k = self._new(shape, dtype or self._default_dtype, stream)
+        elif dtype is not None and k.dtype is not dtype:
+            raise ValueError(f"k is {k.dtype}; {dtype} asked for")
+        if v is not None and self.latent:
+            raise ValueError("a latent cache has no values")
+        if v is None and not self.latent:
+            v = self._new(shape, k.dtype, stream)
+        if k.requires_grad or (v is not None and v.requires_grad):
+            self._refuse_gradients()
+        ks = self._rows(k, "k", shape)
+        vp, vs = (0, (0, 0)) if v is None else (v.data_ptr(), self._rows(v, "v", shape, k.dtype))
+        st = self._read(
+            self._handle(), layer,
+            _READ.pack(T, self._types[k.dtype], self._list(requests, "requests", T),
+                       self._list(positions, "positions", T), *self._table(block_table), k.data_ptr(), vp, *ks, *vs),
+            self._raw_stream(self._index) if stream is None else _stream_handle(stream))
+        if st != 0:
+            raise KVRelayoutError(st, "kv_cache_read")
+        return k, v
 
     def attend(self, layer, q, lengths, block_table, *, out=None, lse=None, scale=None, window=0,
                stream=None):
