@@ -223,6 +223,21 @@ typedef struct kvc_attend {
 kvr_status kv_cache_attend(const kvc_cache *cache, int32_t layer, const kvc_attend *args,
                            void *stream);
 
+/*
+ * Scores of another form, over keys and values (KVR_ERR_UNSUPPORTED over latents): in the formulas above x_j is
+ *   x_j = cap tanh(scale q . k_j / cap) + slopes[g] (j - p),    without cap where that is 0,
+ * for a query of head g at position p. Scores are fp32.
+ */
+typedef struct kvc_scoring {
+    float cap;                 /* 0: none; otherwise 2^-100 to 2^100 */
+    int32_t reserved;          /* 0 */
+    const float *slopes;       /* device [Hq]; NULL: none */
+} kvc_scoring;
+
+/* kv_cache_attend with these scores (NULL, or no cap and no slopes: kv_cache_attend itself). */
+kvr_status kv_cache_attend_scored(const kvc_cache *cache, int32_t layer, const kvc_attend *args,
+                                  const kvc_scoring *scoring, void *stream);
+
 /* Waits for the cache's device (which need not be the current one), reads and clears the flags
  * of what the kernels found out of range:
  * KVR_OK with *flags = 0, or KVR_ERR_DEVICE_BOUNDS with the KVC_FLAG_* bits. */

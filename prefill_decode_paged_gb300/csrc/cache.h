@@ -122,6 +122,7 @@ bool kvc_make_map(CUtensorMap *map, int es, int rank, uint64_t base, int64_t row
 // cache.cpp: whether a call's arguments hold (KVR_OK), but for the current device.
 kvr_status kvc_check_append(const kvc_cache *c, int32_t layer, const kvc_append *a);
 kvr_status kvc_check_attend(const kvc_cache *c, int32_t layer, const kvc_attend *a);
+kvr_status kvc_check_scoring(const kvc_cache *c, const kvc_scoring &s);
 bool kvc_ok_table(const kvc_table &t);
 bool kvc_type_fits(const kvc_cache *c, int32_t dtype);
 bool kvc_on_device(const kvc_cache *c);
@@ -129,6 +130,8 @@ bool kvc_on_device(const kvc_cache *c);
 // cache_attend.cu, cache_latent.cu: the launches behind kv_cache_attend(), and what they want
 // of the workspace. (`setup` runs once a cache: shared memory limits of the kernels.)
 kvr_status kvc_attend_launch(const kvc_cache *c, int32_t layer, const kvc_attend *a, void *stream);
+kvr_status kvc_attend_scored_launch(const kvc_cache *c, int32_t layer, const kvc_attend *a,
+                                    const kvc_scoring *scoring, void *stream);
 size_t kvc_attend_partial_bytes(const kvc_desc &d, int32_t sm_count);
 size_t kvc_attend_jobs(const kvc_desc &d);
 kvr_status kvc_attend_setup(kvc_cache *c);

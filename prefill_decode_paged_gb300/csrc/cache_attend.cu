@@ -11,7 +11,13 @@ namespace {
 
 using namespace kvc;
 
-AttendPick pick(const kvc_desc &d, int32_t M) {
+// (tiles, rows and shared memory of an instance do not depend on `scored`)
+AttendPick pick(const kvc_desc &d, int32_t M, bool scored = false) {
+    if (scored)
+        return d.dtype == KVR_DTYPE_FP8_E4M3 ? attend_pick_scored_e4m3(d.head_dim, M)
+               : d.dtype == KVC_DTYPE_E2M1   ? attend_pick_scored_e2m1(d.head_dim, M)
+               : d.dtype == KVC_DTYPE_F16    ? attend_pick_scored_f16(d.head_dim, M)
+                                             : attend_pick_scored_bf16(d.head_dim, M);
     return d.dtype == KVR_DTYPE_FP8_E4M3 ? attend_pick_e4m3(d.head_dim, M)
            : d.dtype == KVC_DTYPE_E2M1   ? attend_pick_e2m1(d.head_dim, M)
            : d.dtype == KVC_DTYPE_F16    ? attend_pick_f16(d.head_dim, M)
@@ -39,18 +45,24 @@ size_t kvc_attend_jobs(const kvc_desc &d) {
 
 kvr_status kvc_attend_setup(kvc_cache *c) {
     if (c->latent()) return kvc_latent_setup(c);
-    for (int32_t M : {8, 16, 32}) {
-        const AttendPick p = pick(c->d, M);
-        if (cudaFuncSetAttribute(p.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)p.smem(KVC_MAX_REQUESTS)) != cudaSuccess) {
-            cudaGetLastError();
-            return KVR_ERR_CUDA;
+    for (int32_t M : {8, 16, 32})
+        for (bool scored : {false, true}) {
+            const AttendPick p = pick(c->d, M, scored);
+            if (cudaFuncSetAttribute(p.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)p.smem(KVC_MAX_REQUESTS)) != cudaSuccess) {
+                cudaGetLastError();
+                return KVR_ERR_CUDA;
+            }
         }
-    }
     return KVR_OK;
 }
 
 kvr_status kvc_attend_launch(const kvc_cache *c, int32_t layer, const kvc_attend *p, void *stream) {
+    return kvc_attend_scored_launch(c, layer, p, nullptr, stream);
+}
+
+kvr_status kvc_attend_scored_launch(const kvc_cache *c, int32_t layer, const kvc_attend *p,
+                                    const kvc_scoring *scoring, void *stream) {
     if (c->latent()) return kvc_latent_launch(c, layer, p, stream);
     AttendArgs a = {};
     a.k_plane = c->plane(layer, 0);
@@ -70,9 +82,10 @@ kvr_status kvc_attend_launch(const kvc_cache *c, int32_t layer, const kvc_attend
     a.arrived = c->ws.arrived;
     a.m = p->num_new, a.H = c->d.kv_heads, a.G = c->d.query_heads / a.H, a.D = c->d.head_dim;
     a.f16 = p->dtype == KVC_DTYPE_F16, a.scale = p->scale;
+    a.scoring = make_scoring(scoring);
     a.group = kvr_make_div((uint32_t)a.G);
     const int32_t M = a.m * a.G;
-    const AttendPick k = pick(c->d, M);
+    const AttendPick k = pick(c->d, M, a.scoring.cap > 0.0f || a.scoring.slopes != nullptr);
     a.chunks = (int32_t)ceil_div(M, k.rp);
     // most units of a job; the kernel counts those of all jobs in 32 bits
     const int64_t most = ceil_div((int64_t)p->table.width * c->d.block_size, k.unit) + 1;

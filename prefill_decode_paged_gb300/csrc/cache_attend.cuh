@@ -44,6 +44,7 @@
 #include <math.h>
 
 #include "cache.h"
+#include "cache_scores.cuh"
 #include "cache_split.cuh"
 
 namespace kvc {
@@ -64,6 +65,7 @@ struct AttendArgs {
     KvrDiv group, by_chunks;  // by G, chunks
     CutShape shape;
     float scale;
+    Scoring scoring;
 };
 
 constexpr int ATTEND_WARPS = 4;
@@ -106,11 +108,6 @@ struct Attend {
     static constexpr size_t smem(int32_t requests) { return FIXED + 4 * (size_t)(requests + 1); }
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(bytes)
@@ -308,7 +305,7 @@ __device__ __forceinline__ uint2 narrow4(float4 v) {
     return make_uint2(narrow2<F16>(v.x, v.y), narrow2<F16>(v.z, v.w));
 }
 
-template <int DP, int POOL, int NT>
+template <int DP, int POOL, int NT, bool SCORED>
 __global__ void __launch_bounds__(ATTEND_THREADS, (Attend<DP, POOL, NT>::BLOCKS))
 attend_kernel(AttendArgs a) {
     using C = Attend<DP, POOL, NT>;
@@ -482,7 +479,7 @@ attend_kernel(AttendArgs a) {
         }
         __syncthreads();
 
-        float sc[NT][2], top[NT][2], sum[NT][2];
+        float sc[NT][2], top[NT][2], sum[NT][2], slope[NT][2];
         int32_t end[NT][2];                             // first key that the row does not see
         int32_t seen_all = sp.n;                        // keys below it are seen by every row
 #pragma unroll
@@ -495,6 +492,8 @@ attend_kernel(AttendArgs a) {
                 sum[n][e] = 0.0f;
                 const int32_t i = (int32_t)a.group.div((uint32_t)(row0 + min(row, rows - 1)));
                 end[n][e] = sp.n - a.m + i + 1;
+                if constexpr (SCORED)
+                    slope[n][e] = slope_of(a.scoring, h * a.G + row0 + min(row, rows - 1) - i * a.G);
             }
         seen_all = sp.n - a.m + 1;
         const int32_t seen_from = a.split.window > 0 ? sp.n - a.split.window : 0;   // keys from it on, by all
@@ -586,8 +585,9 @@ attend_kernel(AttendArgs a) {
                         for (int u = 0; u < 2; ++u) {
                             float &v = s[k][n][2 * u + e];
                             v *= sc[n][e];
+                            const int32_t j = j0 + k * 16 + u * 8 + g;
+                            if constexpr (SCORED) v = scored(v, a.scoring, slope[n][e], j - end[n][e] + 1);
                             if (mixed) {
-                                const int32_t j = j0 + k * 16 + u * 8 + g;
                                 if (j >= end[n][e] ||
                                     (a.split.window > 0 && j < window_from(end[n][e], a.split.window)))
                                     v = -INFINITY;
@@ -878,29 +878,33 @@ struct AttendPick {
     int32_t unit, rp, blocks;
 };
 
-template <int DP, int POOL, int NT>
+template <int DP, int POOL, int NT, bool SCORED>
 inline AttendPick attend_instance() {
     using C = Attend<DP, POOL, NT>;
-    return {attend_kernel<DP, POOL, NT>, &C::smem, C::UNIT, C::RP, C::BLOCKS};
+    return {attend_kernel<DP, POOL, NT, SCORED>, &C::smem, C::UNIT, C::RP, C::BLOCKS};
 }
 
 // The instance for head dimension D and M rows a job: rows in passes of 8, 16 or 32 (at most 16
 // for D > 128, where 32 rows' accumulators would not fit the registers).
-template <int POOL>
+template <int POOL, bool SCORED>
 inline AttendPick attend_pick(int32_t D, int32_t M) {
     const int nt = M <= 8 ? 1 : M <= 16 || D > 128 ? 2 : 4;
     if (D <= 64)
-        return nt == 1 ? attend_instance<64, POOL, 1>()
-               : nt == 2 ? attend_instance<64, POOL, 2>() : attend_instance<64, POOL, 4>();
+        return nt == 1 ? attend_instance<64, POOL, 1, SCORED>()
+               : nt == 2 ? attend_instance<64, POOL, 2, SCORED>() : attend_instance<64, POOL, 4, SCORED>();
     if (D <= 128)
-        return nt == 1 ? attend_instance<128, POOL, 1>()
-               : nt == 2 ? attend_instance<128, POOL, 2>() : attend_instance<128, POOL, 4>();
-    return nt == 1 ? attend_instance<256, POOL, 1>() : attend_instance<256, POOL, 2>();
+        return nt == 1 ? attend_instance<128, POOL, 1, SCORED>()
+               : nt == 2 ? attend_instance<128, POOL, 2, SCORED>() : attend_instance<128, POOL, 4, SCORED>();
+    return nt == 1 ? attend_instance<256, POOL, 1, SCORED>() : attend_instance<256, POOL, 2, SCORED>();
 }
 
 AttendPick attend_pick_bf16(int32_t D, int32_t M);   // one translation unit each
 AttendPick attend_pick_f16(int32_t D, int32_t M);
 AttendPick attend_pick_e4m3(int32_t D, int32_t M);
 AttendPick attend_pick_e2m1(int32_t D, int32_t M);
+AttendPick attend_pick_scored_bf16(int32_t D, int32_t M);
+AttendPick attend_pick_scored_f16(int32_t D, int32_t M);
+AttendPick attend_pick_scored_e4m3(int32_t D, int32_t M);
+AttendPick attend_pick_scored_e2m1(int32_t D, int32_t M);
 
 }  // namespace kvc

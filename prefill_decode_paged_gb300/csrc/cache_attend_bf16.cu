@@ -2,5 +2,5 @@
 #include "cache_attend.cuh"
 
 kvc::AttendPick kvc::attend_pick_bf16(int32_t D, int32_t M) {
-    return attend_pick<KVR_DTYPE_BF16>(D, M);
+    return attend_pick<KVR_DTYPE_BF16, false>(D, M);
 }

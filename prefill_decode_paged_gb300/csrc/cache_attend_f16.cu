@@ -2,5 +2,5 @@
 #include "cache_attend.cuh"
 
 kvc::AttendPick kvc::attend_pick_f16(int32_t D, int32_t M) {
-    return attend_pick<KVC_DTYPE_F16>(D, M);
+    return attend_pick<KVC_DTYPE_F16, false>(D, M);
 }

@@ -31,6 +31,26 @@ extern "C" kvr_status kv_cache_append_at(const kvc_cache *c, int32_t layer, cons
     return kvc_append_at_launch(c, layer, a, angles, stream);
 }
 
+kvr_status kvc_check_scoring(const kvc_cache *c, const kvc_scoring &s) {
+    if (!(s.cap >= 0.0f) || !std::isfinite(s.cap) || s.reserved != 0) return KVR_ERR_INVALID_ARG;
+    // (so that it and its reciprocal are numbers of fp32, times log2 e as well)
+    if (s.cap > 0.0f && (s.cap < 0x1p-100f || s.cap > 0x1p100f)) return KVR_ERR_UNSUPPORTED;
+    if (address(s.slopes) % 4 != 0) return KVR_ERR_ALIGNMENT;
+    return c->latent() && (s.cap > 0.0f || s.slopes != nullptr) ? KVR_ERR_UNSUPPORTED : KVR_OK;
+}
+
+extern "C" kvr_status kv_cache_attend_scored(const kvc_cache *c, int32_t layer, const kvc_attend *a,
+                                             const kvc_scoring *scoring, void *stream) {
+    if (scoring == nullptr) return kv_cache_attend(c, layer, a, stream);
+    kvr_status st = kvc_check_attend(c, layer, a);
+    if (st == KVR_OK) st = kvc_check_scoring(c, *scoring);
+    if (st != KVR_OK) return st;
+    if (scoring->cap == 0.0f && scoring->slopes == nullptr) return kv_cache_attend(c, layer, a, stream);
+    if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
+    if (a->num_requests == 0) return KVR_OK;
+    return kvc_attend_scored_launch(c, layer, a, scoring, stream);
+}
+
 extern "C" kvr_status kv_cache_read(const kvc_cache *c, int32_t layer, const kvc_read *a, void *stream) {
     if (c == nullptr || a == nullptr) return KVR_ERR_INVALID_ARG;
     if (layer < 0 || layer >= c->d.num_layers) return KVR_ERR_LAYER_RANGE;

@@ -22,12 +22,14 @@ FLAGS = {1: "request index", 2: "position", 4: "length", 8: "block id", 16: "wai
 SCALINGS = {"linear": 1, "base": 2, "ramp": 3, "bands": 4}
 CACHE_EXPORTS = ("kv_cache_create", "kv_cache_destroy", "kv_cache_workspace_bytes",
                  "kv_cache_append", "kv_cache_attend", "kv_cache_status",
-                 "kv_cache_rotary_table", "kv_cache_append_at", "kv_cache_read")
+                 "kv_cache_rotary_table", "kv_cache_append_at", "kv_cache_read",
+                 "kv_cache_attend_scored")
 
-# kvc_append, kvc_attend and kvc_read as the C header lays them out (no padding between their fields)
+# kvc_append, kvc_attend, kvc_read and kvc_scoring as the C header lays them out (no padding between their fields)
 _APPEND = struct.Struct("=iiQQQqiiQQqqqqQiiIiiiQQqqqq")
 _ATTEND = struct.Struct("=iiiifiQQqiiQQQqqqqqq")
 _READ = struct.Struct("=iiQQQqiiQQqqqq")
+_SCORING = struct.Struct("=fiQ")
 
 
 class KvcDesc(ctypes.Structure):
@@ -57,6 +59,7 @@ def _library() -> ctypes.CDLL:
         for name, args in (("kv_cache_create", [p, p]),
                            ("kv_cache_workspace_bytes", [p, i32, p]),
                            ("kv_cache_append", [p, i32, p, p]),
+                           ("kv_cache_attend_scored", [p, i32, p, p, p]),
                            ("kv_cache_append_at", [p, i32, p, p, p]), ("kv_cache_read", [p, i32, p, p]),
                            ("kv_cache_attend", [p, i32, p, p]), ("kv_cache_status", [p, p]),
                            ("kv_cache_rotary_table", [p, i32, i32, ctypes.c_double, p])):
@@ -194,6 +197,7 @@ class KVCache:
         lib = _library()
         self._h, self._pool, self._torch = h.value, (pool, layout, block_scales), torch
         self._append, self._attend = lib.kv_cache_append, lib.kv_cache_attend
+        self._attend_scored = lib.kv_cache_attend_scored
         self._append_at, self._read = lib.kv_cache_append_at, lib.kv_cache_read
         self._index = torch.cuda.current_device()
         self._device = torch.device("cuda", self._index)
@@ -286,6 +290,17 @@ class KVCache:
                 return t.data_ptr(), stride, rows, width     # (rows may overlap: they are only read)
         raise ValueError(f"block table is {t.dtype} {list(t.shape)} on {t.device}; expected "
                          f"int32 [rows][width] on {self._device}, rows contiguous")
+
+    def _scoring(self, cap, slopes):
+        if slopes is None:
+            return _SCORING.pack(cap, 0, 0)
+        if slopes.requires_grad:
+            self._refuse_gradients()
+        if slopes.dtype is self._f32 and slopes.shape == (self.query_heads,) and slopes.is_contiguous() and \
+                slopes.get_device() == self._index:
+            return _SCORING.pack(cap, 0, slopes.data_ptr())
+        raise ValueError(f"slopes are {slopes.dtype} {list(slopes.shape)} on {slopes.device}; expected contiguous "
+                         f"float32 [{self.query_heads}] on {self._device}")
 
     # -- calls -------------------------------------------------------------------
 
@@ -381,11 +396,12 @@ class KVCache:
         return k, v
 
     def attend(self, layer, q, lengths, block_table, *, out=None, lse=None, scale=None, window=0,
-               stream=None):
+               stream=None, cap=0.0, slopes=None):
         """Attention of each request's newest tokens over ``layer``: ``q`` [R][new][Hq][D], or
         [R][Hq][D] for one; ``lengths`` int32 [R] counts the cached tokens, the newest included.
         ``scale``: D ** -0.5 by default; ``window`` > 0: only that many keys, the token's own
-        included. Returns (out, lse): ``out`` like q with ``value_dim`` elements, ``lse`` float32
+        included. ``cap`` > 0: scores become cap tanh(score / cap); ``slopes`` float32 [Hq]: the score of a key
+        d tokens before the query is lowered by slopes[head] d. Returns (out, lse): ``out`` like q with ``value_dim`` elements, ``lse`` float32
         [R][new][Hq], new tensors by default (``lse=False``: none)."""
         if q.requires_grad:
             self._refuse_gradients()
@@ -428,12 +444,14 @@ class KVCache:
         if not (lengths.dtype is self._i32 and lengths.shape == (R,) and lengths.is_contiguous() and
                 lengths.get_device() == index):
             self._list(lengths, "lengths", R)
-        st = self._attend(
-            self._handle(), layer,
-            _ATTEND.pack(R, m, code, window, self._default_scale if scale is None else scale, 0,
-                         lengths.data_ptr(), *self._table(block_table),
-                         q.data_ptr(), out.data_ptr(), lp, *qs, *os),
-            self._raw_stream(index) if stream is None else _stream_handle(stream))
+        args = _ATTEND.pack(R, m, code, window, self._default_scale if scale is None else scale, 0,
+                            lengths.data_ptr(), *self._table(block_table),
+                            q.data_ptr(), out.data_ptr(), lp, *qs, *os)
+        on = self._raw_stream(index) if stream is None else _stream_handle(stream)
+        if slopes is None and cap == 0.0:
+            st = self._attend(self._handle(), layer, args, on)
+        else:
+            st = self._attend_scored(self._handle(), layer, args, self._scoring(cap, slopes), on)
         if st != 0:
             raise KVRelayoutError(st, "kv_cache_attend")
         return out, lse

@@ -91,6 +91,8 @@ def test_null_handles():
     lib = kc._library()
     buf = bytes(256)
     assert kr.STATUS[lib.kv_cache_append_at(None, 0, buf, None, None)] == "KVR_ERR_INVALID_ARG"
+    assert kr.STATUS[lib.kv_cache_attend_scored(None, 0, buf, buf, None)] == "KVR_ERR_INVALID_ARG"
+    assert kr.STATUS[lib.kv_cache_attend_scored(None, 0, buf, None, None)] == "KVR_ERR_INVALID_ARG"
     assert kr.STATUS[lib.kv_cache_read(None, 0, buf, None)] == "KVR_ERR_INVALID_ARG"
 
 
@@ -118,6 +120,11 @@ def test_read_is_laid_out_as_the_binding_packs_it(tmp_path):
                               "offsetof(kvc_read, v_head_stride)", "KVC_DTYPE_E2M1"])
     assert got == [kc._READ.size, _marked(kc._READ, 4), _marked(kc._READ, 8), _marked(kc._READ, 13),
                    kc.DTYPE_FP4_E2M1]
+
+
+def test_scoring_is_laid_out_as_the_binding_packs_it(tmp_path):
+    got = _offsets(tmp_path, ["sizeof(kvc_scoring)", "offsetof(kvc_scoring, slopes)"])
+    assert got == [kc._SCORING.size, _marked(kc._SCORING, 2)]
 
 
 def test_the_references_own_four_bits():
