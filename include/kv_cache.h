@@ -238,6 +238,38 @@ typedef struct kvc_scoring {
 kvr_status kv_cache_attend_scored(const kvc_cache *cache, int32_t layer, const kvc_attend *args,
                                   const kvc_scoring *scoring, void *stream);
 
+/*
+ * How much attention the cached keys got from the newest `num_new` tokens of each request:
+ *   w[r][h][j] = sum over these tokens and the query heads g of key head h of exp(x_j - lse),
+ * x_j as in the attention (0 where the query does not see key j; an lse of -infinity gives 0), lse as it gave it.
+ * add 1: to what is there; 0: in its place. Entries j < lengths[r] are written (a window's lower end leaves 0, or
+ * what was there); those beyond stay as they are. Keys at or beyond weights_width are flagged (KVC_FLAG_LENGTH) and
+ * have no weight. Scores, exponentials and sums are fp32; results do not depend on the run. Uses no workspace:
+ * calls on different streams need no order. Over keys and values (KVR_ERR_UNSUPPORTED over latents).
+ * Requirements: as for kv_cache_attend; lse [R][num_new][Hq], contiguous; rows of weights contiguous,
+ * not overlapping one another.
+ */
+typedef struct kvc_weigh {
+    int32_t num_requests;      /* 0..max_requests */
+    int32_t num_new;           /* 1..max_new */
+    int32_t dtype;             /* of q */
+    int32_t window;            /* 0: none */
+    float scale;               /* finite */
+    int32_t add;               /* 0, 1 */
+    const int32_t *lengths;    /* device [num_requests] */
+    kvc_table table;           /* rows >= num_requests */
+    const void *q;             /* device [num_requests][num_new][Hq][D] */
+    const float *lse;          /* device [num_requests][num_new][Hq] */
+    float *weights;            /* device [num_requests][H][weights_width] */
+    int64_t q_request_stride, q_token_stride, q_head_stride;          /* bytes */
+    int64_t weights_request_stride, weights_head_stride;              /* entries */
+    int32_t weights_width;
+    int32_t reserved;          /* 0 */
+    kvc_scoring scoring;       /* zeros: none */
+} kvc_weigh;
+
+kvr_status kv_cache_weigh(const kvc_cache *cache, int32_t layer, const kvc_weigh *args, void *stream);
+
 /* Waits for the cache's device (which need not be the current one), reads and clears the flags
  * of what the kernels found out of range:
  * KVR_OK with *flags = 0, or KVR_ERR_DEVICE_BOUNDS with the KVC_FLAG_* bits. */

@@ -54,7 +54,7 @@ kvr_status kvc_attend_setup(kvc_cache *c) {
                 return KVR_ERR_CUDA;
             }
         }
-    return KVR_OK;
+    return kvc_weigh_setup(c);
 }
 
 kvr_status kvc_attend_launch(const kvc_cache *c, int32_t layer, const kvc_attend *p, void *stream) {

@@ -288,6 +288,97 @@ __device__ __forceinline__ void values_e2m1(float (&o)[DP / 16][NT][4], const ui
     }
 }
 
+// A query's 8 elements of this lane in the type of the products into row `row` of the queries' memory (a
+// warp's lanes hold one query). Codes are multiplied by f16: the row is scaled to that by a power of two,
+// which goes into *factor.
+template <int DP, int POOL>
+__device__ __forceinline__ void place_query(unsigned char *q_smem, int row, uint4 w, int32_t type_f16, float *factor) {
+    const int lane = threadIdx.x % 32;
+    if constexpr (POOL != KVR_DTYPE_FP8_E4M3 && POOL != KVC_DTYPE_E2M1) {
+        if (lane * 8 < DP) *(uint4 *)(q_smem + swizzled<DP * 2>(row, lane)) = w;
+    } else {
+        float f[8], top = 0.0f;
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 p = type_f16 ? widen2<true>(ws[k]) : widen2<false>(ws[k]);
+            f[2 * k] = p.x, f[2 * k + 1] = p.y;
+            top = fmaxf(top, fmaxf(fabsf(p.x), fabsf(p.y)));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        // down = 2^-e with 2^e <= top < 2^(e+1): exponents kept where both are normal
+        uint32_t e = __float_as_uint(top) >> 23;
+        e = e < 2 || e > 252 ? 127 : e;
+        const float down = __uint_as_float((254 - e) << 23);
+        *factor *= __uint_as_float(e << 23);
+        // 8 bits: element d = 4 t + x of 16 is at 2 t + x (x < 2) or 8 + 2 t + x - 2: where the
+        // codes of four neighbours land when two 8-bit elements load as one 16-bit one.
+        // 4 bits: pair y of elements 8 t + 2 y, 8 t + 2 y + 1 of 32 is at 8 y + 2 t: a lane's 8
+        // codes of a row are two pairs each for two steps of 16 elements
+        if (POOL == KVC_DTYPE_E2M1) {
+            if (lane * 8 < DP)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    *(uint32_t *)(q_smem + swizzled<DP * 2>(row, (lane / 4) * 4 + k) + (lane % 4) * 4) =
+                        narrow2<true>(f[2 * k] * down, f[2 * k + 1] * down);
+        } else if (lane * 8 < DP) {
+            const int grp = lane / 2, half = lane % 2;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int pos = (k & 1 ? 8 : 0) + 4 * half + (k & 2);
+                *(uint32_t *)(q_smem + swizzled<DP * 2>(row, grp * 2 + pos / 8) + (pos % 8) * 2) =
+                    narrow2<true>(f[2 * k] * down, f[2 * k + 1] * down);
+            }
+        }
+    }
+}
+
+// S^T of a tile: its KT keys by rows (block scales of 4-bit ones at `scales`), the queries by columns.
+template <int DP, int POOL, int KT, int NT>
+__device__ __forceinline__ void tile_scores(float (&s)[KT / 16][NT][4], uint32_t kbase, uint32_t q_base,
+                                            const unsigned char *scales) {
+    constexpr bool E4 = POOL == KVR_DTYPE_FP8_E4M3, F16 = POOL != KVR_DTYPE_BF16;
+    constexpr int ROW = E4 ? DP : DP * 2;
+    const int lane = threadIdx.x % 32;
+    if constexpr (POOL == KVC_DTYPE_E2M1) {
+        scores_e2m1<DP, KT, NT>(s, kbase, q_base, scales);
+    } else {
+#pragma unroll
+        for (int d2 = 0; d2 < DP / 32; ++d2) {              // two steps of 16 elements
+            uint32_t b[NT][4];                              // [row tile][step][half]
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                ldmatrix4(b[n], q_base + swizzled<DP * 2>(n * 8 + lane % 8, d2 * 4 + lane / 8));
+#pragma unroll
+            for (int k = 0; k < KT / 16; ++k) {
+                if (!E4) {
+#pragma unroll
+                    for (int st = 0; st < 2; ++st) {
+                        uint32_t f[4];
+                        ldmatrix4(f, kbase + swizzled<ROW>(k * 16 + lane % 16, (d2 * 2 + st) * 2 + lane / 16));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma<F16>(s[k][n], f, b[n][2 * st], b[n][2 * st + 1]);
+                    }
+                } else {
+                    uint32_t w[4];                          // keys 0-7, 8-15 of the 1st, 2nd 16 elements
+                    ldmatrix4(w, kbase + swizzled<ROW>(k * 16 + lane % 16, d2 * 2 + lane / 16));
+#pragma unroll
+                    for (int st = 0; st < 2; ++st) {
+                        uint32_t f[4];
+                        f[0] = e4m3_to_f16x2(w[2 * st]);
+                        f[1] = e4m3_to_f16x2(w[2 * st + 1]);
+                        f[2] = e4m3_to_f16x2(w[2 * st] >> 16);
+                        f[3] = e4m3_to_f16x2(w[2 * st + 1] >> 16);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma<F16>(s[k][n], f, b[n][2 * st], b[n][2 * st + 1]);
+                    }
+                }
+            }
+        }
+    }
+}
+
 // Two weights (>= 0) as the 16-bit numbers next below them: the rests are positive wherever the
 // weights are, so an infinite value times both parts is one infinity, not two that cancel.
 template <bool F16>
@@ -434,47 +525,8 @@ attend_kernel(AttendArgs a) {
 #pragma unroll
         for (int n = 0; n < QW; ++n) {
             const int row = n * ATTEND_WARPS + warp;
-            const uint4 w = qw[n];
             float factor = a.scale * log2e * ks;
-            if (!C::CODES) {
-                if (lane * 8 < DP)
-                    *(uint4 *)(q_smem + swizzled<DP * 2>(row, lane)) = w;
-            } else {
-                float f[8], top = 0.0f;
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 p = a.f16 ? widen2<true>(ws[k]) : widen2<false>(ws[k]);
-                    f[2 * k] = p.x, f[2 * k + 1] = p.y;
-                    top = fmaxf(top, fmaxf(fabsf(p.x), fabsf(p.y)));
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-                // down = 2^-e with 2^e <= top < 2^(e+1): exponents kept where both are normal
-                uint32_t e = __float_as_uint(top) >> 23;
-                e = e < 2 || e > 252 ? 127 : e;
-                const float down = __uint_as_float((254 - e) << 23);
-                factor *= __uint_as_float(e << 23);
-                // 8 bits: element d = 4 t + x of 16 is at 2 t + x (x < 2) or 8 + 2 t + x - 2: where the
-                // codes of four neighbours land when two 8-bit elements load as one 16-bit one.
-                // 4 bits: pair y of elements 8 t + 2 y, 8 t + 2 y + 1 of 32 is at 8 y + 2 t: a lane's 8
-                // codes of a row are two pairs each for two steps of 16 elements
-                if (C::E2) {
-                    if (lane * 8 < DP)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *(uint32_t *)(q_smem + swizzled<DP * 2>(row, (lane / 4) * 4 + k) + (lane % 4) * 4) =
-                                narrow2<true>(f[2 * k] * down, f[2 * k + 1] * down);
-                } else if (lane * 8 < DP) {
-                    const int grp = lane / 2, half = lane % 2;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int pos = (k & 1 ? 8 : 0) + 4 * half + (k & 2);
-                        *(uint32_t *)(q_smem + swizzled<DP * 2>(row, grp * 2 + pos / 8) +
-                                      (pos % 8) * 2) = narrow2<true>(f[2 * k] * down, f[2 * k + 1] * down);
-                    }
-                }
-            }
+            place_query<DP, POOL>(q_smem, row, qw[n], a.f16, &factor);
             if (lane == 0) row_scale[row] = factor;
         }
         __syncthreads();
@@ -528,44 +580,7 @@ attend_kernel(AttendArgs a) {
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[k][n][e] = 0.0f;
-            const uint32_t q_base = smem0 + C::RING;
-            if constexpr (C::E2)
-                scores_e2m1<DP, KT, NT>(s, kbase, q_base, smem + (vbase - smem0) + KT * ROW);
-#pragma unroll
-            for (int d2 = 0; d2 < (C::E2 ? 0 : DP / 32); ++d2) {      // two steps of 16 elements
-                uint32_t b[NT][4];                      // [row tile][step][half]
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    ldmatrix4(b[n], q_base + swizzled<DP * 2>(n * 8 + lane % 8, d2 * 4 + lane / 8));
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    if (!C::CODES) {
-#pragma unroll
-                        for (int st = 0; st < 2; ++st) {
-                            uint32_t f[4];
-                            ldmatrix4(f, kbase + swizzled<ROW>(k * 16 + lane % 16,
-                                                               (d2 * 2 + st) * 2 + lane / 16));
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma<C::F16>(s[k][n], f, b[n][2 * st], b[n][2 * st + 1]);
-                        }
-                    } else {
-                        uint32_t w[4];                  // keys 0-7, 8-15 of the 1st, 2nd 16 elements
-                        ldmatrix4(w, kbase + swizzled<ROW>(k * 16 + lane % 16, d2 * 2 + lane / 16));
-#pragma unroll
-                        for (int st = 0; st < 2; ++st) {
-                            uint32_t f[4];
-                            f[0] = e4m3_to_f16x2(w[2 * st]);
-                            f[1] = e4m3_to_f16x2(w[2 * st + 1]);
-                            f[2] = e4m3_to_f16x2(w[2 * st] >> 16);
-                            f[3] = e4m3_to_f16x2(w[2 * st + 1] >> 16);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma<C::F16>(s[k][n], f, b[n][2 * st], b[n][2 * st + 1]);
-                        }
-                    }
-                }
-            }
+            tile_scores<DP, POOL, KT, NT>(s, kbase, smem0 + C::RING, smem + (vbase - smem0) + KT * ROW);
 
             // softmax over the tile's keys, relative to the maximum of those before; a new maximum is
             // looked for only where it is outgrown (each tile anew, softmax took 420 cycles of a tile of

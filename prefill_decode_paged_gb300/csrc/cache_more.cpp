@@ -2,6 +2,7 @@
 #include <math.h>
 
 #include <initializer_list>
+#include <utility>
 
 #include "cache.h"
 
@@ -16,6 +17,17 @@ bool negative(std::initializer_list<int64_t> xs) {
     for (int64_t x : xs)
         if (x < 0) return true;
     return false;
+}
+// Rows of `row` entries, `outer` by `inner` of them, do not overlap.
+bool disjoint_rows(int64_t outer, int64_t outer_stride, int64_t inner, int64_t inner_stride, int64_t row) {
+    if (outer <= 1) outer_stride = INT64_MAX;
+    if (inner <= 1) inner_stride = INT64_MAX;
+    if (outer_stride < inner_stride) {
+        std::swap(outer, inner);
+        std::swap(outer_stride, inner_stride);
+    }
+    if (inner > 1 && inner_stride < row) return false;
+    return outer <= 1 || (__int128)outer_stride >= (inner > 1 ? (__int128)(inner - 1) * inner_stride : 0) + row;
 }
 int64_t address(const void *p) { return (int64_t)(uintptr_t)p; }
 
@@ -49,6 +61,39 @@ extern "C" kvr_status kv_cache_attend_scored(const kvc_cache *c, int32_t layer, 
     if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
     if (a->num_requests == 0) return KVR_OK;
     return kvc_attend_scored_launch(c, layer, a, scoring, stream);
+}
+
+extern "C" kvr_status kv_cache_weigh(const kvc_cache *c, int32_t layer, const kvc_weigh *a, void *stream) {
+    if (c == nullptr || a == nullptr) return KVR_ERR_INVALID_ARG;
+    const kvc_desc &d = c->d;
+    if (layer < 0 || layer >= d.num_layers) return KVR_ERR_LAYER_RANGE;
+    if (d.query_heads < 1 || c->latent()) return KVR_ERR_UNSUPPORTED;
+    if (a->num_requests < 0 || a->num_requests > d.max_requests || a->num_new < 1 || a->num_new > d.max_new ||
+        a->window < 0 || (a->add != 0 && a->add != 1) || a->reserved != 0 || a->weights_width < 0 ||
+        !std::isfinite(a->scale) || !kvc_ok_table(a->table) || a->table.rows < a->num_requests)
+        return KVR_ERR_INVALID_ARG;
+    if (!kvc_type_fits(c, a->dtype)) return KVR_ERR_UNSUPPORTED;
+    // positions are 32-bit: a table row must not describe more of them
+    if ((int64_t)a->table.width * d.block_size > (int64_t)INT32_MAX - KVC_MAX_REQUESTS)
+        return KVR_ERR_UNSUPPORTED;
+    if (a->num_requests > 0 && (a->lengths == nullptr || a->q == nullptr || a->lse == nullptr ||
+                                (a->weights == nullptr && a->weights_width > 0)))
+        return KVR_ERR_INVALID_ARG;
+    if (negative({a->q_request_stride, a->q_token_stride, a->q_head_stride, a->weights_request_stride,
+                  a->weights_head_stride}))
+        return KVR_ERR_INVALID_ARG;
+    // (each head's weights are written by blocks of its own)
+    if (!disjoint_rows(a->num_requests, a->weights_request_stride, d.kv_heads, a->weights_head_stride,
+                       a->weights_width))
+        return KVR_ERR_POOL_OVERLAP;
+    if (!multiples(4, {address(a->lengths), address(a->lse), address(a->weights)}) ||
+        !multiples(16, {address(a->q), a->q_request_stride, a->q_token_stride, a->q_head_stride}))
+        return KVR_ERR_ALIGNMENT;
+    const kvr_status st = kvc_check_scoring(c, a->scoring);
+    if (st != KVR_OK) return st;
+    if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
+    if (a->num_requests == 0) return KVR_OK;
+    return kvc_weigh_launch(c, layer, a, stream);
 }
 
 extern "C" kvr_status kv_cache_read(const kvc_cache *c, int32_t layer, const kvc_read *a, void *stream) {

@@ -23,12 +23,13 @@ SCALINGS = {"linear": 1, "base": 2, "ramp": 3, "bands": 4}
 CACHE_EXPORTS = ("kv_cache_create", "kv_cache_destroy", "kv_cache_workspace_bytes",
                  "kv_cache_append", "kv_cache_attend", "kv_cache_status",
                  "kv_cache_rotary_table", "kv_cache_append_at", "kv_cache_read",
-                 "kv_cache_attend_scored")
+                 "kv_cache_attend_scored", "kv_cache_weigh")
 
-# kvc_append, kvc_attend, kvc_read and kvc_scoring as the C header lays them out (no padding between their fields)
+# kvc_append, kvc_attend, kvc_read, kvc_weigh and kvc_scoring as the C header lays them out (no padding between their fields)
 _APPEND = struct.Struct("=iiQQQqiiQQqqqqQiiIiiiQQqqqq")
 _ATTEND = struct.Struct("=iiiifiQQqiiQQQqqqqqq")
 _READ = struct.Struct("=iiQQQqiiQQqqqq")
+_WEIGH = struct.Struct("=iiiifiQQqiiQQQqqqqqiifiQ")
 _SCORING = struct.Struct("=fiQ")
 
 
@@ -60,6 +61,7 @@ def _library() -> ctypes.CDLL:
                            ("kv_cache_workspace_bytes", [p, i32, p]),
                            ("kv_cache_append", [p, i32, p, p]),
                            ("kv_cache_attend_scored", [p, i32, p, p, p]),
+                           ("kv_cache_weigh", [p, i32, p, p]),
                            ("kv_cache_append_at", [p, i32, p, p, p]), ("kv_cache_read", [p, i32, p, p]),
                            ("kv_cache_attend", [p, i32, p, p]), ("kv_cache_status", [p, p]),
                            ("kv_cache_rotary_table", [p, i32, i32, ctypes.c_double, p])):
@@ -197,6 +199,7 @@ class KVCache:
         lib = _library()
         self._h, self._pool, self._torch = h.value, (pool, layout, block_scales), torch
         self._append, self._attend = lib.kv_cache_append, lib.kv_cache_attend
+        self._weigh = lib.kv_cache_weigh
         self._attend_scored = lib.kv_cache_attend_scored
         self._append_at, self._read = lib.kv_cache_append_at, lib.kv_cache_read
         self._index = torch.cuda.current_device()
@@ -455,6 +458,48 @@ class KVCache:
         if st != 0:
             raise KVRelayoutError(st, "kv_cache_attend")
         return out, lse
+
+    def _weight_rows(self, t, name, R):
+        """Strides between the requests' and the heads' weights, and how many each head has."""
+        if t.dtype is self._f32 and t.dim() == 3 and t.shape[:2] == (R, self.kv_heads) and \
+                t.get_device() == self._index:
+            S = t.shape[2]
+            a, b, c = t.stride()
+            if c == 1 or S <= 1:
+                return a, b, S
+        raise ValueError(f"{name} are {t.dtype} {list(t.shape)} on {t.device} with strides {list(t.stride())}; expected "
+                         f"float32 [{R}][{self.kv_heads}][width] on {self._device}, rows contiguous")
+
+    def weigh(self, layer, q, lse, lengths, block_table, weights, *, add=True, scale=None, window=0, cap=0.0,
+              slopes=None, stream=None):
+        """How much attention ``layer``'s cached keys got from each request's newest tokens: to ``weights`` float32
+        [R][H][width] is added (``add=False``: there is written) the sum of exp(score - lse) over these tokens and the
+        query heads of each key head, for the ``lengths[r]`` cached keys. ``q``, ``lse`` and the rest are those of
+        :meth:`attend`. Returns ``weights``."""
+        if q.requires_grad or lse.requires_grad or weights.requires_grad:
+            self._refuse_gradients()
+        shape, heads, index = q.shape, self.query_heads, self._index
+        n = len(shape)
+        if n not in (3, 4):
+            raise ValueError(f"q is {list(shape)}; expected [R][new][heads][dim]")
+        R, m = shape[0], shape[1] if n == 4 else 1
+        rows = (R, m, heads) if n == 4 else (R, heads)
+        qs = self._rows(q, "q", rows + (self.head_dim,))
+        qs = qs if n == 4 else (qs[0], 0, qs[1])
+        if not (lse.dtype is self._f32 and lse.shape == rows and lse.is_contiguous() and lse.get_device() == index):
+            raise ValueError(f"lse is {lse.dtype} {list(lse.shape)}; expected contiguous "
+                             f"float32 {list(rows)} on {self._device}")
+        *ws, width = self._weight_rows(weights, "weights", R)
+        st = self._weigh(
+            self._handle(), layer,
+            _WEIGH.pack(R, m, self._types[q.dtype], window, self._default_scale if scale is None else scale,
+                        1 if add else 0, self._list(lengths, "lengths", R), *self._table(block_table), q.data_ptr(),
+                        lse.data_ptr(), weights.data_ptr(), *qs, *ws, width, 0, cap, 0,
+                        _SCORING.unpack(self._scoring(cap, slopes))[2]),
+            self._raw_stream(index) if stream is None else _stream_handle(stream))
+        if st != 0:
+            raise KVRelayoutError(st, "kv_cache_weigh")
+        return weights
 
     def check(self):
         """Wait for the device; raise KVRelayoutError (KVR_ERR_DEVICE_BOUNDS) if a call since

@@ -93,6 +93,7 @@ def test_null_handles():
     assert kr.STATUS[lib.kv_cache_append_at(None, 0, buf, None, None)] == "KVR_ERR_INVALID_ARG"
     assert kr.STATUS[lib.kv_cache_attend_scored(None, 0, buf, buf, None)] == "KVR_ERR_INVALID_ARG"
     assert kr.STATUS[lib.kv_cache_attend_scored(None, 0, buf, None, None)] == "KVR_ERR_INVALID_ARG"
+    assert kr.STATUS[lib.kv_cache_weigh(None, 0, buf, None)] == "KVR_ERR_INVALID_ARG"
     assert kr.STATUS[lib.kv_cache_read(None, 0, buf, None)] == "KVR_ERR_INVALID_ARG"
 
 
@@ -125,6 +126,13 @@ def test_read_is_laid_out_as_the_binding_packs_it(tmp_path):
 def test_scoring_is_laid_out_as_the_binding_packs_it(tmp_path):
     got = _offsets(tmp_path, ["sizeof(kvc_scoring)", "offsetof(kvc_scoring, slopes)"])
     assert got == [kc._SCORING.size, _marked(kc._SCORING, 2)]
+
+
+def test_weigh_is_laid_out_as_the_binding_packs_it(tmp_path):
+    fields = {"add": 5, "lengths": 6, "q": 11, "lse": 12, "weights": 13, "q_head_stride": 16, "weights_head_stride": 18,
+              "weights_width": 19, "scoring.slopes": 23}
+    got = _offsets(tmp_path, ["sizeof(kvc_weigh)"] + [f"offsetof(kvc_weigh, {n})" for n in fields])
+    assert got == [kc._WEIGH.size] + [_marked(kc._WEIGH, f) for f in fields.values()]
 
 
 def test_the_references_own_four_bits():
