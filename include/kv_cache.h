@@ -270,6 +270,38 @@ typedef struct kvc_weigh {
 
 kvr_status kv_cache_weigh(const kvc_cache *cache, int32_t layer, const kvc_weigh *args, void *stream);
 
+/*
+ * Evict tokens of layer `layer` by their weights, each key head for itself. Of the n = lengths[r] cached tokens of a
+ * request stay: all, if n <= keep; otherwise the `recent` newest and, of the others, the keep - recent of the
+ * largest weights (equal ones: the lower slots; NaN counts as above all numbers). What stays keeps its order
+ * and goes to slots 0 .. min(n, keep) - 1 through the table `into` (ids NULL, or the same table: in place). Keys and values are
+ * moved bit for bit. weights_out gets the weights of what stays in the same order, then zeros up to entry n (beyond,
+ * it is left as it was), and kept[r][h] the slots that they had (entries from min(n, keep) on are left). The
+ * lengths do not change: afterwards min(lengths[r], keep) tokens are cached, and the next is appended at that
+ * position, rotated by its own (kv_cache_append_at).
+ * Blocks of `into` must hold no cached token of these requests, unless the table is the same; requests evicted in
+ * place must not share blocks. weights_out is weights itself, with the same strides, or apart from it. A length beyond the block table or
+ * weights_width counts as the nearest in range (KVC_FLAG_LENGTH); a row whose block is out of range, or beyond `into`, is not moved
+ * (KVC_FLAG_BLOCK, KVC_FLAG_LENGTH). Uses no workspace. Keys and values only (KVR_ERR_UNSUPPORTED for latents).
+ */
+typedef struct kvc_evict {
+    int32_t num_requests;      /* 0..KVC_MAX_REQUESTS */
+    int32_t keep;              /* >= 1 */
+    int32_t recent;            /* 0..keep */
+    int32_t weights_width;
+    const int32_t *lengths;    /* device [num_requests] */
+    kvc_table table;           /* rows >= num_requests */
+    kvc_table into;            /* the same */
+    const float *weights;      /* device [num_requests][H][weights_width] */
+    float *weights_out;        /* the same */
+    int32_t *kept;             /* device [num_requests][H][keep], contiguous */
+    int64_t weights_request_stride, weights_head_stride;              /* entries */
+    int64_t out_request_stride, out_head_stride;
+    int64_t reserved;          /* 0 */
+} kvc_evict;
+
+kvr_status kv_cache_evict(const kvc_cache *cache, int32_t layer, const kvc_evict *args, void *stream);
+
 /* Waits for the cache's device (which need not be the current one), reads and clears the flags
  * of what the kernels found out of range:
  * KVR_OK with *flags = 0, or KVR_ERR_DEVICE_BOUNDS with the KVC_FLAG_* bits. */

@@ -18,7 +18,7 @@ SOURCES = ["plan.cpp", "relayout.cu", "sm_stream.cpp", "cache.cpp", "cache_more.
            "cache_attend_bf16.cu", "cache_attend_f16.cu", "cache_attend_e4m3.cu", "cache_attend_e2m1.cu",
            "cache_attend_scored_bf16.cu", "cache_attend_scored_f16.cu", "cache_attend_scored_e4m3.cu",
            "cache_attend_scored_e2m1.cu", "cache_weigh.cu", "cache_weigh_bf16.cu", "cache_weigh_f16.cu",
-           "cache_weigh_e4m3.cu", "cache_weigh_e2m1.cu"]
+           "cache_weigh_e4m3.cu", "cache_weigh_e2m1.cu", "cache_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -132,7 +132,8 @@ bool kvc_on_device(const kvc_cache *c);
 kvr_status kvc_attend_launch(const kvc_cache *c, int32_t layer, const kvc_attend *a, void *stream);
 kvr_status kvc_attend_scored_launch(const kvc_cache *c, int32_t layer, const kvc_attend *a,
                                     const kvc_scoring *scoring, void *stream);
-// cache_weigh.cu
+// cache_evict.cu, cache_weigh.cu
+kvr_status kvc_evict_launch(const kvc_cache *c, int32_t layer, const kvc_evict *a, void *stream);
 kvr_status kvc_weigh_launch(const kvc_cache *c, int32_t layer, const kvc_weigh *a, void *stream);
 kvr_status kvc_weigh_setup(kvc_cache *c);
 size_t kvc_attend_partial_bytes(const kvc_desc &d, int32_t sm_count);

@@ -96,6 +96,43 @@ extern "C" kvr_status kv_cache_weigh(const kvc_cache *c, int32_t layer, const kv
     return kvc_weigh_launch(c, layer, a, stream);
 }
 
+extern "C" kvr_status kv_cache_evict(const kvc_cache *c, int32_t layer, const kvc_evict *a, void *stream) {
+    if (c == nullptr || a == nullptr) return KVR_ERR_INVALID_ARG;
+    const kvc_desc &d = c->d;
+    if (layer < 0 || layer >= d.num_layers) return KVR_ERR_LAYER_RANGE;
+    if (c->latent()) return KVR_ERR_UNSUPPORTED;
+    if (a->num_requests < 0 || a->keep < 1 || a->recent < 0 || a->recent > a->keep || a->reserved != 0 ||
+        a->weights_width < 0 || !kvc_ok_table(a->table) || a->table.rows < a->num_requests ||
+        !kvc_ok_table(a->into) || (a->into.ids != nullptr && a->into.rows < a->num_requests))
+        return KVR_ERR_INVALID_ARG;
+    // a table in another form of the same memory would be neither in place nor apart
+    if (a->into.ids != nullptr && a->into.ids == a->table.ids &&
+        (a->into.width != a->table.width || (a->num_requests > 1 && a->into.stride != a->table.stride)))
+        return KVR_ERR_INVALID_ARG;
+    // positions are 32-bit: a table row must not describe more of them
+    for (const kvc_table *t : {&a->table, &a->into})
+        if ((int64_t)t->width * d.block_size > (int64_t)INT32_MAX - KVC_MAX_REQUESTS) return KVR_ERR_UNSUPPORTED;
+    if (a->num_requests > KVC_MAX_REQUESTS || a->weights_width > INT32_MAX - KVC_MAX_REQUESTS ||
+        a->keep > INT32_MAX - KVC_MAX_REQUESTS)
+        return KVR_ERR_UNSUPPORTED;
+    if (a->num_requests > 0 && (a->lengths == nullptr || a->kept == nullptr ||
+                                (a->weights_width > 0 && (a->weights == nullptr || a->weights_out == nullptr))))
+        return KVR_ERR_INVALID_ARG;
+    if (negative({a->weights_request_stride, a->weights_head_stride, a->out_request_stride, a->out_head_stride}))
+        return KVR_ERR_INVALID_ARG;
+    if (a->weights == a->weights_out && (a->weights_request_stride != a->out_request_stride ||
+                                         a->weights_head_stride != a->out_head_stride))
+        return KVR_ERR_INVALID_ARG;
+    // (each head's weights are written by blocks of its own)
+    if (!disjoint_rows(a->num_requests, a->out_request_stride, d.kv_heads, a->out_head_stride, a->weights_width))
+        return KVR_ERR_POOL_OVERLAP;
+    if (!multiples(4, {address(a->lengths), address(a->weights), address(a->weights_out), address(a->kept)}))
+        return KVR_ERR_ALIGNMENT;
+    if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
+    if (a->num_requests == 0) return KVR_OK;
+    return kvc_evict_launch(c, layer, a, stream);
+}
+
 extern "C" kvr_status kv_cache_read(const kvc_cache *c, int32_t layer, const kvc_read *a, void *stream) {
     if (c == nullptr || a == nullptr) return KVR_ERR_INVALID_ARG;
     if (layer < 0 || layer >= c->d.num_layers) return KVR_ERR_LAYER_RANGE;

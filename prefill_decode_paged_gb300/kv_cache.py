@@ -23,13 +23,14 @@ SCALINGS = {"linear": 1, "base": 2, "ramp": 3, "bands": 4}
 CACHE_EXPORTS = ("kv_cache_create", "kv_cache_destroy", "kv_cache_workspace_bytes",
                  "kv_cache_append", "kv_cache_attend", "kv_cache_status",
                  "kv_cache_rotary_table", "kv_cache_append_at", "kv_cache_read",
-                 "kv_cache_attend_scored", "kv_cache_weigh")
+                 "kv_cache_attend_scored", "kv_cache_weigh", "kv_cache_evict")
 
-# kvc_append, kvc_attend, kvc_read, kvc_weigh and kvc_scoring as the C header lays them out (no padding between their fields)
+# kvc_append, kvc_attend, kvc_read, kvc_weigh, kvc_evict and kvc_scoring as the C header lays them out (no padding between their fields)
 _APPEND = struct.Struct("=iiQQQqiiQQqqqqQiiIiiiQQqqqq")
 _ATTEND = struct.Struct("=iiiifiQQqiiQQQqqqqqq")
 _READ = struct.Struct("=iiQQQqiiQQqqqq")
 _WEIGH = struct.Struct("=iiiifiQQqiiQQQqqqqqiifiQ")
+_EVICT = struct.Struct("=iiiiQQqiiQqiiQQQqqqqq")
 _SCORING = struct.Struct("=fiQ")
 
 
@@ -62,6 +63,7 @@ def _library() -> ctypes.CDLL:
                            ("kv_cache_append", [p, i32, p, p]),
                            ("kv_cache_attend_scored", [p, i32, p, p, p]),
                            ("kv_cache_weigh", [p, i32, p, p]),
+                           ("kv_cache_evict", [p, i32, p, p]),
                            ("kv_cache_append_at", [p, i32, p, p, p]), ("kv_cache_read", [p, i32, p, p]),
                            ("kv_cache_attend", [p, i32, p, p]), ("kv_cache_status", [p, p]),
                            ("kv_cache_rotary_table", [p, i32, i32, ctypes.c_double, p])):
@@ -199,7 +201,7 @@ class KVCache:
         lib = _library()
         self._h, self._pool, self._torch = h.value, (pool, layout, block_scales), torch
         self._append, self._attend = lib.kv_cache_append, lib.kv_cache_attend
-        self._weigh = lib.kv_cache_weigh
+        self._weigh, self._evict = lib.kv_cache_weigh, lib.kv_cache_evict
         self._attend_scored = lib.kv_cache_attend_scored
         self._append_at, self._read = lib.kv_cache_append_at, lib.kv_cache_read
         self._index = torch.cuda.current_device()
@@ -254,11 +256,17 @@ class KVCache:
         of torch's current stream may still be in use by what is queued there."""
         if stream is None:
             return self._torch.empty(shape, dtype=dtype, device=self._device)
-        cuda, handle = self._torch.cuda, _stream_handle(stream) or 0
-        on = cuda.ExternalStream(handle, device=self._device) if handle > 1 else \
-            cuda.default_stream(self._device)              # (0 and 1: the legacy default stream)
-        with cuda.stream(on):
+        with self._torch.cuda.stream(self._as_stream(stream)):
             return self._torch.empty(shape, dtype=dtype, device=self._device)
+
+    def _as_stream(self, stream):
+        """The torch stream of a ``stream`` argument."""
+        cuda = self._torch.cuda
+        if stream is None:
+            return cuda.current_stream(self._device)
+        handle = _stream_handle(stream) or 0
+        return cuda.ExternalStream(handle, device=self._device) if handle > 1 else \
+            cuda.default_stream(self._device)              # (0 and 1: the legacy default stream)
 
     def _rows(self, t, name, shape, dtype=None):
         """Byte strides of a tensor of head rows but the last dimension's, once it is checked."""
@@ -500,6 +508,42 @@ class KVCache:
         if st != 0:
             raise KVRelayoutError(st, "kv_cache_weigh")
         return weights
+
+    def evict(self, layer, weights, lengths, block_table, keep, recent=0, *, into=None, out=None, slots=None,
+              stream=None):
+        """Keep at most ``keep`` of each request's cached tokens in ``layer``, each key head for itself: the ``recent``
+        newest and, of the others, those of the largest ``weights`` (float32 [R][H][width], see :meth:`weigh`; equal ones:
+        the lower slots). Their rows move together to the front, in their order, in place or through another block table
+        ``into`` whose blocks hold no cached token. ``out`` (``weights`` itself by default) gets their
+        weights, then zeros up to ``lengths[r]``. Afterwards min(lengths[r], keep) tokens are cached; the caller's lengths
+        are its own to change. Returns (out, slots): ``slots`` int32 [R][H][keep], the slots that the kept tokens
+        had (entries beyond their number are left as they were, in a new tensor -1)."""
+        if weights.requires_grad or (out is not None and out.requires_grad):
+            self._refuse_gradients()
+        R = weights.shape[0] if weights.dim() == 3 else -1
+        *ws, width = self._weight_rows(weights, "weights", R)
+        out = weights if out is None else out
+        *os, out_width = self._weight_rows(out, "out", R)
+        if out_width != width:
+            raise ValueError(f"out has {out_width} weights a head; weights {width}")
+        shape = (R, self.kv_heads, keep)
+        if slots is None:
+            slots = self._new(shape, self._i32, stream)
+            with self._torch.cuda.stream(self._as_stream(stream)):
+                slots.fill_(-1)
+        elif not (slots.dtype is self._i32 and slots.shape == shape and slots.is_contiguous() and
+                  slots.get_device() == self._index):
+            raise ValueError(f"slots are {slots.dtype} {list(slots.shape)} on {slots.device}; expected contiguous "
+                             f"int32 {list(shape)} on {self._device}")
+        there = (0, 0, 0, 0) if into is None else self._table(into)
+        st = self._evict(
+            self._handle(), layer,
+            _EVICT.pack(R, keep, recent, width, self._list(lengths, "lengths", R), *self._table(block_table), *there,
+                        weights.data_ptr(), out.data_ptr(), slots.data_ptr(), *ws, *os, 0),
+            self._raw_stream(self._index) if stream is None else _stream_handle(stream))
+        if st != 0:
+            raise KVRelayoutError(st, "kv_cache_evict")
+        return out, slots
 
     def check(self):
         """Wait for the device; raise KVRelayoutError (KVR_ERR_DEVICE_BOUNDS) if a call since

@@ -94,6 +94,7 @@ def test_null_handles():
     assert kr.STATUS[lib.kv_cache_attend_scored(None, 0, buf, buf, None)] == "KVR_ERR_INVALID_ARG"
     assert kr.STATUS[lib.kv_cache_attend_scored(None, 0, buf, None, None)] == "KVR_ERR_INVALID_ARG"
     assert kr.STATUS[lib.kv_cache_weigh(None, 0, buf, None)] == "KVR_ERR_INVALID_ARG"
+    assert kr.STATUS[lib.kv_cache_evict(None, 0, buf, None)] == "KVR_ERR_INVALID_ARG"
     assert kr.STATUS[lib.kv_cache_read(None, 0, buf, None)] == "KVR_ERR_INVALID_ARG"
 
 
@@ -133,6 +134,13 @@ def test_weigh_is_laid_out_as_the_binding_packs_it(tmp_path):
               "weights_width": 19, "scoring.slopes": 23}
     got = _offsets(tmp_path, ["sizeof(kvc_weigh)"] + [f"offsetof(kvc_weigh, {n})" for n in fields])
     assert got == [kc._WEIGH.size] + [_marked(kc._WEIGH, f) for f in fields.values()]
+
+
+def test_evict_is_laid_out_as_the_binding_packs_it(tmp_path):
+    fields = {"weights_width": 3, "lengths": 4, "into": 9, "weights": 13, "weights_out": 14, "kept": 15,
+              "out_head_stride": 19, "reserved": 20}
+    got = _offsets(tmp_path, ["sizeof(kvc_evict)"] + [f"offsetof(kvc_evict, {n})" for n in fields])
+    assert got == [kc._EVICT.size] + [_marked(kc._EVICT, f) for f in fields.values()]
 
 
 def test_the_references_own_four_bits():
