@@ -356,7 +356,7 @@ kvr_status kvc_check_append(const kvc_cache *c, int32_t layer, const kvc_append 
                         a->q_head_stride, a->q_out_token_stride, a->q_out_head_stride}))
             return KVR_ERR_ALIGNMENT;
     }
-    // (a thread of the 4-bit pool's kernel takes 32 elements)
+    // (two threads share a group of 16 elements: rotated ones come in whole pairs of threads)
     if (d.dtype == KVC_DTYPE_E2M1 && ((a->rotary != nullptr && a->rotary_dim % 32 != 0) ||
                                       (a->q_heads > 0 && a->q_dim % 32 != 0)))
         return KVR_ERR_UNSUPPORTED;

@@ -139,12 +139,10 @@ kvr_status kvc_weigh_setup(kvc_cache *c);
 size_t kvc_attend_partial_bytes(const kvc_desc &d, int32_t sm_count);
 size_t kvc_attend_jobs(const kvc_desc &d);
 kvr_status kvc_attend_setup(kvc_cache *c);
-// cache_append.cu, cache_append_e2m1.cu (`angles`: NULL for the positions), cache_read.cu
+// cache_append.cu (`angles`: NULL for the positions), cache_read.cu
 kvr_status kvc_append_launch(const kvc_cache *c, int32_t layer, const kvc_append *a, void *stream);
 kvr_status kvc_append_at_launch(const kvc_cache *c, int32_t layer, const kvc_append *a,
                                 const int32_t *angles, void *stream);
-kvr_status kvc_append_e2m1_launch(const kvc_cache *c, int32_t layer, const kvc_append *a,
-                                  const int32_t *angles, void *stream);
 kvr_status kvc_read_launch(const kvc_cache *c, int32_t layer, const kvc_read *a, void *stream);
 
 #if defined(__CUDACC__)

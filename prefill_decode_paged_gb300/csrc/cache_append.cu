@@ -6,6 +6,8 @@
 //   rotated, halves:      pieces at 8 i and 8 i + R / 2 hold pairs 8 i .. 8 i + 7 as (a | b);
 //   rotated, interleaved: pieces at 16 i and 16 i + 8 hold the same pairs side by side;
 //   not rotated:          pieces at 16 i and 16 i + 8, passed through (or quantized).
+// A group of 16 elements of a 4-bit pool, which share a block scale, is one unit, or where pairs are halves apart a
+// piece of two neighbouring threads' units each, which exchange their largest values.
 // A thread asks for BATCH units before it looks at the token's position: the slot (position, then
 // block id) and the angles are on their way meanwhile. Where the row's units divide the block's
 // threads, a thread has the same unit of every row, and loads its angles once. HBM bounds it with
@@ -43,6 +45,7 @@ struct AppendArgs {
     int32_t rotary_rows, R;
     int32_t dim, q_dim;
     const float *k_scale, *v_scale;
+    unsigned char *k_block_scales, *v_block_scales;
     uint32_t *flags;
     int32_t last;             // the rotated elements are the row's last
     int32_t away;             // what is written need not stay in L2
@@ -84,8 +87,9 @@ __device__ __forceinline__ uint4 load16(const unsigned char *p) {
     return v;
 }
 
-// The unit's 16 elements in fp32: x[0..7] piece 0, x[8..15] piece 1; rotated in place.
-template <bool F16, bool INTERLEAVED>
+// The unit's 16 elements in fp32: x[0..7] piece 0, x[8..15] piece 1; rotated in place. SINGLE: products and sum
+// are rounded one by one (for 4 bits, where a value next to a border must go the same way everywhere).
+template <bool F16, bool INTERLEAVED, bool SINGLE>
 __device__ __forceinline__ void turn(const uint4 &p0, const uint4 &p1, const Unit &u, float x[16]) {
     const uint32_t w[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
@@ -98,8 +102,9 @@ __device__ __forceinline__ void turn(const uint4 &p0, const uint4 &p1, const Uni
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float &a = x[INTERLEAVED ? 2 * i : i], &b = x[INTERLEAVED ? 2 * i + 1 : i + 8];
-        const float y = fmaf(a, u.cs[i], -(b * u.sn[i]));
-        b = fmaf(b, u.cs[i], a * u.sn[i]);
+        const float y = SINGLE ? __fsub_rn(__fmul_rn(a, u.cs[i]), __fmul_rn(b, u.sn[i]))
+                               : fmaf(a, u.cs[i], -(b * u.sn[i]));
+        b = SINGLE ? __fadd_rn(__fmul_rn(b, u.cs[i]), __fmul_rn(a, u.sn[i])) : fmaf(b, u.cs[i], a * u.sn[i]);
         a = y;
     }
 }
@@ -141,6 +146,61 @@ __device__ __forceinline__ void store_8bit(unsigned char *row, const Unit &u, co
     store(row + u.e1, make_uint2(quant4f(x + 8, inv), quant4f(x + 12, inv)), away);
 }
 
+// -- 4 bits: b = max(2^-9, E4M3(max |y| / 6)), codes E2M1(y / b), y = x / s; the quotients as products with the
+// fp32 reciprocals
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+// A block scale from its group's largest absolute value (a NaN gives a NaN).
+__device__ __forceinline__ uint32_t block_scale(float top) {
+    unsigned short b;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(0.0f), "f"(__fmul_rn(top, 1.0f / 6.0f)));
+    return b == 0 ? 1u : b;                              // 1: 2^-9
+}
+// Eight codes, the first in the lowest bits.
+__device__ __forceinline__ uint32_t codes8(const float *y, uint32_t scale) {
+    const float by = 1.0f / widen2<true>(e4m3_to_f16x2(scale)).x;
+    uint32_t w;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w)
+        : "f"(__fmul_rn(y[0], by)), "f"(__fmul_rn(y[1], by)), "f"(__fmul_rn(y[2], by)),
+          "f"(__fmul_rn(y[3], by)), "f"(__fmul_rn(y[4], by)), "f"(__fmul_rn(y[5], by)),
+          "f"(__fmul_rn(y[6], by)), "f"(__fmul_rn(y[7], by)));
+    return w;
+}
+// The codes and block scales of a unit; all lanes of the warp, `keep` those that have one. Pieces that are not
+// neighbours (of values too, which are taken like the keys) are of two groups, whose other halves the next lane has.
+__device__ __forceinline__ void store_4bit(unsigned char *codes, unsigned char *scales, const Unit &u, float x[16],
+                                           float inv, bool keep, bool away) {
+    const bool apart = u.e1 != u.e0 + 8;
+    float m0 = 0.0f, m1 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[i] = __fmul_rn(x[i], inv), x[8 + i] = __fmul_rn(x[8 + i], inv);
+        m0 = max_nan(m0, fabsf(x[i])), m1 = max_nan(m1, fabsf(x[8 + i]));
+    }
+    const float o0 = __shfl_xor_sync(~0u, m0, 1), o1 = __shfl_xor_sync(~0u, m1, 1);
+    if (!keep) return;
+    if (apart) {
+        const uint32_t b0 = block_scale(max_nan(m0, o0)), b1 = block_scale(max_nan(m1, o1));
+        store(codes + u.e0 / 2, codes8(x, b0), away);
+        store(codes + u.e1 / 2, codes8(x + 8, b1), away);
+        // (each of the two lanes one of the two scales)
+        const bool second = threadIdx.x & 1;
+        scales[(second ? u.e1 : u.e0) / 16] = (unsigned char)(second ? b1 : b0);
+    } else {
+        const uint32_t b = block_scale(max_nan(m0, m1));
+        store(codes + u.e0 / 2, make_uint2(codes8(x, b), codes8(x + 8, b)), away);
+        scales[u.e0 / 16] = (unsigned char)b;
+    }
+}
+
 // Where unit `t` of the token's units is: queries first, then keys, then values.
 struct Place {
     int32_t row, j;           // head row of its input, unit of the row
@@ -164,10 +224,12 @@ __device__ __forceinline__ Place place_of(const AppendArgs &a, int32_t t, int32_
     return p;
 }
 
-template <bool F16, bool INTERLEAVED, bool E4M3, bool MANY>
-__global__ void __launch_bounds__(MANY ? MANY_THREADS : FEW_THREADS, MANY ? 10 : 2)
+template <bool F16, bool INTERLEAVED, int POOL, bool MANY>
+__global__ void __launch_bounds__(MANY ? MANY_THREADS : FEW_THREADS,
+                  POOL == KVC_DTYPE_E2M1 ? (MANY ? 8 : 1) : MANY ? 10 : 2)
 append_kernel(AppendArgs a) {
     constexpr int BATCH = MANY ? 1 : 2;
+    constexpr bool E4M3 = POOL == KVR_DTYPE_FP8_E4M3, E2M1 = POOL == KVC_DTYPE_E2M1;
     const int32_t THREADS = MANY ? MANY_THREADS : (int32_t)blockDim.x;
     wait_for_previous();
     let_next_start();
@@ -180,7 +242,8 @@ append_kernel(AppendArgs a) {
     int32_t have = -1;                       // the pair whose angles `u` holds
     Unit u;
 
-    for (int32_t t0 = threadIdx.x; t0 < n; t0 += THREADS * BATCH) {
+    // (4 bits: warps stay whole for the exchange of their lanes)
+    for (int32_t t0 = threadIdx.x; (E2M1 ? t0 & ~31 : t0) < n; t0 += THREADS * BATCH) {
         uint4 p0[BATCH], p1[BATCH];
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
@@ -220,19 +283,27 @@ append_kernel(AppendArgs a) {
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
             const Place p = place_of(a, t0 + b * THREADS, n);
-            if (p.kind == 3) continue;
+            if (!E2M1 && p.kind == 3) continue;
             place<INTERLEAVED>(u, a, p.kind == 0 ? a.q_dim : a.dim, p.j);
             if (p.kind == 2) u.rotated = false;
+            if (E2M1 && p.kind == 3) u.rotated = false;
             if (u.rotated && u.pair != have) {
                 load_angles(u, angles, a.R);
                 have = u.pair;
             }
             float x[16];
-            turn<F16, INTERLEAVED>(p0[b], p1[b], u, x);
-            if (p.kind == 0) {
+            turn<F16, INTERLEAVED, E2M1>(p0[b], p1[b], u, x);
+            if (p.kind == 0)
                 store_16bit<F16>(a.q_out + token * a.q_out_token + p.row * a.q_out_head, u, x,
                                  MANY && a.away);
-            } else {
+            if constexpr (E2M1) {
+                const bool key = p.kind == 1, some = p.kind == 1 || p.kind == 2;
+                const int64_t at = slot + p.row * a.k_plane.head_stride;
+                const float s = some ? __ldg((key ? a.k_scale : a.v_scale) + p.row) : 1.0f;
+                store_4bit((key ? a.k_plane : a.v_plane).base + at,
+                           (key ? a.k_block_scales : a.v_block_scales) + at / 8, u, x, 1.0f / s,
+                           some, MANY && a.away);
+            } else if (p.kind != 0) {
                 const KvcPlane &plane = p.kind == 1 ? a.k_plane : a.v_plane;
                 unsigned char *dst = plane.base + slot + p.row * plane.head_stride;
                 if (E4M3)
@@ -251,7 +322,7 @@ append_kernel(AppendArgs a) {
 // units, 4.2 and 5.6 for 256; 2.9 and 3.1 for 300 of 384, 4.9 and 3.8 for 600; and with blocks of 192,
 // 256 and 384 threads 39834 tokens took 186, 190 and 216 where those of 128 took 162. (The register limits, 48
 // for many and 64 for few, make the compiler spill 12 to 64 bytes a thread; looser ones have not been tried.)
-template <bool F16, bool E4M3>
+template <bool F16, int POOL>
 kvr_status go(AppendArgs &a, bool interleaved, int32_t tokens, int sms, void *stream) {
     const int64_t n = (int64_t)a.q.heads * a.q_units.d + (int64_t)(a.k.heads + a.v.heads) * a.units.d;
     const bool many = tokens > BORDER * sms;
@@ -259,8 +330,8 @@ kvr_status go(AppendArgs &a, bool interleaved, int32_t tokens, int sms, void *st
     const int threads = many ? MANY_THREADS : (int)((n + 32 * rounds - 1) / (32 * rounds)) * 32;
     a.away = tokens * n * 16 * 2 > (int64_t)AWAY << 20;
     const auto kernel =
-        many ? (interleaved ? append_kernel<F16, true, E4M3, true> : append_kernel<F16, false, E4M3, true>)
-             : (interleaved ? append_kernel<F16, true, E4M3, false> : append_kernel<F16, false, E4M3, false>);
+        many ? (interleaved ? append_kernel<F16, true, POOL, true> : append_kernel<F16, false, POOL, true>)
+             : (interleaved ? append_kernel<F16, true, POOL, false> : append_kernel<F16, false, POOL, false>);
     return kvc_launch(kernel, a, dim3((unsigned)tokens), threads, 0, stream);
 }
 
@@ -272,7 +343,6 @@ kvr_status kvc_append_launch(const kvc_cache *c, int32_t layer, const kvc_append
 
 kvr_status kvc_append_at_launch(const kvc_cache *c, int32_t layer, const kvc_append *p, const int32_t *angles,
                                 void *stream) {
-    if (c->d.dtype == KVC_DTYPE_E2M1) return kvc_append_e2m1_launch(c, layer, p, angles, stream);
     AppendArgs a = {};
     const int32_t H = c->d.kv_heads;
     a.k = {(const unsigned char *)p->k, p->k_token_stride, p->k_head_stride, H};
@@ -282,6 +352,8 @@ kvr_status kvc_append_at_launch(const kvc_cache *c, int32_t layer, const kvc_app
         a.v = {(const unsigned char *)p->v, p->v_token_stride, p->v_head_stride, H};
         a.v_plane = c->plane(layer, 1);
         a.v_scale = c->scale_of(layer, 1);
+        a.k_block_scales = c->block_scales(layer, 0);
+        a.v_block_scales = c->block_scales(layer, 1);
     }
     a.q = {(const unsigned char *)p->q, p->q_token_stride, p->q_head_stride, p->q_heads};
     a.q_out = (unsigned char *)p->q_out;
@@ -301,9 +373,12 @@ kvr_status kvc_append_at_launch(const kvc_cache *c, int32_t layer, const kvc_app
     a.flags = c->ws.flags;
     a.last = (p->flags & KVC_ROTATE_LAST) != 0;
     const bool il = (p->flags & KVC_INTERLEAVED) != 0, f16 = p->dtype == KVC_DTYPE_F16;
+    if (c->d.dtype == KVC_DTYPE_E2M1)
+        return f16 ? go<true, KVC_DTYPE_E2M1>(a, il, p->num_tokens, c->sm_count, stream)
+                   : go<false, KVC_DTYPE_E2M1>(a, il, p->num_tokens, c->sm_count, stream);
     if (c->d.dtype == KVR_DTYPE_FP8_E4M3)
-        return f16 ? go<true, true>(a, il, p->num_tokens, c->sm_count, stream)
-                   : go<false, true>(a, il, p->num_tokens, c->sm_count, stream);
-    return f16 ? go<true, false>(a, il, p->num_tokens, c->sm_count, stream)
-               : go<false, false>(a, il, p->num_tokens, c->sm_count, stream);
+        return f16 ? go<true, KVR_DTYPE_FP8_E4M3>(a, il, p->num_tokens, c->sm_count, stream)
+                   : go<false, KVR_DTYPE_FP8_E4M3>(a, il, p->num_tokens, c->sm_count, stream);
+    return f16 ? go<true, KVC_DTYPE_F16>(a, il, p->num_tokens, c->sm_count, stream)
+               : go<false, KVR_DTYPE_BF16>(a, il, p->num_tokens, c->sm_count, stream);
 }

@@ -96,6 +96,13 @@ kvr_status kvc_attend_scored_launch(const kvc_cache *c, int32_t layer, const kvc
     const int64_t resident = std::min<int64_t>(k.blocks, (228 << 10) / (int64_t)(smem + 1024));
     const int64_t grid = std::min<int64_t>(resident * kvc_stream_sms(c, stream), all);
     a.by_chunks = kvr_make_div((uint32_t)a.chunks);
+    a.by_heads = kvr_make_div((uint32_t)a.H);
+    if (k.abreast) {
+        // (one part at least, however many heads there are)
+        const int32_t parts = (int32_t)std::max<int64_t>(1, grid / a.H);
+        a.shape = make_cut_shape(p->num_requests, a.chunks, parts, SLACK);
+        return kvc_launch(k.kernel, a, dim3((unsigned)(parts * a.H)), ATTEND_THREADS, smem, stream);
+    }
     a.shape = make_cut_shape(p->num_requests, a.H * a.chunks, (int32_t)grid, SLACK);
     return kvc_launch(k.kernel, a, dim3((unsigned)grid), ATTEND_THREADS, smem, stream);
 }

@@ -62,7 +62,7 @@ struct AttendArgs {
     uint32_t *arrived;
     int32_t m, H, G, D, f16;
     int32_t chunks;           // passes over a job's keys, RP rows each
-    KvrDiv group, by_chunks;  // by G, chunks
+    KvrDiv group, by_chunks, by_heads;   // by G, chunks, H
     CutShape shape;
     float scale;
     Scoring scoring;
@@ -96,6 +96,9 @@ struct Attend {
     static constexpr int STAGES = E2 ? (BLOCKS == 4 && DP == 128 ? 3 : DP > 128 ? 3 : 5) : STAGE >= 8192 ? 3 : 6;
     static constexpr int RING = ATTEND_WARPS * STAGES * STAGE;
     static constexpr int UNIT = ATTEND_WARPS * KT;               // keys of a unit
+    // One block a head goes through the same part of the line: the block scales of a token's heads share a sector
+    // (8 bytes each for D = 128), which so is fetched once
+    static constexpr bool ABREAST = E2;
     static constexpr int RP = 8 * NT;
     static constexpr int MT = DP / 16;
     static constexpr int PITCH = DP + 4;                         // floats of a row to be joined
@@ -108,7 +111,14 @@ struct Attend {
     static constexpr size_t smem(int32_t requests) { return FIXED + 4 * (size_t)(requests + 1); }
 };
 
+// LINE: L2 takes the rest of a line of 128 bytes as well. (Where a row ends within one, the rest is another
+// head's, which its own block asks for.)
+template <bool LINE>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+    if (!LINE) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+        return;
+    }
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(bytes)
                  : "memory");
@@ -422,7 +432,9 @@ attend_kernel(AttendArgs a) {
     let_next_start();
 
     unit_prefix<C::UNIT>(a.split, 1, prefix, shared_int);
-    const int32_t HJ = a.H * a.chunks;
+    // jobs of a request, and blocks that go the same way through them
+    const int32_t HJ = C::ABREAST ? a.chunks : a.H * a.chunks, abreast = C::ABREAST ? a.H : 1;
+    const int32_t part = C::ABREAST ? (int32_t)a.by_heads.div(blockIdx.x) : (int32_t)blockIdx.x;
     const int32_t total = prefix[a.split.requests] * HJ;
     const Cut cut(total, a.shape);
     if (cut.group > 0) {
@@ -430,7 +442,7 @@ attend_kernel(AttendArgs a) {
         __syncthreads();
     }
     int32_t x, x_end;
-    int32_t known = cut.units_of(blockIdx.x, prefix, ahead, a.shape, &x, &x_end);
+    int32_t known = cut.units_of(part, prefix, ahead, a.shape, &x, &x_end);
 
     const int32_t M = a.m * a.G;
     const int32_t slot_floats = RP * (a.D + 2);
@@ -442,7 +454,8 @@ attend_kernel(AttendArgs a) {
         known = -1;
         const int32_t r = seg.r, job = seg.job, u0 = seg.u0, u1 = seg.u1, units = seg.units;
         x += u1 - u0;
-        const int32_t h = (int32_t)a.by_chunks.div((uint32_t)job), row0 = (job - h * a.chunks) * RP;
+        const int32_t h = C::ABREAST ? (int32_t)blockIdx.x - part * a.H : (int32_t)a.by_chunks.div((uint32_t)job);
+        const int32_t row0 = (C::ABREAST ? job : job - h * a.chunks) * RP;
         const int32_t rows = min(RP, M - row0);
         uint32_t bad = 0;
         const Span sp = span_of(a.split, r, 1, &bad);   // tiles begin at the first key
@@ -479,8 +492,8 @@ attend_kernel(AttendArgs a) {
                 const bool there = off >= 0 && in_row;
                 const int64_t at = there ? off + c * 16 : 0;
                 const uint32_t dst = base + swizzled<ROW>(row, c), n = there ? 16 : 0;
-                cp_async16(dst, a.k_plane.base + at, n);
-                cp_async16(dst + KT * ROW, a.v_plane.base + at, n);
+                cp_async16<!C::E2 || ROW >= 128>(dst, a.k_plane.base + at, n);
+                cp_async16<!C::E2 || ROW >= 128>(dst + KT * ROW, a.v_plane.base + at, n);
             }
             if (C::E2) {                                // each lane its own key's block scales
                 constexpr int PIECE = DP == 128 ? 8 : 4;
@@ -723,7 +736,7 @@ attend_kernel(AttendArgs a) {
                 }
             }
         __syncthreads();
-        const int32_t job_index = r * HJ + job;
+        const int32_t job_index = (r * HJ + job) * abreast + (C::ABREAST ? h : 0);
         const bool whole = u0 == 0 && u1 == units;
         const int32_t D4 = a.D / 4;
         float *slot = a.partial + (size_t)(2 * blockIdx.x + (u0 == 0 ? 1 : 0)) * (size_t)slot_floats;
@@ -818,7 +831,8 @@ attend_kernel(AttendArgs a) {
                         for (int32_t k = lane; k < here; k += 32) {
                             const int32_t c = k0 + k;
                             load_bytes(smem0 + k * slot_bytes,
-                                       a.partial + (size_t)(2 * (c0 + c) + (c == 0 ? 1 : 0)) * (size_t)slot_floats,
+                                       a.partial + (size_t)(2 * ((c0 + c) * abreast + (C::ABREAST ? h : 0)) + (c == 0 ? 1 : 0)) *
+                                                       (size_t)slot_floats,
                                        slot_bytes, join_bar);
                         }
                     }
@@ -891,12 +905,13 @@ struct AttendPick {
     void (*kernel)(AttendArgs);
     size_t (*smem)(int32_t requests);
     int32_t unit, rp, blocks;
+    bool abreast;
 };
 
 template <int DP, int POOL, int NT, bool SCORED>
 inline AttendPick attend_instance() {
     using C = Attend<DP, POOL, NT>;
-    return {attend_kernel<DP, POOL, NT, SCORED>, &C::smem, C::UNIT, C::RP, C::BLOCKS};
+    return {attend_kernel<DP, POOL, NT, SCORED>, &C::smem, C::UNIT, C::RP, C::BLOCKS, C::ABREAST};
 }
 
 // The instance for head dimension D and M rows a job: rows in passes of 8, 16 or 32 (at most 16

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
                 const int row = i * RPI + lane / CPR;
                 const int64_t off = __shfl_sync(~0u, slot, row);
                 const bool there = off >= 0 && in_row;
-                cp_async16(base + swizzled<ROW>(row, c), a.k_plane.base + (there ? off + c * 16 : 0),
+                cp_async16<!C::E2 || ROW >= 128>(base + swizzled<ROW>(row, c), a.k_plane.base + (there ? off + c * 16 : 0),
                            there ? 16 : 0);
             }
             if (C::E2) {                                // each lane its own key's block scales
