@@ -298,6 +298,7 @@ append_kernel(AppendArgs a) {
                                  MANY && a.away);
             if constexpr (E2M1) {
                 const bool key = p.kind == 1, some = p.kind == 1 || p.kind == 2;
+                if (!__any_sync(~0u, some)) continue;
                 const int64_t at = slot + p.row * a.k_plane.head_stride;
                 const float s = some ? __ldg((key ? a.k_scale : a.v_scale) + p.row) : 1.0f;
                 store_4bit((key ? a.k_plane : a.v_plane).base + at,

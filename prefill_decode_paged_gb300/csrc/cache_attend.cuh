@@ -92,8 +92,8 @@ struct Attend {
     static constexpr int KT = 2 * 16 * ROW >= 8192 ? 16 : 32;    // keys of a tile
     static constexpr int KS = KT / 16;
     static constexpr int STAGE = 2 * KT * (ROW + SROW);          // keys, values, then their block scales
-    static constexpr int BLOCKS = E2 ? (DP > 128 || NT > 1 ? 2 : 4) : STAGE > 8192 ? 1 : 2;   // resident on an SM
-    static constexpr int STAGES = E2 ? (BLOCKS == 4 && DP == 128 ? 3 : DP > 128 ? 3 : 5) : STAGE >= 8192 ? 3 : 6;
+    static constexpr int BLOCKS = E2 ? (NT > 2 || NT > 1 && DP > 128 ? 2 : NT > 1 || DP > 128 ? 3 : 4) : STAGE > 8192 ? 1 : 2;   // resident on an SM
+    static constexpr int STAGES = E2 ? (DP > 128 ? (NT == 1 ? 2 : 3) : NT == 2 ? 3 : NT == 1 && DP == 128 ? 2 : 5) : STAGE >= 8192 ? 3 : 6;
     static constexpr int RING = ATTEND_WARPS * STAGES * STAGE;
     static constexpr int UNIT = ATTEND_WARPS * KT;               // keys of a unit
     // One block a head goes through the same part of the line: the block scales of a token's heads share a sector
@@ -225,18 +225,20 @@ __device__ __forceinline__ void scores_e2m1(float (&s)[KT / 16][NT][4], uint32_t
     const int lane = threadIdx.x % 32, g = lane / 4, t4 = lane % 4;
     const uint32_t pick = t4 < 2 ? 0x2200 : 0x3311;     // a lane's codes lie within one group of 16
 #pragma unroll
-    for (int k = 0; k < KT / 16; ++k) {
-        uint32_t sc[2][SROW / 4];
+    for (int p = 0; p < DP / 64; ++p) {                 // 64 elements: a word of block scales
+        uint32_t b[2][NT][4];                           // [32 elements][row tile][step, half]
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int p = 0; p < SROW / 4; ++p)
-                sc[u][p] = *(const uint32_t *)(scales + (k * 16 + u * 8 + g) * SROW + 4 * p);
+            for (int n = 0; n < NT; ++n)
+                ldmatrix4(b[c][n], q_base + swizzled<DP * 2>(n * 8 + lane % 8, (p * 2 + c) * 4 + lane / 8));
 #pragma unroll
-        for (int p = 0; p < DP / 64; ++p) {             // 64 elements: a word of block scales
+        for (int k = 0; k < KT / 16; ++k) {
             uint32_t w[4];                              // rows g, g + 8 of the 1st, 2nd 32 elements
             ldmatrix4(w, kbase + swizzled<ROW>(k * 16 + lane % 16, p * 2 + lane / 16));
-            const uint32_t lo = __byte_perm(sc[0][p], 0, pick), hi = __byte_perm(sc[1][p], 0, pick);
+            const unsigned char *at = scales + (k * 16 + g) * SROW + 4 * p;
+            const uint32_t lo = __byte_perm(*(const uint32_t *)at, 0, pick);
+            const uint32_t hi = __byte_perm(*(const uint32_t *)(at + 8 * SROW), 0, pick);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const uint32_t slo = e4m3_to_f16x2(c == 0 ? lo : lo >> 16);
@@ -246,13 +248,11 @@ __device__ __forceinline__ void scores_e2m1(float (&s)[KT / 16][NT][4], uint32_t
                 e2m1_to_f16x2(w[2 * c + 1], y);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] = mul_f16x2(x[e], slo), y[e] = mul_f16x2(y[e], shi);
+                const uint32_t f0[4] = {x[0], y[0], x[1], y[1]}, f1[4] = {x[2], y[2], x[3], y[3]};
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    uint32_t b[4];                      // [step][half]
-                    ldmatrix4(b, q_base + swizzled<DP * 2>(n * 8 + lane % 8, (p * 2 + c) * 4 + lane / 8));
-                    const uint32_t f0[4] = {x[0], y[0], x[1], y[1]}, f1[4] = {x[2], y[2], x[3], y[3]};
-                    mma<true>(s[k][n], f0, b[0], b[1]);
-                    mma<true>(s[k][n], f1, b[2], b[3]);
+                    mma<true>(s[k][n], f0, b[c][n][0], b[c][n][1]);
+                    mma<true>(s[k][n], f1, b[c][n][2], b[c][n][3]);
                 }
             }
         }
@@ -283,7 +283,7 @@ __device__ __forceinline__ void values_e2m1(float (&o)[DP / 16][NT][4], const ui
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const uint32_t v = w[2 * c + u], odd = (v ^ (v >> 12)) & 0x0000F0F0u;
-                e2m1_to_f16x2(v ^ odd ^ (odd << 12), x[u]);
+                e2m1_to_f16x2(v ^ odd * 4097u, x[u]);    // (odd ^ odd << 12, on the multiplier)
                 const uint32_t by = e4m3_to_f16x2(c == 0 ? sc[u] : sc[u] >> 16);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[u][e] = mul_f16x2(x[u][e], by);
@@ -507,6 +507,44 @@ attend_kernel(AttendArgs a) {
                 }
             }
         };
+        // A tile that is whole and in one block, of 4-bit elements (whose instructions count): from its first row on
+        const bool runs = C::E2 && a.split.slots.block.d % KT == 0 && sp.lo % KT == 0;
+        auto issue_run = [&](int32_t stage, int32_t t, int32_t id) {
+            constexpr int CPR = ROW / 16, RPI = 32 / CPR;
+            const uint32_t base = ring + (uint32_t)(stage * C::STAGE);
+            const int32_t j = sp.lo + t * KT, c = lane % CPR;
+            const int32_t in = j - (int32_t)(a.split.slots.block.div((uint32_t)j) * a.split.slots.block.d);
+            const int64_t first = id * a.k_plane.block_stride + in * a.k_plane.token_stride + head_off;
+            const uint32_t n = c * 32 < a.D ? 16 : 0;   // (0: nothing is read, wherever it points)
+            const int64_t at = first + (lane / CPR) * a.k_plane.token_stride + (n != 0 ? c * 16 : 0);
+            const int64_t step = RPI * a.k_plane.token_stride;
+            const unsigned char *k = a.k_plane.base + at, *v = a.v_plane.base + at;
+#pragma unroll
+            for (int i = 0; i < KT / RPI; ++i, k += step, v += step) {
+                const uint32_t dst = base + swizzled<ROW>(i * RPI + lane / CPR, c);
+                cp_async16<ROW >= 128>(dst, k, n);
+                cp_async16<ROW >= 128>(dst + KT * ROW, v, n);
+            }
+            constexpr int PIECE = DP == 128 ? 8 : 4;
+            const int64_t scale = (first + lane * a.k_plane.token_stride) / 8;
+#pragma unroll
+            for (int p = 0; p < C::SROW / PIECE; ++p) {
+                const bool there = p * PIECE * 16 < a.D;
+                const uint32_t dst = base + 2 * KT * ROW + lane * C::SROW + p * PIECE, n = there ? PIECE : 0;
+                cp_async_few<PIECE>(dst, a.k_block_scales + (there ? scale + p * PIECE : 0), n);
+                cp_async_few<PIECE>(dst + KT * C::SROW, a.v_block_scales + (there ? scale + p * PIECE : 0), n);
+            }
+        };
+        // (the block's id is the same in all lanes there)
+        auto issue_tile = [&](int32_t stage, int32_t t, int32_t id) {
+            if constexpr (C::E2) {
+                if (runs && sp.lo + (t + 1) * KT <= sp.n && id >= 0 && id < a.split.slots.num_blocks) {
+                    issue_run(stage, t, id);
+                    return;
+                }
+            }
+            issue(stage, slot_of(t, id));
+        };
         // the queries, one warp a row, asked for ahead of the keys
         constexpr int QW = RP / ATTEND_WARPS;
         uint4 qw[QW];
@@ -528,7 +566,7 @@ attend_kernel(AttendArgs a) {
 #pragma unroll
             for (int k = 0; k < C::STAGES - 1; ++k) {
                 const int32_t t = t_begin + k * ATTEND_WARPS;
-                if (t < t_end) issue(k, slot_of(t, ids[k]));
+                if (t < t_end) issue_tile(k, t, ids[k]);
                 cp_async_commit();
             }
             next_block = ids[C::STAGES - 1];
@@ -578,7 +616,7 @@ attend_kernel(AttendArgs a) {
             {
                 const int32_t tn = t + (C::STAGES - 1) * ATTEND_WARPS;
                 const int into = stage == 0 ? C::STAGES - 1 : stage - 1;
-                if (tn < t_end) issue(into, slot_of(tn, next_block));
+                if (tn < t_end) issue_tile(into, tn, next_block);
                 cp_async_commit();
                 next_block = block_of(tn + ATTEND_WARPS);
             }

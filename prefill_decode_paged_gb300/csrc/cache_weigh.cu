@@ -57,6 +57,8 @@ kvr_status kvc_weigh_launch(const kvc_cache *c, int32_t layer, const kvc_weigh *
     // an SM has 228 KB, of which each block takes 1 KB for itself
     const int64_t resident = std::min<int64_t>(k.blocks, (228 << 10) / (int64_t)(smem + 1024));
     const int64_t grid = std::min<int64_t>(resident * kvc_stream_sms(c, stream), all);
-    a.shape = make_cut_shape(p->num_requests, a.H, (int32_t)grid, 0);
-    return kvc_launch(k.kernel, a, dim3((unsigned)grid), ATTEND_THREADS, smem, stream);
+    a.by_heads = kvr_make_div((uint32_t)a.H);
+    a.parts = (int32_t)(k.abreast ? std::max<int64_t>(1, grid / a.H) : grid);
+    a.shape = make_cut_shape(p->num_requests, k.abreast ? 1 : a.H, a.parts, 0);
+    return kvc_launch(k.kernel, a, dim3((unsigned)(k.abreast ? a.parts * a.H : grid)), ATTEND_THREADS, smem, stream);
 }

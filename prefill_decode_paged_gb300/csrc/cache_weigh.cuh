@@ -7,7 +7,7 @@
 // written and read again, as many bytes as the keys of 4 bits themselves at 8 rows.)
 //
 // Split. The keys of all (request, head) jobs in units of 4 KT keys form one line, cut into equal parts, one a
-// resident block. Inside a block each of 4 warps takes every fourth tile of KT keys through a ring of its own,
+// resident block (4-bit pools: cut for one head, each part done by a block a head). Inside a block each of 4 warps takes every fourth tile of KT keys through a ring of its own,
 // as in attention. S^T = K Q^T by mma.sync m16n8k16, keys by rows; a lane holds 4 keys of 2 rows of every 8,
 // and three exchanges give each lane of four one key's sum, so that a warp writes 32 neighbours at once.
 // Scores, exponentials and sums are fp32.
@@ -28,7 +28,8 @@ struct WeighArgs {
     const unsigned char *k_block_scales;
     int32_t m, H, G, D, f16, width, add;
     int32_t chunks;           // passes over a job's keys, RP rows each
-    KvrDiv group;
+    int32_t parts;
+    KvrDiv group, by_heads;
     CutShape shape;
     float scale;
     Scoring scoring;
@@ -46,6 +47,8 @@ struct Weigh {
     static constexpr int STAGES = STAGE >= 8192 ? 3 : BLOCKS == 4 || STAGE > 4096 ? 5 : 6;
     static constexpr int RING = ATTEND_WARPS * STAGES * STAGE;
     static constexpr int UNIT = ATTEND_WARPS * KT;
+    // (as in attention: the block scales of a token's heads share a sector)
+    static constexpr bool ABREAST = E2;
     static constexpr int RP = 8 * NT;
     static constexpr int Q_BYTES = RP * DP * 2;
     // ring, queries, then floats: row scales, log-sum-exps [RP]; 4 ints; prefix
@@ -69,16 +72,19 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
     wait_for_previous();
     let_next_start();
     unit_prefix<C::UNIT>(a.split, 1, prefix, shared_int);
-    const int32_t total = prefix[a.split.requests] * a.H;
-    const int32_t each = total / (int32_t)gridDim.x, more = total - each * (int32_t)gridDim.x;
-    int32_t x = (int32_t)blockIdx.x * each + min((int32_t)blockIdx.x, more);
-    const int32_t x_end = x + each + ((int32_t)blockIdx.x < more ? 1 : 0);
+    // (abreast: one block a head goes through the same part of the requests' keys)
+    const int32_t parts = C::ABREAST ? a.parts : (int32_t)gridDim.x;
+    const int32_t part = C::ABREAST ? (int32_t)a.by_heads.div(blockIdx.x) : (int32_t)blockIdx.x;
+    const int32_t total = prefix[a.split.requests] * (C::ABREAST ? 1 : a.H);
+    const int32_t each = total / parts, more = total - each * parts;
+    int32_t x = part * each + min(part, more);
+    const int32_t x_end = x + each + (part < more ? 1 : 0);
     const int32_t M = a.m * a.G;
     const uint32_t ring = smem0 + (uint32_t)(warp * C::STAGES * C::STAGE);
 
     while (x < x_end) {
         const Segment seg = segment_at(x, x_end, prefix, a.shape);
-        const int32_t r = seg.r, h = seg.job;
+        const int32_t r = seg.r, h = C::ABREAST ? (int32_t)blockIdx.x - part * a.H : seg.job;
         x += seg.u1 - seg.u0;
         uint32_t bad = 0;
         const Span sp = span_of(a.split, r, 1, &bad);   // tiles begin at the first key
@@ -273,12 +279,13 @@ struct WeighPick {
     void (*kernel)(WeighArgs);
     size_t (*smem)(int32_t requests);
     int32_t unit, rp, blocks;
+    bool abreast;
 };
 
 template <int DP, int POOL, int NT>
 inline WeighPick weigh_instance() {
     using C = Weigh<DP, POOL, NT>;
-    return {weigh_kernel<DP, POOL, NT>, &C::smem, C::UNIT, C::RP, C::BLOCKS};
+    return {weigh_kernel<DP, POOL, NT>, &C::smem, C::UNIT, C::RP, C::BLOCKS, C::ABREAST};
 }
 
 // The instance for head dimension D and M rows a job: rows in passes of 8, 16 or 32.
