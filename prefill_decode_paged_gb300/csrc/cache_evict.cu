@@ -2,9 +2,11 @@
 //
 // Select. Of n tokens the `recent` newest stay, and of the others the `need` = keep - recent of the largest
 // weights: those above the need-th largest, T, and of those equal to it the lowest slots. A cluster of blocks has
-// a head; each block a contiguous share of its weights, held in shared memory. T comes digit by digit (11, 11 and
-// 10 bits of the weights as ordered integers): each block counts its weights that fit the digits so far, every
-// block adds all blocks' counts up and so finds the same digit, with one barrier of the cluster a digit. Then each
+// a head; each block a contiguous share of its weights, held in shared memory. T comes digit by digit (8
+// bits of the weights as ordered integers): each block counts its weights that fit the digits so far, every
+// block adds all blocks' counts up and so finds the same digit, with one barrier of the cluster a digit. (Digits of 11
+// bits are one barrier fewer, but eight times the counts to be read from the other blocks: 44 us where 8 bits
+// take 17, 16 heads of 32768 weights.) Then each
 // warp counts what stays of its share, and writes those slots where the shares before it end. A few
 // thousand weights are read once: barriers and shared memory bound it, not HBM.
 //
@@ -25,11 +27,13 @@ using namespace kvc;
 namespace cg = cooperative_groups;
 
 constexpr int SELECT_THREADS = 512, SELECT_WARPS = SELECT_THREADS / 32;
-constexpr int BINS = 2048;
-constexpr int HELD = 4096;         // weights that a block holds in shared memory; those beyond are read each time
-constexpr int MOVE_THREADS = 256;
+constexpr int BINS = 256;
+constexpr int MOST_BLOCKS = 8;     // of a cluster
+constexpr int SHARE = 2048;        // weights of a block, above which a head gets another, while there is room for it
+constexpr int HELD = 7168;         // weights that a block holds in shared memory; those beyond are read each time
+constexpr int COPY_THREADS = 128, MOVE_THREADS = 256;
 constexpr int UNITS = 8;           // 16-byte units of a thread at a time
-constexpr int WORDS = 9;           // words of a row besides: its weight, and block scales of 4-bit rows (2 D / 64)
+constexpr int WORDS = 9;           // words of a thread besides: a weight, and block scales of 4-bit rows
 
 struct EvictArgs {
     KvcSlots from, into;
@@ -44,7 +48,7 @@ struct EvictArgs {
     int32_t requests, H, width, keep, recent;
     int32_t rows;                  // of a round (or block)
     int32_t chunks;                // blocks of a head, into other blocks
-    int32_t words;                 // besides a row's units
+    int32_t step_rows, step_units; // what as many units as a block has threads are
     KvrDiv by_heads, by_chunks, by_units, by_words;
 };
 
@@ -64,14 +68,24 @@ __device__ __forceinline__ uint32_t ordered(float w) {
     return u >> 31 ? ~u : u | 0x80000000u;
 }
 
+// The sum of what the warps before this one have left in `scan`.
+__device__ __forceinline__ uint32_t before_warp(const uint32_t (*scan)[2], int which) {
+    static_assert(SELECT_WARPS <= 32, "");
+    const int lane = threadIdx.x % 32;
+    return __reduce_add_sync(~0u, lane < (int)threadIdx.x / 32 ? scan[lane][which] : 0u);
+}
+
+template <int BLOCKS>
 __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(EvictArgs a) {
     __shared__ uint32_t held[HELD];
-    __shared__ uint32_t hist[2][BINS];
+    __shared__ __align__(16) uint32_t hist[2][BINS];
     __shared__ uint32_t scan[SELECT_WARPS][2];
-    __shared__ uint32_t found[2], own[2];
+    __shared__ uint32_t found[3];
+    __shared__ __align__(8) uint32_t own[2];
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int32_t blocks = (int32_t)cluster.num_blocks(), part = (int32_t)cluster.block_rank();
+    constexpr int blocks = BLOCKS;
+    const int32_t part = BLOCKS > 1 ? (int32_t)cluster.block_rank() : 0;
     const int32_t head = (int32_t)blockIdx.x / blocks;
     const int32_t r = (int32_t)a.by_heads.div((uint32_t)head), h = head - r * a.H;
     wait_for_previous();
@@ -86,44 +100,52 @@ __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(EvictArgs a) {
         return;
     }
     const int32_t old = n - a.recent, need = a.keep - a.recent;
-    for (int32_t i = part * SELECT_THREADS + tid; i < a.recent; i += blocks * SELECT_THREADS)
-        kept[need + i] = old + i;
-    if (need == 0) return;
+    // (written last: a barrier of the cluster waits for stores before it)
+    auto newest = [&] {
+        for (int32_t i = part * SELECT_THREADS + tid; i < a.recent; i += blocks * SELECT_THREADS)
+            kept[need + i] = old + i;
+    };
+    if (need == 0) {
+        newest();
+        return;
+    }
 
     const float *weights = a.weights + r * a.w_request + h * a.w_head;
     const int32_t share = (old + blocks - 1) / blocks;
     const int32_t j0 = min(old, part * share), size = min(old, j0 + share) - j0;
     auto key = [&](int32_t i) -> uint32_t { return i < HELD ? held[i] : ordered(weights[j0 + i]); };
-    for (int i = tid; i < BINS; i += SELECT_THREADS) hist[0][i] = 0;
+    if (tid < BINS) hist[0][tid] = 0;
     for (int32_t i = tid; i < min(size, HELD); i += SELECT_THREADS) held[i] = ordered(weights[j0 + i]);
 
     uint32_t known = 0, mask = 0;        // T's digits so far, and which bits they are
     uint32_t left = (uint32_t)need;      // of the weights that fit them, how many stay
 #pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
         uint32_t *count = hist[pass & 1];
         __syncthreads();
         for (int32_t i = tid; i < size; i += SELECT_THREADS) {
             const uint32_t k = key(i);
-            if ((k & mask) == known) atomicAdd(count + (k >> shift & (uint32_t)(bins - 1)), 1u);
+            if ((k & mask) == known) atomicAdd(count + (k >> shift & 255u), 1u);
         }
-        cluster.sync();
+        if (BLOCKS > 1)
+            cluster.sync();
+        else
+            __syncthreads();
         // (what the others read last of the other array, they read before this barrier)
-        for (int i = tid; i < BINS; i += SELECT_THREADS) hist[pass & 1 ^ 1][i] = 0;
-        // a thread's bins, from the top down: their counts over all blocks
-        constexpr int PER = BINS / SELECT_THREADS;
-        uint32_t c[PER], sum = 0;
-        const int first = BINS - PER * (tid + 1);          // lowest of its bins
+        if (tid < BINS) hist[pass & 1 ^ 1][tid] = 0;
+        // a thread's bin, from the top down: its count over all blocks
+        static_assert(SELECT_THREADS >= BINS, "");
+        const int bin = BINS - 1 - tid;
+        uint32_t sum = 0;
+        if (tid < BINS) {
+            uint32_t theirs[BLOCKS];                       // (all asked for before the first is used)
 #pragma unroll
-        for (int e = 0; e < PER; ++e) c[e] = 0;
-        for (int32_t b = 0; b < blocks; ++b) {
-            const uint4 v = *(const uint4 *)(cluster.map_shared_rank(count, b) + first);
-            c[0] += v.x, c[1] += v.y, c[2] += v.z, c[3] += v.w;
+            for (int b = 0; b < BLOCKS; ++b)
+                theirs[b] = (BLOCKS > 1 ? cluster.map_shared_rank(count, b) : count)[bin];
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) sum += theirs[b];
         }
-        static_assert(PER == 4, "");
-#pragma unroll
-        for (int e = 0; e < PER; ++e) sum += c[e];
         uint32_t incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
@@ -132,22 +154,17 @@ __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(EvictArgs a) {
         }
         if (lane == 31) scan[warp][0] = incl;
         __syncthreads();
-        uint32_t above = incl - sum;
-        for (int w = 0; w < warp; ++w) above += scan[w][0];
-        if (above < left && left <= above + sum) {
-#pragma unroll
-            for (int e = PER - 1; e >= 0; --e) {
-                if (above < left && left <= above + c[e]) {
-                    found[0] = (uint32_t)(first + e);
-                    found[1] = left - above;
-                }
-                above += c[e];
-            }
+        const uint32_t above = incl - sum + before_warp(scan, 0);
+        if (tid < BINS && above < left && left <= above + sum) {
+            found[0] = (uint32_t)bin;
+            found[1] = left - above;
+            found[2] = sum;
         }
         __syncthreads();
         known |= found[0] << shift;
-        mask |= (uint32_t)(bins - 1) << shift;
+        mask |= 255u << shift;
         left = found[1];
+        if (left == found[2]) break;     // all that fit stay, whatever follows (the same in every block)
     }
 
     // a warp's share of the block's: how many are above T, and how many equal it
@@ -155,7 +172,7 @@ __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(EvictArgs a) {
     const int32_t i0 = min(size, warp * run), i1 = min(size, i0 + run);
     uint32_t above = 0, same = 0;
     for (int32_t i = i0 + lane; i < i1; i += 32) {
-        const uint32_t k = key(i);
+        const uint32_t k = key(i) & mask;
         above += k > known;
         same += k == known;
     }
@@ -166,21 +183,24 @@ __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(EvictArgs a) {
     }
     if (lane == 0) scan[warp][0] = above, scan[warp][1] = same;
     __syncthreads();
-    if (tid < 2) {
-        uint32_t t = 0;
-        for (int w = 0; w < SELECT_WARPS; ++w) t += scan[w][tid];
-        own[tid] = t;
-    }
-    cluster.sync();
     above = same = 0;
-    for (int32_t b = 0; b < part; ++b) {
-        const uint32_t *o = cluster.map_shared_rank(own, b);
-        above += o[0];
-        same += o[1];
+    if (BLOCKS > 1) {
+        if (warp < 2) {
+            const uint32_t t = __reduce_add_sync(~0u, lane < SELECT_WARPS ? scan[lane][warp] : 0u);
+            if (lane == 0) own[warp] = t;
+        }
+        cluster.sync();
+#pragma unroll
+        for (int b = 0; b < BLOCKS - 1; ++b)
+            if (b < part) {
+                const uint2 o = *(const uint2 *)cluster.map_shared_rank(own, b);
+                above += o.x, same += o.y;
+            }
+        cluster.barrier_arrive();        // no block leaves while others read its counts
     }
-    for (int w = 0; w < warp; ++w) above += scan[w][0], same += scan[w][1];
+    above += before_warp(scan, 0), same += before_warp(scan, 1);
     for (int32_t i = i0; i < i1; i += 32) {
-        const uint32_t k = i + lane < i1 ? key(i + lane) : 0u;
+        const uint32_t k = i + lane < i1 ? key(i + lane) & mask : 0u;
         const bool gt = i + lane < i1 && k > known, eq = i + lane < i1 && k == known;
         const uint32_t gts = __ballot_sync(~0u, gt), eqs = __ballot_sync(~0u, eq);
         const uint32_t before = (1u << lane) - 1u;
@@ -189,7 +209,8 @@ __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(EvictArgs a) {
         above += __popc(gts);
         same += __popc(eqs);
     }
-    cluster.sync();                      // no block leaves while others read its counts
+    newest();
+    if (BLOCKS > 1) cluster.barrier_wait();
 }
 
 // Where slot j of request r is in a plane, in bytes; -1: nowhere.
@@ -209,119 +230,99 @@ __device__ __forceinline__ int64_t offset_of(const EvictArgs &a, const KvcSlots 
     return id * a.k_plane.block_stride + in * a.k_plane.token_stride + h * a.k_plane.head_stride;
 }
 
-// A round's rows: from where and to where (equal: nothing to move), and their weights' places.
+// A round's rows: from where (-1: nothing to move) and to where, and the slots that they had.
+template <int THREADS>
 struct Round {
-    int64_t from[MOVE_THREADS], to[MOVE_THREADS];
-    int32_t slot[MOVE_THREADS];
+    int64_t from[THREADS], to[THREADS];
+    int32_t slot[THREADS];
 };
 
 // What a thread holds of a round.
+template <bool FOUR>
 struct Held {
     uint4 unit[UNITS];
-    uint32_t word[WORDS];
+    uint32_t word[FOUR ? WORDS : 1];
 };
 
-template <bool FOUR>
+// A round's rows between memory and the threads' registers.
+template <int THREADS, bool FOUR>
 struct Mover {
     const EvictArgs &a;
-    const Round &rd;
+    const Round<THREADS> &rd;
     const float *weights;
     float *weights_out;
     int32_t i0, count;                   // the round's first row, and how many it has
 
-    // 16-byte unit `u` of the round: its row, and its offset there (both planes of it)
-    __device__ __forceinline__ void unit(int32_t u, int32_t *row, int32_t *off, bool *value) const {
-        *row = (int32_t)a.by_units.div((uint32_t)u);
-        const int32_t c = u - *row * (int32_t)a.by_units.d, half = (int32_t)a.by_units.d / 2;
-        *value = c >= half;
-        *off = 16 * (c - (*value ? half : 0));
-    }
-    // word `u`: of the weight (0), or of the block scales
-    __device__ __forceinline__ void word(int32_t u, int32_t *row, int32_t *c) const {
-        *row = FOUR ? (int32_t)a.by_words.div((uint32_t)u) : u;
-        *c = u - *row * a.words;
-    }
-    __device__ __forceinline__ unsigned char *scales(int32_t c, int64_t at) const {
-        const int32_t half = (a.words - 1) / 2;
-        return c <= half ? a.k_block_scales + at / 8 + 4 * (c - 1)
-                         : a.v_block_scales + at / 8 + 4 * (c - 1 - half);
-    }
-    __device__ __forceinline__ void load(Held &x) const {
-        const int32_t units = count * (int32_t)a.by_units.d;
+    // Each of the thread's 16-byte units: f(e, row, plane, offset in the row). A row's units are its key's, then
+    // its value's; a thread's are THREADS apart.
+    template <typename F>
+    __device__ __forceinline__ void units(F f) const {
+        const int32_t of_row = (int32_t)a.by_units.d, half = of_row / 2;
+        int32_t row = (int32_t)a.by_units.div(threadIdx.x), c = (int32_t)threadIdx.x - row * of_row;
 #pragma unroll
         for (int e = 0; e < UNITS; ++e) {
-            const int32_t u = e * MOVE_THREADS + (int32_t)threadIdx.x;
-            if (u < units) {
-                int32_t row, off;
-                bool value;
-                unit(u, &row, &off, &value);
+            if (row < count) {
+                const bool value = c >= half;
+                f(e, row, (value ? a.v_plane : a.k_plane).base, 16 * (c - (value ? half : 0)));
+            }
+            row += a.step_rows, c += a.step_units;
+            if (c >= of_row) c -= of_row, ++row;
+        }
+    }
+    // The same of its words of block scales: f(e, row, plane, offset in the row's).
+    template <typename F>
+    __device__ __forceinline__ void words(F f) const {
+#pragma unroll
+        for (int e = 0; e < WORDS - 1; ++e) {
+            const int32_t u = e * THREADS + (int32_t)threadIdx.x, row = (int32_t)a.by_words.div((uint32_t)u);
+            const int32_t c = u - row * (int32_t)a.by_words.d, half = (int32_t)a.by_words.d / 2;
+            if (row < count) f(e, row, c >= half ? a.v_block_scales : a.k_block_scales, 4 * (c >= half ? c - half : c));
+        }
+    }
+    __device__ __forceinline__ void load(Held<FOUR> &x) const {
+        units([&](int e, int32_t row, const unsigned char *plane, int32_t off) {
+            const int64_t from = rd.from[row];
+            if (from >= 0) x.unit[e] = *(const uint4 *)(plane + from + off);
+        });
+        if ((int32_t)threadIdx.x < count) x.word[0] = __float_as_uint(weights[rd.slot[threadIdx.x]]);
+        if constexpr (FOUR)
+            words([&](int e, int32_t row, const unsigned char *plane, int32_t off) {
                 const int64_t from = rd.from[row];
-                if (from >= 0 && rd.to[row] >= 0)
-                    x.unit[e] = *(const uint4 *)((value ? a.v_plane : a.k_plane).base + from + off);
-            }
-        }
-        const int32_t words = count * (FOUR ? a.words : 1);
-#pragma unroll
-        for (int e = 0; e < (FOUR ? WORDS : 1); ++e) {
-            const int32_t u = e * MOVE_THREADS + (int32_t)threadIdx.x;
-            if (u < words) {
-                int32_t row, c;
-                word(u, &row, &c);
-                if (!FOUR || c == 0)
-                    x.word[e] = __float_as_uint(weights[rd.slot[row]]);
-                else if (rd.from[row] >= 0 && rd.to[row] >= 0)
-                    x.word[e] = *(const uint32_t *)scales(c, rd.from[row]);
-            }
-        }
+                if (from >= 0) x.word[1 + e] = *(const uint32_t *)(plane + from / 8 + off);
+            });
     }
-    __device__ __forceinline__ void store(const Held &x) const {
-        const int32_t units = count * (int32_t)a.by_units.d;
-#pragma unroll
-        for (int e = 0; e < UNITS; ++e) {
-            const int32_t u = e * MOVE_THREADS + (int32_t)threadIdx.x;
-            if (u < units) {
-                int32_t row, off;
-                bool value;
-                unit(u, &row, &off, &value);
-                const int64_t to = rd.to[row];
-                if (to >= 0 && rd.from[row] >= 0)
-                    *(uint4 *)((value ? a.v_plane : a.k_plane).base + to + off) = x.unit[e];
-            }
-        }
-        const int32_t words = count * (FOUR ? a.words : 1);
-#pragma unroll
-        for (int e = 0; e < (FOUR ? WORDS : 1); ++e) {
-            const int32_t u = e * MOVE_THREADS + (int32_t)threadIdx.x;
-            if (u < words) {
-                int32_t row, c;
-                word(u, &row, &c);
-                if (!FOUR || c == 0)
-                    weights_out[i0 + row] = __uint_as_float(x.word[e]);
-                else if (rd.to[row] >= 0 && rd.from[row] >= 0)
-                    *(uint32_t *)scales(c, rd.to[row]) = x.word[e];
-            }
-        }
+    __device__ __forceinline__ void store(const Held<FOUR> &x) const {
+        units([&](int e, int32_t row, unsigned char *plane, int32_t off) {
+            if (rd.from[row] >= 0) *(uint4 *)(plane + rd.to[row] + off) = x.unit[e];
+        });
+        if ((int32_t)threadIdx.x < count) weights_out[i0 + threadIdx.x] = __uint_as_float(x.word[0]);
+        if constexpr (FOUR)
+            words([&](int e, int32_t row, unsigned char *plane, int32_t off) {
+                if (rd.from[row] >= 0) *(uint32_t *)(plane + rd.to[row] / 8 + off) = x.word[1 + e];
+            });
     }
 };
 
 // Rows [i0, i0 + count) of the kept: their places. By all threads; a barrier has to follow.
-__device__ __forceinline__ void place_rows(const EvictArgs &a, Round &rd, const int32_t *kept, int32_t r, int32_t h,
-                                           int32_t i0, int32_t count, uint32_t *bad) {
+template <int THREADS>
+__device__ __forceinline__ void place_rows(const EvictArgs &a, Round<THREADS> &rd, const int32_t *kept, int32_t r,
+                                           int32_t h, int32_t i0, int32_t count, uint32_t *bad) {
     if ((int32_t)threadIdx.x < count) {
         const int32_t j = kept[i0 + threadIdx.x];
         const int64_t from = offset_of(a, a.from, r, h, j, bad);
         const int64_t to = offset_of(a, a.into, r, h, i0 + (int32_t)threadIdx.x, bad);
         // (a row that is where it goes stays there)
-        rd.from[threadIdx.x] = from == to ? -1 : from;
+        rd.from[threadIdx.x] = from == to || to < 0 ? -1 : from;
         rd.to[threadIdx.x] = to;
         rd.slot[threadIdx.x] = j;
     }
 }
 
-// Into other blocks.
+// Into other blocks. Small blocks, many on an SM: each begins with a chain of waits (length, kept slots, block
+// ids, rows), which the others' rows cover.
 template <bool FOUR>
-__global__ void __launch_bounds__(MOVE_THREADS, 4) copy_kernel(EvictArgs a) {
-    __shared__ Round rd;
+__global__ void __launch_bounds__(COPY_THREADS, 8) copy_kernel(EvictArgs a) {
+    __shared__ Round<COPY_THREADS> rd;
     const int32_t head = (int32_t)a.by_chunks.div(blockIdx.x), chunk = (int32_t)blockIdx.x - head * a.chunks;
     const int32_t r = (int32_t)a.by_heads.div((uint32_t)head), h = head - r * a.H;
     wait_for_previous();
@@ -330,15 +331,15 @@ __global__ void __launch_bounds__(MOVE_THREADS, 4) copy_kernel(EvictArgs a) {
     const int32_t n = tokens_of(a, r, &bad), total = min(n, a.keep);
     bad = 0;                             // (told by the kernel before)
     float *out = a.weights_out + r * a.out_request + h * a.out_head;
-    for (int32_t j = total + chunk * MOVE_THREADS + (int32_t)threadIdx.x; j < n; j += a.chunks * MOVE_THREADS)
+    for (int32_t j = total + chunk * COPY_THREADS + (int32_t)threadIdx.x; j < n; j += a.chunks * COPY_THREADS)
         out[j] = 0.0f;
     const int32_t i0 = chunk * a.rows, count = min(a.rows, total - i0);
     if (count <= 0) return;
     place_rows(a, rd, a.kept + (int64_t)head * a.keep, r, h, i0, count, &bad);
     if (bad != 0) atomicOr(a.flags, bad);
     __syncthreads();
-    const Mover<FOUR> mv = {a, rd, a.weights + r * a.w_request + h * a.w_head, out, i0, count};
-    Held x;
+    const Mover<COPY_THREADS, FOUR> mv = {a, rd, a.weights + r * a.w_request + h * a.w_head, out, i0, count};
+    Held<FOUR> x;
     mv.load(x);
     mv.store(x);
 }
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(MOVE_THREADS, 4) copy_kernel(EvictArgs a) {
 // In place.
 template <bool FOUR>
 __global__ void __launch_bounds__(MOVE_THREADS, 2) gather_kernel(EvictArgs a) {
-    __shared__ Round rounds[2];
+    __shared__ Round<MOVE_THREADS> rounds[2];
     cg::cluster_group cluster = cg::this_cluster();
     const int32_t blocks = (int32_t)cluster.num_blocks(), part = (int32_t)cluster.block_rank();
     const int32_t head = (int32_t)blockIdx.x / blocks;
@@ -361,24 +362,24 @@ __global__ void __launch_bounds__(MOVE_THREADS, 2) gather_kernel(EvictArgs a) {
     float *out = a.weights_out + r * a.out_request + h * a.out_head;
     const int32_t step = blocks * a.rows, count_of = (total + step - 1) / step;
     auto rows_of = [&](int32_t k) { return max(0, min(a.rows, total - (k * step + part * a.rows))); };
-    Held x;
+    Held<FOUR> x;
     if (count_of > 0) {
         place_rows(a, rounds[0], kept, r, h, part * a.rows, rows_of(0), &bad);
         __syncthreads();
-        const Mover<FOUR> mv = {a, rounds[0], weights, out, part * a.rows, rows_of(0)};
+        const Mover<MOVE_THREADS, FOUR> mv = {a, rounds[0], weights, out, part * a.rows, rows_of(0)};
         mv.load(x);
     }
     for (int32_t k = 0; k < count_of; ++k) {
         const int32_t i0 = k * step + part * a.rows;
-        Held next;
+        Held<FOUR> next;
         if (k + 1 < count_of) {
             place_rows(a, rounds[(k + 1) & 1], kept, r, h, i0 + step, rows_of(k + 1), &bad);
             __syncthreads();
-            const Mover<FOUR> mv = {a, rounds[(k + 1) & 1], weights, out, i0 + step, rows_of(k + 1)};
+            const Mover<MOVE_THREADS, FOUR> mv = {a, rounds[(k + 1) & 1], weights, out, i0 + step, rows_of(k + 1)};
             mv.load(next);
         }
         cluster.sync();                  // all of this round's rows are held
-        const Mover<FOUR> mv = {a, rounds[k & 1], weights, out, i0, rows_of(k)};
+        const Mover<MOVE_THREADS, FOUR> mv = {a, rounds[k & 1], weights, out, i0, rows_of(k)};
         mv.store(x);
         __syncthreads();
         x = next;
@@ -411,31 +412,38 @@ kvr_status kvc_evict_launch(const kvc_cache *c, int32_t layer, const kvc_evict *
     a.out_request = p->out_request_stride, a.out_head = p->out_head_stride;
     a.requests = p->num_requests, a.H = H, a.width = p->weights_width;
     a.keep = p->keep, a.recent = p->recent;
-    const int32_t units = (int32_t)(2 * c->row_bytes / 16);
-    a.words = four ? 1 + 2 * (c->d.head_dim / 64) : 1;
-    a.rows = std::max(1, std::min(MOVE_THREADS, UNITS * MOVE_THREADS / units));
+    const bool apart = other && p->weights_out != p->weights;
+    const int32_t units = (int32_t)(2 * c->row_bytes / 16), threads = apart ? COPY_THREADS : MOVE_THREADS;
+    // (block scales: 2 D / 64 words a row, as many as its units or fewer)
+    a.rows = std::max(1, std::min(threads, UNITS * threads / units));
+    a.step_rows = threads / units;
+    a.step_units = threads % units;
     a.by_heads = kvr_make_div((uint32_t)H);
     a.by_units = kvr_make_div((uint32_t)units);
-    a.by_words = kvr_make_div((uint32_t)a.words);
+    a.by_words = kvr_make_div((uint32_t)std::max(1, 2 * (c->d.head_dim / 64)));
     const int64_t heads = (int64_t)p->num_requests * H;
     const int32_t sms = kvc_stream_sms(c, stream);
     const int64_t longest = std::min<int64_t>(p->weights_width, (int64_t)p->table.width * c->d.block_size);
     // blocks of a cluster: as many as keep the SMs busy and have something to do
-    auto cluster_of = [&](int64_t each) {
+    auto cluster_of = [&](int64_t each, int64_t resident) {
         int32_t blocks = 1;
-        while (blocks < 8 && heads * blocks * 2 <= 2 * (int64_t)sms && (longest + blocks - 1) / blocks > each) blocks *= 2;
+        while (blocks < MOST_BLOCKS && heads * blocks * 2 <= resident * sms && (longest + blocks - 1) / blocks > each)
+            blocks *= 2;
         return blocks;
     };
-    const int32_t choose = cluster_of(2048);
+    const int32_t choose = cluster_of(SHARE, 4);
     a.chunks = (int32_t)std::max<int64_t>(1, (std::min<int64_t>(longest, p->keep) + a.rows - 1) / a.rows);
     a.by_chunks = kvr_make_div((uint32_t)a.chunks);
     if (heads * 8 > INT32_MAX || heads * a.chunks > INT32_MAX) return KVR_ERR_UNSUPPORTED;
-    kvr_status st = kvc_launch(select_kernel, a, dim3((unsigned)(heads * choose)), SELECT_THREADS, 0, stream, choose);
+    const auto select = choose == 1   ? select_kernel<1>
+                        : choose == 2 ? select_kernel<2>
+                        : choose == 4 ? select_kernel<4> : select_kernel<8>;
+    kvr_status st = kvc_launch(select, a, dim3((unsigned)(heads * choose)), SELECT_THREADS, 0, stream, choose);
     if (st != KVR_OK) return st;
-    if (other && p->weights_out != p->weights)
+    if (apart)
         return kvc_launch(four ? copy_kernel<true> : copy_kernel<false>, a, dim3((unsigned)(heads * a.chunks)),
-                          MOVE_THREADS, 0, stream);
-    const int32_t blocks = cluster_of(a.rows);
+                          COPY_THREADS, 0, stream);
+    const int32_t blocks = cluster_of(a.rows, 2);
     return kvc_launch(four ? gather_kernel<true> : gather_kernel<false>, a, dim3((unsigned)(heads * blocks)),
                       MOVE_THREADS, 0, stream, blocks);
 }
