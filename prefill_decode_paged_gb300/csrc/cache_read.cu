@@ -2,7 +2,7 @@
 //
 // The inverse of append, for what works on contiguous rows: attention of a new prompt over a cached prefix, or a
 // cache that moves to another type of pool. 16-bit pools are copied, codes become code * block scale * s, exact up
-// to the product with s, which is fp32 and rounded once. One block does one token; a thread takes 16 elements
+// to the product with s, which is fp32 and rounded once. A thread takes 16 elements of each of a block's tokens
 // at a time. Bound by HBM with many tokens (a 4-bit row is 0.56 bytes read for 2 written an element), by the
 // launch and then position, block id and row, one after another, with few.
 #include "cache.h"
@@ -20,91 +20,147 @@ struct ReadArgs {
     KvcSlots slots;
     const float *k_scale, *v_scale;
     uint32_t *flags;
-    int32_t H, comps;
+    int32_t H, tokens;
     KvrDiv units;             // of 16 elements, of a row
 };
 
 constexpr int MOST_THREADS = 256;
 
-template <int POOL, bool F16>
-__global__ void __launch_bounds__(MOST_THREADS) read_kernel(ReadArgs a) {
-    wait_for_previous();
-    let_next_start();
-    const int64_t token = blockIdx.x;
-    const int32_t pos = __ldg(a.positions + token), req = __ldg(a.requests + token);
-    int64_t slot = -1;                       // the token's slot in a plane, in bytes; -1: zeros
-    if (pos >= 0) {
-        const uint32_t entry = a.slots.block.div((uint32_t)pos);
-        uint32_t bad = 0;
-        if (req < 0 || req >= a.slots.rows) {
-            bad = KVC_FLAG_REQUEST;
-        } else if (entry >= (uint32_t)a.slots.width) {
-            bad = KVC_FLAG_POSITION;
-        } else {
-            const int32_t id = __ldg(a.slots.ids + (int64_t)req * a.slots.stride + entry);
-            const int32_t off = pos - (int32_t)(entry * a.slots.block.d);
-            if (id < 0 || id >= a.slots.num_blocks)
-                bad = KVC_FLAG_BLOCK;
-            else
-                slot = id * a.k_plane.block_stride + off * a.k_plane.token_stride;
-        }
-        if (bad != 0 && threadIdx.x == 0) atomicOr(a.flags, bad);
+// Where a token's rows begin in a plane, in bytes; -1: nowhere.
+__device__ __forceinline__ int64_t slot_of(const ReadArgs &a, int32_t pos, int32_t req, uint32_t *bad) {
+    if (pos < 0) return -1;
+    const uint32_t entry = a.slots.block.div((uint32_t)pos);
+    if (req < 0 || req >= a.slots.rows) {
+        *bad |= KVC_FLAG_REQUEST;
+        return -1;
     }
-    const int32_t n = a.comps * a.H * (int32_t)a.units.d;
-    for (int32_t t = threadIdx.x; t < n; t += blockDim.x) {
-        int32_t row = (int32_t)a.units.div((uint32_t)t);
-        const int32_t j = t - row * (int32_t)a.units.d;
-        const bool value = row >= a.H;
-        if (value) row -= a.H;
-        const unsigned char *base = (value ? a.v_plane : a.k_plane).base;
-        const int64_t at = slot + row * a.k_plane.head_stride;
-        unsigned char *to = (value ? a.v + token * a.v_token + row * a.v_head
-                                   : a.k + token * a.k_token + row * a.k_head) + 32 * j;
+    if (entry >= (uint32_t)a.slots.width) {
+        *bad |= KVC_FLAG_POSITION;
+        return -1;
+    }
+    const int32_t id = __ldg(a.slots.ids + (int64_t)req * a.slots.stride + entry);
+    const int32_t off = pos - (int32_t)(entry * a.slots.block.d);
+    if (id < 0 || id >= a.slots.num_blocks) {
+        *bad |= KVC_FLAG_BLOCK;
+        return -1;
+    }
+    return id * a.k_plane.block_stride + off * a.k_plane.token_stride;
+}
+
+// 16 elements of a pool as they lie there, and as 16-bit numbers.
+template <int POOL>
+struct Raw {
+    uint4 w[POOL == KVR_DTYPE_FP8_E4M3 || POOL == KVC_DTYPE_E2M1 ? 1 : 2];
+    uint32_t scale;
+
+    __device__ __forceinline__ void load(const unsigned char *row, const unsigned char *scales, int32_t j) {
+        if constexpr (POOL == KVC_DTYPE_E2M1) {
+            const uint2 c = __ldg((const uint2 *)(row + 8 * j));
+            w[0].x = c.x, w[0].y = c.y;
+            scale = __ldg(scales + j);
+        } else if constexpr (POOL == KVR_DTYPE_FP8_E4M3) {
+            w[0] = __ldg((const uint4 *)(row + 16 * j));
+        } else {
+            w[0] = __ldg((const uint4 *)(row + 32 * j));
+            w[1] = __ldg((const uint4 *)(row + 32 * j) + 1);
+        }
+    }
+    // `s`: the plane's scale
+    template <bool F16>
+    __device__ __forceinline__ void store(unsigned char *to, float s, bool some) const {
         uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if (slot >= 0) {
-            if constexpr (POOL == KVR_DTYPE_FP8_E4M3 || POOL == KVC_DTYPE_E2M1) {
-                const float s = __ldg((value ? a.v_scale : a.k_scale) + row);
-                uint32_t h[8], *o = (uint32_t *)out;
-                float by = s;
-                if constexpr (POOL == KVC_DTYPE_E2M1) {
-                    const uint2 w = __ldg((const uint2 *)(base + at + 8 * j));
-                    const uint32_t b = __ldg((value ? a.v_block_scales : a.k_block_scales) + at / 8 + j);
-                    e2m1_to_f16x2(w.x, h);
-                    e2m1_to_f16x2(w.y, h + 4);
-                    const float scale = widen2<true>(e4m3_to_f16x2(b)).x;
+        uint32_t *o = (uint32_t *)out;
+        if (!some) {
+        } else if constexpr (POOL == KVC_DTYPE_E2M1) {
+            uint32_t h[8];
+            e2m1_to_f16x2(w[0].x, h);
+            e2m1_to_f16x2(w[0].y, h + 4);
+            const float by = widen2<true>(e4m3_to_f16x2(scale)).x;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 f = widen2<true>(h[i]);
-                        o[i] = narrow2<F16>(f.x * scale * by, f.y * scale * by);
-                    }
-                } else {
-                    const uint4 w = __ldg((const uint4 *)(base + at + 16 * j));
-                    const uint32_t c[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 f = widen2<true>(e4m3_to_f16x2(i % 2 == 0 ? c[i / 2] : c[i / 2] >> 16));
-                        o[i] = narrow2<F16>(f.x * by, f.y * by);
-                    }
-                }
-            } else {
-                out[0] = __ldg((const uint4 *)(base + at + 32 * j));
-                out[1] = __ldg((const uint4 *)(base + at + 32 * j) + 1);
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = widen2<true>(h[i]);
+                o[i] = narrow2<F16>(f.x * by * s, f.y * by * s);
             }
+        } else if constexpr (POOL == KVR_DTYPE_FP8_E4M3) {
+            const uint32_t c[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = widen2<true>(e4m3_to_f16x2(i % 2 == 0 ? c[i / 2] : c[i / 2] >> 16));
+                o[i] = narrow2<F16>(f.x * s, f.y * s);
+            }
+        } else {
+            out[0] = w[0], out[1] = w[1];
         }
         *(uint4 *)to = out[0];
         *(uint4 *)(to + 16) = out[1];
     }
+};
+
+template <int POOL, bool F16, int TOKENS>
+__global__ void __launch_bounds__(MOST_THREADS) read_kernel(ReadArgs a) {
+    constexpr bool CODES = POOL == KVR_DTYPE_FP8_E4M3 || POOL == KVC_DTYPE_E2M1;
+    wait_for_previous();
+    let_next_start();
+    const int64_t first = (int64_t)blockIdx.x * TOKENS;
+    int32_t pos[TOKENS], req[TOKENS];
+#pragma unroll
+    for (int k = 0; k < TOKENS; ++k) {
+        const bool some = first + k < a.tokens;
+        pos[k] = some ? __ldg(a.positions + first + k) : -1;
+        req[k] = some ? __ldg(a.requests + first + k) : 0;
+    }
+    int64_t slot[TOKENS];                    // -1: zeros
+    uint32_t bad = 0;
+#pragma unroll
+    for (int k = 0; k < TOKENS; ++k) slot[k] = slot_of(a, pos[k], req[k], &bad);
+    if (bad != 0 && threadIdx.x == 0) atomicOr(a.flags, bad);
+    const int32_t n = a.H * (int32_t)a.units.d;
+    // (a key's unit and its value's by one thread: the same offsets)
+    for (int32_t t = threadIdx.x; t < n; t += blockDim.x) {
+        const int32_t row = (int32_t)a.units.div((uint32_t)t), j = t - row * (int32_t)a.units.d;
+        const int64_t head = row * a.k_plane.head_stride;
+        const bool values = a.v != nullptr;
+        Raw<POOL> key[TOKENS], value[TOKENS];
+#pragma unroll
+        for (int k = 0; k < TOKENS; ++k) {
+            const int64_t at = slot[k] + head;
+            if (slot[k] >= 0) key[k].load(a.k_plane.base + at, a.k_block_scales + at / 8, j);
+            if (slot[k] >= 0 && values) value[k].load(a.v_plane.base + at, a.v_block_scales + at / 8, j);
+        }
+        const float ks = CODES ? __ldg(a.k_scale + row) : 1.0f;
+        const float vs = CODES && values ? __ldg(a.v_scale + row) : 1.0f;
+        unsigned char *k_to = a.k + first * a.k_token + row * a.k_head + 32 * j;
+        unsigned char *v_to = a.v + first * a.v_token + row * a.v_head + 32 * j;
+#pragma unroll
+        for (int k = 0; k < TOKENS; ++k) {
+            if (first + k >= a.tokens) break;
+            key[k].template store<F16>(k_to, ks, slot[k] >= 0);
+            if (values) value[k].template store<F16>(v_to, vs, slot[k] >= 0);
+            k_to += a.k_token, v_to += a.v_token;
+        }
+    }
+}
+
+// Few tokens: a block each. Many: two to a block, so that their chains of waits go side by side (41931
+// tokens of 16 rows of 4 bits 40 us; four 44, one 52).
+template <int POOL, bool F16>
+kvr_status go(ReadArgs &a, int sms, void *stream) {
+    const int64_t n = (int64_t)a.H * a.units.d, rounds = (n + MOST_THREADS - 1) / MOST_THREADS;
+    const int threads = (int)((n + 32 * rounds - 1) / (32 * rounds)) * 32;
+    if (a.tokens > 16 * sms)
+        return kvc_launch(read_kernel<POOL, F16, 2>, a, dim3((unsigned)((a.tokens + 1) / 2)), threads, 0, stream);
+    return kvc_launch(read_kernel<POOL, F16, 1>, a, dim3((unsigned)a.tokens), threads, 0, stream);
 }
 
 }  // namespace
 
 kvr_status kvc_read_launch(const kvc_cache *c, int32_t layer, const kvc_read *p, void *stream) {
     ReadArgs a = {};
-    a.comps = c->d.num_components, a.H = c->d.kv_heads;
+    a.H = c->d.kv_heads;
     a.k_plane = c->plane(layer, 0);
     a.k_scale = c->scale_of(layer, 0);
     a.k_block_scales = c->block_scales(layer, 0);
-    if (a.comps == 2) {
+    if (!c->latent()) {
         a.v_plane = c->plane(layer, 1);
         a.v_scale = c->scale_of(layer, 1);
         a.v_block_scales = c->block_scales(layer, 1);
@@ -117,14 +173,13 @@ kvr_status kvc_read_launch(const kvc_cache *c, int32_t layer, const kvc_read *p,
     a.slots = c->slots(p->table);
     a.flags = c->ws.flags;
     a.units = kvr_make_div((uint32_t)c->d.head_dim / 16);
-    const int64_t n = (int64_t)a.comps * a.H * a.units.d, rounds = (n + MOST_THREADS - 1) / MOST_THREADS;
-    const int threads = (int)((n + 32 * rounds - 1) / (32 * rounds)) * 32;
+    a.tokens = p->num_tokens;
     const bool f16 = p->dtype == KVC_DTYPE_F16;
-    const auto kernel =
-        c->d.dtype == KVC_DTYPE_E2M1
-            ? (f16 ? read_kernel<KVC_DTYPE_E2M1, true> : read_kernel<KVC_DTYPE_E2M1, false>)
-        : c->d.dtype == KVR_DTYPE_FP8_E4M3
-            ? (f16 ? read_kernel<KVR_DTYPE_FP8_E4M3, true> : read_kernel<KVR_DTYPE_FP8_E4M3, false>)
-            : read_kernel<KVR_DTYPE_BF16, false>;       // (16-bit rows are copied, whichever they are)
-    return kvc_launch(kernel, a, dim3((unsigned)p->num_tokens), threads, 0, stream);
+    if (c->d.dtype == KVC_DTYPE_E2M1)
+        return f16 ? go<KVC_DTYPE_E2M1, true>(a, c->sm_count, stream)
+                   : go<KVC_DTYPE_E2M1, false>(a, c->sm_count, stream);
+    if (c->d.dtype == KVR_DTYPE_FP8_E4M3)
+        return f16 ? go<KVR_DTYPE_FP8_E4M3, true>(a, c->sm_count, stream)
+                   : go<KVR_DTYPE_FP8_E4M3, false>(a, c->sm_count, stream);
+    return go<KVR_DTYPE_BF16, false>(a, c->sm_count, stream);      // (16-bit rows are copied, whichever they are)
 }
