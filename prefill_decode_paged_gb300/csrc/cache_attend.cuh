@@ -356,33 +356,56 @@ __device__ __forceinline__ void tile_scores(float (&s)[KT / 16][NT][4], uint32_t
     } else {
 #pragma unroll
         for (int d2 = 0; d2 < DP / 32; ++d2) {              // two steps of 16 elements
-            uint32_t b[NT][4];                              // [row tile][step][half]
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                ldmatrix4(b[n], q_base + swizzled<DP * 2>(n * 8 + lane % 8, d2 * 4 + lane / 8));
-#pragma unroll
-            for (int k = 0; k < KT / 16; ++k) {
+            // 16 keys: 8-bit codes of both steps, keys 0-7, 8-15 of the 1st, 2nd 16 elements; a step's fragment
+            auto codes = [&](uint32_t w[4], int k) {
+                if (E4) ldmatrix4(w, kbase + swizzled<ROW>(k * 16 + lane % 16, d2 * 2 + lane / 16));
+            };
+            auto fragment = [&](uint32_t f[4], const uint32_t w[4], int k, int st) {
                 if (!E4) {
-#pragma unroll
-                    for (int st = 0; st < 2; ++st) {
-                        uint32_t f[4];
-                        ldmatrix4(f, kbase + swizzled<ROW>(k * 16 + lane % 16, (d2 * 2 + st) * 2 + lane / 16));
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma<F16>(s[k][n], f, b[n][2 * st], b[n][2 * st + 1]);
-                    }
+                    ldmatrix4(f, kbase + swizzled<ROW>(k * 16 + lane % 16, (d2 * 2 + st) * 2 + lane / 16));
                 } else {
-                    uint32_t w[4];                          // keys 0-7, 8-15 of the 1st, 2nd 16 elements
-                    ldmatrix4(w, kbase + swizzled<ROW>(k * 16 + lane % 16, d2 * 2 + lane / 16));
+                    f[0] = e4m3_to_f16x2(w[2 * st]);
+                    f[1] = e4m3_to_f16x2(w[2 * st + 1]);
+                    f[2] = e4m3_to_f16x2(w[2 * st] >> 16);
+                    f[3] = e4m3_to_f16x2(w[2 * st + 1] >> 16);
+                }
+            };
+            auto queries = [&](uint32_t b[4], int n) {      // 8 rows: [step][half]
+                ldmatrix4(b, q_base + swizzled<DP * 2>(n * 8 + lane % 8, d2 * 4 + lane / 8));
+            };
+            if constexpr (NT <= 4) {
+                uint32_t b[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) queries(b[n], n);
+#pragma unroll
+                for (int k = 0; k < KT / 16; ++k) {
+                    uint32_t w[4];
+                    codes(w, k);
 #pragma unroll
                     for (int st = 0; st < 2; ++st) {
                         uint32_t f[4];
-                        f[0] = e4m3_to_f16x2(w[2 * st]);
-                        f[1] = e4m3_to_f16x2(w[2 * st + 1]);
-                        f[2] = e4m3_to_f16x2(w[2 * st] >> 16);
-                        f[3] = e4m3_to_f16x2(w[2 * st + 1] >> 16);
+                        fragment(f, w, k, st);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma<F16>(s[k][n], f, b[n][2 * st], b[n][2 * st + 1]);
                     }
+                }
+            } else {                                        // (more than registers would hold at once)
+                uint32_t f[KT / 16][2][4];
+#pragma unroll
+                for (int k = 0; k < KT / 16; ++k) {
+                    uint32_t w[4];
+                    codes(w, k);
+                    fragment(f[k][0], w, k, 0);
+                    fragment(f[k][1], w, k, 1);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    uint32_t b[4];
+                    queries(b, n);
+#pragma unroll
+                    for (int st = 0; st < 2; ++st)
+#pragma unroll
+                        for (int k = 0; k < KT / 16; ++k) mma<F16>(s[k][n], f[k][st], b[2 * st], b[2 * st + 1]);
                 }
             }
         }

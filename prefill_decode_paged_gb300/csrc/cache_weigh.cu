@@ -19,7 +19,7 @@ WeighPick pick(const kvc_desc &d, int32_t M) {
 }  // namespace
 
 kvr_status kvc_weigh_setup(kvc_cache *c) {
-    for (int32_t M : {8, 16, 32}) {
+    for (int32_t M : {8, 16, 32, 64}) {
         const WeighPick p = pick(c->d, M);
         if (cudaFuncSetAttribute(p.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)p.smem(KVC_MAX_REQUESTS)) != cudaSuccess) {

@@ -44,15 +44,16 @@ struct Weigh {
     static constexpr int KS = KT / 16;
     static constexpr int STAGE = KT * (ROW + SROW);
     static constexpr int BLOCKS = E2 && NT < 4 && DP <= 128 ? 4 : 2;   // resident on an SM
-    static constexpr int STAGES = STAGE >= 8192 ? 3 : BLOCKS == 4 || STAGE > 4096 ? 5 : 6;
+    static constexpr int STAGES =
+        STAGE >= 8192 ? (NT * DP >= 1024 ? 2 : 3) : NT * DP >= 1024 ? 4 : BLOCKS == 4 || STAGE > 4096 ? 5 : 6;
     static constexpr int RING = ATTEND_WARPS * STAGES * STAGE;
     static constexpr int UNIT = ATTEND_WARPS * KT;
     // (as in attention: the block scales of a token's heads share a sector)
     static constexpr bool ABREAST = E2;
     static constexpr int RP = 8 * NT;
     static constexpr int Q_BYTES = RP * DP * 2;
-    // ring, queries, then floats: row scales, log-sum-exps [RP]; 4 ints; prefix
-    static constexpr int FIXED = RING + Q_BYTES + 2 * 4 * RP + 16;
+    // ring, queries, then of each row a float2 (its factor, its log-sum-exp), its end and its slope; 4 ints; prefix
+    static constexpr int FIXED = RING + Q_BYTES + 16 * RP + 16;
     static constexpr size_t smem(int32_t requests) { return FIXED + 4 * (size_t)(requests + 1); }
 };
 
@@ -63,8 +64,10 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t smem0 = (uint32_t)__cvta_generic_to_shared(smem);
     unsigned char *q_smem = smem + C::RING;
-    float *row_scale = (float *)(q_smem + C::Q_BYTES), *row_lse = row_scale + RP;
-    int32_t *shared_int = (int32_t *)(row_lse + RP);    // [4]
+    float2 *row_of = (float2 *)(q_smem + C::Q_BYTES);   // factor of the products, log-sum-exp, in powers of two
+    int32_t *row_end = (int32_t *)(row_of + RP);        // first key that the row does not see; none: no row
+    float *row_slope = (float *)(row_end + RP);
+    int32_t *shared_int = (int32_t *)(row_slope + RP);  // [4]
     int32_t *prefix = shared_int + 4;                   // [requests + 1], in units of one job
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
     const float log2e = 1.4426950408889634f;
@@ -177,25 +180,22 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
                 float factor = a.scale * log2e * ks;
                 place_query<DP, POOL>(q_smem, row, qw[k], a.f16, &factor);
                 if (lane == 0) {
-                    row_scale[row] = factor;
                     // (a row that sees nothing has nothing to give)
-                    row_lse[row] = lw[k] == -INFINITY ? INFINITY : lw[k] * log2e;
+                    row_of[row] = make_float2(factor, lw[k] == -INFINITY ? INFINITY : lw[k] * log2e);
+                    const int32_t rho = row0 + min(row, rows - 1), i = (int32_t)a.group.div((uint32_t)rho);
+                    row_end[row] = row < rows ? sp.n - a.m + i + 1 : INT32_MIN;
+                    row_slope[row] = slope_of(a.scoring, h * a.G + rho - i * a.G);
                 }
             }
             __syncthreads();
 
-            float sc[NT][2], z[NT][2], slope[NT][2];
-            int32_t end[NT][2];                         // first key that the row does not see; none: no row
+            float sc[NT][2], z[NT][2];
 #pragma unroll
             for (int k = 0; k < NT; ++k)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int row = k * 8 + 2 * t4 + e;
-                    sc[k][e] = row_scale[row];
-                    z[k][e] = row_lse[row];
-                    const int32_t i = (int32_t)a.group.div((uint32_t)(row0 + min(row, rows - 1)));
-                    end[k][e] = row < rows ? sp.n - a.m + i + 1 : INT32_MIN;
-                    slope[k][e] = slope_of(a.scoring, h * a.G + row0 + min(row, rows - 1) - i * a.G);
+                    const float2 of = row_of[k * 8 + 2 * t4 + e];
+                    sc[k][e] = of.x, z[k][e] = of.y;
                 }
             const bool plain = a.scoring.cap == 0.0f && a.scoring.slopes == nullptr;
             const int32_t seen_all = rows < RP ? INT32_MIN : sp.n - a.m + 1;     // keys below it are seen by every row
@@ -235,29 +235,38 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
                 tile_scores<DP, POOL, KT, NT>(s, kbase, smem0 + C::RING, smem + (kbase - smem0) + KT * ROW);
 
                 const int32_t j0 = sp.lo + t * KT;
-                const bool mixed = j0 + KT > seen_all || j0 < seen_from;
                 float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};            // keys g, g + 8 of each 16
+                if (plain && j0 + KT <= seen_all && j0 >= seen_from) {
 #pragma unroll
-                for (int c = 0; c < NT; ++c)
+                    for (int c = 0; c < NT; ++c)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                        for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int k = 0; k < KS; ++k)
+                            for (int k = 0; k < KS; ++k)
 #pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const int32_t j = j0 + k * 16 + u * 8 + g;
-                                float p;
-                                if (plain) {
-                                    p = ex2(fmaf(s[k][c][2 * u + e], sc[c][e], -z[c][e]));
-                                } else {
-                                    p = ex2(scored(s[k][c][2 * u + e] * sc[c][e], a.scoring, slope[c][e],
-                                                   j - end[c][e] + 1) - z[c][e]);
+                                for (int u = 0; u < 2; ++u)
+                                    sum[2 * k + u] += ex2(fmaf(s[k][c][2 * u + e], sc[c][e], -z[c][e]));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < NT; ++c)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int32_t end = row_end[c * 8 + 2 * t4 + e];
+                            const float slope = row_slope[c * 8 + 2 * t4 + e];
+#pragma unroll
+                            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    const int32_t j = j0 + k * 16 + u * 8 + g;
+                                    const float v = s[k][c][2 * u + e];
+                                    const float p =
+                                        plain ? ex2(fmaf(v, sc[c][e], -z[c][e]))
+                                              : ex2(scored(v * sc[c][e], a.scoring, slope, j - end + 1) - z[c][e]);
+                                    const bool seen = j < end && (a.split.window == 0 || j >= window_from(end, a.split.window));
+                                    sum[2 * k + u] += seen ? p : 0.0f;
                                 }
-                                if (mixed && (j >= end[c][e] ||
-                                              (a.split.window > 0 && j < window_from(end[c][e], a.split.window))))
-                                    p = 0.0f;
-                                sum[2 * k + u] += p;
-                            }
+                        }
+                }
                 // each lane of four keeps a quarter of the keys
                 const bool odd = t4 & 1, high = t4 & 2;
                 const float lo = (odd ? sum[1] : sum[0]) + __shfl_xor_sync(~0u, odd ? sum[0] : sum[1], 1);
@@ -288,18 +297,21 @@ inline WeighPick weigh_instance() {
     return {weigh_kernel<DP, POOL, NT>, &C::smem, C::UNIT, C::RP, C::BLOCKS, C::ABREAST};
 }
 
-// The instance for head dimension D and M rows a job: rows in passes of 8, 16 or 32.
+// The instance for head dimension D and M rows a job: rows in passes of 8, 16, 32 or 64.
 template <int POOL>
 inline WeighPick weigh_pick(int32_t D, int32_t M) {
-    const int nt = M <= 8 ? 1 : M <= 16 ? 2 : 4;
+    const int nt = M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : 8;
     if (D <= 64)
-        return nt == 1 ? weigh_instance<64, POOL, 1>()
-               : nt == 2 ? weigh_instance<64, POOL, 2>() : weigh_instance<64, POOL, 4>();
+        return nt == 1   ? weigh_instance<64, POOL, 1>()
+               : nt == 2 ? weigh_instance<64, POOL, 2>()
+               : nt == 4 ? weigh_instance<64, POOL, 4>() : weigh_instance<64, POOL, 8>();
     if (D <= 128)
-        return nt == 1 ? weigh_instance<128, POOL, 1>()
-               : nt == 2 ? weigh_instance<128, POOL, 2>() : weigh_instance<128, POOL, 4>();
-    return nt == 1 ? weigh_instance<256, POOL, 1>()
-           : nt == 2 ? weigh_instance<256, POOL, 2>() : weigh_instance<256, POOL, 4>();
+        return nt == 1   ? weigh_instance<128, POOL, 1>()
+               : nt == 2 ? weigh_instance<128, POOL, 2>()
+               : nt == 4 ? weigh_instance<128, POOL, 4>() : weigh_instance<128, POOL, 8>();
+    return nt == 1   ? weigh_instance<256, POOL, 1>()
+           : nt == 2 ? weigh_instance<256, POOL, 2>()
+           : nt == 4 ? weigh_instance<256, POOL, 4>() : weigh_instance<256, POOL, 8>();
 }
 
 WeighPick weigh_pick_bf16(int32_t D, int32_t M);     // one translation unit each
