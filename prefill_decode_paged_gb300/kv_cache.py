@@ -395,13 +395,19 @@ class KVCache:
             v = self._new(shape, k.dtype, stream)
         if k.requires_grad or (v is not None and v.requires_grad):
             self._refuse_gradients()
-        ks = self._rows(k, "k", shape)
-        vp, vs = (0, (0, 0)) if v is None else (v.data_ptr(), self._rows(v, "v", shape, k.dtype))
+        kind, index = k.dtype, self._index
+        ks = self._row_bytes if kind in self._types and k.shape == shape and k.is_contiguous() and \
+            k.get_device() == index else self._rows(k, "k", shape)
+        vp, vs = 0, (0, 0)
+        if v is not None:
+            vp, vs = v.data_ptr(), self._row_bytes
+            if not (v.dtype is kind and v.shape == shape and v.is_contiguous() and v.get_device() == index):
+                vs = self._rows(v, "v", shape, kind)
         st = self._read(
             self._handle(), layer,
-            _READ.pack(T, self._types[k.dtype], self._list(requests, "requests", T),
+            _READ.pack(T, self._types[kind], self._list(requests, "requests", T),
                        self._list(positions, "positions", T), *self._table(block_table), k.data_ptr(), vp, *ks, *vs),
-            self._raw_stream(self._index) if stream is None else _stream_handle(stream))
+            self._raw_stream(index) if stream is None else _stream_handle(stream))
         if st != 0:
             raise KVRelayoutError(st, "kv_cache_read")
         return k, v
@@ -469,9 +475,12 @@ class KVCache:
 
     def _weight_rows(self, t, name, R):
         """Strides between the requests' and the heads' weights, and how many each head has."""
-        if t.dtype is self._f32 and t.dim() == 3 and t.shape[:2] == (R, self.kv_heads) and \
+        shape = t.shape
+        if t.dtype is self._f32 and len(shape) == 3 and shape[0] == R and shape[1] == self.kv_heads and \
                 t.get_device() == self._index:
-            S = t.shape[2]
+            S = shape[2]
+            if t.is_contiguous():
+                return shape[1] * S, S, S
             a, b, c = t.stride()
             if c == 1 or S <= 1:
                 return a, b, S
@@ -492,8 +501,13 @@ class KVCache:
             raise ValueError(f"q is {list(shape)}; expected [R][new][heads][dim]")
         R, m = shape[0], shape[1] if n == 4 else 1
         rows = (R, m, heads) if n == 4 else (R, heads)
-        qs = self._rows(q, "q", rows + (self.head_dim,))
-        qs = qs if n == 4 else (qs[0], 0, qs[1])
+        if q.dtype in self._types and shape == rows + (self.head_dim,) and q.is_contiguous() and \
+                q.get_device() == index:
+            row = 2 * self.head_dim
+            qs = m * heads * row, heads * row, row
+        else:
+            qs = self._rows(q, "q", rows + (self.head_dim,))
+            qs = qs if n == 4 else (qs[0], 0, qs[1])
         if not (lse.dtype is self._f32 and lse.shape == rows and lse.is_contiguous() and lse.get_device() == index):
             raise ValueError(f"lse is {lse.dtype} {list(lse.shape)}; expected contiguous "
                              f"float32 {list(rows)} on {self._device}")
@@ -503,7 +517,7 @@ class KVCache:
             _WEIGH.pack(R, m, self._types[q.dtype], window, self._default_scale if scale is None else scale,
                         1 if add else 0, self._list(lengths, "lengths", R), *self._table(block_table), q.data_ptr(),
                         lse.data_ptr(), weights.data_ptr(), *qs, *ws, width, 0, cap, 0,
-                        _SCORING.unpack(self._scoring(cap, slopes))[2]),
+                        0 if slopes is None else _SCORING.unpack(self._scoring(cap, slopes))[2]),
             self._raw_stream(index) if stream is None else _stream_handle(stream))
         if st != 0:
             raise KVRelayoutError(st, "kv_cache_weigh")
@@ -520,12 +534,14 @@ class KVCache:
         had (entries beyond their number are left as they were, in a new tensor -1)."""
         if weights.requires_grad or (out is not None and out.requires_grad):
             self._refuse_gradients()
-        R = weights.shape[0] if weights.dim() == 3 else -1
-        *ws, width = self._weight_rows(weights, "weights", R)
-        out = weights if out is None else out
-        *os, out_width = self._weight_rows(out, "out", R)
-        if out_width != width:
-            raise ValueError(f"out has {out_width} weights a head; weights {width}")
+        R, index = weights.shape[0] if weights.dim() == 3 else -1, self._index
+        wr, wh, width = self._weight_rows(weights, "weights", R)
+        if out is None or out is weights:
+            out, os, oh = weights, wr, wh
+        else:
+            os, oh, out_width = self._weight_rows(out, "out", R)
+            if out_width != width:
+                raise ValueError(f"out has {out_width} weights a head; weights {width}")
         shape = (R, self.kv_heads, keep)
         if slots is None:
             slots = self._new(shape, self._i32, stream)
@@ -539,8 +555,8 @@ class KVCache:
         st = self._evict(
             self._handle(), layer,
             _EVICT.pack(R, keep, recent, width, self._list(lengths, "lengths", R), *self._table(block_table), *there,
-                        weights.data_ptr(), out.data_ptr(), slots.data_ptr(), *ws, *os, 0),
-            self._raw_stream(self._index) if stream is None else _stream_handle(stream))
+                        weights.data_ptr(), out.data_ptr(), slots.data_ptr(), wr, wh, os, oh, 0),
+            self._raw_stream(index) if stream is None else _stream_handle(stream))
         if st != 0:
             raise KVRelayoutError(st, "kv_cache_evict")
         return out, slots
