@@ -29,6 +29,15 @@ bool disjoint_rows(int64_t outer, int64_t outer_stride, int64_t inner, int64_t i
     if (inner > 1 && inner_stride < row) return false;
     return outer <= 1 || (__int128)outer_stride >= (inner > 1 ? (__int128)(inner - 1) * inner_stride : 0) + row;
 }
+// No C++ exception crosses the ABI.
+template <typename F>
+kvr_status guarded(F launch) {
+    try {
+        return launch();
+    } catch (...) {
+        return KVR_ERR_NOMEM;
+    }
+}
 int64_t address(const void *p) { return (int64_t)(uintptr_t)p; }
 
 }  // namespace
@@ -40,7 +49,7 @@ extern "C" kvr_status kv_cache_append_at(const kvc_cache *c, int32_t layer, cons
     if (address(angles) % 4 != 0) return KVR_ERR_ALIGNMENT;
     if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
     if (a->num_tokens == 0) return KVR_OK;
-    return kvc_append_at_launch(c, layer, a, angles, stream);
+    return guarded([&] { return kvc_append_at_launch(c, layer, a, angles, stream); });
 }
 
 kvr_status kvc_check_scoring(const kvc_cache *c, const kvc_scoring &s) {
@@ -60,7 +69,7 @@ extern "C" kvr_status kv_cache_attend_scored(const kvc_cache *c, int32_t layer, 
     if (scoring->cap == 0.0f && scoring->slopes == nullptr) return kv_cache_attend(c, layer, a, stream);
     if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
     if (a->num_requests == 0) return KVR_OK;
-    return kvc_attend_scored_launch(c, layer, a, scoring, stream);
+    return guarded([&] { return kvc_attend_scored_launch(c, layer, a, scoring, stream); });
 }
 
 extern "C" kvr_status kv_cache_weigh(const kvc_cache *c, int32_t layer, const kvc_weigh *a, void *stream) {
@@ -93,7 +102,7 @@ extern "C" kvr_status kv_cache_weigh(const kvc_cache *c, int32_t layer, const kv
     if (st != KVR_OK) return st;
     if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
     if (a->num_requests == 0) return KVR_OK;
-    return kvc_weigh_launch(c, layer, a, stream);
+    return guarded([&] { return kvc_weigh_launch(c, layer, a, stream); });
 }
 
 extern "C" kvr_status kv_cache_evict(const kvc_cache *c, int32_t layer, const kvc_evict *a, void *stream) {
@@ -130,7 +139,7 @@ extern "C" kvr_status kv_cache_evict(const kvc_cache *c, int32_t layer, const kv
         return KVR_ERR_ALIGNMENT;
     if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
     if (a->num_requests == 0) return KVR_OK;
-    return kvc_evict_launch(c, layer, a, stream);
+    return guarded([&] { return kvc_evict_launch(c, layer, a, stream); });
 }
 
 extern "C" kvr_status kv_cache_read(const kvc_cache *c, int32_t layer, const kvc_read *a, void *stream) {
@@ -149,5 +158,5 @@ extern "C" kvr_status kv_cache_read(const kvc_cache *c, int32_t layer, const kvc
         return KVR_ERR_ALIGNMENT;
     if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
     if (a->num_tokens == 0) return KVR_OK;
-    return kvc_read_launch(c, layer, a, stream);
+    return guarded([&] { return kvc_read_launch(c, layer, a, stream); });
 }
