@@ -224,7 +224,8 @@ __device__ __forceinline__ Place place_of(const AppendArgs &a, int32_t t, int32_
     return p;
 }
 
-template <bool F16, bool INTERLEAVED, int POOL, bool MANY>
+// APART: positions of rotation of their own (as a branch in one kernel they cost the others 5 % of short calls).
+template <bool F16, bool INTERLEAVED, int POOL, bool MANY, bool APART>
 __global__ void __launch_bounds__(MANY ? MANY_THREADS : FEW_THREADS,
                   POOL == KVC_DTYPE_E2M1 ? (MANY ? 8 : 1) : MANY ? 10 : 2)
 append_kernel(AppendArgs a) {
@@ -235,7 +236,7 @@ append_kernel(AppendArgs a) {
     let_next_start();
     const int64_t token = blockIdx.x;
     const int32_t pos = __ldg(a.positions + token), req = __ldg(a.requests + token);
-    const int32_t turned = a.angles != nullptr ? __ldg(a.angles + token) : pos;
+    const int32_t turned = APART ? __ldg(a.angles + token) : pos;
     const int32_t n = a.q.heads * (int32_t)a.q_units.d + (a.k.heads + a.v.heads) * (int32_t)a.units.d;
     int64_t slot = -1;                       // the token's slot in a plane, in bytes
     const float *angles = nullptr;
@@ -264,7 +265,7 @@ append_kernel(AppendArgs a) {
             if (req < 0 || req >= a.slots.rows) {
                 bad = KVC_FLAG_REQUEST;
             } else if (entry >= (uint32_t)a.slots.width ||
-                       (a.rotary != nullptr && (turned < 0 || turned >= a.rotary_rows))) {
+                       (a.rotary != nullptr && ((APART && turned < 0) || turned >= a.rotary_rows))) {
                 bad = KVC_FLAG_POSITION;
             } else {
                 const int32_t id = __ldg(a.slots.ids + (int64_t)req * a.slots.stride + entry);
@@ -323,17 +324,24 @@ append_kernel(AppendArgs a) {
 // units, 4.2 and 5.6 for 256; 2.9 and 3.1 for 300 of 384, 4.9 and 3.8 for 600; and with blocks of 192,
 // 256 and 384 threads 39834 tokens took 186, 190 and 216 where those of 128 took 162. (The register limits, 48
 // for many and 64 for few, make the compiler spill 12 to 64 bytes a thread; looser ones have not been tried.)
-template <bool F16, int POOL>
-kvr_status go(AppendArgs &a, bool interleaved, int32_t tokens, int sms, void *stream) {
+template <bool F16, int POOL, bool APART>
+kvr_status go_at(AppendArgs &a, bool interleaved, int32_t tokens, int sms, void *stream) {
     const int64_t n = (int64_t)a.q.heads * a.q_units.d + (int64_t)(a.k.heads + a.v.heads) * a.units.d;
     const bool many = tokens > BORDER * sms;
     const int64_t rounds = (n + FEW_THREADS - 1) / FEW_THREADS;
     const int threads = many ? MANY_THREADS : (int)((n + 32 * rounds - 1) / (32 * rounds)) * 32;
     a.away = tokens * n * 16 * 2 > (int64_t)AWAY << 20;
     const auto kernel =
-        many ? (interleaved ? append_kernel<F16, true, POOL, true> : append_kernel<F16, false, POOL, true>)
-             : (interleaved ? append_kernel<F16, true, POOL, false> : append_kernel<F16, false, POOL, false>);
+        many ? (interleaved ? append_kernel<F16, true, POOL, true, APART> : append_kernel<F16, false, POOL, true, APART>)
+             : (interleaved ? append_kernel<F16, true, POOL, false, APART>
+                            : append_kernel<F16, false, POOL, false, APART>);
     return kvc_launch(kernel, a, dim3((unsigned)tokens), threads, 0, stream);
+}
+
+template <bool F16, int POOL>
+kvr_status go(AppendArgs &a, bool interleaved, int32_t tokens, int sms, void *stream) {
+    return a.angles != nullptr ? go_at<F16, POOL, true>(a, interleaved, tokens, sms, stream)
+                               : go_at<F16, POOL, false>(a, interleaved, tokens, sms, stream);
 }
 
 }  // namespace
