@@ -92,8 +92,15 @@ struct Attend {
     static constexpr int KT = 2 * 16 * ROW >= 8192 ? 16 : 32;    // keys of a tile
     static constexpr int KS = KT / 16;
     static constexpr int STAGE = 2 * KT * (ROW + SROW);          // keys, values, then their block scales
-    static constexpr int BLOCKS = E2 ? (NT > 2 || NT > 1 && DP > 128 ? 2 : NT > 1 || DP > 128 ? 3 : 4) : STAGE > 8192 ? 1 : 2;   // resident on an SM
-    static constexpr int STAGES = E2 ? (DP > 128 ? (NT == 1 ? 2 : 3) : NT == 2 ? 3 : NT == 1 && DP == 128 ? 2 : 5) : STAGE >= 8192 ? 3 : 6;
+    // Blocks resident on an SM, and tiles of a warp's ring. 4 bits: as many blocks as their registers allow, for
+    // instructions bound them (64 requests of 8192 keys, 8 queries a head: 2 blocks of 5 tiles 142 us, 3 of 3 132.5,
+    // 4 of 2 134); a small ring costs long requests' joins (one of 65536: 31, 36 and 44).
+    static constexpr int BLOCKS = !E2                                ? (STAGE > 8192 ? 1 : 2)
+                                  : NT > 2 || (NT > 1 && DP > 128)   ? 2
+                                  : NT == 1 && DP == 64              ? 4 : 3;
+    static constexpr int STAGES = !E2         ? (STAGE >= 8192 ? 3 : 6)
+                                  : DP > 128  ? (NT == 1 ? 2 : 3)
+                                  : BLOCKS == 3 ? 3 : 5;
     static constexpr int RING = ATTEND_WARPS * STAGES * STAGE;
     static constexpr int UNIT = ATTEND_WARPS * KT;               // keys of a unit
     // One block a head goes through the same part of the line: the block scales of a token's heads share a sector
