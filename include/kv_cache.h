@@ -1,6 +1,7 @@
 /*
  * kv_cache.h -- C ABI of what a decode instance does with the KV it was handed: append the
- * new tokens' keys and values, and attend to the cache.
+ * new tokens' keys and values, attend to the cache, weigh its keys by the attention they got and
+ * evict tokens by these weights.
  *
  * A cache is ONE shard pool of a decode side as kv_relayout.h describes it,
  *   [num_layers][num_components][num_blocks][block_size][kv_heads][head_dim],

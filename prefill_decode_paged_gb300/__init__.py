@@ -16,8 +16,9 @@ Public API (see ``include/kv_relayout.h`` for the C ABI it binds):
 * :func:`relayout_all_prealloc` -- ``run_all`` without any device allocation, for
   callers that cannot allocate (work lists up to 1 MiB).
 * :class:`KVCache` -- a decode pool after the hand-off: ``append()`` new tokens with the position
-  rotation applied on the way, ``attend()`` to the paged keys and values or latents
-  (``include/kv_cache.h``); :func:`rotary_table` fills the table of rotations.
+  rotation applied on the way, ``attend()`` to the paged keys and values or latents, ``read()`` rows back;
+  16-bit, E4M3 and 4-bit pools; under a memory budget ``weigh()`` the cached keys by the attention they got and
+  ``evict()`` the others (``include/kv_cache.h``); :func:`rotary_table` fills the table of rotations.
 * ``kv_relayout.checked_library()`` / ``build.build_checked()`` -- the same C ABI
   built with device-side address checks (tests).
 """

@@ -12,7 +12,9 @@
 // block id) and the angles are on their way meanwhile. Where the row's units divide the block's
 // threads, a thread has the same unit of every row, and loads its angles once. HBM bounds it with
 // many tokens: 39834 tokens of 32 + 16 heads of 128, 982 MB, 152 to 159 us from card to card
-// (6180 to 6450 GB/s, 91 to 95 % of a plain copy's rate).
+// (6180 to 6450 GB/s, 91 to 95 % of a plain copy's rate). Into 4 bits instructions do: 41931 tokens, 952 MB, 182 us
+// (with 32 elements a thread 200; with the queries in a kernel of their own 229; with the next unit's loads ahead of this
+// one's arithmetic 200).
 #include <algorithm>
 
 #include "cache.h"

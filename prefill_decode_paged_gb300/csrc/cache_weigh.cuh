@@ -11,6 +11,10 @@
 // as in attention. S^T = K Q^T by mma.sync m16n8k16, keys by rows; a lane holds 4 keys of 2 rows of every 8,
 // and three exchanges give each lane of four one key's sum, so that a warp writes 32 neighbours at once.
 // Scores, exponentials and sums are fp32.
+//
+// Measured: 64 requests of 8192 keys, 8 heads of 128, 8 rows: bf16 170 us (6.4 TB/s, HBM), E4M3 102 (5.4), 4 bits 74
+// (4.4; conversions). 4 requests of up to 32768 E4M3 keys under 64 rows 47 us: mma.sync at half its rate. With 32 rows a
+// pass, which takes the keys and their conversion twice, 67; with tiles of 16 keys and three blocks an SM 49.
 #pragma once
 
 #include "cache_attend.cuh"

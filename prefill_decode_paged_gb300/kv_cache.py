@@ -1,7 +1,7 @@
 """ctypes binding of the C ABI in ``include/kv_cache.h`` (argument marshalling only).
 
 What a decode instance does with the KV it was handed: :class:`KVCache` appends new tokens to
-one shard pool and attends to it, :func:`rotary_table` fills the table of rotations. Every step
+one shard pool, attends to it, and evicts what got little attention; :func:`rotary_table` fills the table of rotations. Every step
 runs in the CUDA library; there is no fallback.
 """
 from __future__ import annotations
@@ -131,7 +131,7 @@ def _defaults(g):
 
 
 class KVCache:
-    """One shard pool of a decode side: append tokens to it, attend to it.
+    """One shard pool of a decode side: append tokens to it, read them back, attend to it, evict from it.
 
     ``pool``: a contiguous tensor (or address) [num_layers][num_components][num_blocks][block]
     [kv_heads][head_dim] -- the decode pool that a :class:`RelayoutPlan` wrote -- with ``kv_heads``
