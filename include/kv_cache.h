@@ -280,10 +280,11 @@ kvr_status kv_cache_weigh(const kvc_cache *cache, int32_t layer, const kvc_weigh
  * it is left as it was), and kept[r][h] the slots that they had (entries from min(n, keep) on are left). The
  * lengths do not change: afterwards min(lengths[r], keep) tokens are cached, and the next is appended at that
  * position, rotated by its own (kv_cache_append_at).
- * Blocks of `into` must hold no cached token of these requests, unless the table is the same; requests evicted in
- * place must not share blocks. weights_out is weights itself, with the same strides, or apart from it. A length beyond the block table or
- * weights_width counts as the nearest in range (KVC_FLAG_LENGTH); a row whose block is out of range, or beyond `into`, is not moved
- * (KVC_FLAG_BLOCK, KVC_FLAG_LENGTH). Uses no workspace. Keys and values only (KVR_ERR_UNSUPPORTED for latents).
+ * Blocks of `into` must hold no cached token of these requests, unless it is the same table: the same memory, not a
+ * copy (one of its ids with another width or stride is refused). Requests evicted in place must not share blocks.
+ * weights_out is weights itself, with the same strides, or apart from it. A length beyond the block table or
+ * weights_width counts as the nearest in range (KVC_FLAG_LENGTH); a row whose block is out of range, or beyond `into`,
+ * is not moved (KVC_FLAG_BLOCK, KVC_FLAG_LENGTH). Uses no workspace. Keys and values only (KVR_ERR_UNSUPPORTED for latents).
  */
 typedef struct kvc_evict {
     int32_t num_requests;      /* 0..KVC_MAX_REQUESTS */

@@ -528,7 +528,7 @@ class KVCache:
         """Keep at most ``keep`` of each request's cached tokens in ``layer``, each key head for itself: the ``recent``
         newest and, of the others, those of the largest ``weights`` (float32 [R][H][width], see :meth:`weigh`; equal ones:
         the lower slots). Their rows move together to the front, in their order, in place or through another block table
-        ``into`` whose blocks hold no cached token. ``out`` (``weights`` itself by default) gets their
+        ``into`` whose blocks hold no cached token (so no copy of ``block_table``). ``out`` (``weights`` itself by default) gets their
         weights, then zeros up to ``lengths[r]``. Afterwards min(lengths[r], keep) tokens are cached; the caller's lengths
         are its own to change. Returns (out, slots): ``slots`` int32 [R][H][keep], the slots that the kept tokens
         had (entries beyond their number are left as they were, in a new tensor -1)."""
