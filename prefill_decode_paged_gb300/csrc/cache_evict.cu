@@ -2,22 +2,22 @@
 //
 // Select. Of n tokens the `recent` newest stay, and of the others the `need` = keep - recent of the largest
 // weights: those above the need-th largest, T, and of those equal to it the lowest slots. A cluster of blocks has
-// a head; each block a contiguous share of its weights, held in shared memory. T comes digit by digit (8
-// bits of the weights as ordered integers): each block counts its weights that fit the digits so far, every
-// block adds all blocks' counts up and so finds the same digit, with one barrier of the cluster a digit. (Digits of 11
-// bits are one barrier fewer, but eight times the counts to be read from the other blocks: 44 us where 8 bits
-// take 17, 16 heads of 32768 weights.) Then each
-// warp counts what stays of its share, and writes those slots where the shares before it end. A few
-// thousand weights are read once: barriers and shared memory bound it, not HBM.
+// a head; each block a contiguous share of its weights, each warp of that, held in registers. T comes digit by digit (8
+// bits of the weights as ordered integers): each block counts its weights that fit the digits so far and sends the
+// counts to all, every block adds them up and so finds the same digit, with one barrier of the cluster a digit. From
+// the same counts it knows what stays of the blocks before it; each warp counts what stays of its own share and
+// writes those slots where the shares before it end. The weights are read once: barriers bound it, not HBM. (Digits of
+// 11 bits are one barrier fewer, but eight times the counts between blocks: 44 us where 8 bits took 17, 16 heads of
+// 32768 weights. Counts fetched after the barrier, weights in shared memory: 41 us with the rows, now 38.)
 //
 // Move. Row i of the kept goes to slot i, which is not after its own. Into other blocks, rows in any
 // order by any block. In place, slot i may still hold a row that has to go further down; it is the source of
 // a row i' <= i. A cluster has a head, goes up the kept rows in rounds of a few rows a block, and each
 // round's rows are all in registers before any of them is stored (one barrier of the cluster a round; the
-// next round's are asked for before that, as no store of this round reaches slots of rows behind it).
+// next ones are asked for before that, as no store reaches slots of rows behind its own).
 //
-// Measured, into other blocks: 16 requests of 2000 to 8192 tokens cut to 2048, 8 heads of 128 in bf16 (274 MB) 57 us, of
-// which select 13; 4 of 32768 to 8192, 4 heads, 41 us, select 15. Rows move at 5.9 TB/s.
+// Measured, into other blocks: 16 requests of 2000 to 8192 tokens cut to 2048, 8 heads of 128 in bf16 (274 MB) 56 us, of
+// which select 12; 4 of 32768 to 8192, 4 heads, 38 us, select 13. Rows move at 5.9 TB/s.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -33,7 +33,7 @@ constexpr int SELECT_THREADS = 512, SELECT_WARPS = SELECT_THREADS / 32;
 constexpr int BINS = 256;
 constexpr int MOST_BLOCKS = 8;     // of a cluster
 constexpr int SHARE = 2048;        // weights of a block, above which a head gets another, while there is room for it
-constexpr int HELD = 7168;         // weights that a block holds in shared memory; those beyond are read each time
+constexpr int HELD = 8;            // weights that a thread holds; those beyond are read each time
 constexpr int COPY_THREADS = 128, MOVE_THREADS = 256;
 constexpr int UNITS = 8;           // 16-byte units of a thread at a time
 constexpr int WORDS = 9;           // words of a thread besides: a weight, and block scales of 4-bit rows
@@ -80,11 +80,10 @@ __device__ __forceinline__ uint32_t before_warp(const uint32_t (*scan)[2], int w
 
 template <int BLOCKS>
 __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(EvictArgs a) {
-    __shared__ uint32_t held[HELD];
-    __shared__ __align__(16) uint32_t hist[2][BINS];
+    __shared__ uint32_t hist[BINS];
+    __shared__ uint32_t all[2][BLOCKS][BINS];              // all blocks' counts, as each sends its own
     __shared__ uint32_t scan[SELECT_WARPS][2];
-    __shared__ uint32_t found[3];
-    __shared__ __align__(8) uint32_t own[2];
+    __shared__ uint32_t found[5];
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     constexpr int blocks = BLOCKS;
@@ -113,72 +112,105 @@ __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(EvictArgs a) {
         return;
     }
 
+    if (BLOCKS > 1) cluster.barrier_arrive();              // (that the others have begun; waited for below)
     const float *weights = a.weights + r * a.w_request + h * a.w_head;
     const int32_t share = (old + blocks - 1) / blocks;
     const int32_t j0 = min(old, part * share), size = min(old, j0 + share) - j0;
-    auto key = [&](int32_t i) -> uint32_t { return i < HELD ? held[i] : ordered(weights[j0 + i]); };
-    if (tid < BINS) hist[0][tid] = 0;
-    for (int32_t i = tid; i < min(size, HELD); i += SELECT_THREADS) held[i] = ordered(weights[j0 + i]);
+    // a warp's part of the block's share; its lanes' weights, those beyond what registers hold read each time
+    const int32_t run = (size + SELECT_WARPS - 1) / SELECT_WARPS;
+    const int32_t i0 = min(size, warp * run), i1 = min(size, i0 + run);
+    uint32_t held[HELD];
+#pragma unroll
+    for (int t = 0; t < HELD; ++t) {
+        const int32_t i = i0 + 32 * t + lane;
+        held[t] = i < i1 ? ordered(weights[j0 + i]) : 0u;
+    }
+    // f(i, key, whether there is one) for each; warps stay whole
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int t = 0; t < HELD; ++t)
+            if (i0 + 32 * t < i1) f(i0 + 32 * t + lane, held[t], i0 + 32 * t + lane < i1);
+        for (int32_t i = i0 + 32 * HELD; i < i1; i += 32) {
+            const bool some = i + lane < i1;
+            f(i + lane, some ? ordered(weights[j0 + i + lane]) : 0u, some);
+        }
+    };
+    if (tid < BINS) hist[tid] = 0;
 
     uint32_t known = 0, mask = 0;        // T's digits so far, and which bits they are
     uint32_t left = (uint32_t)need;      // of the weights that fit them, how many stay
+    uint32_t lower_above = 0, lower_same = 0;   // of the blocks before this one: above T, and equal
 #pragma unroll
     for (int pass = 0; pass < 4; ++pass) {
         const int shift = 24 - 8 * pass;
-        uint32_t *count = hist[pass & 1];
+        uint32_t(*counts)[BINS] = all[pass & 1];
         __syncthreads();
-        for (int32_t i = tid; i < size; i += SELECT_THREADS) {
-            const uint32_t k = key(i);
-            if ((k & mask) == known) atomicAdd(count + (k >> shift & 255u), 1u);
+        each([&](int32_t, uint32_t k, bool some) {
+            if (some && (k & mask) == known) atomicAdd(hist + (k >> shift & 255u), 1u);
+        });
+        __syncthreads();
+        if (BLOCKS > 1 && pass == 0) cluster.barrier_wait();
+        // (what the others read of this array, two digits ago, they read before the barrier of the last)
+        static_assert(SELECT_THREADS >= BINS && BINS % 32 == 0, "");
+        if (tid < BINS) {
+            const uint32_t c = hist[tid];
+            hist[tid] = 0;
+            if (BLOCKS > 1) {
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b) *cluster.map_shared_rank(&counts[part][tid], b) = c;
+            } else {
+                counts[0][tid] = c;
+            }
         }
         if (BLOCKS > 1)
             cluster.sync();
         else
             __syncthreads();
-        // (what the others read last of the other array, they read before this barrier)
-        if (tid < BINS) hist[pass & 1 ^ 1][tid] = 0;
-        // a thread's bin, from the top down: its count over all blocks
-        static_assert(SELECT_THREADS >= BINS, "");
+        // a thread's bin, from the top down: its count over all blocks, and over those before this one
         const int bin = BINS - 1 - tid;
-        uint32_t sum = 0;
+        uint32_t sum = 0, lower = 0, sums = 0, lowers = 0;
         if (tid < BINS) {
-            uint32_t theirs[BLOCKS];                       // (all asked for before the first is used)
 #pragma unroll
-            for (int b = 0; b < BLOCKS; ++b)
-                theirs[b] = (BLOCKS > 1 ? cluster.map_shared_rank(count, b) : count)[bin];
+            for (int b = 0; b < BLOCKS; ++b) {
+                const uint32_t c = counts[b][bin];
+                sum += c;
+                lower += b < part ? c : 0u;
+            }
+            sums = sum, lowers = lower;
 #pragma unroll
-            for (int b = 0; b < BLOCKS; ++b) sum += theirs[b];
+            for (int o = 1; o < 32; o *= 2) {
+                const uint32_t y = __shfl_up_sync(~0u, sums, o), z = __shfl_up_sync(~0u, lowers, o);
+                if (lane >= o) sums += y, lowers += z;
+            }
+            if (lane == 31) scan[warp][0] = sums, scan[warp][1] = lowers;
         }
-        uint32_t incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const uint32_t y = __shfl_up_sync(~0u, incl, o);
-            if (lane >= o) incl += y;
-        }
-        if (lane == 31) scan[warp][0] = incl;
         __syncthreads();
-        const uint32_t above = incl - sum + before_warp(scan, 0);
-        if (tid < BINS && above < left && left <= above + sum) {
-            found[0] = (uint32_t)bin;
-            found[1] = left - above;
-            found[2] = sum;
+        if (tid < BINS) {
+            const uint32_t above = sums - sum + before_warp(scan, 0);
+            const uint32_t lower_before = lowers - lower + before_warp(scan, 1);
+            if (above < left && left <= above + sum) {
+                found[0] = (uint32_t)bin;
+                found[1] = left - above;
+                found[2] = sum;
+                found[3] = lower_before;
+                found[4] = lower;
+            }
         }
         __syncthreads();
         known |= found[0] << shift;
         mask |= 255u << shift;
         left = found[1];
+        lower_above += found[3];
+        lower_same = found[4];
         if (left == found[2]) break;     // all that fit stay, whatever follows (the same in every block)
     }
 
-    // a warp's share of the block's: how many are above T, and how many equal it
-    const int32_t run = (size + SELECT_WARPS - 1) / SELECT_WARPS;
-    const int32_t i0 = min(size, warp * run), i1 = min(size, i0 + run);
+    // of the warp's: how many are above T, and how many equal it
     uint32_t above = 0, same = 0;
-    for (int32_t i = i0 + lane; i < i1; i += 32) {
-        const uint32_t k = key(i) & mask;
-        above += k > known;
-        same += k == known;
-    }
+    each([&](int32_t, uint32_t k, bool some) {
+        above += some && (k & mask) > known;
+        same += some && (k & mask) == known;
+    });
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) {
         above += __shfl_xor_sync(~0u, above, o);
@@ -186,34 +218,17 @@ __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(EvictArgs a) {
     }
     if (lane == 0) scan[warp][0] = above, scan[warp][1] = same;
     __syncthreads();
-    above = same = 0;
-    if (BLOCKS > 1) {
-        if (warp < 2) {
-            const uint32_t t = __reduce_add_sync(~0u, lane < SELECT_WARPS ? scan[lane][warp] : 0u);
-            if (lane == 0) own[warp] = t;
-        }
-        cluster.sync();
-#pragma unroll
-        for (int b = 0; b < BLOCKS - 1; ++b)
-            if (b < part) {
-                const uint2 o = *(const uint2 *)cluster.map_shared_rank(own, b);
-                above += o.x, same += o.y;
-            }
-        cluster.barrier_arrive();        // no block leaves while others read its counts
-    }
-    above += before_warp(scan, 0), same += before_warp(scan, 1);
-    for (int32_t i = i0; i < i1; i += 32) {
-        const uint32_t k = i + lane < i1 ? key(i + lane) & mask : 0u;
-        const bool gt = i + lane < i1 && k > known, eq = i + lane < i1 && k == known;
+    above = lower_above + before_warp(scan, 0), same = lower_same + before_warp(scan, 1);
+    each([&](int32_t i, uint32_t k, bool some) {
+        const bool gt = some && (k & mask) > known, eq = some && (k & mask) == known;
         const uint32_t gts = __ballot_sync(~0u, gt), eqs = __ballot_sync(~0u, eq);
         const uint32_t before = (1u << lane) - 1u;
         const uint32_t g = above + __popc(gts & before), e = same + __popc(eqs & before);
-        if (gt || (eq && e < left)) kept[g + min(e, left)] = j0 + i + lane;
+        if (gt || (eq && e < left)) kept[g + min(e, left)] = j0 + i;
         above += __popc(gts);
         same += __popc(eqs);
-    }
+    });
     newest();
-    if (BLOCKS > 1) cluster.barrier_wait();
 }
 
 // Where slot j of request r is in a plane, in bytes; -1: nowhere.
@@ -381,7 +396,7 @@ __global__ void __launch_bounds__(MOVE_THREADS, 2) gather_kernel(EvictArgs a) {
             const Mover<MOVE_THREADS, FOUR> mv = {a, rounds[(k + 1) & 1], weights, out, i0 + step, rows_of(k + 1)};
             mv.load(next);
         }
-        cluster.sync();                  // all of this round's rows are held
+        cluster.sync();                  // all of these rows are held
         const Mover<MOVE_THREADS, FOUR> mv = {a, rounds[k & 1], weights, out, i0, rows_of(k)};
         mv.store(x);
         __syncthreads();
@@ -434,7 +449,7 @@ kvr_status kvc_evict_launch(const kvc_cache *c, int32_t layer, const kvc_evict *
             blocks *= 2;
         return blocks;
     };
-    const int32_t choose = cluster_of(SHARE, 4);
+    const int32_t choose = cluster_of(SHARE, 2);
     a.chunks = (int32_t)std::max<int64_t>(1, (std::min<int64_t>(longest, p->keep) + a.rows - 1) / a.rows);
     a.by_chunks = kvr_make_div((uint32_t)a.chunks);
     if (heads * 8 > INT32_MAX || heads * a.chunks > INT32_MAX) return KVR_ERR_UNSUPPORTED;
