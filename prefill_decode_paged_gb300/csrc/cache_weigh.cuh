@@ -56,7 +56,7 @@ struct Weigh {
     static constexpr bool ABREAST = E2;
     static constexpr int RP = 8 * NT;
     static constexpr int Q_BYTES = RP * DP * 2;
-    // ring, queries, then of each row a float2 (its factor, its log-sum-exp), its end and its slope; 4 ints; prefix
+    // ring, queries, then of each row its factor, its log-sum-exp, its end and its slope; 4 ints; prefix
     static constexpr int FIXED = RING + Q_BYTES + 16 * RP + 16;
     static constexpr size_t smem(int32_t requests) { return FIXED + 4 * (size_t)(requests + 1); }
 };
@@ -68,8 +68,9 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t smem0 = (uint32_t)__cvta_generic_to_shared(smem);
     unsigned char *q_smem = smem + C::RING;
-    float2 *row_of = (float2 *)(q_smem + C::Q_BYTES);   // factor of the products, log-sum-exp, in powers of two
-    int32_t *row_end = (int32_t *)(row_of + RP);        // first key that the row does not see; none: no row
+    float *row_scale = (float *)(q_smem + C::Q_BYTES);  // factors of the products, log-sum-exps: in powers of two
+    float *row_lse = row_scale + RP;
+    int32_t *row_end = (int32_t *)(row_lse + RP);       // first key that the row does not see; none: no row
     float *row_slope = (float *)(row_end + RP);
     int32_t *shared_int = (int32_t *)(row_slope + RP);  // [4]
     int32_t *prefix = shared_int + 4;                   // [requests + 1], in units of one job
@@ -151,7 +152,6 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
             // the queries, one warp a row, asked for ahead of the keys
             constexpr int QW = RP / ATTEND_WARPS;
             uint4 qw[QW];
-            float lw[QW];
 #pragma unroll
             for (int k = 0; k < QW; ++k) {
                 const int row = k * ATTEND_WARPS + warp;
@@ -161,8 +161,17 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
                 const unsigned char *q = a.q + r * a.q_request + i * a.q_token + head * a.q_head;
                 qw[k] = make_uint4(0, 0, 0, 0);
                 if (row < rows && lane * 8 < a.D) qw[k] = __ldg((const uint4 *)q + lane);
-                lw[k] = 0.0f;
-                if (row < rows) lw[k] = __ldg(a.lse + ((int64_t)r * a.m + i) * ((int64_t)a.H * a.G) + head);
+            }
+            // (and one thread a row what else there is of it)
+            static_assert(RP <= ATTEND_THREADS, "");
+            float z_own = 0.0f, slope_own = 0.0f;
+            int32_t end_own = INT32_MIN;
+            if (tid < rows) {
+                const int32_t rho = row0 + tid, i = (int32_t)a.group.div((uint32_t)rho);
+                const int64_t head = (int64_t)h * a.G + rho - i * a.G;
+                z_own = __ldg(a.lse + ((int64_t)r * a.m + i) * ((int64_t)a.H * a.G) + head);
+                end_own = sp.n - a.m + i + 1;
+                slope_own = slope_of(a.scoring, (int32_t)head);
             }
             int32_t next_block;
             {
@@ -183,13 +192,13 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
                 const int row = k * ATTEND_WARPS + warp;
                 float factor = a.scale * log2e * ks;
                 place_query<DP, POOL>(q_smem, row, qw[k], a.f16, &factor);
-                if (lane == 0) {
-                    // (a row that sees nothing has nothing to give)
-                    row_of[row] = make_float2(factor, lw[k] == -INFINITY ? INFINITY : lw[k] * log2e);
-                    const int32_t rho = row0 + min(row, rows - 1), i = (int32_t)a.group.div((uint32_t)rho);
-                    row_end[row] = row < rows ? sp.n - a.m + i + 1 : INT32_MIN;
-                    row_slope[row] = slope_of(a.scoring, h * a.G + rho - i * a.G);
-                }
+                if (lane == 0) row_scale[row] = factor;
+            }
+            if (tid < RP) {
+                // (a row that sees nothing has nothing to give)
+                row_lse[tid] = z_own == -INFINITY ? INFINITY : z_own * log2e;
+                row_end[tid] = end_own;
+                row_slope[tid] = slope_own;
             }
             __syncthreads();
 
@@ -198,8 +207,8 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
             for (int k = 0; k < NT; ++k)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float2 of = row_of[k * 8 + 2 * t4 + e];
-                    sc[k][e] = of.x, z[k][e] = of.y;
+                    sc[k][e] = row_scale[k * 8 + 2 * t4 + e];
+                    z[k][e] = row_lse[k * 8 + 2 * t4 + e];
                 }
             const bool plain = a.scoring.cap == 0.0f && a.scoring.slopes == nullptr;
             const int32_t seen_all = rows < RP ? INT32_MIN : sp.n - a.m + 1;     // keys below it are seen by every row
