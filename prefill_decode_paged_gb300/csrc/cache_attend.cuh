@@ -311,14 +311,25 @@ __device__ __forceinline__ void values_e2m1(float (&o)[DP / 16][NT][4], const ui
     }
 }
 
-// A query's 8 elements of this lane in the type of the products into row `row` of the queries' memory (a
-// warp's lanes hold one query). Codes are multiplied by f16: the row is scaled to that by a power of two,
-// which goes into *factor.
+// Queries on their way to shared memory: a lane holds 8 elements of one, a warp so many at a time.
+template <int DP, int RP>
+struct QueryLanes {
+    static constexpr int LANES = DP / 8, ROWS = 32 / LANES;      // of a query; queries
+    static constexpr int TIMES = RP > ATTEND_WARPS * ROWS ? RP / (ATTEND_WARPS * ROWS) : 1;
+    static __device__ __forceinline__ int row(int time) {        // RP or more: none (of the whole warp)
+        return (time * ATTEND_WARPS + (int)threadIdx.x / 32) * ROWS + (int)threadIdx.x % 32 / LANES;
+    }
+    static __device__ __forceinline__ int lane() { return (int)threadIdx.x % LANES; }
+};
+
+// A query's 8 elements of this lane in the type of the products into row `row` of the queries' memory. Codes are
+// multiplied by f16: the row is scaled to that by a power of two, which goes into *factor.
 template <int DP, int POOL>
 __device__ __forceinline__ void place_query(unsigned char *q_smem, int row, uint4 w, int32_t type_f16, float *factor) {
-    const int lane = threadIdx.x % 32;
+    constexpr int LANES = DP / 8;
+    const int lane = threadIdx.x % LANES;
     if constexpr (POOL != KVR_DTYPE_FP8_E4M3 && POOL != KVC_DTYPE_E2M1) {
-        if (lane * 8 < DP) *(uint4 *)(q_smem + swizzled<DP * 2>(row, lane)) = w;
+        *(uint4 *)(q_smem + swizzled<DP * 2>(row, lane)) = w;
     } else {
         float f[8], top = 0.0f;
         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
@@ -329,7 +340,7 @@ __device__ __forceinline__ void place_query(unsigned char *q_smem, int row, uint
             top = fmaxf(top, fmaxf(fabsf(p.x), fabsf(p.y)));
         }
 #pragma unroll
-        for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        for (int o = LANES / 2; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
         // down = 2^-e with 2^e <= top < 2^(e+1): exponents kept where both are normal
         uint32_t e = __float_as_uint(top) >> 23;
         e = e < 2 || e > 252 ? 127 : e;
@@ -340,12 +351,11 @@ __device__ __forceinline__ void place_query(unsigned char *q_smem, int row, uint
         // 4 bits: pair y of elements 8 t + 2 y, 8 t + 2 y + 1 of 32 is at 8 y + 2 t: a lane's 8
         // codes of a row are two pairs each for two steps of 16 elements
         if (POOL == KVC_DTYPE_E2M1) {
-            if (lane * 8 < DP)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    *(uint32_t *)(q_smem + swizzled<DP * 2>(row, (lane / 4) * 4 + k) + (lane % 4) * 4) =
-                        narrow2<true>(f[2 * k] * down, f[2 * k + 1] * down);
-        } else if (lane * 8 < DP) {
+            for (int k = 0; k < 4; ++k)
+                *(uint32_t *)(q_smem + swizzled<DP * 2>(row, (lane / 4) * 4 + k) + (lane % 4) * 4) =
+                    narrow2<true>(f[2 * k] * down, f[2 * k + 1] * down);
+        } else {
             const int grp = lane / 2, half = lane % 2;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -581,18 +591,18 @@ attend_kernel(AttendArgs a) {
             }
             issue(stage, slot_of(t, id));
         };
-        // the queries, one warp a row, asked for ahead of the keys
-        constexpr int QW = RP / ATTEND_WARPS;
-        uint4 qw[QW];
+        // the queries, asked for ahead of the keys
+        using Queries = QueryLanes<DP, RP>;
+        uint4 qw[Queries::TIMES];
 #pragma unroll
-        for (int n = 0; n < QW; ++n) {
-            const int row = n * ATTEND_WARPS + warp;
+        for (int n = 0; n < Queries::TIMES; ++n) {
+            const int row = Queries::row(n);
             const int32_t rho = row0 + row;
             const int32_t i = (int32_t)a.group.div((uint32_t)rho), gq = rho - i * a.G;
             const unsigned char *q = a.q + r * a.q_request + i * a.q_token +
                                      ((int64_t)h * a.G + gq) * a.q_head;
             qw[n] = make_uint4(0, 0, 0, 0);
-            if (row < rows && lane * 8 < a.D) qw[n] = __ldg((const uint4 *)q + lane);
+            if (row < rows && Queries::lane() * 8 < a.D) qw[n] = __ldg((const uint4 *)q + Queries::lane());
         }
         int32_t next_block;
         {
@@ -610,11 +620,12 @@ attend_kernel(AttendArgs a) {
 
         // the queries in the type of the products; rows beyond M are zero
 #pragma unroll
-        for (int n = 0; n < QW; ++n) {
-            const int row = n * ATTEND_WARPS + warp;
+        for (int n = 0; n < Queries::TIMES; ++n) {
+            const int row = Queries::row(n);
+            if (row >= RP) continue;
             float factor = a.scale * log2e * ks;
             place_query<DP, POOL>(q_smem, row, qw[n], a.f16, &factor);
-            if (lane == 0) row_scale[row] = factor;
+            if (Queries::lane() == 0) row_scale[row] = factor;
         }
         __syncthreads();
 

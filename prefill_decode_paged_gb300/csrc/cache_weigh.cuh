@@ -149,18 +149,18 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
         for (int32_t chunk = 0; chunk < a.chunks; ++chunk) {
             const int32_t row0 = chunk * RP, rows = min(RP, M - row0);
             const bool adding = a.add || chunk > 0;
-            // the queries, one warp a row, asked for ahead of the keys
-            constexpr int QW = RP / ATTEND_WARPS;
-            uint4 qw[QW];
+            // the queries, asked for ahead of the keys
+            using Queries = QueryLanes<DP, RP>;
+            uint4 qw[Queries::TIMES];
 #pragma unroll
-            for (int k = 0; k < QW; ++k) {
-                const int row = k * ATTEND_WARPS + warp;
+            for (int k = 0; k < Queries::TIMES; ++k) {
+                const int row = Queries::row(k);
                 const int32_t rho = row0 + row;
                 const int32_t i = (int32_t)a.group.div((uint32_t)rho), gq = rho - i * a.G;
                 const int64_t head = (int64_t)h * a.G + gq;
                 const unsigned char *q = a.q + r * a.q_request + i * a.q_token + head * a.q_head;
                 qw[k] = make_uint4(0, 0, 0, 0);
-                if (row < rows && lane * 8 < a.D) qw[k] = __ldg((const uint4 *)q + lane);
+                if (row < rows && Queries::lane() * 8 < a.D) qw[k] = __ldg((const uint4 *)q + Queries::lane());
             }
             // (and one thread a row what else there is of it)
             static_assert(RP <= ATTEND_THREADS, "");
@@ -188,11 +188,12 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
             }
             __syncthreads();                            // the queries before these have been used
 #pragma unroll
-            for (int k = 0; k < QW; ++k) {
-                const int row = k * ATTEND_WARPS + warp;
+            for (int k = 0; k < Queries::TIMES; ++k) {
+                const int row = Queries::row(k);
+                if (row >= RP) continue;
                 float factor = a.scale * log2e * ks;
                 place_query<DP, POOL>(q_smem, row, qw[k], a.f16, &factor);
-                if (lane == 0) row_scale[row] = factor;
+                if (Queries::lane() == 0) row_scale[row] = factor;
             }
             if (tid < RP) {
                 // (a row that sees nothing has nothing to give)
