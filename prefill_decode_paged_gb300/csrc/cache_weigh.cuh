@@ -12,9 +12,10 @@
 // and three exchanges give each lane of four one key's sum, so that a warp writes 32 neighbours at once.
 // Scores, exponentials and sums are fp32.
 //
-// Measured: 64 requests of 8192 keys, 8 heads of 128, 8 rows: bf16 170 us (6.4 TB/s, HBM), E4M3 102 (5.4), 4 bits 74
-// (4.4; conversions). 4 requests of up to 32768 E4M3 keys under 64 rows 47 us: mma.sync at half its rate. With 32 rows a
-// pass, which takes the keys and their conversion twice, 67; with tiles of 16 keys and three blocks an SM 49.
+// Measured: 64 requests of 8192 keys, 8 heads of 128, 8 rows: bf16 166 to 170 us from card to card (6.4 to 6.6 TB/s,
+// HBM), E4M3 96 to 102 (5.4 to 5.8), 4 bits 68 (4.7; conversions). 4 requests of up to 32768 E4M3 keys under 64 rows
+// 38.7 us: mma.sync at 57 % of its rate. With 32 rows a pass, which takes the keys and their conversion twice, and tiles
+// of 16 keys it took 1.4 and 1.04 times as long.
 #pragma once
 
 #include "cache_attend.cuh"
@@ -54,6 +55,9 @@ struct Weigh {
     static constexpr int UNIT = ATTEND_WARPS * KT;
     // (as in attention: the block scales of a token's heads share a sector)
     static constexpr bool ABREAST = E2;
+    // Tiles that lie in one block are addressed from their first row on where instructions count: 4 bits (64 requests
+    // of 8192 keys 74 -> 68 us) and 8 bits under many rows (4 prompts, 64 rows 39.9 -> 38.7), not under few (102 -> 104.5)
+    static constexpr bool RUNS = E2 || (E4 && NT > 2);
     static constexpr int RP = 8 * NT;
     static constexpr int Q_BYTES = RP * DP * 2;
     // ring, queries, then of each row its factor, its log-sum-exp, its end and its slope; 4 ints; prefix
@@ -146,6 +150,43 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
             }
         };
 
+        // A tile that is whole and in one block: from its first row on
+        const bool runs = C::RUNS && a.split.slots.block.d % KT == 0 && sp.lo % KT == 0;
+        auto issue_run = [&](int32_t stage, int32_t t, int32_t id) {
+            constexpr int CPR = ROW / 16, RPI = 32 / CPR;
+            const uint32_t base = ring + (uint32_t)(stage * C::STAGE);
+            const int32_t j = sp.lo + t * KT, c = lane % CPR;
+            const int32_t in = j - (int32_t)(a.split.slots.block.div((uint32_t)j) * a.split.slots.block.d);
+            const int64_t first = id * a.k_plane.block_stride + in * a.k_plane.token_stride + head_off;
+            const uint32_t n = (C::E2 ? c * 32 < a.D : c * 16 < a.D) ? 16 : 0;   // (0: nothing is read)
+            const unsigned char *k =
+                a.k_plane.base + first + (lane / CPR) * a.k_plane.token_stride + (n != 0 ? c * 16 : 0);
+            const int64_t step = RPI * a.k_plane.token_stride;
+#pragma unroll
+            for (int i = 0; i < KT / RPI; ++i, k += step)
+                cp_async16<!C::E2 || ROW >= 128>(base + swizzled<ROW>(i * RPI + lane / CPR, c), k, n);
+            if (C::E2) {
+                constexpr int PIECE = DP == 128 ? 8 : 4;
+                const int64_t scale = (first + lane * a.k_plane.token_stride) / 8;
+#pragma unroll
+                for (int p = 0; p < C::SROW / PIECE; ++p) {
+                    const bool there = p * PIECE * 16 < a.D;
+                    cp_async_few<PIECE>(base + KT * ROW + lane * C::SROW + p * PIECE,
+                                        a.k_block_scales + (there ? scale + p * PIECE : 0), there ? PIECE : 0);
+                }
+            }
+        };
+        // (the block's id is the same in all lanes there)
+        auto issue_tile = [&](int32_t stage, int32_t t, int32_t id) {
+            if constexpr (C::RUNS) {
+                if (runs && sp.lo + (t + 1) * KT <= sp.n && id >= 0 && id < a.split.slots.num_blocks) {
+                    issue_run(stage, t, id);
+                    return;
+                }
+            }
+            issue(stage, slot_of(t, id));
+        };
+
         for (int32_t chunk = 0; chunk < a.chunks; ++chunk) {
             const int32_t row0 = chunk * RP, rows = min(RP, M - row0);
             const bool adding = a.add || chunk > 0;
@@ -181,7 +222,7 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
 #pragma unroll
                 for (int k = 0; k < C::STAGES - 1; ++k) {
                     const int32_t t = t_begin + k * ATTEND_WARPS;
-                    if (t < t_end) issue(k, slot_of(t, ids[k]));
+                    if (t < t_end) issue_tile(k, t, ids[k]);
                     cp_async_commit();
                 }
                 next_block = ids[C::STAGES - 1];
@@ -230,7 +271,7 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
                 {
                     const int32_t tn = t + (C::STAGES - 1) * ATTEND_WARPS;
                     const int into = stage == 0 ? C::STAGES - 1 : stage - 1;
-                    if (tn < t_end) issue(into, slot_of(tn, next_block));
+                    if (tn < t_end) issue_tile(into, tn, next_block);
                     cp_async_commit();
                     next_block = block_of(tn + ATTEND_WARPS);
                 }
