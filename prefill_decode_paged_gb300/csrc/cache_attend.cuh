@@ -100,13 +100,14 @@ struct Attend {
     static constexpr int STAGE = 2 * KT * (ROW + SROW);          // keys, values, then their block scales
     // Blocks resident on an SM, and tiles of a warp's ring. 4 bits: as many blocks as their registers allow, for
     // instructions bound them (64 requests of 8192 keys, 8 queries a head: 2 blocks of 5 tiles 142 us, 3 of 3 132.5,
-    // 4 of 2 134); a small ring costs long requests' joins (one of 65536: 31, 36 and 44).
+    // 4 of 2 134; heads of 64: 4 blocks of 5 95, 4 of 3 90.5, 5 of 3 94; of 256 under 16 rows: rings of 3, which leave
+    // room for one block, 208, of 2 160); a small ring costs long requests' joins (one of 65536: 31, 36 and 44).
     static constexpr int BLOCKS = !E2                                ? (STAGE > 8192 ? 1 : 2)
                                   : NT > 2 || (NT > 1 && DP > 128)   ? 2
                                   : NT == 1 && DP == 64              ? 4 : 3;
     static constexpr int STAGES = !E2         ? (STAGE >= 8192 ? 3 : 6)
-                                  : DP > 128  ? (NT == 1 ? 2 : 3)
-                                  : BLOCKS == 3 ? 3 : 5;
+                                  : DP > 128  ? 2
+                                  : BLOCKS > 2 ? 3 : 5;
     static constexpr int RING = ATTEND_WARPS * STAGES * STAGE;
     static constexpr int UNIT = ATTEND_WARPS * KT;               // keys of a unit
     // One block a head goes through the same part of the line: the block scales of a token's heads share a sector
