@@ -369,7 +369,12 @@ extern "C" kvr_status kv_cache_append(const kvc_cache *c, int32_t layer, const k
     if (st != KVR_OK) return st;
     if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
     if (a->num_tokens == 0) return KVR_OK;
-    return kvc_append_launch(c, layer, a, stream);
+    try {
+        std::lock_guard<std::mutex> lock(c->use);
+        return kvc_append_launch(c, layer, a, stream);
+    } catch (...) {
+        return KVR_ERR_NOMEM;
+    }
 }
 
 kvr_status kvc_check_attend(const kvc_cache *c, int32_t layer, const kvc_attend *a) {

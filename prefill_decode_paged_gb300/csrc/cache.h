@@ -56,7 +56,9 @@ struct kvc_cache {
     int32_t piece = 0;                // tokens of a map's box; 0: there are no maps
     int device = 0;
     int sm_count = 0;
-    mutable std::mutex use;           // held over the two launches of an attention over latents
+    // Held over the launches of a call that has two, an attention over latents or an eviction, and over those of
+    // calls that write what an eviction reads or moves: append, weigh.
+    mutable std::mutex use;
 
     KvcPlane plane(int32_t layer, int32_t comp) const {
         return {(unsigned char *)(uintptr_t)base[(size_t)layer * d.num_components + comp],

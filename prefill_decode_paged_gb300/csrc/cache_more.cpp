@@ -38,6 +38,15 @@ kvr_status guarded(F launch) {
         return KVR_ERR_NOMEM;
     }
 }
+// The same for calls that write rows or weights: an eviction chooses by a first launch what a second moves, and no
+// other thread's call may change it between them on their stream.
+template <typename F>
+kvr_status together(const kvc_cache *c, F launch) {
+    return guarded([&] {
+        std::lock_guard<std::mutex> lock(c->use);
+        return launch();
+    });
+}
 int64_t address(const void *p) { return (int64_t)(uintptr_t)p; }
 
 }  // namespace
@@ -49,7 +58,7 @@ extern "C" kvr_status kv_cache_append_at(const kvc_cache *c, int32_t layer, cons
     if (address(angles) % 4 != 0) return KVR_ERR_ALIGNMENT;
     if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
     if (a->num_tokens == 0) return KVR_OK;
-    return guarded([&] { return kvc_append_at_launch(c, layer, a, angles, stream); });
+    return together(c, [&] { return kvc_append_at_launch(c, layer, a, angles, stream); });
 }
 
 kvr_status kvc_check_scoring(const kvc_cache *c, const kvc_scoring &s) {
@@ -102,7 +111,7 @@ extern "C" kvr_status kv_cache_weigh(const kvc_cache *c, int32_t layer, const kv
     if (st != KVR_OK) return st;
     if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
     if (a->num_requests == 0) return KVR_OK;
-    return guarded([&] { return kvc_weigh_launch(c, layer, a, stream); });
+    return together(c, [&] { return kvc_weigh_launch(c, layer, a, stream); });
 }
 
 extern "C" kvr_status kv_cache_evict(const kvc_cache *c, int32_t layer, const kvc_evict *a, void *stream) {
@@ -139,7 +148,7 @@ extern "C" kvr_status kv_cache_evict(const kvc_cache *c, int32_t layer, const kv
         return KVR_ERR_ALIGNMENT;
     if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
     if (a->num_requests == 0) return KVR_OK;
-    return guarded([&] { return kvc_evict_launch(c, layer, a, stream); });
+    return together(c, [&] { return kvc_evict_launch(c, layer, a, stream); });
 }
 
 extern "C" kvr_status kv_cache_read(const kvc_cache *c, int32_t layer, const kvc_read *a, void *stream) {
