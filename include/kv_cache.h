@@ -276,7 +276,7 @@ kvr_status kv_cache_weigh(const kvc_cache *cache, int32_t layer, const kvc_weigh
  * Evict tokens of layer `layer` by their weights, each key head for itself. Of the n = lengths[r] cached tokens of a
  * request stay: all, if n <= keep; otherwise the `recent` newest and, of the others, the keep - recent of the
  * largest weights (equal ones: the lower slots; NaN counts as above all numbers). What stays keeps its order
- * and goes to slots 0 .. min(n, keep) - 1 through the table `into` (ids NULL, or the same table: in place). Keys and values are
+ * and goes to slots 0 .. min(n, keep) - 1 through the table `into` (all zeros, or the same table: in place). Keys and values are
  * moved bit for bit. weights_out gets the weights of what stays in the same order, then zeros up to entry n (beyond,
  * it is left as it was), and kept[r][h] the slots that they had (entries from min(n, keep) on are left). The
  * lengths do not change: afterwards min(lengths[r], keep) tokens are cached, and the next is appended at that

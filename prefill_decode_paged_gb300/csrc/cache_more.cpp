@@ -123,6 +123,10 @@ extern "C" kvr_status kv_cache_evict(const kvc_cache *c, int32_t layer, const kv
         a->weights_width < 0 || !kvc_ok_table(a->table) || a->table.rows < a->num_requests ||
         !kvc_ok_table(a->into) || (a->into.ids != nullptr && a->into.rows < a->num_requests))
         return KVR_ERR_INVALID_ARG;
+    // (no table at all means in place; one without entries is a mistake that would rewrite the requests' own blocks)
+    if (a->num_requests > 0 && a->into.ids == nullptr &&
+        (a->into.rows != 0 || a->into.width != 0 || a->into.stride != 0))
+        return KVR_ERR_INVALID_ARG;
     // a table in another form of the same memory would be neither in place nor apart
     if (a->into.ids != nullptr && a->into.ids == a->table.ids &&
         (a->into.width != a->table.width || (a->num_requests > 1 && a->into.stride != a->table.stride)))

@@ -552,6 +552,8 @@ class KVCache:
             raise ValueError(f"slots are {slots.dtype} {list(slots.shape)} on {slots.device}; expected contiguous "
                              f"int32 {list(shape)} on {self._device}")
         there = (0, 0, 0, 0) if into is None else self._table(into)
+        if into is not None and there[3] == 0 and R > 0:
+            raise ValueError(f"into is {list(into.shape)}: a table without blocks")
         st = self._evict(
             self._handle(), layer,
             _EVICT.pack(R, keep, recent, width, self._list(lengths, "lengths", R), *self._table(block_table), *there,

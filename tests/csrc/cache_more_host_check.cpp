@@ -145,7 +145,29 @@ static int threads() {
     return 0;
 }
 
+// What an eviction goes into: no table at all is in place, an empty one is refused.
+static int into() {
+    kvc_cache *c;
+    REQUIRE(make_cache(&c) == KVR_OK);
+    kvc_evict e = an_eviction();
+    REQUIRE(kv_cache_evict(c, 0, &e, nullptr) == KVR_OK && launches == 1);
+    e.into = a_table();
+    REQUIRE(kv_cache_evict(c, 0, &e, nullptr) == KVR_OK && launches == 2);
+    for (int what = 0; what < 3; ++what) {
+        e.into = {};
+        (what == 0 ? e.into.rows : e.into.width) = what == 2 ? 0 : 3;      // (no columns; no rows)
+        if (what == 2) e.into.stride = 3;
+        REQUIRE(kv_cache_evict(c, 0, &e, nullptr) == KVR_ERR_INVALID_ARG && launches == 2);
+    }
+    // of no requests nothing is asked
+    e.num_requests = 0, e.into.width = 3;
+    REQUIRE(kv_cache_evict(c, 0, &e, nullptr) == KVR_OK && launches == 2);
+    kv_cache_destroy(c);
+    return 0;
+}
+
 int main(int argc, char **argv) {
+    if (argc > 1 && strcmp(argv[1], "into") == 0) return into();
     if (argc > 1 && strcmp(argv[1], "threads") == 0) return threads();
     return 2;
 }

@@ -26,3 +26,7 @@ def play(harness, what):
 
 def test_an_evictions_steps_stay_together_among_host_threads(harness):
     play(harness, "threads")
+
+
+def test_an_empty_table_is_not_an_eviction_in_place(harness):
+    play(harness, "into")
