@@ -171,7 +171,8 @@ kvr_status kv_cache_append_at(const kvc_cache *cache, int32_t layer, const kvc_a
  * Read tokens back: row t of k and v gets what the pool holds for token positions[t] of request requests[t],
  * as numbers of `dtype` (the pool's type if that has 16 bits; others are decoded, scaled in fp32 and
  * rounded once, nearest-even). Padding (a negative position) and tokens whose request, position or block is out of range
- * (flagged) give zeros. Requirements as for kv_cache_append.
+ * (flagged) give zeros. Requirements as for kv_cache_append; rows of k, and of v, that overlap one another are
+ * KVR_ERR_POOL_OVERLAP, and k, v and the pool must not overlap.
  */
 typedef struct kvc_read {
     int32_t num_tokens;        /* >= 0 */

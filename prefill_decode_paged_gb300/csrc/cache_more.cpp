@@ -18,7 +18,7 @@ bool negative(std::initializer_list<int64_t> xs) {
         if (x < 0) return true;
     return false;
 }
-// Rows of `row` entries, `outer` by `inner` of them, do not overlap.
+// Rows of `row` entries (or bytes), `outer` by `inner` of them, do not overlap.
 bool disjoint_rows(int64_t outer, int64_t outer_stride, int64_t inner, int64_t inner_stride, int64_t row) {
     if (outer <= 1) outer_stride = INT64_MAX;
     if (inner <= 1) inner_stride = INT64_MAX;
@@ -169,6 +169,12 @@ extern "C" kvr_status kv_cache_read(const kvc_cache *c, int32_t layer, const kvc
         !multiples(16, {address(a->k), address(a->v), a->k_token_stride, a->k_head_stride,
                         a->v_token_stride, a->v_head_stride}))
         return KVR_ERR_ALIGNMENT;
+    // (each row is written by threads of its own)
+    const int32_t H = c->d.kv_heads, row = 2 * c->d.head_dim;
+    if (a->num_tokens > 0 &&
+        (!disjoint_rows(a->num_tokens, a->k_token_stride, H, a->k_head_stride, row) ||
+         (!c->latent() && !disjoint_rows(a->num_tokens, a->v_token_stride, H, a->v_head_stride, row))))
+        return KVR_ERR_POOL_OVERLAP;
     if (!kvc_on_device(c)) return KVR_ERR_INVALID_ARG;
     if (a->num_tokens == 0) return KVR_OK;
     return guarded([&] { return kvc_read_launch(c, layer, a, stream); });

@@ -166,7 +166,37 @@ static int into() {
     return 0;
 }
 
+// Where read writes: rows that overlap one another are refused, whichever input has them.
+static int overlap() {
+    kvc_cache *c;
+    REQUIRE(make_cache(&c) == KVR_OK);
+    kvc_read good = {};
+    good.num_tokens = 3, good.dtype = KVR_DTYPE_BF16, good.requests = good.positions = AT(const int32_t);
+    good.table = a_table(), good.k = good.v = AT(void);
+    good.k_token_stride = good.v_token_stride = 256, good.k_head_stride = good.v_head_stride = 128;
+    // [T][H][D], wider rows, [H][T][D], and one token's strides of zero
+    const int64_t fits[][3] = {{3, 256, 128}, {3, 768, 128}, {3, 128, 384}, {1, 0, 128}, {0, 0, 0}};
+    // all tokens at one place, all heads, rows within one another, heads that reach the next token
+    const int64_t bad[][3] = {{3, 0, 128}, {3, 256, 0}, {3, 112, 1024}, {3, 256, 112}, {3, 240, 128}, {3, 128, 240}};
+    for (int which = 0; which < 2; ++which) {
+        auto with = [&](const int64_t s[3]) {
+            kvc_read r = good;
+            r.num_tokens = (int32_t)s[0];
+            (which == 0 ? r.k_token_stride : r.v_token_stride) = s[1];
+            (which == 0 ? r.k_head_stride : r.v_head_stride) = s[2];
+            return kv_cache_read(c, 0, &r, nullptr);
+        };
+        for (const auto &s : fits) REQUIRE(with(s) == KVR_OK);
+        const int before = launches;
+        for (const auto &s : bad) REQUIRE(with(s) == KVR_ERR_POOL_OVERLAP);
+        REQUIRE(launches == before);
+    }
+    kv_cache_destroy(c);
+    return 0;
+}
+
 int main(int argc, char **argv) {
+    if (argc > 1 && strcmp(argv[1], "overlap") == 0) return overlap();
     if (argc > 1 && strcmp(argv[1], "into") == 0) return into();
     if (argc > 1 && strcmp(argv[1], "threads") == 0) return threads();
     return 2;

@@ -30,3 +30,7 @@ def test_an_evictions_steps_stay_together_among_host_threads(harness):
 
 def test_an_empty_table_is_not_an_eviction_in_place(harness):
     play(harness, "into")
+
+
+def test_rows_that_are_read_into_do_not_overlap(harness):
+    play(harness, "overlap")
