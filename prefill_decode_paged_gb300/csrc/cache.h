@@ -161,6 +161,19 @@ __device__ __forceinline__ void let_next_start() {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// The entries of [from, end) that one of `threads` threads (at most 2^30) takes, every `threads`-th from its own on: for
+// (Share s(..); s.more(); s.next()) s.at(). Without a sign: `end` may be so large that the next would pass 2^31.
+class Share {
+    uint32_t i, end, step;
+
+public:
+    __host__ __device__ __forceinline__ Share(int32_t from, int32_t end_, int32_t thread, int32_t threads)
+        : i((uint32_t)from + (uint32_t)thread), end((uint32_t)end_), step((uint32_t)threads) {}
+    __host__ __device__ __forceinline__ bool more() const { return i < end; }
+    __host__ __device__ __forceinline__ void next() { i += step; }
+    __host__ __device__ __forceinline__ int32_t at() const { return (int32_t)i; }
+};
+
 // The two halves of a 32-bit word as fp32 (exact), and back with one rounding each.
 template <bool F16>
 __device__ __forceinline__ float2 widen2(uint32_t w) {

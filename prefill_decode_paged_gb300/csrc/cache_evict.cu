@@ -35,6 +35,7 @@ constexpr int MOST_BLOCKS = 8;     // of a cluster
 constexpr int SHARE = 2048;        // weights of a block, above which a head gets another, while there is room for it
 constexpr int HELD = 8;            // weights that a thread holds; those beyond are read each time
 constexpr int COPY_THREADS = 128, MOVE_THREADS = 256;
+constexpr int MOST_CLEARING = 1 << 20;   // blocks of a head that clear weights behind what stays, into other blocks
 constexpr int UNITS = 8;           // 16-byte units of a thread at a time
 constexpr int WORDS = 9;           // words of a thread besides: a weight, and block scales of 4-bit rows
 
@@ -98,14 +99,14 @@ __global__ void __launch_bounds__(SELECT_THREADS) select_kernel(EvictArgs a) {
     int32_t *kept = a.kept + (int64_t)head * a.keep;
     // (every block of the cluster goes the same way here and below)
     if (n <= a.keep) {
-        for (int32_t i = part * SELECT_THREADS + tid; i < n; i += blocks * SELECT_THREADS) kept[i] = i;
+        for (Share s(0, n, part * SELECT_THREADS + tid, blocks * SELECT_THREADS); s.more(); s.next()) kept[s.at()] = s.at();
         return;
     }
     const int32_t old = n - a.recent, need = a.keep - a.recent;
     // (written last: a barrier of the cluster waits for stores before it)
     auto newest = [&] {
-        for (int32_t i = part * SELECT_THREADS + tid; i < a.recent; i += blocks * SELECT_THREADS)
-            kept[need + i] = old + i;
+        for (Share s(0, a.recent, part * SELECT_THREADS + tid, blocks * SELECT_THREADS); s.more(); s.next())
+            kept[need + s.at()] = old + s.at();
     };
     if (need == 0) {
         newest();
@@ -349,8 +350,11 @@ __global__ void __launch_bounds__(COPY_THREADS, 8) copy_kernel(EvictArgs a) {
     const int32_t n = tokens_of(a, r, &bad), total = min(n, a.keep);
     bad = 0;                             // (told by the kernel before)
     float *out = a.weights_out + r * a.out_request + h * a.out_head;
-    for (int32_t j = total + chunk * COPY_THREADS + (int32_t)threadIdx.x; j < n; j += a.chunks * COPY_THREADS)
-        out[j] = 0.0f;
+    // (a head of 2^28 tokens has so many blocks that not all of their threads can be counted in 32 bits)
+    const int32_t clearing = min(a.chunks, MOST_CLEARING);
+    if (chunk < clearing)
+        for (Share s(total, n, chunk * COPY_THREADS + (int32_t)threadIdx.x, clearing * COPY_THREADS); s.more(); s.next())
+            out[s.at()] = 0.0f;
     const int32_t i0 = chunk * a.rows, count = min(a.rows, total - i0);
     if (count <= 0) return;
     place_rows(a, rd, a.kept + (int64_t)head * a.keep, r, h, i0, count, &bad);
@@ -404,8 +408,8 @@ __global__ void __launch_bounds__(MOVE_THREADS, 2) gather_kernel(EvictArgs a) {
     }
     if (bad != 0) atomicOr(a.flags, bad);
     // (every source of a row has been read)
-    for (int32_t j = total + part * MOVE_THREADS + (int32_t)threadIdx.x; j < n; j += blocks * MOVE_THREADS)
-        out[j] = 0.0f;
+    for (Share s(total, n, part * MOVE_THREADS + (int32_t)threadIdx.x, blocks * MOVE_THREADS); s.more(); s.next())
+        out[s.at()] = 0.0f;
 }
 
 }  // namespace

@@ -28,9 +28,9 @@ def run(bodies):
 
 
 def test_weights_of_another_thread_do_not_come_between_choice_and_move():
-    """One thread writes either of two patterns of weights, again and again, another evicts by them, on one stream:
+    """Threads write either of two patterns of weights, again and again, another evicts by them, on one stream:
     each eviction's slots and weights are those of the one pattern or of the other."""
-    R, H, keep, recent, times = 2, 2, 150, 10, 400
+    R, H, keep, recent, times = 2, 2, 150, 10, 1500
     case = More(121, [700, 333], heads=H, queries=4, dim=64)
     stream = torch.cuda.Stream()
     need = -(-keep // 16)
@@ -67,7 +67,7 @@ def test_weights_of_another_thread_do_not_come_between_choice_and_move():
         finally:
             done.set()
 
-    run([write, evict])
+    run([write] * 4 + [evict])
     cache.check()
     of = [((outs == w).flatten(1).all(1), (slots == s).flatten(1).all(1)) for w, s in want]
     mixed = sum(int((of[a][0] & of[b][1]).sum()) for a, b in ((0, 1), (1, 0)))
