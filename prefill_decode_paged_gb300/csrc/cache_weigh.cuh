@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
     unsigned char *q_smem = smem + C::RING;
     float *row_scale = (float *)(q_smem + C::Q_BYTES);  // factors of the products, log-sum-exps: in powers of two
     float *row_lse = row_scale + RP;
-    int32_t *row_end = (int32_t *)(row_lse + RP);       // first key that the row does not see; none: no row
+    int32_t *row_end = (int32_t *)(row_lse + RP);       // first key that the row does not see; 0: no row
     float *row_slope = (float *)(row_end + RP);
     int32_t *shared_int = (int32_t *)(row_slope + RP);  // [4]
     int32_t *prefix = shared_int + 4;                   // [requests + 1], in units of one job
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
             // (and one thread a row what else there is of it)
             static_assert(RP <= ATTEND_THREADS, "");
             float z_own = 0.0f, slope_own = 0.0f;
-            int32_t end_own = INT32_MIN;
+            int32_t end_own = 0;                        // (no row: sees no key, and its distances stay within 32 bits)
             if (tid < rows) {
                 const int32_t rho = row0 + tid, i = (int32_t)a.group.div((uint32_t)rho);
                 const int64_t head = (int64_t)h * a.G + rho - i * a.G;
