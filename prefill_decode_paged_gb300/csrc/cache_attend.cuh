@@ -98,13 +98,14 @@ struct Attend {
     static constexpr int KT = 2 * 16 * ROW >= 8192 ? 16 : 32;    // keys of a tile
     static constexpr int KS = KT / 16;
     static constexpr int STAGE = 2 * KT * (ROW + SROW);          // keys, values, then their block scales
-    // Blocks resident on an SM, and tiles of a warp's ring. 4 bits: as many blocks as their registers allow, for
-    // instructions bound them (64 requests of 8192 keys, 8 queries a head: 2 blocks of 5 tiles 142 us, 3 of 3 132.5,
-    // 4 of 2 134; heads of 64: 4 blocks of 5 95, 4 of 3 90.5, 5 of 3 94; of 256 under 16 rows: rings of 3, which leave
-    // room for one block, 208, of 2 160); a small ring costs long requests' joins (one of 65536: 31, 36 and 44).
-    static constexpr int BLOCKS = !E2                                ? (STAGE > 8192 ? 1 : 2)
-                                  : NT > 2 || (NT > 1 && DP > 128)   ? 2
-                                  : NT == 1 && DP == 64              ? 4 : 3;
+    // Blocks resident on an SM, and tiles of a warp's ring. 4 bits: as many blocks as their registers allow up to heads
+    // of 128 (64 requests of 8192 keys, 8 queries a head: 2 blocks of 5 tiles 142 us, 3 of 3 132.5, 4 of 2 134; heads of
+    // 64: 4 blocks of 5 95, 4 of 3 90.5, 5 of 3 94). A small ring costs long requests' joins (one of 65536: 31, 36 and
+    // 44). Larger heads: as many as shared memory holds, two with rings of 2 (4 heads of 256, 16 rows: rings of 3, which
+    // leave room for one block, 208, of 2 160; 8 rows: with registers for three blocks, which never fit, 124, for two 121).
+    static constexpr int BLOCKS = !E2                     ? (STAGE > 8192 ? 1 : 2)
+                                  : NT > 2 || DP > 128    ? 2
+                                  : NT == 1 && DP == 64   ? 4 : 3;
     static constexpr int STAGES = !E2         ? (STAGE >= 8192 ? 3 : 6)
                                   : DP > 128  ? 2
                                   : BLOCKS > 2 ? 3 : 5;
@@ -997,6 +998,7 @@ struct AttendPick {
 template <int DP, int POOL, int NT, bool SCORED>
 inline AttendPick attend_instance() {
     using C = Attend<DP, POOL, NT>;
+    static_assert(C::BLOCKS * (C::smem(1) + 1024) <= 228 << 10, "blocks that shared memory holds");
     return {attend_kernel<DP, POOL, NT, SCORED>, &C::smem, C::UNIT, C::RP, C::BLOCKS, C::ABREAST};
 }
 

@@ -349,6 +349,7 @@ struct WeighPick {
 template <int DP, int POOL, int NT>
 inline WeighPick weigh_instance() {
     using C = Weigh<DP, POOL, NT>;
+    static_assert(C::BLOCKS * (C::smem(1) + 1024) <= 228 << 10, "blocks that shared memory holds");
     return {weigh_kernel<DP, POOL, NT>, &C::smem, C::UNIT, C::RP, C::BLOCKS, C::ABREAST};
 }
 
