@@ -383,7 +383,8 @@ class KVCache:
         """Tokens' rows out of ``layer``, the inverse of :meth:`append`: (k, v) [T][H][D] (v None for latents),
         new tensors by default, of ``dtype`` (torch.bfloat16 by default, the pool's type if that has 16 bits).
         Padding (a negative position) and tokens out of range give zeros."""
-        T = positions.shape[0] if positions.dim() == 1 else -1
+        T = positions.numel()
+        at = self._list(positions, "positions", T)
         shape = (T, self.kv_heads, self.head_dim)
         if k is None:
             k = self._new(shape, dtype or self._default_dtype, stream)
@@ -406,7 +407,7 @@ class KVCache:
         st = self._read(
             self._handle(), layer,
             _READ.pack(T, self._types[kind], self._list(requests, "requests", T),
-                       self._list(positions, "positions", T), *self._table(block_table), k.data_ptr(), vp, *ks, *vs),
+                       at, *self._table(block_table), k.data_ptr(), vp, *ks, *vs),
             self._raw_stream(index) if stream is None else _stream_handle(stream))
         if st != 0:
             raise KVRelayoutError(st, "kv_cache_read")
@@ -542,7 +543,7 @@ class KVCache:
             os, oh, out_width = self._weight_rows(out, "out", R)
             if out_width != width:
                 raise ValueError(f"out has {out_width} weights a head; weights {width}")
-        shape = (R, self.kv_heads, keep)
+        shape = (R, self.kv_heads, max(keep, 0))             # (the library refuses less than 1)
         if slots is None:
             slots = self._new(shape, self._i32, stream)
             with self._torch.cuda.stream(self._as_stream(stream)):

@@ -43,3 +43,19 @@ def test_read_into_rows_that_overlap(pool):
         for a, b in zip(case.cache.read(0, one, pos, case.dtables[0], **kw), want):
             assert torch.equal(a.contiguous().view(torch.int16), b.view(torch.int16))
     case.cache.check()
+
+
+def test_arguments_of_another_form_are_refused_as_such():
+    """A tensor that does not fit is a ValueError, what the library refuses a KVRelayoutError, and neither is torch's own."""
+    case = Pool(133, [30], 10)
+    pos = torch.arange(6, dtype=torch.int32, device="cuda")
+    for bad in (pos.view(2, 3), pos[0], pos.long(), pos[::2], pos.cpu()):
+        with pytest.raises(ValueError, match="positions"):
+            case.cache.read(0, pos, bad, case.dtables[0])
+    with pytest.raises(ValueError, match="requests"):
+        case.cache.read(0, pos[:5], pos, case.dtables[0])
+    w = case.weights()
+    for keep in (0, -1, -2 ** 31):
+        with pytest.raises(KVRelayoutError, match="INVALID"):
+            case.cache.evict(0, w, case.dlen, case.dtables[0], keep)
+    assert torch.equal(case.dev, case.first)
