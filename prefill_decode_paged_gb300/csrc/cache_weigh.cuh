@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
                 const int32_t rho = row0 + tid, i = (int32_t)a.group.div((uint32_t)rho);
                 const int64_t head = (int64_t)h * a.G + rho - i * a.G;
                 z_own = __ldg(a.lse + ((int64_t)r * a.m + i) * ((int64_t)a.H * a.G) + head);
-                end_own = sp.n - a.m + i + 1;
+                // (one without a sum has nothing to give, whatever its scores are: it sees no key)
+                end_own = z_own == -INFINITY ? 0 : sp.n - a.m + i + 1;
                 slope_own = slope_of(a.scoring, (int32_t)head);
             }
             int32_t next_block;
@@ -237,8 +238,7 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
                 if (Queries::lane() == 0) row_scale[row] = factor;
             }
             if (tid < RP) {
-                // (a row that sees nothing has nothing to give)
-                row_lse[tid] = z_own == -INFINITY ? INFINITY : z_own * log2e;
+                row_lse[tid] = z_own * log2e;
                 row_end[tid] = end_own;
                 row_slope[tid] = slope_own;
             }
@@ -253,7 +253,10 @@ __global__ void __launch_bounds__(ATTEND_THREADS, (Weigh<DP, POOL, NT>::BLOCKS))
                     z[k][e] = row_lse[k * 8 + 2 * t4 + e];
                 }
             const bool plain = a.scoring.cap == 0.0f && a.scoring.slopes == nullptr;
-            const int32_t seen_all = rows < RP ? INT32_MIN : sp.n - a.m + 1;     // keys below it are seen by every row
+            bool none = rows < RP;                                // a row that sees nothing, whatever its place
+#pragma unroll
+            for (int k = 0; k < NT; ++k) none |= z[k][0] == -INFINITY || z[k][1] == -INFINITY;
+            const int32_t seen_all = __any_sync(~0u, none) ? INT32_MIN : sp.n - a.m + 1;   // keys below it are seen by every row
             const int32_t seen_from = a.split.window > 0 ? sp.n - a.split.window : 0;   // keys from it on, by all
 
             // the lane's own key of a tile, and its weight so far, asked for a tile ahead
