@@ -163,7 +163,8 @@ kvr_status kv_cache_append(const kvc_cache *cache, int32_t layer, const kvc_appe
 
 /* The same, with keys and queries rotated by angles[t] (device [num_tokens]; NULL: positions[t]), so that a
  * token may be stored at another place than its own: behind what an eviction has left. An angle below zero, or
- * beyond the rotation table, is KVC_FLAG_POSITION and nothing of that token is written. */
+ * beyond the rotation table, is KVC_FLAG_POSITION and nothing of that token is written (without a table angles are not
+ * looked at). */
 kvr_status kv_cache_append_at(const kvc_cache *cache, int32_t layer, const kvc_append *args,
                               const int32_t *angles, void *stream);
 
@@ -203,7 +204,8 @@ kvr_status kv_cache_read(const kvc_cache *cache, int32_t layer, const kvc_read *
  * Weights below 2^-24 of a row's largest count as zero where the cache holds f16, E4M3 or E2M1. Before they
  * meet the values, weights count with 15 bits or more over bf16 and f16 keys and values and under at most
  * 32 rows (num_new Hq) of latents, with those of an f16 over E4M3 and E2M1, and with those of the pool's type
- * under more rows of latents; sums are fp32.
+ * under more rows of latents; sums are fp32. Over E4M3 and E2M1 a query counts as f16 numbers times a power of two:
+ * elements below 2^-14 of its largest are rounded to multiples of 2^-24 of that.
  * Requirements: q and out of `dtype` (the pool's type if that has 16 bits), rows contiguous,
  * every address and stride a multiple of 16 bytes; lse NULL or [R][num_new][Hq], contiguous.
  */
@@ -229,7 +231,9 @@ kvr_status kv_cache_attend(const kvc_cache *cache, int32_t layer, const kvc_atte
 /*
  * Scores of another form, over keys and values (KVR_ERR_UNSUPPORTED over latents): in the formulas above x_j is
  *   x_j = cap tanh(scale q . k_j / cap) + slopes[g] (j - p),    without cap where that is 0,
- * for a query of head g at position p. Scores are fp32.
+ * for a query of head g at position p. Scores are fp32; a capped one is within 2^-19 of itself, besides what the score
+ * before it is off by. Positions count the cached tokens: distances, and windows, are between slots where an eviction has
+ * moved tokens together.
  */
 typedef struct kvc_scoring {
     float cap;                 /* 0: none; otherwise 2^-100 to 2^100 */

@@ -16,6 +16,11 @@
 // HBM), E4M3 96 to 102 (5.4 to 5.8), 4 bits 68 (4.7; conversions). 4 requests of up to 32768 E4M3 keys under 64 rows
 // 38.7 us: mma.sync at 57 % of its rate. With 32 rows a pass, which takes the keys and their conversion twice, and tiles
 // of 16 keys it took 1.4 and 1.04 times as long.
+//
+// Tiles take the form with a mask, each score compared with its row's end, where scores are capped or biased, rows do not
+// fill the instance, or a row sees nothing: 64 requests of 8192 keys capped 173 us in bf16, 119 in E4M3, 93 in 4 bits,
+// biased 172, 110 and 79; under 4 of 8 rows 171, 104 and 73. (4 bits in blocks of 16 tokens, each lane looking its own
+// key up, 75.)
 #pragma once
 
 #include "cache_attend.cuh"

@@ -1,8 +1,8 @@
 """ctypes binding of the C ABI in ``include/kv_cache.h`` (argument marshalling only).
 
 What a decode instance does with the KV it was handed: :class:`KVCache` appends new tokens to
-one shard pool, attends to it, and evicts what got little attention; :func:`rotary_table` fills the table of rotations. Every step
-runs in the CUDA library; there is no fallback.
+one shard pool, attends to it, and evicts what got little attention; :func:`rotary_table` fills the
+table of rotations. Every step runs in the CUDA library; there is no fallback.
 """
 from __future__ import annotations
 
@@ -419,7 +419,8 @@ class KVCache:
         [R][Hq][D] for one; ``lengths`` int32 [R] counts the cached tokens, the newest included.
         ``scale``: D ** -0.5 by default; ``window`` > 0: only that many keys, the token's own
         included. ``cap`` > 0: scores become cap tanh(score / cap); ``slopes`` float32 [Hq]: the score of a key
-        d tokens before the query is lowered by slopes[head] d. Returns (out, lse): ``out`` like q with ``value_dim`` elements, ``lse`` float32
+        d tokens before the query is lowered by slopes[head] d. Distances, those of ``window`` too, are between slots: after an
+        eviction they are not those of the text. Returns (out, lse): ``out`` like q with ``value_dim`` elements, ``lse`` float32
         [R][new][Hq], new tensors by default (``lse=False``: none)."""
         if q.requires_grad:
             self._refuse_gradients()
