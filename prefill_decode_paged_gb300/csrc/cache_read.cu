@@ -148,7 +148,7 @@ kvr_status go(ReadArgs &a, int sms, void *stream) {
     const int64_t n = (int64_t)a.H * a.units.d, rounds = (n + MOST_THREADS - 1) / MOST_THREADS;
     const int threads = (int)((n + 32 * rounds - 1) / (32 * rounds)) * 32;
     if (a.tokens > 16 * sms)
-        return kvc_launch(read_kernel<POOL, F16, 2>, a, dim3((unsigned)((a.tokens + 1) / 2)), threads, 0, stream);
+        return kvc_launch(read_kernel<POOL, F16, 2>, a, dim3((unsigned)(a.tokens / 2 + a.tokens % 2)), threads, 0, stream);
     return kvc_launch(read_kernel<POOL, F16, 1>, a, dim3((unsigned)a.tokens), threads, 0, stream);
 }
 
